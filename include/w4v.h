@@ -404,6 +404,172 @@ w4v_status gdn_step(float *state, const uint16_t *k_prev, const uint16_t *v_prev
                     const float *beta, int B, int T, int H, int dk, int dv, uint16_t *o,
                     w4v_stream_t stream);
 
+/* ------------------------------------------------- paged key/value cache --
+ * What follows serves the target's softmax-attention layers, which a hybrid
+ * target has next to its recurrent ones.  The pages give no layout; this is
+ * the library's own.
+ *
+ * One layer's cache is two device arrays of pages, k and v, each fp16
+ * [n_pages][kv_heads][page][head_dim]; a page holds `page` consecutive tokens
+ * of one sequence.  Row b of `table` lists sequence b's pages in token order
+ * (token p lies in page table[b][p / page], slot p % page); entries past the
+ * sequence's last page are never read.  lengths[b] counts the sequence's
+ * cached tokens INCLUDING the new ones of the call, and offsets[b] ..
+ * offsets[b+1]-1 are the rows of q, k, v that hold its new tokens (none when
+ * the two are equal), so new row offsets[b] + i of n sits at position
+ * lengths[b] - n + i.  A block of K+1 verified positions, one decoded token
+ * and a chunk of a prompt are all this one form, mixed freely in a batch.
+ *   - head_dim 64, 128 or 256; page a power of two, 8 to 256; kv_heads >= 1;
+ *     table_width * page < 2^31; n_pages * kv_heads * page < 2^34.
+ *   - The device arrays are read as they are: a length is clamped to
+ *     [0, table_width * page], an offset to [0, n_tokens], and a page id
+ *     outside [0, n_pages) is never followed (a read gives zeros, a write is
+ *     dropped).
+ *   - table, lengths and offsets are int32 on the device, so a captured
+ *     graph can be replayed while they change. */
+typedef struct {
+    uint16_t *k, *v;
+    const int32_t *table;      /* [B][table_width] */
+    const int32_t *lengths;    /* [B]              */
+    const int32_t *offsets;    /* [B+1]            */
+    int B, table_width, n_pages, kv_heads, page, head_dim;
+} w4v_kv_t;
+
+/* ------------------------------------------------------------ rope_append
+ * Rotary positions, and the new tokens' keys and values into the cache.
+ * With phi_i = p f_i at position p, pair i of the first `rot` elements of
+ * every query and key head becomes
+ *     (x_a, x_b) -> mul (x_a cos phi_i - x_b sin phi_i,
+ *                        x_b cos phi_i + x_a sin phi_i),
+ * (a, b) = (i, i + rot/2), or (2i, 2i+1) with W4V_ROPE_INTERLEAVED; elements
+ * from rot on and the values are copied.  Arithmetic is fp32, rounded to
+ * fp16 once.  Rotated queries go to q_out, keys and values to their pages.
+ *   q, k, v     device, fp16 rows of q_heads / kv_heads / kv_heads heads of
+ *               head_dim elements; *_stride elements from row to row (a
+ *               multiple of 8, so the three may be slices of one projection's
+ *               output)
+ *   positions   device, int32 [n_tokens] or NULL: the rotation's position of
+ *               each row where it is not the cache position
+ *   phases      device, uint64 [rot/2]: the fraction of a full turn that one
+ *               position adds to pair i, times 2^64 (rope_phases).  p * phase
+ *               mod 2^64 is exact, so no position is too long.
+ *   q_out       device, fp16 [n_tokens][q_heads][head_dim]; may be q itself
+ *               where q is dense
+ * A row that no sequence's offsets cover is left alone.
+ * Sizes: n_tokens >= 0 (0 is a no-op), q_heads >= 1, rot even,
+ * 0 <= rot <= head_dim. */
+#define W4V_ROPE_INTERLEAVED 4u
+w4v_status rope_append(const w4v_kv_t *kv, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                       long long q_stride, long long k_stride, long long v_stride, int n_tokens, int q_heads,
+                       const int32_t *positions, const uint64_t *phases, int rot, float mul, unsigned flags,
+                       uint16_t *q_out, w4v_stream_t stream);
+
+/* Host only: phases and mul of a base and a scaling for long contexts.
+ * f_i = base^(-2i/rot), then
+ *   W4V_ROPE_PLAIN    as it is;
+ *   W4V_ROPE_LINEAR   f_i / factor                       params = {factor}
+ *   W4V_ROPE_NTK      base * factor^(rot/(rot-2)) for base       {factor}
+ *   W4V_ROPE_YARN     f_i / factor for slow pairs, f_i for fast ones, a ramp
+ *                     over the pair index between the pairs that turn
+ *                     `slow` and `fast` times in `context` tokens;
+ *                     mul = 0.1 ln(factor) + 1      {factor, context, fast, slow}
+ *   W4V_ROPE_BANDED   the same by a ramp over the turns themselves, from
+ *                     `low` to `high`               {factor, low, high, context}
+ * mul is 1 where not stated.  params holds 4 doubles (NULL for PLAIN). */
+typedef enum {
+    W4V_ROPE_PLAIN = 0, W4V_ROPE_LINEAR = 1, W4V_ROPE_NTK = 2, W4V_ROPE_YARN = 3, W4V_ROPE_BANDED = 4
+} w4v_rope_scaling;
+w4v_status rope_phases(int rot, double base, int scaling, const double *params, uint64_t *phases_out,
+                       float *mul_out);
+
+/* ------------------------------------------------------------- paged_attn
+ * Causal attention of the new tokens over the cache that holds them:
+ *     o_t = sum_j softmax_j(scale q_t . k_j) v_j   over p_t - window < j <= p_t
+ * (window 0: every j <= p_t), p_t the row's position, query head h reading
+ * key/value head h / (q_heads / kv_heads).  Scores, softmax statistics and
+ * sums are fp32; the weights enter the product with v as fp16 (11 significant
+ * bits, scaled by up to 2^14 so that none above 2^-38 of the largest is
+ * lost).  A row that sees no token gives zeros and lse = -inf.  What the
+ * cache holds past a sequence's length is never used.
+ *   q      device, fp16 rows of q_heads heads, q_stride elements apart
+ *   out    device, fp16 [n_tokens][q_heads][head_dim] (written, never read)
+ *   lse    device, float [n_tokens][q_heads] or NULL:
+ *          ln sum_j exp(scale q_t . k_j)
+ * Sizes: n_tokens >= 0 (0 is a no-op), q_heads a multiple of kv_heads and at
+ * most 128 times as many, scale > 0 and finite, window >= 0.
+ * W4V_BATCH_INVARIANT: each row's result is bit for bit the same whatever
+ * rows and sequences share the call and however many new tokens come with
+ * it, so verified positions equal the one-token steps they stand for.
+ * Without it the contexts are cut where that balances the GPU.
+ * Workspace: paged_attn_workspace_bytes(...) with the call's own n_tokens and
+ * B or larger ones, max_context = table_width * page; zero-filled before
+ * first use.  With W4V_BATCH_INVARIANT it grows with the number of rows times
+ * up to 32 pieces of the context, so a long prompt goes through in chunks. */
+size_t paged_attn_workspace_bytes(int n_tokens, int B, int q_heads, int kv_heads, int head_dim, int max_context,
+                                  unsigned flags);
+w4v_status paged_attn(const w4v_kv_t *kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
+                      float scale, int window, uint16_t *out, float *lse, void *workspace,
+                      size_t workspace_bytes, unsigned flags, w4v_stream_t stream);
+
+/* ------------------------------------------------------------ kv_* pages --
+ * Bookkeeping of the pages, on the device (the accepted lengths that drive
+ * it are there).  A page id stands for that page of every plane: pool is
+ * [planes][n_pages][page_bytes], for instance layer l's k in plane 2l and v
+ * in plane 2l+1.  refs[p] counts the sequences that hold page p (0: free).
+ * Free pages are handed out lowest id first, to sequences in ascending order.
+ *   pool     device, page_bytes a multiple of 16 (only what copies needs it)
+ *   refs     device, int32 [n_pages]
+ *   table    device, int32 [S][table_width]; entries past a row's last page
+ *            are -1 once one of these calls has dropped or forked the row
+ *   lengths  device, int32 [S]
+ * Sizes: 1 <= n_pages <= 2^24, 0 <= S <= 65535 (0 is a no-op),
+ * table_width >= 1, page a power of two, 8 to 256, table_width * page < 2^31.
+ * Workspace: kv_workspace_bytes(n_pages, S), zero-filled before first use. */
+typedef struct {
+    void *pool;
+    int32_t *refs, *table, *lengths;
+    size_t page_bytes;
+    int planes, n_pages, S, table_width, page;
+} w4v_pages_t;
+size_t kv_workspace_bytes(int n_pages, int S);
+
+/* Pages for new_lengths[s] >= lengths[s] tokens (a smaller one changes
+ * nothing).  A last page that is partly filled and shared is first replaced
+ * by a copy of its own, so that appending never touches another sequence.
+ * All or nothing: *short_out (device) is 0, or the number of pages that are
+ * missing, or -1 if a new length does not fit its table row; then nothing is
+ * changed. */
+w4v_status kv_extend(const w4v_pages_t *pages, const int32_t *new_lengths, int32_t *short_out, void *workspace,
+                     size_t workspace_bytes, w4v_stream_t stream);
+
+/* Lengths down to new_lengths[s] (a larger one changes nothing, a negative
+ * one counts as 0); pages that are no longer needed lose one reference, and
+ * are free when none is left.  Rolls back rejected drafts; 0 ends a sequence.
+ * No workspace; pool is not used. */
+w4v_status kv_truncate(const w4v_pages_t *pages, const int32_t *new_lengths, w4v_stream_t stream);
+
+/* Sequence children[i] becomes a copy of parents[i]: full pages are shared,
+ * a partly filled last page is copied.  Children must be empty, named once
+ * and no parents.  *short_out: 0, the number of pages that are missing, or -1
+ * for an index outside [0, S) or such a child; then nothing is changed.
+ * 0 <= n <= S. */
+w4v_status kv_fork(const w4v_pages_t *pages, const int32_t *parents, const int32_t *children, int n,
+                   int32_t *short_out, void *workspace, size_t workspace_bytes, w4v_stream_t stream);
+
+/* Live pages at or above their count move, in ascending order, to the free
+ * pages below it, in ascending order, so that all live pages come first.
+ * refs_out / table_out get the new counts and tables; they may be the old
+ * arrays.  Moved pages keep their old contents until they are handed out
+ * again, so a step in flight may finish on the old tables. */
+w4v_status kv_compact(const w4v_pages_t *pages, int32_t *refs_out, int32_t *table_out, void *workspace,
+                      size_t workspace_bytes, w4v_stream_t stream);
+
+/* Contents of page src[i] to page dst[i] in every plane, i < n (device int32;
+ * a pair with an id outside [0, n_pages) is skipped).  No page of dst may be
+ * named twice or be in src. */
+w4v_status kv_copy(void *pool, int planes, int n_pages, size_t page_bytes, const int32_t *src,
+                   const int32_t *dst, int n, w4v_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,7 @@
 // api.cpp -- the C ABI: argument validation (before anything touches the
 // GPU), workspace sizing, the host int4 packer, and dispatch to launchers.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "runtime.h"
@@ -364,6 +365,213 @@ w4v_status spec_accept(const int32_t *target, const int32_t *draft, int B, int K
         return W4V_ERR_ALIGN;
     return w4v::launch_spec_accept(target, draft, B, K, n_accepted, out_tokens,
                                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool page_ok(int page) { return page >= 8 && page <= 256 && (page & (page - 1)) == 0; }
+
+// The cache, and the rows that go with it (after n_tokens == 0 returned).
+w4v_status kv_check(const w4v_kv_t *kv, int n_tokens, int q_heads) {
+    if (kv == nullptr) return W4V_ERR_ARG;
+    const int D = kv->head_dim;
+    if (n_tokens < 0 || q_heads < 1 || kv->B < 0 || kv->table_width < 1 || kv->n_pages < 1 || kv->kv_heads < 1 ||
+        !page_ok(kv->page) || (D != 64 && D != 128 && D != 256))
+        return W4V_ERR_SHAPE;
+    if ((long long)kv->table_width * kv->page >= 1ll << 31) return W4V_ERR_SHAPE;
+    if ((long long)kv->n_pages * kv->kv_heads >= (1ll << 34) / kv->page) return W4V_ERR_SHAPE;
+    if (n_tokens == 0 || kv->B == 0) return W4V_OK;
+    if (kv->k == nullptr || kv->v == nullptr || kv->table == nullptr || kv->lengths == nullptr ||
+        kv->offsets == nullptr)
+        return W4V_ERR_ARG;
+    if (!w4v::aligned16(kv->k) || !w4v::aligned16(kv->v) || !aligned4(kv->table) || !aligned4(kv->lengths) ||
+        !aligned4(kv->offsets))
+        return W4V_ERR_ALIGN;
+    return W4V_OK;
+}
+bool stride_ok(long long stride, int heads, int head_dim) {
+    return stride % 8 == 0 && stride >= (long long)heads * head_dim && stride < 1ll << 38;
+}
+}  // namespace
+
+w4v_status rope_append(const w4v_kv_t *kv, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                       long long q_stride, long long k_stride, long long v_stride, int n_tokens, int q_heads,
+                       const int32_t *positions, const uint64_t *phases, int rot, float mul, unsigned flags,
+                       uint16_t *q_out, w4v_stream_t stream) {
+    if ((flags & ~unsigned(W4V_ROPE_INTERLEAVED)) != 0u) return W4V_ERR_ARG;
+    const w4v_status st = kv_check(kv, n_tokens, q_heads);
+    if (st != W4V_OK) return st;
+    const int D = kv->head_dim, Hk = kv->kv_heads;
+    if (rot < 0 || rot > D || rot % 2 != 0 || !stride_ok(q_stride, q_heads, D) || !stride_ok(k_stride, Hk, D) ||
+        !stride_ok(v_stride, Hk, D))
+        return W4V_ERR_SHAPE;
+    if (n_tokens == 0 || kv->B == 0) return W4V_OK;
+    if (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr || (rot > 0 && phases == nullptr))
+        return W4V_ERR_ARG;
+    if (q_out == q && q_stride != (long long)q_heads * D) return W4V_ERR_ARG;
+    if (!w4v::aligned16(q) || !w4v::aligned16(k) || !w4v::aligned16(v) || !w4v::aligned16(q_out) ||
+        !aligned4(positions) || (reinterpret_cast<uintptr_t>(phases) & 7u) != 0u)
+        return W4V_ERR_ALIGN;
+    return w4v::launch_rope_append(*kv, q, k, v, q_stride, k_stride, v_stride, n_tokens, q_heads, positions, phases,
+                                   rot, mul, (flags & W4V_ROPE_INTERLEAVED) != 0u, q_out,
+                                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+w4v_status rope_phases(int rot, double base, int scaling, const double *params, uint64_t *phases, float *mul_out) {
+    if (scaling < W4V_ROPE_PLAIN || scaling > W4V_ROPE_BANDED || phases == nullptr || mul_out == nullptr ||
+        (scaling != W4V_ROPE_PLAIN && params == nullptr))
+        return W4V_ERR_ARG;
+    if (rot < 2 || rot % 2 != 0 || rot > 256 || !(base > 1.0) || !std::isfinite(base)) return W4V_ERR_SHAPE;
+    const double factor = scaling != W4V_ROPE_PLAIN ? params[0] : 1.0;
+    if (!(factor >= 1.0) || !std::isfinite(factor)) return W4V_ERR_SHAPE;
+    constexpr double kTurn = 6.283185307179586476925286766559;
+    double lo = 0.0, hi = 1.0, context = 0.0;
+    *mul_out = 1.f;
+    if (scaling == W4V_ROPE_NTK) {
+        if (rot == 2) return W4V_ERR_SHAPE;
+        base *= std::pow(factor, double(rot) / (rot - 2));
+    } else if (scaling == W4V_ROPE_YARN) {
+        context = params[1];
+        const double fast = params[2], slow = params[3];
+        if (!(context > 0.0) || !(slow > 0.0) || !(fast > slow)) return W4V_ERR_SHAPE;
+        // the pair index that turns b times in `context` positions
+        auto pair = [&](double b) { return rot * std::log(context / (b * kTurn)) / (2.0 * std::log(base)); };
+        lo = std::max(std::floor(pair(fast)), 0.0);
+        hi = std::min(std::ceil(pair(slow)), rot - 1.0);
+        *mul_out = float(0.1 * std::log(factor) + 1.0);
+    } else if (scaling == W4V_ROPE_BANDED) {
+        lo = params[1];
+        hi = params[2];
+        context = params[3];
+        if (!(context > 0.0) || !(lo > 0.0) || !(hi > lo)) return W4V_ERR_SHAPE;
+    }
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot);
+        if (scaling == W4V_ROPE_LINEAR) f /= factor;
+        if (scaling == W4V_ROPE_YARN) {
+            const double slow_part = std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
+            f = f / factor * slow_part + f * (1.0 - slow_part);
+        }
+        if (scaling == W4V_ROPE_BANDED) {
+            const double kept = std::min(std::max((context * f / kTurn - lo) / (hi - lo), 0.0), 1.0);
+            f = f / factor * (1.0 - kept) + f * kept;
+        }
+        phases[i] = uint64_t(std::ldexp(f / kTurn, 64));      // f <= 1 radian: below 2^62
+    }
+    return W4V_OK;
+}
+
+size_t paged_attn_workspace_bytes(int n_tokens, int B, int q_heads, int kv_heads, int head_dim, int max_context,
+                                  unsigned flags) {
+    if (n_tokens < 0 || B < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 ||
+        q_heads / kv_heads > w4v::kAttnMaxGroup || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+        max_context < 0 || (flags & ~unsigned(W4V_BATCH_INVARIANT)) != 0u)
+        return 0;
+    return w4v::paged_attn_ws_bytes(n_tokens, B, q_heads, kv_heads, head_dim, max_context,
+                                    (flags & W4V_BATCH_INVARIANT) != 0u);
+}
+
+w4v_status paged_attn(const w4v_kv_t *kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
+                      float scale, int window, uint16_t *out, float *lse, void *ws, size_t ws_bytes, unsigned flags,
+                      w4v_stream_t stream) {
+    if ((flags & ~unsigned(W4V_BATCH_INVARIANT)) != 0u) return W4V_ERR_ARG;
+    const w4v_status st = kv_check(kv, n_tokens, q_heads);
+    if (st != W4V_OK) return st;
+    if (q_heads % kv->kv_heads != 0 || q_heads / kv->kv_heads > w4v::kAttnMaxGroup || window < 0 ||
+        !stride_ok(q_stride, q_heads, kv->head_dim))
+        return W4V_ERR_SHAPE;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return W4V_ERR_ARG;
+    if (n_tokens == 0 || kv->B == 0) return W4V_OK;
+    if (q == nullptr || out == nullptr) return W4V_ERR_ARG;
+    if (!w4v::aligned16(q) || !w4v::aligned16(out) || !aligned4(lse)) return W4V_ERR_ALIGN;
+    const bool inv = (flags & W4V_BATCH_INVARIANT) != 0u;
+    if (ws == nullptr || ws_bytes < w4v::paged_attn_ws_bytes(n_tokens, kv->B, q_heads, kv->kv_heads, kv->head_dim,
+                                                             kv->table_width * kv->page, inv))
+        return W4V_ERR_WORKSPACE;
+    if (!w4v::aligned16(ws)) return W4V_ERR_ALIGN;
+    return w4v::launch_paged_attn(*kv, q, q_stride, n_tokens, q_heads, scale, window, out, lse, ws, inv,
+                                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t kv_workspace_bytes(int n_pages, int S) {
+    if (n_pages < 1 || n_pages > 1 << 24 || S < 0 || S > 65535) return 0;
+    return w4v::kv_pages_ws_bytes(n_pages, S);
+}
+
+namespace {
+w4v_status pages_check(const w4v_pages_t *g, bool copies) {
+    if (g == nullptr) return W4V_ERR_ARG;
+    if (g->n_pages < 1 || g->n_pages > 1 << 24 || g->S < 0 || g->S > 65535 || g->table_width < 1 ||
+        !page_ok(g->page) || (long long)g->table_width * g->page >= 1ll << 31)
+        return W4V_ERR_SHAPE;
+    if (copies && (g->planes < 0 || g->page_bytes % 16 != 0 || g->page_bytes >= size_t(1) << 31)) return W4V_ERR_SHAPE;
+    if (g->S == 0) return W4V_OK;
+    if (g->refs == nullptr || g->table == nullptr || g->lengths == nullptr ||
+        (copies && g->planes > 0 && g->pool == nullptr))
+        return W4V_ERR_ARG;
+    if (!aligned4(g->refs) || !aligned4(g->table) || !aligned4(g->lengths) || (copies && !w4v::aligned16(g->pool)))
+        return W4V_ERR_ALIGN;
+    return W4V_OK;
+}
+w4v_status pages_ws_check(const w4v_pages_t *g, const void *ws, size_t ws_bytes) {
+    if (ws == nullptr || ws_bytes < w4v::kv_pages_ws_bytes(g->n_pages, g->S)) return W4V_ERR_WORKSPACE;
+    return w4v::aligned16(ws) ? W4V_OK : W4V_ERR_ALIGN;
+}
+}  // namespace
+
+w4v_status kv_extend(const w4v_pages_t *pages, const int32_t *new_lengths, int32_t *short_out, void *ws,
+                     size_t ws_bytes, w4v_stream_t stream) {
+    w4v_status st = pages_check(pages, true);
+    if (st != W4V_OK || pages->S == 0) return st;
+    if (new_lengths == nullptr || short_out == nullptr) return W4V_ERR_ARG;
+    if (!aligned4(new_lengths) || !aligned4(short_out)) return W4V_ERR_ALIGN;
+    st = pages_ws_check(pages, ws, ws_bytes);
+    if (st != W4V_OK) return st;
+    return w4v::launch_kv_extend(*pages, new_lengths, short_out, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+w4v_status kv_truncate(const w4v_pages_t *pages, const int32_t *new_lengths, w4v_stream_t stream) {
+    const w4v_status st = pages_check(pages, false);
+    if (st != W4V_OK || pages->S == 0) return st;
+    if (new_lengths == nullptr) return W4V_ERR_ARG;
+    if (!aligned4(new_lengths)) return W4V_ERR_ALIGN;
+    return w4v::launch_kv_truncate(*pages, new_lengths, reinterpret_cast<cudaStream_t>(stream));
+}
+
+w4v_status kv_fork(const w4v_pages_t *pages, const int32_t *parents, const int32_t *children, int n,
+                   int32_t *short_out, void *ws, size_t ws_bytes, w4v_stream_t stream) {
+    w4v_status st = pages_check(pages, true);
+    if (st != W4V_OK) return st;
+    if (n < 0 || n > pages->S) return W4V_ERR_SHAPE;
+    if (pages->S == 0) return W4V_OK;
+    if ((n > 0 && (parents == nullptr || children == nullptr)) || short_out == nullptr) return W4V_ERR_ARG;
+    if (!aligned4(parents) || !aligned4(children) || !aligned4(short_out)) return W4V_ERR_ALIGN;
+    st = pages_ws_check(pages, ws, ws_bytes);
+    if (st != W4V_OK) return st;
+    return w4v::launch_kv_fork(*pages, parents, children, n, short_out, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+w4v_status kv_compact(const w4v_pages_t *pages, int32_t *refs_out, int32_t *table_out, void *ws, size_t ws_bytes,
+                      w4v_stream_t stream) {
+    w4v_status st = pages_check(pages, true);
+    if (st != W4V_OK || pages->S == 0) return st;
+    if (refs_out == nullptr || table_out == nullptr) return W4V_ERR_ARG;
+    if (!aligned4(refs_out) || !aligned4(table_out)) return W4V_ERR_ALIGN;
+    st = pages_ws_check(pages, ws, ws_bytes);
+    if (st != W4V_OK) return st;
+    return w4v::launch_kv_compact(*pages, refs_out, table_out, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+w4v_status kv_copy(void *pool, int planes, int n_pages, size_t page_bytes, const int32_t *src, const int32_t *dst,
+                   int n, w4v_stream_t stream) {
+    if (planes < 1 || n_pages < 1 || n_pages > 1 << 24 || page_bytes == 0 || page_bytes % 16 != 0 ||
+        page_bytes >= size_t(1) << 31 || n < 0)
+        return W4V_ERR_SHAPE;
+    if (n == 0) return W4V_OK;
+    if (pool == nullptr || src == nullptr || dst == nullptr) return W4V_ERR_ARG;
+    if (!w4v::aligned16(pool) || !aligned4(src) || !aligned4(dst)) return W4V_ERR_ALIGN;
+    return w4v::launch_kv_copy(pool, planes, n_pages, page_bytes, src, dst, n,
+                               reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

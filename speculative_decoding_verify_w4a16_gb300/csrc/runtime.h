@@ -143,4 +143,27 @@ size_t w8_lmhead_ws_bytes(int M, int V);
 w4v_status launch_spec_accept(const int32_t *target, const int32_t *draft, int B, int K,
                               int32_t *n_accepted, int32_t *out_tokens, cudaStream_t stream);
 
+// Paged key/value cache: rotary positions and appending, attention, pages.
+w4v_status launch_rope_append(const w4v_kv_t &kv, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                              long long q_stride, long long k_stride, long long v_stride, int n_tokens, int q_heads,
+                              const int32_t *positions, const uint64_t *phases, int rot, float mul, bool interleaved,
+                              uint16_t *q_out, cudaStream_t stream);
+// Largest query heads per key/value head (a tile's 128 rows hold one token's).
+constexpr int kAttnMaxGroup = 128;
+size_t paged_attn_ws_bytes(int n_tokens, int B, int q_heads, int kv_heads, int head_dim, int max_context,
+                           bool invariant);
+w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
+                             float scale, int window, uint16_t *out, float *lse, void *ws, bool invariant,
+                             cudaStream_t stream);
+size_t kv_pages_ws_bytes(int n_pages, int S);
+w4v_status launch_kv_extend(const w4v_pages_t &pages, const int32_t *want, int32_t *short_out, void *ws,
+                            cudaStream_t stream);
+w4v_status launch_kv_truncate(const w4v_pages_t &pages, const int32_t *want, cudaStream_t stream);
+w4v_status launch_kv_fork(const w4v_pages_t &pages, const int32_t *parents, const int32_t *children, int n,
+                          int32_t *short_out, void *ws, cudaStream_t stream);
+w4v_status launch_kv_compact(const w4v_pages_t &pages, int32_t *refs_out, int32_t *table_out, void *ws,
+                             cudaStream_t stream);
+w4v_status launch_kv_copy(void *pool, int planes, int n_pages, size_t page_bytes, const int32_t *src,
+                          const int32_t *dst, int n, cudaStream_t stream);
+
 }  // namespace w4v

@@ -39,6 +39,21 @@ class GroupedHandle(ctypes.Structure):
                 ("check", ctypes.c_uint)]
 
 
+class KV(ctypes.Structure):
+    """w4v_kv_t (include/w4v.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("B", ctypes.c_int),
+                ("table_width", ctypes.c_int), ("n_pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("page", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class Pages(ctypes.Structure):
+    """w4v_pages_t (include/w4v.h)."""
+    _fields_ = [("pool", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t), ("planes", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("S", ctypes.c_int), ("table_width", ctypes.c_int), ("page", ctypes.c_int)]
+
+
 class W4VError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -101,6 +116,27 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.gdn_commit.restype = I
             lib.gdn_step.argtypes = [P, P, P, P, P, P, I, P, P, P, P, P, I, I, I, I, I, P, P]
             lib.gdn_step.restype = I
+            L, F, U = ctypes.c_longlong, ctypes.c_float, ctypes.c_uint
+            lib.rope_append.argtypes = [P, P, P, P, L, L, L, I, I, P, P, I, F, U, P, P]
+            lib.rope_append.restype = I
+            lib.rope_phases.argtypes = [I, ctypes.c_double, I, P, P, P]
+            lib.rope_phases.restype = I
+            lib.paged_attn_workspace_bytes.argtypes = [I, I, I, I, I, I, U]
+            lib.paged_attn_workspace_bytes.restype = S
+            lib.paged_attn.argtypes = [P, P, L, I, I, F, I, P, P, P, S, U, P]
+            lib.paged_attn.restype = I
+            lib.kv_workspace_bytes.argtypes = [I, I]
+            lib.kv_workspace_bytes.restype = S
+            lib.kv_extend.argtypes = [P, P, P, P, S, P]
+            lib.kv_extend.restype = I
+            lib.kv_truncate.argtypes = [P, P, P]
+            lib.kv_truncate.restype = I
+            lib.kv_fork.argtypes = [P, P, P, I, P, P, S, P]
+            lib.kv_fork.restype = I
+            lib.kv_compact.argtypes = [P, P, P, P, S, P]
+            lib.kv_compact.restype = I
+            lib.kv_copy.argtypes = [P, I, I, S, P, P, I, P]
+            lib.kv_copy.restype = I
             _lib = lib
     return _lib
 
@@ -362,3 +398,239 @@ def gdn_commit(state, k, v, alpha, beta, n_accepted, stream=None):
                              dk, dv, _stream(stream))
     _check(code, "gdn_commit")
     return state
+
+
+# ---------------------------------------------------------------- paged cache --
+ROPE_INTERLEAVED = 4
+ROPE_SCALINGS = {"linear": (1, 1), "ntk": (2, 1), "yarn": (3, 4), "banded": (4, 4)}
+
+
+class Rope:
+    """Rotary positions of `rot` elements a head (rope_phases): the phase table on
+    the device and the factor of cos and sin.  scaling: None, ("linear", factor),
+    ("ntk", factor), ("yarn", factor, context[, fast = 32, slow = 1]) or
+    ("banded", factor, low, high, context)."""
+
+    def __init__(self, rot: int, base: float = 10000.0, interleaved: bool = False, scaling=None, device="cuda"):
+        import torch
+        self.rot, self.interleaved = int(rot), bool(interleaved)
+        phases, mul = np.zeros(max(self.rot // 2, 1), np.uint64), ctypes.c_float(1.0)
+        if self.rot:
+            kind, params = 0, None
+            if scaling is not None:
+                if scaling[0] not in ROPE_SCALINGS:
+                    raise W4VError(ERR_ARG, "rope_phases")
+                kind, count = ROPE_SCALINGS[scaling[0]]
+                values = [float(x) for x in scaling[1:]]
+                if scaling[0] == "yarn":
+                    values += [32.0, 1.0][len(values) - 2:] if len(values) >= 2 else []
+                if len(values) != count:
+                    raise W4VError(ERR_ARG, "rope_phases")
+                params = (ctypes.c_double * 4)(*values)
+            _check(load().rope_phases(self.rot, float(base), kind, params, phases.ctypes.data, ctypes.byref(mul)),
+                   "rope_phases")
+        self.mul = mul.value
+        self.phases = torch.from_numpy(phases.view(np.int64)).to(device)
+
+
+def _typed(where, dtype, *tensors):
+    for t in tensors:
+        if t is not None and t.dtype != dtype:
+            raise W4VError(ERR_ARG, where)
+
+
+def _dense(where, *tensors):
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            raise W4VError(ERR_ARG, where)
+
+
+def _rows(where, t, heads, head_dim):
+    """Row stride of a [tokens][heads][head_dim] tensor whose rows are dense."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise W4VError(ERR_SHAPE, where)
+    if t.shape[0] > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
+        raise W4VError(ERR_ARG, where)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * head_dim) if t.shape[0] else heads * head_dim
+
+
+def _kv(where, k_cache, v_cache, table, lengths, offsets):
+    import torch
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or table.dim() != 2:
+        raise W4VError(ERR_SHAPE, where)
+    B = table.shape[0]
+    if lengths.shape != (B,) or offsets.shape != (B + 1,):
+        raise W4VError(ERR_SHAPE, where)
+    _typed(where, torch.float16, k_cache, v_cache)
+    _typed(where, torch.int32, table, lengths, offsets)
+    _dense(where, k_cache, v_cache, table, lengths, offsets)
+    n_pages, heads, page, D = k_cache.shape
+    return KV(_ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(lengths), _ptr(offsets), B, table.shape[1], n_pages,
+              heads, page, D)
+
+
+def rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: Rope, q_out=None, positions=None,
+                stream=None):
+    """Rotate the new tokens' q [n][Hq][D] and k [n][Hkv][D] by their positions, write k and v [n][Hkv][D]
+    into their pages of k_cache, v_cache [n_pages][Hkv][page][D] and return the rotated q.  q, k, v may
+    be slices of one projection's rows; lengths count the new tokens.  positions: int32 [n], where the
+    rotation's position is not the cache position."""
+    import torch
+    where = "rope_append"
+    kv = _kv(where, k_cache, v_cache, table, lengths, offsets)
+    n, Hq = q.shape[0], q.shape[1]
+    strides = [_rows(where, q, Hq, kv.head_dim), _rows(where, k, kv.kv_heads, kv.head_dim),
+               _rows(where, v, kv.kv_heads, kv.head_dim)]
+    if k.shape[0] != n or v.shape[0] != n or (positions is not None and positions.shape != (n,)):
+        raise W4VError(ERR_SHAPE, where)
+    if q_out is None:
+        q_out = torch.empty((n, Hq, kv.head_dim), dtype=torch.float16, device=q.device)
+    elif q_out.shape != q.shape:
+        raise W4VError(ERR_SHAPE, where)
+    _typed(where, torch.float16, q, k, v, q_out)
+    _typed(where, torch.int32, positions)
+    _dense(where, q_out, positions)
+    _check(load().rope_append(ctypes.byref(kv), _ptr(q), _ptr(k), _ptr(v), *strides, n, Hq, _ptr(positions),
+                              _ptr(rope.phases), rope.rot, rope.mul, ROPE_INTERLEAVED if rope.interleaved else 0,
+                              _ptr(q_out), _stream(stream)), where)
+    return q_out
+
+
+def paged_attn_workspace_bytes(n_tokens: int, B: int, q_heads: int, kv_heads: int, head_dim: int, max_context: int,
+                               batch_invariant: bool = False) -> int:
+    return load().paged_attn_workspace_bytes(n_tokens, B, q_heads, kv_heads, head_dim, max_context,
+                                             BATCH_INVARIANT if batch_invariant else 0)
+
+
+def paged_attn(q, k_cache, v_cache, table, lengths, offsets, scale=None, window: int = 0, out=None, lse=None, ws=None,
+               stream=None, batch_invariant=False):
+    """Causal attention of the new tokens' q [n][Hq][D] over the paged cache that holds them (scale
+    1/sqrt(D) unless given; window > 0: the last `window` tokens only).  Returns out [n][Hq][D].
+    lse: float [n][Hq] to fill with the rows' log-sum-exp.
+    batch_invariant: each row's result does not depend on what shares the call (W4V_BATCH_INVARIANT)."""
+    import torch
+    where = "paged_attn"
+    kv = _kv(where, k_cache, v_cache, table, lengths, offsets)
+    n, Hq = q.shape[0], q.shape[1]
+    stride = _rows(where, q, Hq, kv.head_dim)
+    if out is None:
+        out = torch.empty((n, Hq, kv.head_dim), dtype=torch.float16, device=q.device)
+    elif out.shape != q.shape:
+        raise W4VError(ERR_SHAPE, where)
+    if lse is not None and lse.shape != (n, Hq):
+        raise W4VError(ERR_SHAPE, where)
+    _typed(where, torch.float16, q, out)
+    _typed(where, torch.float32, lse)
+    _dense(where, out, lse)
+    if ws is None:
+        ws = workspace(paged_attn_workspace_bytes(n, kv.B, Hq, kv.kv_heads, kv.head_dim, kv.table_width * kv.page,
+                                                  batch_invariant), q.device)
+    _check(load().paged_attn(ctypes.byref(kv), _ptr(q), stride, n, Hq, kv.head_dim ** -0.5 if scale is None else scale,
+                             int(window), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+                             BATCH_INVARIANT if batch_invariant else 0, _stream(stream)), where)
+    return out
+
+
+def kv_workspace_bytes(n_pages: int, S: int) -> int:
+    return load().kv_workspace_bytes(n_pages, S)
+
+
+def _pages(where, pool, refs, table, lengths, page=None):
+    import torch
+    if table.dim() != 2 or lengths.shape != (table.shape[0],) or refs.dim() != 1:
+        raise W4VError(ERR_SHAPE, where)
+    _typed(where, torch.int32, refs, table, lengths)
+    _dense(where, refs, table, lengths, pool)
+    n_pages, planes, nbytes = refs.shape[0], 0, 0
+    if pool is not None:
+        if pool.dim() < 5 or pool.shape[-4] != n_pages:
+            raise W4VError(ERR_SHAPE, where)
+        page = pool.shape[-2]
+        nbytes = pool.shape[-3] * page * pool.shape[-1] * pool.element_size()
+        planes = pool.numel() * pool.element_size() // max(nbytes * n_pages, 1)
+    return Pages(_ptr(pool), _ptr(refs), _ptr(table), _ptr(lengths), nbytes, planes, n_pages, table.shape[0],
+                 table.shape[1], page)
+
+
+def _kv_scratch(pages, short, ws, device):
+    import torch
+    if short is None:
+        short = torch.zeros(1, dtype=torch.int32, device=device)
+    if ws is None:
+        ws = workspace(kv_workspace_bytes(pages.n_pages, pages.S), device)
+    return short, ws
+
+
+def kv_extend(pool, refs, table, lengths, new_lengths, short=None, ws=None, stream=None):
+    """Pages for new_lengths [S] tokens a sequence (pool [..., n_pages][Hkv][page][D], the planes in front;
+    refs int32 [n_pages], table int32 [S][width], lengths int32 [S], all changed in place).  Returns the
+    int32 [1] tensor `short`: 0, or what keeps the call from changing anything (see include/w4v.h)."""
+    import torch
+    where = "kv_extend"
+    pages = _pages(where, pool, refs, table, lengths)
+    if new_lengths.shape != lengths.shape:
+        raise W4VError(ERR_SHAPE, where)
+    short, ws = _kv_scratch(pages, short, ws, refs.device)
+    _typed(where, torch.int32, new_lengths, short)
+    _dense(where, new_lengths)
+    _check(load().kv_extend(ctypes.byref(pages), _ptr(new_lengths), _ptr(short), _ptr(ws), ws.numel(),
+                            _stream(stream)), where)
+    return short
+
+
+def kv_truncate(refs, table, lengths, new_lengths, page: int, stream=None):
+    """Lengths down to new_lengths [S], in place; pages that nothing holds any more become free."""
+    import torch
+    where = "kv_truncate"
+    pages = _pages(where, None, refs, table, lengths, int(page))
+    if new_lengths.shape != lengths.shape:
+        raise W4VError(ERR_SHAPE, where)
+    _typed(where, torch.int32, new_lengths)
+    _dense(where, new_lengths)
+    _check(load().kv_truncate(ctypes.byref(pages), _ptr(new_lengths), _stream(stream)), where)
+
+
+def kv_fork(pool, refs, table, lengths, parents, children, short=None, ws=None, stream=None):
+    """Sequences children[i] become copies of parents[i] (int32 [n]): full pages shared, a partly
+    filled last one copied.  Returns `short` as kv_extend does."""
+    import torch
+    where = "kv_fork"
+    pages = _pages(where, pool, refs, table, lengths)
+    if parents.dim() != 1 or children.shape != parents.shape:
+        raise W4VError(ERR_SHAPE, where)
+    short, ws = _kv_scratch(pages, short, ws, refs.device)
+    _typed(where, torch.int32, parents, children, short)
+    _dense(where, parents, children)
+    _check(load().kv_fork(ctypes.byref(pages), _ptr(parents), _ptr(children), parents.shape[0], _ptr(short), _ptr(ws),
+                          ws.numel(), _stream(stream)), where)
+    return short
+
+
+def kv_compact(pool, refs, table, lengths, refs_out=None, table_out=None, ws=None, stream=None):
+    """All live pages to the lowest ids; returns (refs_out, table_out), the old arrays unless given."""
+    import torch
+    where = "kv_compact"
+    pages = _pages(where, pool, refs, table, lengths)
+    refs_out, table_out = refs if refs_out is None else refs_out, table if table_out is None else table_out
+    if refs_out.shape != refs.shape or table_out.shape != table.shape:
+        raise W4VError(ERR_SHAPE, where)
+    _typed(where, torch.int32, refs_out, table_out)
+    _dense(where, refs_out, table_out)
+    _, ws = _kv_scratch(pages, refs, ws, refs.device)
+    _check(load().kv_compact(ctypes.byref(pages), _ptr(refs_out), _ptr(table_out), _ptr(ws), ws.numel(),
+                             _stream(stream)), where)
+    return refs_out, table_out
+
+
+def kv_copy(pool, src, dst, stream=None):
+    """Contents of pages src[i] to pages dst[i] (int32 [n]) in every plane of pool [..., n_pages][Hkv][page][D]."""
+    import torch
+    where = "kv_copy"
+    if pool.dim() < 5 or src.dim() != 1 or dst.shape != src.shape:
+        raise W4VError(ERR_SHAPE, where)
+    _typed(where, torch.int32, src, dst)
+    _dense(where, pool, src, dst)
+    n_pages = pool.shape[-4]
+    nbytes = pool.shape[-3] * pool.shape[-2] * pool.shape[-1] * pool.element_size()
+    _check(load().kv_copy(_ptr(pool), pool.numel() * pool.element_size() // max(nbytes * n_pages, 1), n_pages, nbytes,
+                          _ptr(src), _ptr(dst), src.shape[0], _stream(stream)), where)

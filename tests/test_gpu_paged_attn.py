@@ -1,0 +1,204 @@
+"""paged_attn on the GPU against the oracle (double precision), at the sizes,
+masks and layouts where it can go wrong.  Bounds: paged_helpers."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import to_dev
+from oracle import paged
+from paged_helpers import attention_bounds, cache
+
+pytestmark = pytest.mark.gpu
+
+
+def run(w, gpu, c, scale=None, window=0, lse=True, invariant=False, ws=None):
+    d = {x: to_dev(a, gpu) for x, a in c.items()}
+    n, Hq, _ = c["q"].shape
+    L = torch.full((n, Hq), 7.0, dtype=torch.float32, device=gpu) if lse else None
+    out = torch.full(c["q"].shape, 9.0, dtype=torch.float16, device=gpu)
+    o = w.paged_attn(d["q"], d["k"], d["v"], d["table"], d["lengths"], d["offsets"], scale=scale, window=window,
+                     out=out, lse=L, batch_invariant=invariant, ws=ws)
+    torch.cuda.synchronize()
+    assert w.get_status() == w.OK
+    return o.cpu().numpy(), L.cpu().numpy() if lse else None
+
+
+def check(w, gpu, c, scale=None, window=0, invariant=False):
+    s = c["q"].shape[2] ** -0.5 if scale is None else scale
+    got, lse = run(w, gpu, c, scale, window, invariant=invariant)
+    ref = paged.attention(c["q"], c["k"], c["v"], c["table"], c["lengths"], c["offsets"], s, window)
+    (o, l, _, _), (bo, bl) = ref, attention_bounds(c, ref)
+    err = np.abs(got.astype(np.float64) - o)
+    assert np.all(err <= bo), (float(np.max(err / bo)), np.unravel_index(np.argmax(err / bo), err.shape))
+    fin = np.isfinite(l)
+    assert np.array_equal(np.isneginf(lse), ~fin)
+    assert np.all(np.abs(lse[fin] - l[fin]) <= bl[fin]), float(np.max(np.abs(lse[fin] - l[fin]) / bl[fin]))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [8, 16, 64, 128, 256])
+def test_lengths_around_tiles_and_pages(w4v_mod, gpu, D, page):
+    """One and several new tokens over lengths around every edge of a page and of 128 keys."""
+    rng = np.random.default_rng([D, page])
+    lengths = [1, 2, 7, 8, 9, 15, 16, 17, 127, 128, 129, 255, 256, 257, 383, 400]
+    check(w4v_mod, gpu, cache(rng, [1 + i % 3 if n > 3 else 1 for i, n in enumerate(lengths)], lengths, 8, 2, D, page))
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (5, 5), (10, 2), (21, 3), (8, 1), (66, 1), (128, 1), (40, 2)])
+def test_head_groups(w4v_mod, gpu, Hq, Hkv):
+    """Groups that divide 128 rows and groups that do not, tiles of one token and of many."""
+    rng = np.random.default_rng([Hq, Hkv])
+    check(w4v_mod, gpu, cache(rng, [3, 0, 40, 1], [90, 50, 300, 1], Hq, Hkv, 64, 16))
+    check(w4v_mod, gpu, cache(rng, [16], [150], Hq, Hkv, 128, 32))
+
+
+@pytest.mark.parametrize("D,page", [(64, 8), (128, 16), (256, 256)])
+@pytest.mark.parametrize("window", [1, 2, 100, 128, 129, 1000])
+def test_windows(w4v_mod, gpu, D, page, window):
+    rng = np.random.default_rng([D, window])
+    check(w4v_mod, gpu, cache(rng, [1, 30, 150], [300, 290, 420], 4, 2, D, page), window=window)
+
+
+@pytest.mark.parametrize("stale", [np.nan, np.inf, -np.inf, 65504.0])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_what_lies_past_a_sequence_is_never_used(w4v_mod, gpu, stale, D):
+    rng = np.random.default_rng(5)
+    check(w4v_mod, gpu, cache(rng, [1, 5, 0, 17, 1], [3, 130, 40, 257, 128], 6, 2, D, 32, stale=stale))
+
+
+def test_rows_that_see_nothing(w4v_mod, gpu):
+    """More new tokens than cached ones: the first rows sit before position 0; length 0: all of them."""
+    rng = np.random.default_rng(6)
+    c = cache(rng, [4, 3, 200, 2], [10, 3, 200, 4], 4, 2, 128, 16)
+    c["lengths"] = np.array([2, 0, 130, -5], np.int32)
+    got, lse = run(w4v_mod, gpu, c)
+    ref = paged.attention(c["q"], c["k"], c["v"], c["table"], [2, 0, 130, 0], c["offsets"], 128 ** -0.5)
+    o, l = ref[:2]
+    assert np.all(got[~np.isfinite(l)] == 0) and np.array_equal(np.isneginf(lse), ~np.isfinite(l))
+    assert np.all(np.abs(got - o) <= attention_bounds(c, ref)[0])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long_contexts_split_over_the_gpu(w4v_mod, gpu, D):
+    rng = np.random.default_rng(7)
+    check(w4v_mod, gpu, cache(rng, [16], [20011], 4, 1, D, 16))
+    check(w4v_mod, gpu, cache(rng, [1, 21, 1], [9000, 5003, 17], 4, 2, D, 64))
+
+
+def test_a_chunk_of_a_prompt(w4v_mod, gpu):
+    rng = np.random.default_rng(8)
+    check(w4v_mod, gpu, cache(rng, [700, 129], [1500, 129], 3, 1, 128, 16))
+    check(w4v_mod, gpu, cache(rng, [300], [1000], 8, 2, 256, 64))
+    check(w4v_mod, gpu, cache(rng, [520], [520], 2, 2, 64, 8))
+
+
+@pytest.mark.parametrize("spread", [0.0, 8.0, 40.0])
+def test_scores_from_equal_to_one_hot(w4v_mod, gpu, spread):
+    """Rising scores force the running maximum up again and again; equal ones never."""
+    rng = np.random.default_rng(9)
+    c = cache(rng, [3], [1300], 2, 1, 64, 16)
+    c["q"][:] = 0
+    c["q"][:, :, 0] = 8.0
+    ramp = (np.arange(c["table"].shape[1] * 16) / 1300.0 * spread).astype(np.float16)
+    for p in range(-(-1300 // 16)):
+        c["k"][c["table"][0, p], 0, :, 0] = ramp[16 * p:16 * p + 16]
+    check(w4v_mod, gpu, c, scale=0.25)
+
+
+def test_many_sequences(w4v_mod, gpu):
+    rng = np.random.default_rng(10)
+    n = rng.integers(0, 4, 700)
+    check(w4v_mod, gpu, cache(rng, n, n + rng.integers(0, 40, 700), 2, 1, 64, 8))
+
+
+def test_strided_rows_and_another_stream(w4v_mod, gpu):
+    """q as a slice of a wider projection's rows, and a call on a stream of its own."""
+    rng = np.random.default_rng(11)
+    c = cache(rng, [9, 20], [100, 333], 4, 2, 128, 16)
+    want, _ = run(w4v_mod, gpu, c)
+    wide = torch.full((29, 6, 128), float("nan"), dtype=torch.float16, device=gpu)
+    wide[:, 1:5] = to_dev(c["q"], gpu)
+    d = {x: to_dev(a, gpu) for x, a in c.items()}
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = w4v_mod.paged_attn(wide[:, 1:5], d["k"], d["v"], d["table"], d["lengths"], d["offsets"])
+    s.synchronize()
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
+def test_repeatable_and_graph_replay(w4v_mod, gpu):
+    """The same bits on every call with one workspace; a captured call follows lengths that change."""
+    rng = np.random.default_rng(12)
+    c = cache(rng, [16, 16], [3000, 1777], 8, 2, 128, 16)
+    d = {x: to_dev(a, gpu) for x, a in c.items()}
+    w = w4v_mod
+    ws = w.workspace(w.paged_attn_workspace_bytes(32, 2, 8, 2, 128, d["table"].shape[1] * 16))
+    out = torch.empty_like(d["q"])
+    call = lambda: w.paged_attn(d["q"], d["k"], d["v"], d["table"], d["lengths"], d["offsets"], out=out, ws=ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    first = out.clone()
+    for _ in range(3):
+        out.fill_(3.0)
+        call()
+        assert torch.equal(out, first)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    d["lengths"].copy_(torch.tensor([1000, 40], dtype=torch.int32))
+    g.replay()
+    torch.cuda.synchronize()
+    got = out.cpu().numpy()
+    ref = paged.attention(c["q"], c["k"], c["v"], c["table"], [1000, 40], c["offsets"], 128 ** -0.5)
+    assert np.all(np.abs(got - ref[0]) <= attention_bounds(c, ref)[0])
+
+
+@pytest.mark.parametrize("D,window", [(64, 0), (128, 0), (256, 0), (128, 300)])
+def test_batch_invariance(w4v_mod, gpu, D, window):
+    """Verified positions equal the one-token steps they stand for, bit for bit, alone or in a batch."""
+    rng = np.random.default_rng(13)
+    T, lens = 16, [2100, 530, 16, 1029]
+    c = cache(rng, [T] * 4, lens, 10, 2, D, 16)
+    check(w4v_mod, gpu, c, window=window, invariant=True)
+    got, lse = run(w4v_mod, gpu, c, window=window, invariant=True)
+    for b in range(4):
+        for t in (0, 1, 7, T - 1):
+            one = dict(c, q=c["q"][b * T + t:b * T + t + 1], table=c["table"][b:b + 1],
+                       lengths=np.array([lens[b] - T + t + 1], np.int32), offsets=np.array([0, 1], np.int32))
+            o1, l1 = run(w4v_mod, gpu, one, window=window, invariant=True)
+            assert np.array_equal(o1[0], got[b * T + t]) and np.array_equal(l1[0], lse[b * T + t])
+
+
+def test_ids_outside_the_cache_read_as_zeros(w4v_mod, gpu):
+    rng = np.random.default_rng(14)
+    c = cache(rng, [2], [200], 2, 1, 64, 16)
+    bad = dict(c, table=c["table"].copy())
+    bad["table"][0, 3], bad["table"][0, 5] = -7, c["k"].shape[0] + 2
+    zero = dict(c, k=c["k"].copy(), v=c["v"].copy())
+    for i in (3, 5):
+        zero["k"][c["table"][0, i]] = 0
+        zero["v"][c["table"][0, i]] = 0
+    a, _ = run(w4v_mod, gpu, bad)
+    b, _ = run(w4v_mod, gpu, zero)
+    assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_token_that_is_not_finite_touches_only_rows_that_see_it(w4v_mod, gpu, value, D):
+    """A drafted token whose key or value overflowed: earlier positions are as without it, later ones carry it."""
+    rng = np.random.default_rng(15)
+    c = cache(rng, [8, 3], [140, 60], 4, 2, D, 16)
+    clean, _ = run(w4v_mod, gpu, c)
+    for name in ("v", "k"):
+        bad = dict(c, **{name: c[name].copy()})
+        p = 136                                                     # row 4 of the first sequence's eight
+        bad[name][c["table"][0, p // 16], 1, p % 16, 3] = value
+        got, _ = run(w4v_mod, gpu, bad)
+        assert np.array_equal(got[:4], clean[:4]) and np.array_equal(got[8:], clean[8:])
+        assert np.array_equal(got[4:8, :2], clean[4:8, :2])         # the other key/value head
+        if name == "v":
+            assert not np.isfinite(got[4:8, 2:, 3]).any()
+            rest = np.arange(D) != 3
+            assert np.array_equal(got[4:8, 2:][..., rest], clean[4:8, 2:][..., rest])
