@@ -124,6 +124,23 @@ w4v_status encode_tmap_kblocks(CUtensorMap *map, CUtensorMapDataType dtype, uint
     return r == CUDA_SUCCESS ? W4V_OK : W4V_ERR_ARG;
 }
 
+w4v_status encode_tmap_sw128(CUtensorMap *map, CUtensorMapDataType dtype, int rank, const void *base,
+                             const uint64_t *dims, const uint64_t *strides, const uint32_t *box) {
+    if (g_encode == nullptr || rank < 2 || rank > 5) return W4V_ERR_CUDA;
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], estr[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        estr[i] = 1;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    CUresult r = g_encode(map, dtype, rank, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? W4V_OK : W4V_ERR_ARG;
+}
+
 }  // namespace w4v
 
 extern "C" w4v_status w4v_init(void) {

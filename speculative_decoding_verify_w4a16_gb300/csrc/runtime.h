@@ -40,6 +40,11 @@ w4v_status encode_tmap_kblocks(CUtensorMap *map, CUtensorMapDataType dtype, uint
                                uint64_t inner, uint64_t rows, uint32_t inner_box, uint32_t box_rows,
                                uint32_t box_blocks, CUtensorMapSwizzle swizzle);
 
+// Tensor map of any rank up to 5: dims and box innermost first, strides in
+// bytes of the dims from the second on, 128-byte swizzle, zero fill.
+w4v_status encode_tmap_sw128(CUtensorMap *map, CUtensorMapDataType dtype, int rank, const void *base,
+                             const uint64_t *dims, const uint64_t *strides, const uint32_t *box);
+
 // Launches `kernel` with programmatic stream serialization, so its grid can
 // be scheduled while the previous kernel of the stream drains; the kernel
 // itself orders its memory accesses after that kernel (grid_dep_wait).

@@ -181,6 +181,22 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// 4-D tiled tensor copy; (x, y, z, w) element coordinates, x innermost.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+// Makes this thread's shared-memory writes visible to the async proxy (TMA,
+// the tensor cores' operand reads).
+__device__ __forceinline__ void fence_proxy_async_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // Warms L2 with `bytes` (multiple of 16) of global memory from a 16-byte
 // aligned address; nothing lands in shared memory.
 __device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
@@ -280,6 +296,19 @@ __device__ __forceinline__ void mma_f16_ts_lane0(uint32_t d_tmem, uint32_t a_tme
         : "memory");
 }
 
+// The same with A from shared memory too.
+__device__ __forceinline__ void mma_f16_ss_lane0(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 l;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.u32 l, %%laneid;\n\t"
+        "setp.eq.u32 e, l, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // mma_commit by lane 0 of a converged warp (the lane that issued the MMAs).
 __device__ __forceinline__ void mma_commit_lane0(uint32_t bar) {
     asm volatile(
@@ -313,6 +342,21 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
     d |= uint64_t(2) << 61;              // 128-byte swizzle
     return d;
 }
+
+// The same for 8-row atoms that lie `stride` bytes apart (another matrix's
+// atoms, or another 64-element block's, in between).
+__device__ __forceinline__ uint64_t sdesc_sw128_stride(uint32_t saddr, uint32_t stride) {
+    return (sdesc_sw128(saddr) & ~(uint64_t(0x3FFF) << 32)) | uint64_t(stride >> 4) << 32;
+}
+
+// An operand whose N (or M) runs along the 128-byte rows and K across them:
+// atoms of 64 elements by 8 k, `block` bytes from one 64-element block to
+// the next and `stride` bytes from one group of 8 k to the next.  The
+// instruction descriptor names it as MN-major (kIdescBMnMajor for B).
+__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t block, uint32_t stride) {
+    return (sdesc_sw128_stride(saddr, stride) & ~(uint64_t(0x3FFF) << 16)) | uint64_t(block >> 4) << 16;
+}
+constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
 // tcgen05.ld / tcgen05.st run asynchronously: the registers of a load are
 // valid only after tcgen05.wait::ld, and the registers of a store must not
@@ -520,6 +564,18 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+
+// Arrival without a wait (a role that gives up releases its partner).
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// 2^x in one instruction (2 units in the last place; below 2^-126: 0).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // ----------------------------------------------------------- int -> fp16 bits
 // (a0, a1) += s * (d0, d1) as fp32 bit patterns, in one packed instruction
