@@ -40,11 +40,19 @@
 // clears what is not finite; the rows that do see it add it in the epilogue.
 // A drafted token that overflowed thus spoils no position before it.
 //
-// Roles (12 warps): 0 producer (page ids, TMA), 1 MMA issuer, 2 schedule and
-// tensor-memory owner, 3 idle, 4-11 softmax.  Softmax warps w and w + 4
-// share 32 rows, 64 of the 128 columns each, and agree on the maximum
-// through shared memory.  S is double buffered: the next tile's Q K^T runs
-// under this one's softmax.
+// Roles (12 warps): 0 producer (page ids, TMA), 1 MMA issuer, 2 guard (the
+// looking over) and tensor-memory owner, 3 scheduler (parts of the CTA's
+// range, through a ring in shared memory), 4-7 and 8-11 softmax.  S and P
+// have buffers of their own, so Q K^T runs ahead (two tiles; one for heads of
+// 256, whose O leaves room for one S) and waits only until the scores are in
+// registers.  The two softmax groups take alternate key tiles, a thread a
+// whole row; what passes between them is the rows' reference.
+//
+// Code size is part of the design: between them the roles run through their
+// loops once per tile, and what does not stay in the instruction cache costs
+// some 250 cycles a miss.  So each loop body is there once (the first
+// products of a part are the loop's own, with the later ones off), waits are
+// a few instructions, and the schedule is worked out by one warp.
 #include <algorithm>
 
 #include "runtime.h"
@@ -56,9 +64,12 @@ namespace {
 constexpr int kKeys = 128;                      // keys per tile
 constexpr int kRows = 128;                      // rows per tile
 constexpr int kThreads = 384;
-constexpr int kWarpProd = 0, kWarpMma = 1, kWarpPlan = 2, kWarpSoft = 4;
+constexpr int kWarpProd = 0, kWarpMma = 1, kWarpGuard = 2, kWarpPlan = 3, kWarpSoft = 4;
+constexpr int kParts = 4;                       // ring of parts
+constexpr int kPartReaders = 11;                // every warp but the scheduler
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kOcol = 256;                 // S buffers at columns 0 and 128
+// Tensor memory: S in one or two buffers of 128 columns, P in two of 64, O.
+constexpr uint32_t kPcols = kKeys / 2;
 constexpr float kShift = 8.f, kSlack = 6.f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kInvTiles = 4;                    // least tiles of a batch-invariant part
@@ -72,13 +83,18 @@ struct Plan {
     static constexpr int kGroupBytes = kStageBlocks * 1024;      // 8 tokens of a stage
     static constexpr int kStageBytes = kKeys / 8 * kGroupBytes;
     static constexpr int kQBytes = kBlocks * kRows * 128;
-    static constexpr int kStages = D == 64 ? 11 : D == 128 ? 6 : 5;
+    static constexpr int kStages = D == 64 ? 10 : D == 128 ? 6 : 5;
     static constexpr int kBar = kQBytes + kStages * kStageBytes;
-    static constexpr int kNumBars = 2 + 2 * kStages + 2 + 2 + 2 + 1;
-    static constexpr int kMisc = kBar + 256;
-    static constexpr int kMax = kBar + 512;                      // float[2][2][kRows]
-    static constexpr int kBytes = kMax + 2 * 2 * kRows * 4;
-    static_assert(8 * kNumBars <= 256 && kBytes <= 227 * 1024, "shared memory plan");
+    static constexpr int kScores = D >= 256 ? 1 : 2;             // S buffers, and tiles that Q K^T runs ahead
+    static constexpr uint32_t kPcol = kScores * kKeys, kOcol = kPcol + 2 * kPcols;
+    static constexpr int kNumBars = 2 + 2 * kStages + 8 + 4 + 8 + 4 + 2 * kParts;
+    static constexpr int kMisc = kBar + 8 * kNumBars;
+    static constexpr int kRing = (kMisc + 16 + 15) & ~15;
+    static constexpr int kRef = kRing + kParts * 48;             // float[kRows]: the rows' references
+    static constexpr int kSums = kRef + kRows * 4;               // float[2][kRows]: the groups' sums
+    static constexpr int kBytes = kSums + 2 * kRows * 4;
+    static_assert(kOcol + D <= kTmemCols, "tensor memory plan");
+    static_assert(kBytes <= 227 * 1024, "shared memory plan");
 };
 
 struct Args {
@@ -90,7 +106,7 @@ struct Args {
     const int32_t *table, *lengths, *offsets;
     uint32_t *status;
     int n_tokens, q_heads, kv_heads, group, tok;   // query heads per key/value head, tokens per tile
-    int B, width, n_pages, page, window, slot_rows;
+    int B, width, n_pages, page_bits, window, slot_rows;   // 2^page_bits tokens a page
     int inv;                    // 0, or tiles per batch-invariant part
     float scale_log2;
 };
@@ -103,7 +119,7 @@ __device__ __forceinline__ Seq seq_of(const Args &p, int b) {
     Seq s;
     s.first = min(max(p.offsets[b], 0), p.n_tokens);
     s.n = max(min(max(p.offsets[b + 1], 0), p.n_tokens) - s.first, 0);
-    s.len = min(max(p.lengths[b], 0), p.width * p.page);
+    s.len = min(max(p.lengths[b], 0), p.width << p.page_bits);
     return s;
 }
 
@@ -111,7 +127,7 @@ __device__ __forceinline__ Seq seq_of(const Args &p, int b) {
 struct Extent {
     int lo, hi, units;          // tiles [lo, hi); a tile without keys is one unit
 };
-__device__ __forceinline__ Extent extent_of(const Args &p, const Seq &s, int qt) {
+__device__ __noinline__ Extent extent_of(const Args &p, const Seq &s, int qt) {
     const int t0 = qt * p.tok, t1 = min(s.n, t0 + p.tok) - 1;
     const int p0 = s.len - s.n + t0, p1 = s.len - s.n + t1;
     Extent e{0, 0, 1};
@@ -123,17 +139,19 @@ __device__ __forceinline__ Extent extent_of(const Args &p, const Seq &s, int qt)
 }
 
 // Units of one key/value head of 32 sequences, one per lane (0 past the end).
-__device__ int lane_units(const Args &p, int b) {
+__device__ __noinline__ int lane_units(const Args &p, int b) {
     const int lane = threadIdx.x & 31;
     Seq s{0, 0, 0};
     if (b < p.B) s = seq_of(p, b);
     const int tiles = (s.n + p.tok - 1) / p.tok;
     int u = tiles == 1 ? extent_of(p, s, 0).units : 0;
+#pragma unroll 1
     for (uint32_t many = __ballot_sync(0xFFFFFFFFu, tiles > 1); many != 0; many &= many - 1) {
         const int src = __ffs(many) - 1;
         const Seq o{0, __shfl_sync(0xFFFFFFFFu, s.n, src), __shfl_sync(0xFFFFFFFFu, s.len, src)};
         const int ot = __shfl_sync(0xFFFFFFFFu, tiles, src);
         int sum = 0;
+#pragma unroll 1
         for (int qt = lane; qt < ot; qt += 32) sum += extent_of(p, o, qt).units;
         sum = __reduce_add_sync(0xFFFFFFFFu, sum);
         if (lane == src) u = sum;
@@ -141,34 +159,51 @@ __device__ int lane_units(const Args &p, int b) {
     return u;
 }
 
-template <typename T>
-__device__ __forceinline__ T warp_scan(T x) {
+// The same value in every lane, as one that the compiler knows to be so.
+__device__ __forceinline__ int warp_uniform(int x) { return __reduce_max_sync(0xFFFFFFFFu, x); }
+
+__device__ __forceinline__ int warp_scan(int x) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const T y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, d);
         if ((threadIdx.x & 31) >= d) x += y;
     }
     return x;
 }
 
-__device__ long long all_units(const Args &p) {
-    long long sum = 0;
+__device__ __forceinline__ int all_units(const Args &p) {
+    int sum = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32) sum += lane_units(p, b0 + (threadIdx.x & 31));
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    return sum * p.kv_heads;
+    return __reduce_add_sync(0xFFFFFFFFu, sum) * p.kv_heads;
 }
+
+// An even split of `units` over at most `ctas` ranges, none of them empty.
+struct Split {
+    int ranges, each, more;     // the first `more` ranges hold one unit more than `each`
+    __device__ __forceinline__ Split(int units, int ctas) {
+        ranges = min(units, ctas);
+        each = ranges > 0 ? units / ranges : 0;
+        more = units - each * ranges;
+    }
+    __device__ __forceinline__ int begin(int c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int owner(int u) const {
+        const int edge = more * (each + 1);
+        return u < edge ? u / (each + 1) : more + (u - edge) / each;
+    }
+};
 
 struct Place {
     int b, kvh, qt, u;          // unit u of a row tile
 };
 // The place of unit `at` (one warp; at < all_units).
-__device__ Place place_of(const Args &p, long long at) {
+__device__ __forceinline__ Place place_of(const Args &p, int at) {
     const int lane = threadIdx.x & 31;
     Place w{0, 0, 0, 0};
+#pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int u = lane_units(p, b0 + lane);
-        const long long upto = warp_scan((long long)u * p.kv_heads);
+        const int upto = warp_scan(u * p.kv_heads);
         const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > at);
         if (past == 0) {
             at -= __shfl_sync(0xFFFFFFFFu, upto, 31);
@@ -176,11 +211,12 @@ __device__ Place place_of(const Args &p, long long at) {
         }
         const int src = __ffs(past) - 1;
         const int su = __shfl_sync(0xFFFFFFFFu, u, src);
-        at -= __shfl_sync(0xFFFFFFFFu, upto, src) - (long long)su * p.kv_heads;
+        at -= __shfl_sync(0xFFFFFFFFu, upto, src) - su * p.kv_heads;
         w.b = b0 + src;
-        w.kvh = int(at / su);
-        int rest = int(at % su);
+        w.kvh = at / su;
+        int rest = at % su;
         const Seq s = seq_of(p, w.b);
+#pragma unroll 1
         for (int q0 = 0;; q0 += 32) {
             const bool in = q0 + lane < (s.n + p.tok - 1) / p.tok;
             const int mine = in ? extent_of(p, s, q0 + lane).units : 0;
@@ -201,42 +237,47 @@ __device__ Place place_of(const Args &p, long long at) {
 
 // A run of units of one row tile.
 struct Part {
-    Seq s;
-    int b, kvh, t0, rows;       // first token, rows in use
-    int kt0, nt;                // first key tile, key tiles
-    int keys_end;               // keys that any of its rows sees end here
-    int u, take, units;         // units [u, u + take) of the row tile's
+    int nt, kt0;                // key tiles (-1: no more parts), the first one
+    int row0, rows;             // the first row's token, rows in use
+    int pos0, keys_end;         // its position; keys that any of the rows sees end here
+    int b, kvh;
+    int slot;                   // where its partial result goes, -1: it is the whole
+    int u, units;               // its first unit, the row tile's units
 };
+static_assert(sizeof(Part) <= 48, "ring of parts");
 struct Cursor {
     Place w;
-    long long unit, left;       // index of the next unit, units left in the range
+    int unit, left;             // index of the next unit, units left in the range
     Seq s;
     __device__ __forceinline__ void load(const Args &p) { s = seq_of(p, w.b); }
-    __device__ __forceinline__ bool next(const Args &p, Part &g) {
+    __device__ __forceinline__ bool next(const Args &p, int cta, Part &g) {
         if (left <= 0) return false;
         const Extent e = extent_of(p, s, w.qt);
-        g.s = s;
+        const int t0 = w.qt * p.tok, toks = min(p.tok, s.n - t0);
+        g.row0 = s.first + t0;
+        g.rows = toks * p.group;
+        g.pos0 = s.len - s.n + t0;
+        g.keys_end = max(g.pos0 + toks, 0);
         g.b = w.b;
         g.kvh = w.kvh;
-        g.t0 = w.qt * p.tok;
-        const int toks = min(p.tok, s.n - g.t0);
-        g.rows = toks * p.group;
-        g.keys_end = max(s.len - s.n + g.t0 + toks, 0);
         g.u = w.u;
         g.units = e.units;
+        int take = 1;
         if (p.inv == 0) {
-            g.take = int(min((long long)(e.units - w.u), left));
+            take = min(e.units - w.u, left);
             g.kt0 = e.lo + w.u;
-            g.nt = e.hi > e.lo ? g.take : 0;
+            g.nt = e.hi > e.lo ? take : 0;
+            g.slot = 2 * cta + (w.u == 0);
         } else {
-            g.take = 1;
             const int c = (e.lo / p.inv + w.u) * p.inv;
             g.kt0 = max(e.lo, c);
             g.nt = max(min(e.hi, c + p.inv) - g.kt0, 0);
+            g.slot = unit;
         }
-        w.u += g.take;
-        unit += g.take;
-        left -= g.take;
+        if (take == e.units) g.slot = -1;
+        w.u += take;
+        unit += take;
+        left -= take;
         if (w.u == e.units) {
             w.u = 0;
             if ((w.qt + 1) * p.tok < s.n) {
@@ -245,7 +286,9 @@ struct Cursor {
                 w.qt = 0;
                 if (++w.kvh == p.kv_heads) {
                     w.kvh = 0;
-                    if (left > 0) do {
+                    if (left > 0)
+#pragma unroll 1
+                    do {
                         ++w.b;
                         load(p);
                     } while (s.n == 0 && w.b < p.B - 1);
@@ -256,10 +299,10 @@ struct Cursor {
     }
 };
 
-// Whether none of eight fp16 values is infinite or NaN (exponent all ones).
-__device__ __forceinline__ bool finite_halves(const uint4 &v) {
+// 0 if none of eight fp16 values is infinite or NaN (exponent all ones).
+__device__ __forceinline__ uint32_t not_finite(const uint4 &v) {
     auto carry = [](uint32_t w) { return (w & 0x7C007C00u) + 0x04000400u; };
-    return ((carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) & 0x80008000u) == 0u;
+    return (carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) & 0x80008000u;
 }
 __device__ __forceinline__ void clear_not_finite(uint4 &v) {
     auto clear = [](uint32_t w) {
@@ -270,6 +313,28 @@ __device__ __forceinline__ void clear_not_finite(uint4 &v) {
     v.y = clear(v.y);
     v.z = clear(v.z);
     v.w = clear(v.w);
+}
+
+// Whether a tile's values are looked over before the product: some row does
+// not see some key of it (the first row sees those up to pos0, the last one
+// those from keys_end - window on), or its last step has spare keys.
+__device__ __forceinline__ bool guarded(const Args &p, int key, int keys_end, int pos0) {
+    const int seen = min(keys_end - key, kKeys);
+    return seen % 16 != 0 || pos0 + 1 - key < seen || (p.window > 0 && keys_end - p.window > key);
+}
+
+// A whole warp's wait for a phase, in as few instructions as it takes: they
+// are at two dozen places.  A role that gave up leaves; those that wait for
+// it give up in turn.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+    bool done = mbar_test_wait(bar, parity);
+    if (!__all_sync(0xFFFFFFFFu, done)) {
+        const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+        while (!done && global_timer_ns() - t0 < kWaitLimitNs) done = mbar_try_wait(bar, parity);
+        done = __all_sync(0xFFFFFFFFu, done);
+    }
+    return done;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -284,17 +349,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     const uint32_t q_full = bar0, q_empty = bar0 + 8u;
     auto kv_full = [&](int s) { return bar0 + 16u + 8u * s; };
     auto kv_empty = [&](int s) { return bar0 + 16u + 8u * (P::kStages + s); };
-    const uint32_t tail = bar0 + 16u + 16u * P::kStages;
-    auto s_full = [&](int i) { return tail + 8u * i; };
-    auto p_full = [&](int i) { return tail + 16u + 8u * i; };
-    auto pv_done = [&](int i) { return tail + 32u + 8u * i; };
-    const uint32_t done_bar = tail + 48u;
-    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + P::kMisc);    // [0] tmem, [1] abort, [2..3] below
+    const uint32_t rest = bar0 + 16u + 16u * P::kStages;
+    auto s_full = [&](int i) { return rest + 8u * i; };          // by softmax group
+    auto p_full = [&](int i) { return rest + 16u + 8u * i; };
+    auto pv_done = [&](int i) { return rest + 32u + 8u * i; };
+    auto s_empty = [&](int i) { return rest + 48u + 8u * i; };
+    const uint32_t v_ask = rest + 64u, v_ready = rest + 72u, o_empty = rest + 80u, done_bar = rest + 88u;
+    auto turn = [&](int quad, int i) { return rest + 96u + 16u * quad + 8u * i; };
+    auto pair = [&](int quad) { return rest + 160u + 8u * quad; };
+    auto part_full = [&](int i) { return rest + 192u + 8u * i; };
+    auto part_empty = [&](int i) { return rest + 192u + 8u * (kParts + i); };
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + P::kMisc);    // [0] tmem, [2..3] below
     volatile uint32_t *spoilt = misc + 2;                    // [i & 1]: part i (from 1) had values cleared
-    volatile Cursor *start = reinterpret_cast<volatile Cursor *>(smem + P::kMisc + 16);
-    float *xmax = reinterpret_cast<float *>(smem + P::kMax);
+    Part *ring = reinterpret_cast<Part *>(smem + P::kRing);
+    float *ref = reinterpret_cast<float *>(smem + P::kRef), *sums = reinterpret_cast<float *>(smem + P::kSums);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    AbortState ab{reinterpret_cast<volatile uint32_t *>(&misc[1]), p.status};
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -305,14 +374,27 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
-            mbar_init(p_full(i), 8);             // the softmax warps
-            mbar_init(pv_done(i), 2);            // the MMAs, and the issuer's own writes
+            mbar_init(p_full(i), 4);             // the warps of one softmax group
+            mbar_init(pv_done(i), 2);            // the MMAs, and the issuer's own arrival
+            mbar_init(s_empty(i), 4);
         }
+        mbar_init(v_ask, 1);
+        mbar_init(v_ready, 1);
+        mbar_init(o_empty, 8);                   // both softmax groups
         mbar_init(done_bar, 1);
-        misc[1] = misc[2] = misc[3] = 0;
+        for (int q = 0; q < 4; ++q) {
+            mbar_init(turn(q, 0), 1);
+            mbar_init(turn(q, 1), 1);
+            mbar_init(pair(q), 2);               // the two warps that share 32 rows
+        }
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(part_full(i), 1);
+            mbar_init(part_empty(i), kPartReaders);
+        }
+        misc[2] = misc[3] = 0;
         fence_barrier_init();
     }
-    if (warp == kWarpPlan) {
+    if (warp == kWarpGuard) {
         tmem_alloc(smem_u32(&misc[0]), kTmemCols);
         tmem_relinquish();
     }
@@ -321,368 +403,504 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
     }
-    grid_dep_wait();
-    grid_dep_launch();
-    if (warp == kWarpPlan) {
-        const long long all = all_units(p);
-        const long long ctas = min((long long)gridDim.x, all);
-        Cursor c{};
-        if (blockIdx.x < ctas) {
-            c.unit = split_begin(blockIdx.x, all, ctas);
-            c.left = split_begin(blockIdx.x + 1, all, ctas) - c.unit;
-            c.w = place_of(p, c.unit);
-        }
-        if (lane == 0) {
-            start->unit = c.unit;
-            start->left = c.left;
-            start->w.b = c.w.b;
-            start->w.kvh = c.w.kvh;
-            start->w.qt = c.w.qt;
-            start->w.u = c.w.u;
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = misc[0];
-    Cursor cur;
-    cur.unit = start->unit;
-    cur.left = start->left;
-    cur.w.b = start->w.b;
-    cur.w.kvh = start->w.kvh;
-    cur.w.qt = start->w.qt;
-    cur.w.u = start->w.u;
-    if (cur.left > 0) cur.load(p);
-    Part g;
+    const uint32_t tmem = warp_uniform(misc[0]);
+    grid_dep_wait();
+    grid_dep_launch();
     bool ok = (base & 1023u) == 0u;              // the operands' swizzle needs it
-    if (!ok && threadIdx.x == 0) raise_abort(ab);
 
-    if (warp == kWarpProd) {
-        const int box = min(p.page, kKeys);                  // tokens per TMA box
-        const uint32_t box_bytes = uint32_t(box / 8) * P::kGroupBytes;
-        const int boxes = kKeys / box;
-        const int groups = p.page / 8;                       // 8-token groups of a page
-        int it = 0, nq = 0;
-        // this lane's page (box) of tile kt: its first 8-token group, or one
-        // past the cache, which TMA fills with zeros
-        auto group_of = [&](const Part &g, int kt) -> int {
-            const int key = kt * kKeys + lane * box;
-            if (lane >= boxes || key >= g.keys_end) return -1;
-            const int id = p.table[size_t(g.b) * p.width + key / p.page];
-            if (id < 0 || id >= p.n_pages) return p.n_pages * p.kv_heads * groups;
-            return (id * p.kv_heads + g.kvh) * groups + (key % p.page) / 8;
-        };
-        auto load = [&](const CUtensorMap *map, int grp) {
-            const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, grp >= 0));
-            for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
-                const int s = it % P::kStages;
-                if (it >= P::kStages) ok = warp_wait(kv_empty(s), (it / P::kStages - 1) & 1, ab);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(kv_full(s), n * box_bytes);
-                __syncwarp();
-                if (grp >= 0)
-                    tma_load_4d(base + P::kQBytes + s * P::kStageBytes + lane * box_bytes, map, 0, 0,
-                                h * P::kStageBlocks, grp, kv_full(s));
+    // The next part (its number in the ring is `i`); the warp gives it back
+    // with release() once it has read what it needs.
+    auto part_of = [&](int i) -> const Part & { return ring[i % kParts]; };
+    auto acquire = [&](int i) {
+        ok = ok && wait(part_full(i % kParts), (i / kParts) & 1);
+        return ok && part_of(i).nt >= 0;
+    };
+    auto release = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(part_empty(i % kParts));
+    };
+
+    // registers from the four single warps to the softmax groups: 128 x 88 +
+    // 256 x 208 of the 384 x 168 that the CTA was launched with
+    if (warp < kWarpSoft) set_max_registers_down<88>();
+    if (warp == kWarpPlan) {
+        const Split split(all_units(p), gridDim.x);
+        Cursor cur{};
+        if (int(blockIdx.x) < split.ranges) {
+            cur.unit = split.begin(blockIdx.x);
+            cur.left = split.begin(blockIdx.x + 1) - cur.unit;
+            cur.w = place_of(p, cur.unit);
+            cur.load(p);
+        }
+        Part g{};
+        for (int i = 0; ok && g.nt >= 0; ++i) {
+            if (!cur.next(p, blockIdx.x, g)) g.nt = -1;
+            if (i >= kParts) ok = wait(part_empty(i % kParts), (i / kParts - 1) & 1);
+            if (!ok) break;
+            if (lane == 0) {
+                ring[i % kParts] = g;
+                mbar_arrive(part_full(i % kParts));
             }
-        };
-        while (ok && cur.next(p, g)) {
+        }
+    } else if (warp == kWarpProd) {
+        const int box_bits = min(p.page_bits, 7), box = 1 << box_bits;       // tokens per TMA box
+        const uint32_t box_bytes = uint32_t(box / 8) * P::kGroupBytes;
+        const int boxes = kKeys >> box_bits;
+        const int groups = 1 << (p.page_bits - 3);           // 8-token groups of a page
+        int it = 0, nq = 0;
+        for (int i = 0; acquire(i); ++i) {
+            const Part g = part_of(i);
+            release(i);
             if (g.nt == 0) continue;
-            int now = group_of(g, g.kt0), soon = g.nt > 1 ? group_of(g, g.kt0 + 1) : -1;
-            if (nq > 0) ok = warp_wait(q_empty, (nq - 1) & 1, ab);
+            // this lane's page (box) of key tile j: its first 8-token group, or
+            // one past the cache, which TMA fills with zeros
+            auto group_of = [&](int j) -> int {
+                const int key = (g.kt0 + j) * kKeys + (lane << box_bits);
+                if (j >= g.nt || lane >= boxes || key >= g.keys_end) return -1;
+                const int id = p.table[size_t(g.b) * p.width + (key >> p.page_bits)];
+                if (id < 0 || id >= p.n_pages) return p.n_pages * p.kv_heads * groups;
+                return (id * p.kv_heads + g.kvh) * groups + ((key >> 3) & (groups - 1));
+            };
+            // K runs kScores tiles ahead of V, in the issuer's order: the ids
+            // of tiles j - kScores .. j + 1 are at hand
+            int ids[P::kScores + 2];
+#pragma unroll
+            for (int k = 0; k < P::kScores; ++k) ids[k] = -1;
+            ids[P::kScores] = group_of(0);
+            ids[P::kScores + 1] = group_of(1);
+            if (nq > 0) ok = wait(q_empty, (nq - 1) & 1);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(q_full, P::kBlocks * p.tok * p.group * 128u);
             __syncwarp();
             if (lane < P::kBlocks)
-                tma_load_4d(base + lane * kRows * 128, &qmap, 0, g.kvh * p.group, g.s.first + g.t0, lane, q_full);
+                tma_load_4d(base + lane * kRows * 128, &qmap, 0, g.kvh * p.group, g.row0, lane, q_full);
             ++nq;
-            load(&kmap, now);
-            for (int j = 0; j < g.nt && ok; ++j) {
-                const int after = j + 2 < g.nt ? group_of(g, g.kt0 + j + 2) : -1;
-                if (j + 1 < g.nt) load(&kmap, soon);
-                load(&vmap, now);
-                now = soon;
-                soon = after;
+            for (int j = 0; j < g.nt + P::kScores && ok; ++j) {
+                const int ahead = group_of(j + 2);
+#pragma unroll 1
+                for (int kv = j < g.nt ? 0 : 1; kv < (j >= P::kScores ? 2 : 1) && ok; ++kv) {
+                    const CUtensorMap *map = kv == 0 ? &kmap : &vmap;
+                    const int grp = kv == 0 ? ids[P::kScores] : ids[0];
+                    const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, grp >= 0));
+#pragma unroll 1
+                    for (int h = 0; h < P::kHalves; ++h, ++it) {
+                        const int s = it % P::kStages;
+                        if (it >= P::kStages) ok = wait(kv_empty(s), (it / P::kStages - 1) & 1);
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(kv_full(s), n * box_bytes);
+                        __syncwarp();
+                        if (grp >= 0)
+                            tma_load_4d(base + P::kQBytes + s * P::kStageBytes + lane * box_bytes, map, 0, 0,
+                                        h * P::kStageBlocks, grp, kv_full(s));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < P::kScores + 1; ++k) ids[k] = ids[k + 1];
+                ids[P::kScores + 1] = ahead;
             }
         }
-        if (*ab.flag) {                                      // copies in flight land before the CTA ends
-            for (int i = max(0, it - P::kStages); i < it; ++i)
-                mbar_wait_bounded(kv_full(i % P::kStages), (i / P::kStages) & 1);
-            if (nq > 0) mbar_wait_bounded(q_full, (nq - 1) & 1);
-        }
+        // every copy has landed before the CTA ends, also where its reader gave up
+        for (int i = max(0, it - P::kStages); i < it; ++i)
+            ok = mbar_wait_bounded(kv_full(i % P::kStages), (i / P::kStages) & 1) && ok;
+        if (nq > 0) ok = mbar_wait_bounded(q_full, (nq - 1) & 1) && ok;
     } else if (warp == kWarpMma) {
         constexpr uint32_t idesc_s = idesc_f16_f32(kRows, kKeys);
         constexpr uint32_t idesc_o = idesc_f16_f32(kRows, 64 * P::kStageBlocks) | kIdescBMnMajor;
-        const uint32_t st0 = base + P::kQBytes;
-        int it = 0, nq = 0, t = 0;                           // stages, parts and tiles so far
-        auto scores = [&](int tile) {                        // S[tile & 1] = Q K^T
-            for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
-                const int s = it % P::kStages;
-                ok = warp_wait(kv_full(s), (it / P::kStages) & 1, ab);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 4 * P::kStageBlocks; ++k)
-                    mma_f16_ss_lane0(tmem + (tile & 1) * kKeys,
-                                     sdesc_sw128(base + (h * P::kStageBlocks + (k >> 2)) * (kRows * 128) + (k & 3) * 32),
-                                     sdesc_sw128_stride(st0 + s * P::kStageBytes + (k >> 2) * 1024 + (k & 3) * 32,
-                                                        P::kGroupBytes),
-                                     idesc_s, h > 0 || k > 0);
-                mma_commit_lane0(kv_empty(s));
-            }
-            if (ok) mma_commit_lane0(s_full(tile & 1));
-        };
-        while (ok && cur.next(p, g)) {
-            if (g.nt == 0) continue;
-            ok = warp_wait(q_full, nq & 1, ab);
-            if (!ok) break;
+        // Descriptors: the high words are constants, and the low ones (address
+        // / 16) grow by constants from one per operand.  (Put together from
+        // the address for each MMA they cost more to issue than the MMA runs.)
+        constexpr uint64_t kHighQ = uint64_t(sdesc_high(1024)) << 32, kHighKv = uint64_t(sdesc_high(P::kGroupBytes)) << 32;
+        const uint32_t q_low = sdesc_low(base, 16), k_low = sdesc_low(base + P::kQBytes, 16),
+                       v_low = sdesc_low(base + P::kQBytes, 1024);
+        int it = 0, nq = 0, t = 0, looked = 0;               // stages, parts, tiles, guarded tiles so far
+        // What steers the loop goes through a warp-wide vote or reduction:
+        // their results are uniform to the compiler, so stage numbers and
+        // descriptors stay in uniform registers.
+        for (int i = 0; __any_sync(0xFFFFFFFFu, acquire(i)); ++i) {
+            const int nt = warp_uniform(part_of(i).nt), keys_end = warp_uniform(part_of(i).keys_end);
+            const int key0 = warp_uniform(part_of(i).kt0 * kKeys), pos0 = warp_uniform(part_of(i).pos0);
+            release(i);
+            if (nt == 0) continue;
+            ok = wait(q_full, nq & 1);
             ++nq;
-            tc_fence_after();
-            scores(t);
-            if (ok && g.nt == 1) mma_commit_lane0(q_empty);
-            for (int j = 0; j < g.nt && ok; ++j, ++t) {
-                if (j + 1 < g.nt) {
-                    scores(t + 1);
-                    if (ok && j + 2 == g.nt) mma_commit_lane0(q_empty);
-                }
-                // O += P V over the keys that some row sees.  While the
-                // softmax runs: what the last 16 of them hold past those keys
-                // (other tokens, nothing at all) is cleared, and so is what
-                // is not finite among keys that only some rows see.
-                const int key = (g.kt0 + j) * kKeys, seen = min(g.keys_end - key, kKeys), steps = (seen + 15) / 16;
-                const int above = max(g.s.len - g.s.n + g.t0 + 1 - key, 0);          // the first row sees those before
-                const int below = p.window > 0 ? min(g.keys_end - p.window - key, seen) : 0;   // the last row, those from
-                if (seen < 16 * steps || above < seen || below > 0) {
-                    bool found = false;
-                    for (int h = 0; h < P::kHalves && ok; ++h) {
-                        const int s = (it + h) % P::kStages;
-                        const uint32_t st = st0 + s * P::kStageBytes;
-                        ok = warp_wait(kv_full(s), ((it + h) / P::kStages) & 1, ab);
+            for (int j = 0; j < nt + P::kScores && ok; ++j) {
+                if (j < nt) {                                // S = Q K^T of tile t + j
+                    const int tile = t + j, b = tile % P::kScores, u = tile / P::kScores;
+                    if (u > 0) ok = wait(s_empty(b), (u - 1) & 1);
+#pragma unroll 1
+                    for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
+                        const int s = it % P::kStages;
+                        ok = wait(kv_full(s), (it / P::kStages) & 1);
                         if (!ok) break;
-                        constexpr int kPieces = P::kStageBlocks * 8;                 // 16-byte pieces of a token
-                        auto piece = [&](int tok, int i) {
-                            return st + (tok / 8) * P::kGroupBytes + (i / 8) * 1024 + (tok % 8) * 128 + (i % 8) * 16;
-                        };
-                        auto look = [&](int a, int b) {
-                            for (int i = a * kPieces + lane; i < b * kPieces; i += 32) {
-                                const uint32_t at = piece(i / kPieces, i % kPieces);
-                                uint4 v = lds128(at);
-                                if (finite_halves(v)) continue;
-                                clear_not_finite(v);
-                                sts_f32x4(at, __uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
-                                          __uint_as_float(v.w));
-                                found = true;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 4 * P::kStageBlocks; ++k)
+                                mma_f16_ss(tmem + b * kKeys,
+                                           kHighQ | (q_low + h * (P::kStageBlocks * kRows * 128 / 16) +
+                                                     ((k >> 2) * (kRows * 128) + (k & 3) * 32) / 16),
+                                           kHighKv | (k_low + s * (P::kStageBytes / 16) +
+                                                      ((k >> 2) * 1024 + (k & 3) * 32) / 16),
+                                           idesc_s, h > 0 || k > 0);
+                            mma_commit(kv_empty(s));
+                            if (h + 1 == P::kHalves) {
+                                mma_commit(s_full(tile & 1));        // by group: each waits for its own tiles alone
+                                if (j + 1 == nt) mma_commit(q_empty);
                             }
-                        };
-                        if (above < seen) look(above, seen);
-                        if (below > 0) look(0, min(below, above));
-                        for (int i = seen * kPieces + lane; i < 16 * steps * kPieces; i += 32)
-                            sts_f32x4(piece(i / kPieces, i % kPieces), 0.f, 0.f, 0.f, 0.f);
-                        fence_proxy_async_shared();
+                        }
+                        __syncwarp();
                     }
-                    if (__any_sync(0xFFFFFFFFu, found)) spoilt[nq & 1] = nq;
                 }
-                if (ok) ok = warp_wait(p_full(t & 1), (t >> 1) & 1, ab);
-                if (!ok) break;
-                tc_fence_after();
+                if (j < P::kScores || !ok) continue;
+                // O += P V of tile v, over the keys that some row sees
+                const int jv = j - P::kScores, v = t + jv;
+                const int key = key0 + jv * kKeys, steps = min((keys_end - key + 15) / 16, kKeys / 16);
+                const bool look = guarded(p, key, keys_end, pos0);
+                if (look) {
+                    if (elect_one()) mbar_arrive(v_ask);
+                    __syncwarp();
+                }
+                ok = wait(p_full(v & 1), (v >> 1) & 1);
+                if (ok && look) ok = wait(v_ready, (looked++) & 1);
+                if (ok && jv == 0 && nq > 1) ok = wait(o_empty, nq & 1);         // part nq - 1 is read
+#pragma unroll 1
                 for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
                     const int s = it % P::kStages;
-                    const uint32_t st = st0 + s * P::kStageBytes;
-                    ok = warp_wait(kv_full(s), (it / P::kStages) & 1, ab);
+                    ok = wait(kv_full(s), (it / P::kStages) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    for (int k = 0; k < steps; ++k)
-                        mma_f16_ts_lane0(tmem + kOcol + h * 64 * P::kStageBlocks, tmem + (t & 1) * kKeys + 8 * k,
-                                         sdesc_sw128_mn(st + 2 * k * P::kGroupBytes, 1024, P::kGroupBytes), idesc_o,
-                                         j > 0 || k > 0);
-                    mma_commit_lane0(kv_empty(s));
+                    if (elect_one()) {
+                        const uint32_t d = tmem + P::kOcol + h * 64 * P::kStageBlocks, a = tmem + P::kPcol + (v & 1) * kPcols;
+                        const uint32_t low = v_low + s * (P::kStageBytes / 16);
+#pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            if (k < steps)
+                                mma_f16_ts(d, a + 8 * k, kHighKv | (low + k * (2 * P::kGroupBytes / 16)), idesc_o,
+                                           jv > 0 || k > 0);
+                        mma_commit(kv_empty(s));
+                        if (h + 1 == P::kHalves) {
+                            mma_commit(pv_done(v & 1));
+                            mbar_arrive(pv_done(v & 1));     // passes the guard's findings on
+                        }
+                    }
+                    __syncwarp();
                 }
-                if (ok) mma_commit_lane0(pv_done(t & 1));
-                if (ok && lane == 0) mbar_arrive(pv_done(t & 1));
             }
+            t += nt;
         }
-        mma_commit_lane0(done_bar);
+        if (elect_one()) mma_commit(done_bar);
+        __syncwarp();
         mbar_wait_bounded(done_bar, 0);
         __syncwarp();
-    } else if (warp >= kWarpSoft) {
+    } else if (warp == kWarpGuard) {
+        // In guarded tiles, what the last 16 keys hold past those that some
+        // row sees (other tokens, nothing at all) is cleared, and so is what
+        // is not finite among keys that only some rows see.
+        constexpr int kPieces = P::kStageBlocks * 8;         // 16-byte pieces of a token in a stage
+        int it = 0, np = 0, looked = 0;
+        for (int i = 0; acquire(i); ++i) {
+            const Part g = part_of(i);
+            release(i);
+            if (g.nt == 0) continue;
+            ++np;
+            bool found = false;
+            for (int j = 0; j < g.nt + P::kScores && ok; ++j) {
+                if (j < g.nt) it += P::kHalves;              // K
+                if (j < P::kScores) continue;
+                const int key = (g.kt0 + j - P::kScores) * kKeys;
+                if (!guarded(p, key, g.keys_end, g.pos0)) {
+                    it += P::kHalves;
+                    continue;
+                }
+                // the issuer is at this tile: its stages are this fill or the one before
+                ok = wait(v_ask, (looked++) & 1);
+                const int seen = min(g.keys_end - key, kKeys), cleared = (seen + 15) / 16 * 16;
+                const int above = min(max(g.pos0 + 1 - key, 0), seen);
+                const int below = p.window > 0 ? min(g.keys_end - p.window - key, above) : 0;
+#pragma unroll 1
+                for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
+                    const int s = it % P::kStages;
+                    ok = wait(kv_full(s), (it / P::kStages) & 1);
+                    if (!ok) break;
+                    uint8_t *st = smem + P::kQBytes + s * P::kStageBytes;
+                    // a lane's 16-byte column, of every kStep'th token
+                    constexpr int kStep = 32 / kPieces, kAhead = 4;          // loads in flight
+                    uint8_t *col = st + (lane % kPieces / 8) * 1024 + (lane % 8) * 16;
+                    const int first = lane / kPieces;
+                    auto piece = [&](int tok) {
+                        return reinterpret_cast<uint4 *>(col + (tok / 8) * P::kGroupBytes + (tok % 8) * 128);
+                    };
+#pragma unroll 1
+                    for (int side = 0; side < 2; ++side) {
+                        const int end = side == 0 ? seen : below;
+#pragma unroll 1
+                        for (int k0 = (side == 0 ? above : 0) + first; k0 < end; k0 += kStep * kAhead) {
+                            uint32_t bad = 0;
+#pragma unroll
+                            for (int k = 0; k < kAhead; ++k) bad |= not_finite(*piece(min(k0 + kStep * k, end - 1)));
+                            if (bad == 0) continue;
+                            found = true;
+#pragma unroll 1
+                            for (int k = k0; k < min(k0 + kStep * kAhead, end); k += kStep) {
+                                uint4 v = *piece(k);
+                                clear_not_finite(v);
+                                *piece(k) = v;
+                            }
+                        }
+                    }
+#pragma unroll 1
+                    for (int k = seen + first; k < cleared; k += kStep) *piece(k) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_shared();
+                }
+                if (found) spoilt[np & 1] = np;
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(v_ready);
+            }
+        }
+    } else {
+        set_max_registers_up<208>();
         const int half = (warp - kWarpSoft) >> 2, quad = warp & 3, row = 32 * quad + lane;
         const uint32_t lanes = uint32_t(32 * quad) << 16;
         const float c = p.scale_log2;
-        constexpr int kCols = D / 2;                         // this warp's columns of O
-        const uint32_t ocol = tmem + lanes + kOcol + half * kCols;
+        constexpr int kCols = D / 2;                         // this warp's columns of O in the epilogue
+        const uint32_t ocol = tmem + lanes + P::kOcol + half * kCols;
         int t = 0, np = 0;                                   // tiles and parts (with keys) so far
-        while (ok && cur.next(p, g)) {
-            np += g.nt > 0;
-            const bool mine = row < g.rows;
-            const bool busy = 32 * quad < g.rows;            // some row of this warp is in use
-            const int tok = g.t0 + row / p.group;
-            const int head = g.kvh * p.group + row % p.group;
-            const int pos = g.s.len - g.s.n + tok;
+        int use = 0, pairs = 0;                              // references handed on, parts ended by this pair of warps
+        for (int i = 0; acquire(i); ++i) {
+            const int nt = part_of(i).nt, rows = part_of(i).rows, kt0 = part_of(i).kt0;
+            np += nt > 0;
+            const bool mine = row < rows;
+            const bool busy = 32 * quad < rows;              // some row of this warp is in use
+            const int pos = part_of(i).pos0 + row / p.group;
             const int from = p.window > 0 ? pos - p.window + 1 : 0;
             // every key of [sure_lo, sure_hi] is seen by all of the warp's rows
             const int sure_hi = __reduce_min_sync(0xFFFFFFFFu, mine ? pos : 0x7FFFFFFF);
             const int sure_lo = __reduce_max_sync(0xFFFFFFFFu, mine ? from : 0);
-            float m = -INFINITY, l = 0.f;                    // reference (in units of q . k), sum of this warp's half
-            for (int j = 0; j < g.nt; ++j, ++t) {
-                // tile t - 2's product is done by now (its MMAs were issued
-                // before this tile's); seeing its phase keeps the later waits
-                // on pv_done, two phases a barrier, unambiguous
-                ok = warp_wait(s_full(t & 1), (t >> 1) & 1, ab) &&
-                     (t < 2 || warp_wait(pv_done(t & 1), ((t >> 1) - 1) & 1, ab));
+            float m = -INFINITY, l = 0.f;                    // reference (in units of q . k), this group's sum by it
+            for (int j = 0; j < nt; ++j, ++t, ++use) {
+                if ((t & 1) != half) continue;               // the other group's tile
+                const int sb = t % P::kScores;
+                ok = wait(s_full(t & 1), (t >> 1) & 1);
                 if (!ok) break;
                 if (!busy) {
+                    // Nothing to do but keep the pace: a phase is told from
+                    // the next but one only by who waited for the one between,
+                    // and a second arrival within a phase would stand in for a
+                    // warp that still works.
+                    if (lane == 0) mbar_arrive(s_empty(sb));
+                    if (t > 1) ok = wait(pv_done(t & 1), ((t >> 1) - 1) & 1);
+                    if (!ok) break;
                     if (lane == 0) mbar_arrive(p_full(t & 1));
                     continue;
                 }
                 tc_fence_after();
-                uint32_t x[2][32];
-                const uint32_t scol = tmem + lanes + (t & 1) * kKeys + half * 64;
-                tmem_ld_32x32b_x32(scol, x[0]);
-                tmem_ld_32x32b_x32(scol + 32, x[1]);
-                tc_wait_ld_keep<32>(x[0]);
-                tc_wait_ld_keep<32>(x[1]);
-                const int key = (g.kt0 + j) * kKeys + half * 64;
-                if (key + 63 > sure_hi || key < sure_lo) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (key + i > pos || key + i < from) x[i >> 5][i & 31] = 0xFF800000u;   // -inf
-                }
-                float top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 64; ++i) top = fmaxf(top, __uint_as_float(x[i >> 5][i & 31]));
-                // the row's maximum over both halves; past the barrier both
-                // warps hold their scores in registers, so P may overwrite S
-                xmax[((t & 1) * 2 + half) * kRows + row] = top;
-                tc_fence_before();
-                named_bar_sync(1 + quad, 64);
-                tc_fence_after();
-                top = fmaxf(top, xmax[((t & 1) * 2 + (half ^ 1)) * kRows + row]);
-                if (*ab.flag) {
-                    ok = false;
-                    break;
-                }
-                const bool raise = mine && top > m && (m == -INFINITY || (top - m) * c > kSlack);
-                if (__any_sync(0xFFFFFFFFu, raise)) {
-                    const float a = raise ? ex2((m - top) * c) : 1.f;
-                    if (raise) m = top;
-                    l *= a;
-                    if (j > 0) {
-                        ok = warp_wait(pv_done((t - 1) & 1), ((t - 1) >> 1) & 1, ab);
-                        if (!ok) break;
-                        tc_fence_after();
+                uint32_t x[4][32];
+                const int key = (kt0 + j) * kKeys;
+                bool raise = false;
+                float was = 0.f;
 #pragma unroll 1
-                        for (int o = 0; o < kCols; o += 32) {
-                            uint32_t r[32];
-                            tmem_ld_32x32b_x32(ocol + o, r);
-                            tc_wait_ld_keep<32>(r);
+                for (bool again = false;; again = true) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * a);
-                            tmem_st_32x32b_x32(ocol + o, r);
-                            tc_wait_st();
-                            tc_keep_alive<32>(r);
+                    for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(tmem + lanes + sb * kKeys + 32 * k, x[k]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tc_wait_ld_keep<32>(x[k]);
+                    if (key + kKeys - 1 > sure_hi || key < sure_lo) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const int hi = pos - key - 32 * b, lo = from - key - 32 * b;     // keys lo .. hi are seen
+                            const uint32_t seen = (hi < 0 ? 0u : 0xFFFFFFFFu >> (31 - min(hi, 31))) &
+                                                  (lo > 31 ? 0u : 0xFFFFFFFFu << max(lo, 0));
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if ((seen & (1u << k)) == 0u) x[b][k] = 0xFF800000u;         // -inf
                         }
                     }
-                }
-                const float off = m == -INFINITY ? 0.f : kShift - m * c;
-                uint32_t w[32];
-                float sum0 = 0.f, sum1 = 0.f;
+                    if (again) break;
+                    float top4[4];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float p0 = ex2(fmaf(__uint_as_float(x[(2 * i) >> 5][(2 * i) & 31]), c, off));
-                    const float p1 = ex2(fmaf(__uint_as_float(x[(2 * i + 1) >> 5][(2 * i + 1) & 31]), c, off));
-                    sum0 += p0;
-                    sum1 += p1;
-                    w[i] = h2_as_u32(__floats2half2_rn(p0, p1));
+                    for (int b = 0; b < 4; ++b) {
+                        top4[b] = __uint_as_float(x[b][0]);
+#pragma unroll
+                        for (int k = 1; k < 31; k += 2)
+                            top4[b] = max3(top4[b], __uint_as_float(x[b][k]), __uint_as_float(x[b][k + 1]));
+                        top4[b] = fmaxf(top4[b], __uint_as_float(x[b][31]));
+                    }
+                    const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+                    // the reference that the tile before left, raised if need be
+                    if (use > 0) {
+                        ok = wait(turn(quad, (use - 1) & 1), ((use - 1) >> 1) & 1);
+                        if (!ok) break;
+                    }
+                    was = j > 0 ? ref[row] : -INFINITY;
+                    raise = mine && top > was && (was == -INFINITY || (top - was) * c > kSlack);
+                    const float now = raise ? top : was;
+                    if (raise || j == 0) ref[row] = now;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(turn(quad, use & 1));
+                    if (now != m) {
+                        l *= ex2((m - now) * c);             // m = -inf: l is 0 and stays
+                        m = now;
+                    }
+                    if (j == 0 || !__any_sync(0xFFFFFFFFu, raise)) break;
+                    // O by the new reference, once the tile before is added in.
+                    // (The barrier's phase before that one, tile t - 3's, is
+                    // over: that product was issued before this tile's
+                    // scores.)  The scores are read again rather than held in
+                    // 128 registers meanwhile.
+                    ok = wait(pv_done((t - 1) & 1), ((t - 1) >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float a = raise ? ex2((was - now) * c) : 1.f;
+#pragma unroll 1
+                    for (int o = 0; o < D; o += 32) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(tmem + lanes + P::kOcol + o, r);
+                        tc_wait_ld_keep<32>(r);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * a);
+                        tmem_st_32x32b_x32(tmem + lanes + P::kOcol + o, r);
+                        tc_wait_st();
+                        tc_keep_alive<32>(r);
+                    }
                 }
-                l += sum0 + sum1;
-                tmem_st_32x32b_x32(tmem + lanes + (t & 1) * kKeys + half * 32, w);
-                tc_wait_st();
-                tc_keep_alive<32>(w);
+                if (!ok) break;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_empty(sb));     // the scores are in registers
+                // P's buffer: tile t - 2's product has read it
+                if (t > 1) ok = wait(pv_done(t & 1), ((t >> 1) - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const float off = m == -INFINITY ? 0.f : kShift - m * c;
+                const float2 cc = make_float2(c, c), oo = make_float2(off, off);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int e = 64 * h + 2 * k;
+                        float2 y = __ffma2_rn(make_float2(__uint_as_float(x[e >> 5][e & 31]),
+                                                          __uint_as_float(x[e >> 5][(e & 31) + 1])), cc, oo);
+                        y.x = ex2(y.x);
+                        y.y = ex2(y.y);
+                        sum[k & 1] = __fadd2_rn(sum[k & 1], y);
+                        w[k] = h2_as_u32(__float22half2_rn(y));
+                    }
+                    tmem_st_32x32b_x32(tmem + lanes + P::kPcol + (t & 1) * kPcols + 32 * h, w);
+                    tc_wait_st();
+                    tc_keep_alive<32>(w);
+                }
+                const float2 all = __fadd2_rn(sum[0], sum[1]);
+                l += all.x + all.y;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full(t & 1));
             }
-            if (!ok) {
-                if (busy) named_bar_arrive(1 + quad, 64);    // the partner may wait there; it sees the flag after
-                break;
-            }
-            if (g.nt > 0) {
-                ok = warp_wait(pv_done((t - 1) & 1), ((t - 1) >> 1) & 1, ab);
-                if (ok) tc_fence_after();
-                if (busy) {
-                    // the row's sum, lower half first
-                    xmax[half * kRows + row] = l;
-                    named_bar_sync(1 + quad, 64);
-                    l = xmax[row] + xmax[kRows + row];
-                    named_bar_sync(1 + quad, 64);            // read before the next tile's maxima are written
-                    if (*ab.flag) ok = false;
+            if (!ok) break;
+            if (!busy) {
+                use -= nt;                                   // a pair that skips a part hands nothing on
+                if (nt > 0 && ((t - 1) & 1) == half) {       // for both of the pair, at the product's end
+                    ok = wait(pv_done((t - 1) & 1), ((t - 1) >> 1) & 1);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_n(o_empty, 2);
                 }
-                if (!ok) break;
+                release(i);
+                continue;
             }
-            if (!busy) continue;
-            const bool fix = g.nt > 0 && spoilt[np & 1] == np;
-            const bool whole = g.take == g.units;
-            const float inv = g.nt > 0 && l != 0.f ? 1.f / l : 0.f;
+            if (nt > 0) {
+                // the last tile's reference; its product, which the group that
+                // had the tile waits for (it has waited for tile t - 3's, the
+                // barrier's phase before), the other after it; and the row's
+                // sum by the last reference, the first group's share first
+                const uint32_t last_pv = pv_done((t - 1) & 1), last_phase = ((t - 1) >> 1) & 1;
+                ok = wait(turn(quad, (use - 1) & 1), ((use - 1) >> 1) & 1);
+                if (ok && ((t - 1) & 1) == half) ok = wait(last_pv, last_phase);
+                if (!ok) break;
+                const float last = ref[row];
+                if (last != m) l *= ex2((m - last) * c);
+                m = last;
+                sums[half * kRows + row] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pair(quad));
+                ok = wait(pair(quad), (pairs++) & 1) && wait(last_pv, last_phase);
+                if (!ok) break;
+                tc_fence_after();
+                l = sums[row] + sums[kRows + row];
+            }
+            const bool fix = nt > 0 && spoilt[np & 1] == np;
+            const Part g = part_of(i);
+            const bool whole = g.slot < 0;
+            const float inv = nt > 0 && l != 0.f ? 1.f / l : 0.f;
             const float m2 = m * c - kShift;
-            const size_t slot = p.inv ? size_t(cur.unit - g.take) : 2 * size_t(blockIdx.x) + (g.u == 0);
-            const size_t orow = size_t(g.s.first + tok) * p.q_heads + head;
-            const size_t srow = slot * p.slot_rows + row;
+            const size_t orow = size_t(g.row0 + row / p.group) * p.q_heads + g.kvh * p.group + row % p.group;
+            const size_t srow = size_t(whole ? 0 : g.slot) * p.slot_rows + row;
             if (mine && half == 0) {
                 if (!whole) p.part_ml[srow] = make_float2(m2, l);
-                else if (p.lse != nullptr) p.lse[orow] = g.nt > 0 ? (m2 + log2f(l)) * kLn2 : -INFINITY;
+                else if (p.lse != nullptr) p.lse[orow] = nt > 0 ? (m2 + log2f(l)) * kLn2 : -INFINITY;
             }
             __syncwarp();
+            __half *out = p.out + orow * D + half * kCols;
+            float *part = p.part_o + srow * D + half * kCols;
 #pragma unroll 1
             for (int o = 0; o < kCols; o += 32) {
                 uint32_t r[32];
-                if (g.nt > 0) {
-                    tmem_ld_32x32b_x32(ocol + o, r);
-                    tc_wait_ld_keep<32>(r);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = 0u;
-                }
-                if (fix && mine) {
-                    // the values that were cleared, for a row that sees them
-                    const int k0 = max(g.kt0 * kKeys, from), k1 = min((g.kt0 + g.nt) * kKeys - 1, pos);
-                    const int above = g.s.len - g.s.n + g.t0 + 1, below = p.window > 0 ? g.keys_end - p.window : 0;
-                    for (int k = k0; k <= k1; ++k) {
-                        if (k >= below && k < above) k = above;          // seen by every row: not cleared
-                        if (k > k1) break;
-                        const int id = p.table[size_t(g.b) * p.width + k / p.page];
-                        if (id < 0 || id >= p.n_pages) continue;
-                        const uint16_t *v = reinterpret_cast<const uint16_t *>(p.v) +
-                                            ((size_t(id) * p.kv_heads + g.kvh) * p.page + k % p.page) * D + half * kCols + o;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if ((v[i] & 0x7C00u) == 0x7C00u)
-                                r[i] = __float_as_uint(__uint_as_float(r[i]) + __half2float(__ushort_as_half(v[i])));
-                    }
-                }
+                tmem_ld_32x32b_x32(ocol + o, r);
+                tc_wait_ld_keep<32>(r);
                 if (mine && whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * D + half * kCols + o);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int k = 0; k < 4; ++k) {
                         uint32_t h[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            h[e] = h2_as_u32(__floats2half2_rn(l != 0.f ? __uint_as_float(r[8 * i + 2 * e]) * inv : 0.f,
-                                                              l != 0.f ? __uint_as_float(r[8 * i + 2 * e + 1]) * inv : 0.f));
-                        dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 y = make_float2(__uint_as_float(r[8 * k + 2 * e]), __uint_as_float(r[8 * k + 2 * e + 1]));
+                            h[e] = inv != 0.f ? h2_as_u32(__floats2half2_rn(y.x * inv, y.y * inv)) : 0u;
+                        }
+                        reinterpret_cast<uint4 *>(out + o)[k] = make_uint4(h[0], h[1], h[2], h[3]);
                     }
                 } else if (mine) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + srow * D + half * kCols + o);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dst[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                    for (int k = 0; k < 8; ++k)
+                        reinterpret_cast<uint4 *>(part + o)[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
                 }
                 __syncwarp();
             }
             tc_fence_before();
+            __syncwarp();
+            if (nt > 0 && lane == 0) mbar_arrive(o_empty);
+            if (fix && mine) {
+                // the values that were cleared, for a row that sees them: the
+                // weight is above 0, so they make the sum what they are
+                const int below = p.window > 0 ? g.keys_end - p.window : 0;
+                const int last = min((kt0 + nt) * kKeys - 1, pos);
+#pragma unroll 1
+                for (int k = max(kt0 * kKeys, from); k <= last; ++k) {
+                    if (k >= below && k <= g.pos0) k = g.pos0 + 1;       // seen by every row: not cleared
+                    if (k > last) break;
+                    const int id = p.table[size_t(g.b) * p.width + (k >> p.page_bits)];
+                    if (id < 0 || id >= p.n_pages) continue;
+                    const size_t slot = ((size_t(id) * p.kv_heads + g.kvh) << p.page_bits) + (k & ((1 << p.page_bits) - 1));
+                    const __half *v = p.v + slot * D + half * kCols;
+#pragma unroll 1
+                    for (int o = 0; o < kCols; ++o) {
+                        const float y = __half2float(v[o]);
+                        if (isfinite(y)) continue;
+                        if (whole) out[o] = __float2half_rn(__half2float(out[o]) + y);
+                        else part[o] += y;
+                    }
+                }
+            }
+            release(i);
         }
     }
 
+    if (!ok && lane == 0) atomicOr(p.status, 1u << kStatusTimeout);
     tc_fence_before();
     __syncthreads();
-    if (warp == kWarpPlan) {
+    if (warp == kWarpGuard) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -692,8 +910,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
 constexpr int kJoinThreads = 256;
 
 // Rows [r0, r1) of a row tile from its parts, in order: slot(i), i < n.
-template <int D, typename Slot>
-__device__ void join_rows(const Args &p, const Part &g, int r0, int r1, int n, Slot slot, float *weights) {
+template <int D>
+__device__ __noinline__ void join_rows(const Args &p, const Part &g, int r0, int r1, int n, int slot0, float *weights) {
+    // the parts of ranges first .. first + n - 1, or batch-invariant ones in a row
+    auto slot = [&](int i) { return size_t(p.inv ? slot0 + i : i == 0 ? slot0 : slot0 - 1 + 2 * i); };
     __syncthreads();                                         // weights may still be read
     for (int r = r0 + int(threadIdx.x >> 5); r < r1; r += kJoinThreads / 32) {
         const int lane = threadIdx.x & 31;
@@ -717,7 +937,7 @@ __device__ void join_rows(const Args &p, const Part &g, int r0, int r1, int n, S
         if (lane == 0) {
             weights[(r1 - r0) * n + (r - r0)] = inv;
             if (p.lse != nullptr)
-                p.lse[size_t(g.s.first + g.t0 + r / p.group) * p.q_heads + g.kvh * p.group + r % p.group] =
+                p.lse[size_t(g.row0 + r / p.group) * p.q_heads + g.kvh * p.group + r % p.group] =
                     l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
         }
     }
@@ -728,6 +948,7 @@ __device__ void join_rows(const Args &p, const Part &g, int r0, int r1, int n, S
         const float *w = weights + (r - r0) * n;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         constexpr int kAhead = 8;
+#pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += kAhead) {
             float4 v[kAhead];
 #pragma unroll
@@ -744,7 +965,7 @@ __device__ void join_rows(const Args &p, const Part &g, int r0, int r1, int n, S
                 }
         }
         const float inv = weights[(r1 - r0) * n + (r - r0)];
-        const size_t orow = size_t(g.s.first + g.t0 + r / p.group) * p.q_heads + g.kvh * p.group + r % p.group;
+        const size_t orow = size_t(g.row0 + r / p.group) * p.q_heads + g.kvh * p.group + r % p.group;
         uint2 h;
         h.x = h2_as_u32(inv != 0.f ? __floats2half2_rn(o.x * inv, o.y * inv) : __floats2half2_rn(0.f, 0.f));
         h.y = h2_as_u32(inv != 0.f ? __floats2half2_rn(o.z * inv, o.w * inv) : __floats2half2_rn(0.f, 0.f));
@@ -761,17 +982,17 @@ paged_attn_join_kernel(const Args p, int ranges) {
     // (rows / (n - 1) + 1) (n + 1) with n >= 2 parts
     __shared__ float weights[3 * kRows + 3 + 2 * kMaxCtas];
     __shared__ Cursor start;
-    __shared__ long long total;
+    __shared__ int total;
     grid_dep_launch();
     // the sequences' sizes were final before the kernel in front of this one began
     if (threadIdx.x < 32) {
-        const long long all = all_units(p);
-        const long long ctas = min((long long)ranges, all);
-        const long long c = blockIdx.x + (p.inv ? 0 : 1);
+        const int all = all_units(p);
+        const Split split(all, ranges);
+        const int c = int(blockIdx.x) + (p.inv ? 0 : 1);
         Cursor s{};
-        if (c < ctas) {
-            s.unit = split_begin(c, all, ctas);
-            s.left = split_begin(c + 1, all, ctas) - s.unit;
+        if (c < split.ranges) {
+            s.unit = split.begin(c);
+            s.left = split.begin(c + 1) - s.unit;
             s.w = place_of(p, s.unit);
         }
         if (threadIdx.x == 0) {
@@ -786,20 +1007,17 @@ paged_attn_join_kernel(const Args p, int ranges) {
     if (cur.left <= 0) return;
     Part g;
     if (p.inv == 0) {
-        const long long ctas = min((long long)ranges, total);
-        const long long at = cur.unit;
-        cur.next(p, g);
+        const Split split(total, ranges);
+        const int at = cur.unit;
+        cur.next(p, 0, g);
         if (g.u == 0) return;                                // the boundary lies between two tiles
-        const int first = split_owner(at - g.u, total, ctas), last = split_owner(at - g.u + g.units - 1, total, ctas);
+        const int first = split.owner(at - g.u), last = split.owner(at - g.u + g.units - 1);
         const int m = last - first, i = int(blockIdx.x) + 1 - first - 1;
-        join_rows<D>(p, g, i * g.rows / m, (i + 1) * g.rows / m, m + 1,
-                     [&](int k) { return 2 * size_t(first + k) + (k == 0); }, weights);
+        join_rows<D>(p, g, i * g.rows / m, (i + 1) * g.rows / m, m + 1, 2 * first + 1, weights);
     } else {
-        while (cur.next(p, g)) {
+        while (cur.next(p, 0, g)) {
             if (g.units == 1) continue;
-            const size_t s0 = size_t(cur.unit - 1 - g.u);
-            join_rows<D>(p, g, g.u * g.rows / g.units, (g.u + 1) * g.rows / g.units, g.units,
-                         [&](int k) { return s0 + k; }, weights);
+            join_rows<D>(p, g, g.u * g.rows / g.units, (g.u + 1) * g.rows / g.units, g.units, cur.unit - 1 - g.u, weights);
         }
     }
 }
@@ -890,7 +1108,8 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     a.B = kv.B;
     a.width = kv.table_width;
     a.n_pages = kv.n_pages;
-    a.page = kv.page;
+    a.page_bits = 0;
+    while (1 << a.page_bits < kv.page) ++a.page_bits;
     a.window = window;
     a.slot_rows = slots.rows;
     a.inv = invariant ? inv_tiles(kv.table_width * kv.page) : 0;

@@ -38,6 +38,11 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// n arrivals at once.
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
@@ -296,15 +301,25 @@ __device__ __forceinline__ void mma_f16_ts_lane0(uint32_t d_tmem, uint32_t a_tme
         : "memory");
 }
 
-// The same with A from shared memory too.
-__device__ __forceinline__ void mma_f16_ss_lane0(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                uint32_t accumulate) {
+// One lane of a converged warp, in the form that the compiler knows: code
+// under it runs in one lane, with its operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b32 l;\n\t"
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t"
+        "selp.b32 %0, 1, 0, e;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.u32 l, %%laneid;\n\t"
-        "setp.eq.u32 e, l, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
@@ -343,18 +358,17 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
     return d;
 }
 
-// The same for 8-row atoms that lie `stride` bytes apart (another matrix's
-// atoms, or another 64-element block's, in between).
-__device__ __forceinline__ uint64_t sdesc_sw128_stride(uint32_t saddr, uint32_t stride) {
-    return (sdesc_sw128(saddr) & ~(uint64_t(0x3FFF) << 32)) | uint64_t(stride >> 4) << 32;
+// The two words of such descriptors for any distances: atoms of 8 rows by
+// 128 bytes, `stride` bytes from one 8-row group to the next (high word).
+// K-major: the rows are M or N, a 16-element K slice starts 32-byte steps
+// into the atom, and `lead` is not used.  MN-major (kIdescBMnMajor for B):
+// the rows are k, 64 elements of N along each, and `lead` bytes lie from one
+// 64-element block to the next.
+__device__ __forceinline__ uint32_t sdesc_low(uint32_t saddr, uint32_t lead) {
+    return ((saddr & 0x3FFFFu) >> 4) | (lead >> 4) << 16;
 }
-
-// An operand whose N (or M) runs along the 128-byte rows and K across them:
-// atoms of 64 elements by 8 k, `block` bytes from one 64-element block to
-// the next and `stride` bytes from one group of 8 k to the next.  The
-// instruction descriptor names it as MN-major (kIdescBMnMajor for B).
-__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t block, uint32_t stride) {
-    return (sdesc_sw128_stride(saddr, stride) & ~(uint64_t(0x3FFF) << 16)) | uint64_t(block >> 4) << 16;
+__host__ __device__ constexpr uint32_t sdesc_high(uint32_t stride) {
+    return stride >> 4 | 1u << 14 | 2u << 29;    // distance, version (sm_100 family), 128-byte swizzle
 }
 constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
@@ -565,9 +579,23 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
 }
 
 
-// Arrival without a wait (a role that gives up releases its partner).
-__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+// The largest of three (sm_100 and later, one instruction).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Moves registers between warpgroups; every warp of an aligned group of four
+// executes it.  The groups' shares must add up to no more than the CTA was
+// launched with.
+template <int n>
+__device__ __forceinline__ void set_max_registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n));
+}
+template <int n>
+__device__ __forceinline__ void set_max_registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
 }
 
 // 2^x in one instruction (2 units in the last place; below 2^-126: 0).

@@ -8,8 +8,10 @@ missing or the GPU is not sm_103, calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
+import struct
 import threading
 from typing import Optional
 
@@ -39,19 +41,10 @@ class GroupedHandle(ctypes.Structure):
                 ("check", ctypes.c_uint)]
 
 
-class KV(ctypes.Structure):
-    """w4v_kv_t (include/w4v.h)."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
-                ("lengths", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("B", ctypes.c_int),
-                ("table_width", ctypes.c_int), ("n_pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
-                ("page", ctypes.c_int), ("head_dim", ctypes.c_int)]
-
-
-class Pages(ctypes.Structure):
-    """w4v_pages_t (include/w4v.h)."""
-    _fields_ = [("pool", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("table", ctypes.c_void_p),
-                ("lengths", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t), ("planes", ctypes.c_int),
-                ("n_pages", ctypes.c_int), ("S", ctypes.c_int), ("table_width", ctypes.c_int), ("page", ctypes.c_int)]
+# w4v_kv_t and w4v_pages_t (include/w4v.h), packed per call: a ctypes structure
+# takes several times as long to fill, next to kernels of a few microseconds.
+_KV = struct.Struct("PPPPP6i")       # k, v, table, lengths, offsets, B, table_width, n_pages, kv_heads, page, head_dim
+_PAGES = struct.Struct("PPPPN5i4x")  # pool, refs, table, lengths, page_bytes, planes, n_pages, S, table_width, page
 
 
 class W4VError(RuntimeError):
@@ -63,6 +56,8 @@ class W4VError(RuntimeError):
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libw4v.so (built by ``_build.build()``); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -162,9 +157,12 @@ def _check(code: int, where: str) -> None:
 
 
 def _stream(stream=None) -> Optional[int]:
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream if hasattr(s, "cuda_stream") else s
+    if stream is None:
+        import torch
+        if torch.cuda.is_initialized():          # the raw handle: a Stream object costs more than a small call's checks
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
 def _ptr(t) -> Optional[int]:
@@ -433,40 +431,58 @@ class Rope:
         self.phases = torch.from_numpy(phases.view(np.int64)).to(device)
 
 
-def _typed(where, dtype, *tensors):
-    for t in tensors:
-        if t is not None and t.dtype != dtype:
-            raise W4VError(ERR_ARG, where)
-
-
-def _dense(where, *tensors):
-    for t in tensors:
-        if t is not None and not t.is_contiguous():
-            raise W4VError(ERR_ARG, where)
-
-
-def _rows(where, t, heads, head_dim):
-    """Row stride of a [tokens][heads][head_dim] tensor whose rows are dense."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+def _i32(t, where, shape):
+    """A dense int32 tensor of that shape: its address (0 for None)."""
+    import torch
+    if t is None:
+        return 0
+    if t.shape != shape:
         raise W4VError(ERR_SHAPE, where)
-    if t.shape[0] > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
+    if t.dtype is not torch.int32 or not t.is_contiguous():
         raise W4VError(ERR_ARG, where)
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * head_dim) if t.shape[0] else heads * head_dim
+    return t.data_ptr()
+
+
+def _rows(t, where, n, heads, head_dim):
+    """Rows of dense heads: the row stride of a fp16 [n][heads][head_dim] tensor."""
+    import torch
+    if t.shape != (n, heads, head_dim):
+        raise W4VError(ERR_SHAPE, where)
+    if t.dtype is not torch.float16:
+        raise W4VError(ERR_ARG, where)
+    stride = t.stride()
+    if n and (stride[2] != 1 or (heads > 1 and stride[1] != head_dim)):
+        raise W4VError(ERR_ARG, where)
+    return stride[0] if n > 1 else heads * head_dim
+
+
+def _dense_out(t, where, like, dtype):
+    """The result tensor: t, or a new one of that type and shape."""
+    import torch
+    if t is None:
+        return torch.empty(like.shape, dtype=dtype, device=like.device)
+    if t.shape != like.shape:
+        raise W4VError(ERR_SHAPE, where)
+    if t.dtype is not dtype or not t.is_contiguous():
+        raise W4VError(ERR_ARG, where)
+    return t
 
 
 def _kv(where, k_cache, v_cache, table, lengths, offsets):
+    """(packed w4v_kv_t, sequences, table width, kv heads, page, head_dim)."""
     import torch
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or table.dim() != 2:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or table.dim() != 2:
         raise W4VError(ERR_SHAPE, where)
-    B = table.shape[0]
-    if lengths.shape != (B,) or offsets.shape != (B + 1,):
-        raise W4VError(ERR_SHAPE, where)
-    _typed(where, torch.float16, k_cache, v_cache)
-    _typed(where, torch.int32, table, lengths, offsets)
-    _dense(where, k_cache, v_cache, table, lengths, offsets)
-    n_pages, heads, page, D = k_cache.shape
-    return KV(_ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(lengths), _ptr(offsets), B, table.shape[1], n_pages,
-              heads, page, D)
+    half = torch.float16
+    if k_cache.dtype is not half or v_cache.dtype is not half or not k_cache.is_contiguous() or \
+            not v_cache.is_contiguous():
+        raise W4VError(ERR_ARG, where)
+    n_pages, heads, page, D = shape
+    B, width = table.shape
+    return (_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), _i32(table, where, (B, width)),
+                     _i32(lengths, where, (B,)), _i32(offsets, where, (B + 1,)), B, width, n_pages, heads, page, D),
+            B, width, heads, page, D)
 
 
 def rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: Rope, q_out=None, positions=None,
@@ -477,22 +493,15 @@ def rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: Rope, 
     rotation's position is not the cache position."""
     import torch
     where = "rope_append"
-    kv = _kv(where, k_cache, v_cache, table, lengths, offsets)
-    n, Hq = q.shape[0], q.shape[1]
-    strides = [_rows(where, q, Hq, kv.head_dim), _rows(where, k, kv.kv_heads, kv.head_dim),
-               _rows(where, v, kv.kv_heads, kv.head_dim)]
-    if k.shape[0] != n or v.shape[0] != n or (positions is not None and positions.shape != (n,)):
-        raise W4VError(ERR_SHAPE, where)
-    if q_out is None:
-        q_out = torch.empty((n, Hq, kv.head_dim), dtype=torch.float16, device=q.device)
-    elif q_out.shape != q.shape:
-        raise W4VError(ERR_SHAPE, where)
-    _typed(where, torch.float16, q, k, v, q_out)
-    _typed(where, torch.int32, positions)
-    _dense(where, q_out, positions)
-    _check(load().rope_append(ctypes.byref(kv), _ptr(q), _ptr(k), _ptr(v), *strides, n, Hq, _ptr(positions),
-                              _ptr(rope.phases), rope.rot, rope.mul, ROPE_INTERLEAVED if rope.interleaved else 0,
-                              _ptr(q_out), _stream(stream)), where)
+    kv, _, _, heads, _, D = _kv(where, k_cache, v_cache, table, lengths, offsets)
+    n, Hq = q.shape[:2]
+    strides = _rows(q, where, n, Hq, D), _rows(k, where, n, heads, D), _rows(v, where, n, heads, D)
+    q_out = _dense_out(q_out, where, q, torch.float16)
+    code = load().rope_append(kv, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, n, Hq,
+                              _i32(positions, where, (n,)), rope.phases.data_ptr(), rope.rot, rope.mul,
+                              ROPE_INTERLEAVED if rope.interleaved else 0, q_out.data_ptr(), _stream(stream))
+    if code != OK:
+        raise W4VError(code, where)
     return q_out
 
 
@@ -510,24 +519,19 @@ def paged_attn(q, k_cache, v_cache, table, lengths, offsets, scale=None, window:
     batch_invariant: each row's result does not depend on what shares the call (W4V_BATCH_INVARIANT)."""
     import torch
     where = "paged_attn"
-    kv = _kv(where, k_cache, v_cache, table, lengths, offsets)
-    n, Hq = q.shape[0], q.shape[1]
-    stride = _rows(where, q, Hq, kv.head_dim)
-    if out is None:
-        out = torch.empty((n, Hq, kv.head_dim), dtype=torch.float16, device=q.device)
-    elif out.shape != q.shape:
-        raise W4VError(ERR_SHAPE, where)
-    if lse is not None and lse.shape != (n, Hq):
-        raise W4VError(ERR_SHAPE, where)
-    _typed(where, torch.float16, q, out)
-    _typed(where, torch.float32, lse)
-    _dense(where, out, lse)
+    kv, B, width, heads, page, D = _kv(where, k_cache, v_cache, table, lengths, offsets)
+    n, Hq = q.shape[:2]
+    stride = _rows(q, where, n, Hq, D)
+    out = _dense_out(out, where, q, torch.float16)
+    if lse is not None and (lse.shape != (n, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous()):
+        raise W4VError(ERR_SHAPE if lse.shape != (n, Hq) else ERR_ARG, where)
     if ws is None:
-        ws = workspace(paged_attn_workspace_bytes(n, kv.B, Hq, kv.kv_heads, kv.head_dim, kv.table_width * kv.page,
-                                                  batch_invariant), q.device)
-    _check(load().paged_attn(ctypes.byref(kv), _ptr(q), stride, n, Hq, kv.head_dim ** -0.5 if scale is None else scale,
-                             int(window), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                             BATCH_INVARIANT if batch_invariant else 0, _stream(stream)), where)
+        ws = workspace(paged_attn_workspace_bytes(n, B, Hq, heads, D, width * page, batch_invariant), q.device)
+    code = load().paged_attn(kv, q.data_ptr(), stride, n, Hq, D ** -0.5 if scale is None else scale, int(window),
+                             out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+                             BATCH_INVARIANT if batch_invariant else 0, _stream(stream))
+    if code != OK:
+        raise W4VError(code, where)
     return out
 
 
@@ -535,102 +539,102 @@ def kv_workspace_bytes(n_pages: int, S: int) -> int:
     return load().kv_workspace_bytes(n_pages, S)
 
 
+def _plane(pool):
+    """(planes, n_pages, page, bytes of one page in one plane) of [..., n_pages][heads][page][head_dim]."""
+    shape = pool.shape
+    if len(shape) < 5:
+        raise W4VError(ERR_SHAPE, "pool")
+    nbytes = shape[-3] * shape[-2] * shape[-1] * pool.element_size()
+    return math.prod(shape[:-4]), shape[-4], shape[-2], nbytes
+
+
 def _pages(where, pool, refs, table, lengths, page=None):
-    import torch
-    if table.dim() != 2 or lengths.shape != (table.shape[0],) or refs.dim() != 1:
+    """(packed w4v_pages_t, n_pages, S, table width)."""
+    if refs.dim() != 1 or table.dim() != 2:
         raise W4VError(ERR_SHAPE, where)
-    _typed(where, torch.int32, refs, table, lengths)
-    _dense(where, refs, table, lengths, pool)
-    n_pages, planes, nbytes = refs.shape[0], 0, 0
+    n_pages, (S, width) = refs.shape[0], table.shape
+    planes, nbytes, at = 0, 0, 0
     if pool is not None:
-        if pool.dim() < 5 or pool.shape[-4] != n_pages:
+        planes, pool_pages, page, nbytes = _plane(pool)
+        if pool_pages != n_pages:
             raise W4VError(ERR_SHAPE, where)
-        page = pool.shape[-2]
-        nbytes = pool.shape[-3] * page * pool.shape[-1] * pool.element_size()
-        planes = pool.numel() * pool.element_size() // max(nbytes * n_pages, 1)
-    return Pages(_ptr(pool), _ptr(refs), _ptr(table), _ptr(lengths), nbytes, planes, n_pages, table.shape[0],
-                 table.shape[1], page)
+        if not pool.is_contiguous():
+            raise W4VError(ERR_ARG, where)
+        at = pool.data_ptr()
+    return (_PAGES.pack(at, _i32(refs, where, (n_pages,)), _i32(table, where, (S, width)), _i32(lengths, where, (S,)),
+                        nbytes, planes, n_pages, S, width, page), n_pages, S, width)
 
 
-def _kv_scratch(pages, short, ws, device):
+def _short(short, where, device):
     import torch
     if short is None:
         short = torch.zeros(1, dtype=torch.int32, device=device)
-    if ws is None:
-        ws = workspace(kv_workspace_bytes(pages.n_pages, pages.S), device)
-    return short, ws
+    return short, _i32(short, where, (1,))
 
 
 def kv_extend(pool, refs, table, lengths, new_lengths, short=None, ws=None, stream=None):
     """Pages for new_lengths [S] tokens a sequence (pool [..., n_pages][Hkv][page][D], the planes in front;
     refs int32 [n_pages], table int32 [S][width], lengths int32 [S], all changed in place).  Returns the
     int32 [1] tensor `short`: 0, or what keeps the call from changing anything (see include/w4v.h)."""
-    import torch
     where = "kv_extend"
-    pages = _pages(where, pool, refs, table, lengths)
-    if new_lengths.shape != lengths.shape:
-        raise W4VError(ERR_SHAPE, where)
-    short, ws = _kv_scratch(pages, short, ws, refs.device)
-    _typed(where, torch.int32, new_lengths, short)
-    _dense(where, new_lengths)
-    _check(load().kv_extend(ctypes.byref(pages), _ptr(new_lengths), _ptr(short), _ptr(ws), ws.numel(),
-                            _stream(stream)), where)
+    pages, n_pages, S, _ = _pages(where, pool, refs, table, lengths)
+    want = _i32(new_lengths, where, (S,))
+    short, at = _short(short, where, refs.device)
+    if ws is None:
+        ws = workspace(kv_workspace_bytes(n_pages, S), refs.device)
+    code = load().kv_extend(pages, want, at, ws.data_ptr(), ws.numel(), _stream(stream))
+    if code != OK:
+        raise W4VError(code, where)
     return short
 
 
 def kv_truncate(refs, table, lengths, new_lengths, page: int, stream=None):
     """Lengths down to new_lengths [S], in place; pages that nothing holds any more become free."""
-    import torch
     where = "kv_truncate"
-    pages = _pages(where, None, refs, table, lengths, int(page))
-    if new_lengths.shape != lengths.shape:
-        raise W4VError(ERR_SHAPE, where)
-    _typed(where, torch.int32, new_lengths)
-    _dense(where, new_lengths)
-    _check(load().kv_truncate(ctypes.byref(pages), _ptr(new_lengths), _stream(stream)), where)
+    pages, _, S, _ = _pages(where, None, refs, table, lengths, int(page))
+    code = load().kv_truncate(pages, _i32(new_lengths, where, (S,)), _stream(stream))
+    if code != OK:
+        raise W4VError(code, where)
 
 
 def kv_fork(pool, refs, table, lengths, parents, children, short=None, ws=None, stream=None):
     """Sequences children[i] become copies of parents[i] (int32 [n]): full pages shared, a partly
     filled last one copied.  Returns `short` as kv_extend does."""
-    import torch
     where = "kv_fork"
-    pages = _pages(where, pool, refs, table, lengths)
-    if parents.dim() != 1 or children.shape != parents.shape:
-        raise W4VError(ERR_SHAPE, where)
-    short, ws = _kv_scratch(pages, short, ws, refs.device)
-    _typed(where, torch.int32, parents, children, short)
-    _dense(where, parents, children)
-    _check(load().kv_fork(ctypes.byref(pages), _ptr(parents), _ptr(children), parents.shape[0], _ptr(short), _ptr(ws),
-                          ws.numel(), _stream(stream)), where)
+    pages, n_pages, S, _ = _pages(where, pool, refs, table, lengths)
+    n = parents.numel()
+    a, c = _i32(parents, where, (n,)), _i32(children, where, (n,))
+    short, at = _short(short, where, refs.device)
+    if ws is None:
+        ws = workspace(kv_workspace_bytes(n_pages, S), refs.device)
+    code = load().kv_fork(pages, a, c, n, at, ws.data_ptr(), ws.numel(), _stream(stream))
+    if code != OK:
+        raise W4VError(code, where)
     return short
 
 
 def kv_compact(pool, refs, table, lengths, refs_out=None, table_out=None, ws=None, stream=None):
     """All live pages to the lowest ids; returns (refs_out, table_out), the old arrays unless given."""
-    import torch
     where = "kv_compact"
-    pages = _pages(where, pool, refs, table, lengths)
+    pages, n_pages, S, width = _pages(where, pool, refs, table, lengths)
     refs_out, table_out = refs if refs_out is None else refs_out, table if table_out is None else table_out
-    if refs_out.shape != refs.shape or table_out.shape != table.shape:
-        raise W4VError(ERR_SHAPE, where)
-    _typed(where, torch.int32, refs_out, table_out)
-    _dense(where, refs_out, table_out)
-    _, ws = _kv_scratch(pages, refs, ws, refs.device)
-    _check(load().kv_compact(ctypes.byref(pages), _ptr(refs_out), _ptr(table_out), _ptr(ws), ws.numel(),
-                             _stream(stream)), where)
+    r, t = _i32(refs_out, where, (n_pages,)), _i32(table_out, where, (S, width))
+    if ws is None:
+        ws = workspace(kv_workspace_bytes(n_pages, S), refs.device)
+    code = load().kv_compact(pages, r, t, ws.data_ptr(), ws.numel(), _stream(stream))
+    if code != OK:
+        raise W4VError(code, where)
     return refs_out, table_out
 
 
 def kv_copy(pool, src, dst, stream=None):
     """Contents of pages src[i] to pages dst[i] (int32 [n]) in every plane of pool [..., n_pages][Hkv][page][D]."""
-    import torch
     where = "kv_copy"
-    if pool.dim() < 5 or src.dim() != 1 or dst.shape != src.shape:
-        raise W4VError(ERR_SHAPE, where)
-    _typed(where, torch.int32, src, dst)
-    _dense(where, pool, src, dst)
-    n_pages = pool.shape[-4]
-    nbytes = pool.shape[-3] * pool.shape[-2] * pool.shape[-1] * pool.element_size()
-    _check(load().kv_copy(_ptr(pool), pool.numel() * pool.element_size() // max(nbytes * n_pages, 1), n_pages, nbytes,
-                          _ptr(src), _ptr(dst), src.shape[0], _stream(stream)), where)
+    planes, n_pages, _, nbytes = _plane(pool)
+    if not pool.is_contiguous():
+        raise W4VError(ERR_ARG, where)
+    n = src.numel()
+    code = load().kv_copy(pool.data_ptr(), planes, n_pages, nbytes, _i32(src, where, (n,)), _i32(dst, where, (n,)), n,
+                          _stream(stream))
+    if code != OK:
+        raise W4VError(code, where)

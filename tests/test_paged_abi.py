@@ -14,14 +14,14 @@ def _kv(w, **kw):
     d = dict(k=FAKE, v=FAKE, table=FAKE, lengths=FAKE, offsets=FAKE, B=2, table_width=10, n_pages=40, kv_heads=4,
              page=16, head_dim=128)
     d.update(kw)
-    return ctypes.byref(w.KV(*d.values()))
+    return w._KV.pack(*(x or 0 for x in d.values()))
 
 
 def _pages(w, **kw):
     d = dict(pool=FAKE, refs=FAKE, table=FAKE, lengths=FAKE, page_bytes=4096, planes=2, n_pages=40, S=3,
              table_width=10, page=16)
     d.update(kw)
-    return ctypes.byref(w.Pages(*d.values()))
+    return w._PAGES.pack(*(x or 0 for x in d.values()))
 
 
 KV_FAULTS = [(dict(page=12), "SHAPE"), (dict(page=4), "SHAPE"), (dict(page=512), "SHAPE"),
