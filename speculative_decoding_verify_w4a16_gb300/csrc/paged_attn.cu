@@ -40,19 +40,21 @@
 // clears what is not finite; the rows that do see it add it in the epilogue.
 // A drafted token that overflowed thus spoils no position before it.
 //
-// Roles (12 warps): 0 producer (page ids, TMA), 1 MMA issuer, 2 guard (the
-// looking over) and tensor-memory owner, 3 scheduler (parts of the CTA's
-// range, through a ring in shared memory), 4-7 and 8-11 softmax.  S and P
-// have buffers of their own, so Q K^T runs ahead (two tiles; one for heads of
-// 256, whose O leaves room for one S) and waits only until the scores are in
-// registers.  The two softmax groups take alternate key tiles, a thread a
-// whole row; what passes between them is the rows' reference.
+// Roles (12 warps): 0 producer (the CTA's parts, which it hands on through a
+// ring in shared memory, page ids, TMA), 1 issuer of Q K^T, 2 issuer of P V,
+// 3 guard (the looking over) and tensor-memory owner, 4-7 and 8-11 softmax.
+// S and P have buffers of their own, so Q K^T runs ahead (two tiles; one for
+// heads of 256, whose O leaves room for one S) and waits only until the
+// scores are in registers.  An issuer is held up by its MMAs' execution and
+// in between by its own waits and loop; with two, one's MMAs run meanwhile.
+// The two softmax groups take alternate key tiles, a thread a whole row; what
+// passes between them is the rows' reference.
 //
 // Code size is part of the design: between them the roles run through their
-// loops once per tile, and what does not stay in the instruction cache costs
-// some 250 cycles a miss.  So each loop body is there once (the first
-// products of a part are the loop's own, with the later ones off), waits are
-// a few instructions, and the schedule is worked out by one warp.
+// loops once per tile, and what falls out of the instruction caches is
+// fetched again.  So each loop body is there once, waits are a few
+// instructions and the schedule is worked out by one warp (from 138 KB of
+// code to 77 the 8192-token prompt went from 537 to 441 us).
 #include <algorithm>
 
 #include "runtime.h"
@@ -64,15 +66,15 @@ namespace {
 constexpr int kKeys = 128;                      // keys per tile
 constexpr int kRows = 128;                      // rows per tile
 constexpr int kThreads = 384;
-constexpr int kWarpProd = 0, kWarpMma = 1, kWarpGuard = 2, kWarpPlan = 3, kWarpSoft = 4;
+constexpr int kWarpProd = 0, kWarpScores = 1, kWarpOut = 2, kWarpGuard = 3, kWarpSoft = 4;
 constexpr int kParts = 4;                       // ring of parts
-constexpr int kPartReaders = 11;                // every warp but the scheduler
+constexpr int kPartReaders = 11;                // every warp but the producer
 constexpr uint32_t kTmemCols = 512;
 // Tensor memory: S in one or two buffers of 128 columns, P in two of 64, O.
 constexpr uint32_t kPcols = kKeys / 2;
 constexpr float kShift = 8.f, kSlack = 6.f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kInvTiles = 4;                    // least tiles of a batch-invariant part
+constexpr int kInvBits = 2;                     // least tiles of a batch-invariant part (2^this)
 constexpr int kInvParts = 32;                   // most parts of a row tile
 
 template <int D>
@@ -83,11 +85,12 @@ struct Plan {
     static constexpr int kGroupBytes = kStageBlocks * 1024;      // 8 tokens of a stage
     static constexpr int kStageBytes = kKeys / 8 * kGroupBytes;
     static constexpr int kQBytes = kBlocks * kRows * 128;
-    static constexpr int kStages = D == 64 ? 10 : D == 128 ? 6 : 5;
+    static constexpr int kStagesK = D == 64 ? 5 : 3, kStagesV = D == 64 ? 5 : D == 128 ? 3 : 2;
+    static constexpr int kStages = kStagesK + kStagesV;          // rings of their own, each with one reader
     static constexpr int kBar = kQBytes + kStages * kStageBytes;
     static constexpr int kScores = D >= 256 ? 1 : 2;             // S buffers, and tiles that Q K^T runs ahead
     static constexpr uint32_t kPcol = kScores * kKeys, kOcol = kPcol + 2 * kPcols;
-    static constexpr int kNumBars = 2 + 2 * kStages + 8 + 4 + 8 + 4 + 2 * kParts;
+    static constexpr int kNumBars = 2 + 2 * kStages + 10 + 4 + 8 + 4 + 2 * kParts;
     static constexpr int kMisc = kBar + 8 * kNumBars;
     static constexpr int kRing = (kMisc + 16 + 15) & ~15;
     static constexpr int kRef = kRing + kParts * 48;             // float[kRows]: the rows' references
@@ -95,6 +98,17 @@ struct Plan {
     static constexpr int kBytes = kSums + 2 * kRows * 4;
     static_assert(kOcol + D <= kTmemCols, "tensor memory plan");
     static_assert(kBytes <= 227 * 1024, "shared memory plan");
+};
+
+// Rows of a row tile that one CTA of the second kernel joins: the share-th of
+// `shares` equal shares, from n parts (n = 0: nothing).  Default: entry c is
+// for the tile that range c begins inside of, from slot 2 first + 1 and then
+// slots 2 (first + i); batch-invariant: entry u for unit u, from slots in a row.
+struct Share {
+    int row0, rows, kvh;
+    int slot0, n;
+    int share, shares;
+    int count;                  // entry 0: how many entries there are
 };
 
 struct Args {
@@ -107,7 +121,8 @@ struct Args {
     uint32_t *status;
     int n_tokens, q_heads, kv_heads, group, tok;   // query heads per key/value head, tokens per tile
     int B, width, n_pages, page_bits, window, slot_rows;   // 2^page_bits tokens a page
-    int inv;                    // 0, or tiles per batch-invariant part
+    int inv_bits;               // -1, or 2^inv_bits tiles per batch-invariant part
+    struct Share *shares;       // what the second kernel joins
     float scale_log2;
 };
 
@@ -127,34 +142,40 @@ __device__ __forceinline__ Seq seq_of(const Args &p, int b) {
 struct Extent {
     int lo, hi, units;          // tiles [lo, hi); a tile without keys is one unit
 };
-__device__ __noinline__ Extent extent_of(const Args &p, const Seq &s, int qt) {
+__device__ __forceinline__ Extent extent_of(const Args &p, const Seq &s, int qt) {
     const int t0 = qt * p.tok, t1 = min(s.n, t0 + p.tok) - 1;
     const int p0 = s.len - s.n + t0, p1 = s.len - s.n + t1;
     Extent e{0, 0, 1};
-    if (p1 < 0) return e;
-    e.lo = p.window > 0 ? max(0, p0 - p.window + 1) / kKeys : 0;
-    e.hi = p1 / kKeys + 1;
-    e.units = p.inv == 0 ? e.hi - e.lo : (e.hi - 1) / p.inv - e.lo / p.inv + 1;
+    if (p1 >= 0) {
+        e.lo = p.window > 0 ? max(0, p0 - p.window + 1) / kKeys : 0;
+        e.hi = p1 / kKeys + 1;
+        e.units = p.inv_bits < 0 ? e.hi - e.lo : ((e.hi - 1) >> p.inv_bits) - (e.lo >> p.inv_bits) + 1;
+    }
     return e;
 }
 
 // Units of one key/value head of 32 sequences, one per lane (0 past the end).
-__device__ __noinline__ int lane_units(const Args &p, int b) {
+// A lane counts a few row tiles by itself; the warp together those of a
+// sequence with more.
+__device__ __forceinline__ int lane_units(const Args &p, int b) {
+    constexpr int kFew = 4;
     const int lane = threadIdx.x & 31;
     Seq s{0, 0, 0};
     if (b < p.B) s = seq_of(p, b);
     const int tiles = (s.n + p.tok - 1) / p.tok;
-    int u = tiles == 1 ? extent_of(p, s, 0).units : 0;
+    int u = 0;
 #pragma unroll 1
-    for (uint32_t many = __ballot_sync(0xFFFFFFFFu, tiles > 1); many != 0; many &= many - 1) {
+    for (int qt = 0; qt < min(tiles, kFew); ++qt) u += extent_of(p, s, qt).units;
+#pragma unroll 1
+    for (uint32_t many = __ballot_sync(0xFFFFFFFFu, tiles > kFew); many != 0; many &= many - 1) {
         const int src = __ffs(many) - 1;
         const Seq o{0, __shfl_sync(0xFFFFFFFFu, s.n, src), __shfl_sync(0xFFFFFFFFu, s.len, src)};
         const int ot = __shfl_sync(0xFFFFFFFFu, tiles, src);
         int sum = 0;
 #pragma unroll 1
-        for (int qt = lane; qt < ot; qt += 32) sum += extent_of(p, o, qt).units;
+        for (int qt = kFew + lane; qt < ot; qt += 32) sum += extent_of(p, o, qt).units;
         sum = __reduce_add_sync(0xFFFFFFFFu, sum);
-        if (lane == src) u = sum;
+        if (lane == src) u += sum;
     }
     return u;
 }
@@ -169,13 +190,6 @@ __device__ __forceinline__ int warp_scan(int x) {
         if ((threadIdx.x & 31) >= d) x += y;
     }
     return x;
-}
-
-__device__ __forceinline__ int all_units(const Args &p) {
-    int sum = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < p.B; b0 += 32) sum += lane_units(p, b0 + (threadIdx.x & 31));
-    return __reduce_add_sync(0xFFFFFFFFu, sum) * p.kv_heads;
 }
 
 // An even split of `units` over at most `ctas` ranges, none of them empty.
@@ -196,13 +210,23 @@ struct Split {
 struct Place {
     int b, kvh, qt, u;          // unit u of a row tile
 };
-// The place of unit `at` (one warp; at < all_units).
-__device__ __forceinline__ Place place_of(const Args &p, int at) {
+// All units (one warp), and the lane_units of the last 32 sequences.
+__device__ __forceinline__ int all_units(const Args &p, int &last) {
+    int sum = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        last = lane_units(p, b0 + (threadIdx.x & 31));
+        sum += last;
+    }
+    return __reduce_add_sync(0xFFFFFFFFu, sum) * p.kv_heads;
+}
+// The place of unit `at` (one warp; at < all_units, which left `last`).
+__device__ __forceinline__ Place place_of(const Args &p, int at, int last) {
     const int lane = threadIdx.x & 31;
     Place w{0, 0, 0, 0};
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int u = lane_units(p, b0 + lane);
+        const int u = p.B <= 32 ? last : lane_units(p, b0 + lane);
         const int upto = warp_scan(u * p.kv_heads);
         const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > at);
         if (past == 0) {
@@ -263,15 +287,15 @@ struct Cursor {
         g.u = w.u;
         g.units = e.units;
         int take = 1;
-        if (p.inv == 0) {
+        if (p.inv_bits < 0) {
             take = min(e.units - w.u, left);
             g.kt0 = e.lo + w.u;
             g.nt = e.hi > e.lo ? take : 0;
             g.slot = 2 * cta + (w.u == 0);
         } else {
-            const int c = (e.lo / p.inv + w.u) * p.inv;
+            const int c = ((e.lo >> p.inv_bits) + w.u) << p.inv_bits;
             g.kt0 = max(e.lo, c);
-            g.nt = max(min(e.hi, c + p.inv) - g.kt0, 0);
+            g.nt = max(min(e.hi, c + (1 << p.inv_bits)) - g.kt0, 0);
             g.slot = unit;
         }
         if (take == e.units) g.slot = -1;
@@ -347,18 +371,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     const uint32_t base = smem_u32(smem);
     const uint32_t bar0 = base + P::kBar;
     const uint32_t q_full = bar0, q_empty = bar0 + 8u;
-    auto kv_full = [&](int s) { return bar0 + 16u + 8u * s; };
+    auto kv_full = [&](int s) { return bar0 + 16u + 8u * s; };   // K's stages, then V's
     auto kv_empty = [&](int s) { return bar0 + 16u + 8u * (P::kStages + s); };
     const uint32_t rest = bar0 + 16u + 16u * P::kStages;
     auto s_full = [&](int i) { return rest + 8u * i; };          // by softmax group
     auto p_full = [&](int i) { return rest + 16u + 8u * i; };
-    auto pv_done = [&](int i) { return rest + 32u + 8u * i; };
-    auto s_empty = [&](int i) { return rest + 48u + 8u * i; };
-    const uint32_t v_ask = rest + 64u, v_ready = rest + 72u, o_empty = rest + 80u, done_bar = rest + 88u;
-    auto turn = [&](int quad, int i) { return rest + 96u + 16u * quad + 8u * i; };
-    auto pair = [&](int quad) { return rest + 160u + 8u * quad; };
-    auto part_full = [&](int i) { return rest + 192u + 8u * i; };
-    auto part_empty = [&](int i) { return rest + 192u + 8u * (kParts + i); };
+    // Four phases apart: who has seen tile t - 4's product may wait for any of
+    // t - 3 .. t without taking one phase for the next but one.
+    auto pv_done = [&](int tile) { return rest + 32u + 8u * (tile & 3); };
+    auto pv_phase = [&](int tile) { return uint32_t(tile >> 2) & 1u; };
+    auto s_empty = [&](int i) { return rest + 64u + 8u * i; };
+    const uint32_t v_ask = rest + 80u, v_ready = rest + 88u, o_empty = rest + 96u, done_bar = rest + 104u;
+    auto turn = [&](int quad, int i) { return rest + 112u + 16u * quad + 8u * i; };
+    auto pair = [&](int quad) { return rest + 176u + 8u * quad; };
+    auto part_full = [&](int i) { return rest + 208u + 8u * i; };
+    auto part_empty = [&](int i) { return rest + 208u + 8u * (kParts + i); };
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + P::kMisc);    // [0] tmem, [2..3] below
     volatile uint32_t *spoilt = misc + 2;                    // [i & 1]: part i (from 1) had values cleared
     Part *ring = reinterpret_cast<Part *>(smem + P::kRing);
@@ -375,13 +402,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
             mbar_init(p_full(i), 4);             // the warps of one softmax group
-            mbar_init(pv_done(i), 2);            // the MMAs, and the issuer's own arrival
             mbar_init(s_empty(i), 4);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(pv_done(i), 2);    // the MMAs, and the issuer's own arrival
         mbar_init(v_ask, 1);
         mbar_init(v_ready, 1);
         mbar_init(o_empty, 8);                   // both softmax groups
-        mbar_init(done_bar, 1);
+        mbar_init(done_bar, 2);                  // both issuers
         for (int q = 0; q < 4; ++q) {
             mbar_init(turn(q, 0), 1);
             mbar_init(turn(q, 1), 1);
@@ -426,34 +453,47 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     // registers from the four single warps to the softmax groups: 128 x 88 +
     // 256 x 208 of the 384 x 168 that the CTA was launched with
     if (warp < kWarpSoft) set_max_registers_down<88>();
-    if (warp == kWarpPlan) {
-        const Split split(all_units(p), gridDim.x);
+    if (warp == kWarpProd) {
+        int last = 0;
+        const int all = all_units(p, last);
+        const Split split(all, gridDim.x);
         Cursor cur{};
         if (int(blockIdx.x) < split.ranges) {
             cur.unit = split.begin(blockIdx.x);
             cur.left = split.begin(blockIdx.x + 1) - cur.unit;
-            cur.w = place_of(p, cur.unit);
+            cur.w = place_of(p, cur.unit, last);
             cur.load(p);
         }
-        Part g{};
-        for (int i = 0; ok && g.nt >= 0; ++i) {
+        const int box_bits = min(p.page_bits, 7), box = 1 << box_bits;       // tokens per TMA box
+        const uint32_t box_bytes = uint32_t(box / 8) * P::kGroupBytes;
+        const int boxes = kKeys >> box_bits;
+        const int groups = 1 << (p.page_bits - 3);           // 8-token groups of a page
+        int itk = 0, itv = 0, nq = 0;
+        for (int i = 0; ok; ++i) {
+            Part g{};
+            const int unit = cur.unit;
             if (!cur.next(p, blockIdx.x, g)) g.nt = -1;
+            // the share of this range's first row tile, or of every unit's
+            if (lane == 0 && (p.inv_bits < 0 ? i == 0 : g.nt >= 0 || all == 0)) {
+                Share e{g.row0, g.rows, g.kvh, unit - g.u, 0, g.u, g.units, p.inv_bits < 0 ? int(gridDim.x) : all};
+                if (p.inv_bits >= 0) {
+                    if (g.units > 1) e.n = g.units;
+                } else if (g.nt >= 0 && g.u > 0) {
+                    const int first = split.owner(unit - g.u), n = split.owner(unit - g.u + g.units - 1) - first + 1;
+                    e.slot0 = 2 * first + 1;
+                    e.n = n;
+                    e.share = int(blockIdx.x) - first - 1;
+                    e.shares = n - 1;
+                }
+                p.shares[p.inv_bits < 0 ? int(blockIdx.x) : unit] = e;
+            }
             if (i >= kParts) ok = wait(part_empty(i % kParts), (i / kParts - 1) & 1);
             if (!ok) break;
             if (lane == 0) {
                 ring[i % kParts] = g;
                 mbar_arrive(part_full(i % kParts));
             }
-        }
-    } else if (warp == kWarpProd) {
-        const int box_bits = min(p.page_bits, 7), box = 1 << box_bits;       // tokens per TMA box
-        const uint32_t box_bytes = uint32_t(box / 8) * P::kGroupBytes;
-        const int boxes = kKeys >> box_bits;
-        const int groups = 1 << (p.page_bits - 3);           // 8-token groups of a page
-        int it = 0, nq = 0;
-        for (int i = 0; acquire(i); ++i) {
-            const Part g = part_of(i);
-            release(i);
+            if (g.nt < 0) break;
             if (g.nt == 0) continue;
             // this lane's page (box) of key tile j: its first 8-token group, or
             // one past the cache, which TMA fills with zeros
@@ -485,10 +525,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     const CUtensorMap *map = kv == 0 ? &kmap : &vmap;
                     const int grp = kv == 0 ? ids[P::kScores] : ids[0];
                     const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, grp >= 0));
+                    const int depth = kv == 0 ? P::kStagesK : P::kStagesV, first = kv == 0 ? 0 : P::kStagesK;
+                    int it = kv == 0 ? itk : itv;
 #pragma unroll 1
                     for (int h = 0; h < P::kHalves; ++h, ++it) {
-                        const int s = it % P::kStages;
-                        if (it >= P::kStages) ok = wait(kv_empty(s), (it / P::kStages - 1) & 1);
+                        const int s = first + it % depth;
+                        if (it >= depth) ok = wait(kv_empty(s), (it / depth - 1) & 1);
                         if (!ok) break;
                         if (lane == 0) mbar_arrive_expect_tx(kv_full(s), n * box_bytes);
                         __syncwarp();
@@ -496,6 +538,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                             tma_load_4d(base + P::kQBytes + s * P::kStageBytes + lane * box_bytes, map, 0, 0,
                                         h * P::kStageBlocks, grp, kv_full(s));
                     }
+                    (kv == 0 ? itk : itv) = it;
                 }
 #pragma unroll
                 for (int k = 0; k < P::kScores + 1; ++k) ids[k] = ids[k + 1];
@@ -503,93 +546,103 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             }
         }
         // every copy has landed before the CTA ends, also where its reader gave up
-        for (int i = max(0, it - P::kStages); i < it; ++i)
-            ok = mbar_wait_bounded(kv_full(i % P::kStages), (i / P::kStages) & 1) && ok;
+        for (int i = max(0, itk - P::kStagesK); i < itk; ++i)
+            ok = mbar_wait_bounded(kv_full(i % P::kStagesK), (i / P::kStagesK) & 1) && ok;
+        for (int i = max(0, itv - P::kStagesV); i < itv; ++i)
+            ok = mbar_wait_bounded(kv_full(P::kStagesK + i % P::kStagesV), (i / P::kStagesV) & 1) && ok;
         if (nq > 0) ok = mbar_wait_bounded(q_full, (nq - 1) & 1) && ok;
-    } else if (warp == kWarpMma) {
-        constexpr uint32_t idesc_s = idesc_f16_f32(kRows, kKeys);
-        constexpr uint32_t idesc_o = idesc_f16_f32(kRows, 64 * P::kStageBlocks) | kIdescBMnMajor;
-        // Descriptors: the high words are constants, and the low ones (address
-        // / 16) grow by constants from one per operand.  (Put together from
-        // the address for each MMA they cost more to issue than the MMA runs.)
-        constexpr uint64_t kHighQ = uint64_t(sdesc_high(1024)) << 32, kHighKv = uint64_t(sdesc_high(P::kGroupBytes)) << 32;
-        const uint32_t q_low = sdesc_low(base, 16), k_low = sdesc_low(base + P::kQBytes, 16),
-                       v_low = sdesc_low(base + P::kQBytes, 1024);
-        int it = 0, nq = 0, t = 0, looked = 0;               // stages, parts, tiles, guarded tiles so far
-        // What steers the loop goes through a warp-wide vote or reduction:
-        // their results are uniform to the compiler, so stage numbers and
-        // descriptors stay in uniform registers.
+    } else if (warp == kWarpScores) {
+        // S = Q K^T.  Descriptors: the high words are constants, and the low
+        // ones (address / 16) grow by constants from one per operand.  (Put
+        // together from the address for each MMA they cost more to issue than
+        // the MMA runs.)  What steers the loops goes through a warp-wide vote
+        // or reduction: their results are uniform to the compiler, so stage
+        // numbers and descriptors stay in uniform registers.
+        constexpr uint32_t idesc = idesc_f16_f32(kRows, kKeys);
+        constexpr uint64_t kHighQ = uint64_t(sdesc_high(1024)) << 32, kHighK = uint64_t(sdesc_high(P::kGroupBytes)) << 32;
+        const uint32_t q_low = sdesc_low(base, 16), k_low = sdesc_low(base + P::kQBytes, 16);
+        int it = 0, nq = 0, t = 0;                           // stages, parts, tiles so far
         for (int i = 0; __any_sync(0xFFFFFFFFu, acquire(i)); ++i) {
-            const int nt = warp_uniform(part_of(i).nt), keys_end = warp_uniform(part_of(i).keys_end);
-            const int key0 = warp_uniform(part_of(i).kt0 * kKeys), pos0 = warp_uniform(part_of(i).pos0);
+            const int nt = warp_uniform(part_of(i).nt);
             release(i);
             if (nt == 0) continue;
             ok = wait(q_full, nq & 1);
             ++nq;
-            for (int j = 0; j < nt + P::kScores && ok; ++j) {
-                if (j < nt) {                                // S = Q K^T of tile t + j
-                    const int tile = t + j, b = tile % P::kScores, u = tile / P::kScores;
-                    if (u > 0) ok = wait(s_empty(b), (u - 1) & 1);
-#pragma unroll 1
-                    for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
-                        const int s = it % P::kStages;
-                        ok = wait(kv_full(s), (it / P::kStages) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < 4 * P::kStageBlocks; ++k)
-                                mma_f16_ss(tmem + b * kKeys,
-                                           kHighQ | (q_low + h * (P::kStageBlocks * kRows * 128 / 16) +
-                                                     ((k >> 2) * (kRows * 128) + (k & 3) * 32) / 16),
-                                           kHighKv | (k_low + s * (P::kStageBytes / 16) +
-                                                      ((k >> 2) * 1024 + (k & 3) * 32) / 16),
-                                           idesc_s, h > 0 || k > 0);
-                            mma_commit(kv_empty(s));
-                            if (h + 1 == P::kHalves) {
-                                mma_commit(s_full(tile & 1));        // by group: each waits for its own tiles alone
-                                if (j + 1 == nt) mma_commit(q_empty);
-                            }
-                        }
-                        __syncwarp();
-                    }
-                }
-                if (j < P::kScores || !ok) continue;
-                // O += P V of tile v, over the keys that some row sees
-                const int jv = j - P::kScores, v = t + jv;
-                const int key = key0 + jv * kKeys, steps = min((keys_end - key + 15) / 16, kKeys / 16);
-                const bool look = guarded(p, key, keys_end, pos0);
-                if (look) {
-                    if (elect_one()) mbar_arrive(v_ask);
-                    __syncwarp();
-                }
-                ok = wait(p_full(v & 1), (v >> 1) & 1);
-                if (ok && look) ok = wait(v_ready, (looked++) & 1);
-                if (ok && jv == 0 && nq > 1) ok = wait(o_empty, nq & 1);         // part nq - 1 is read
+            const int end = t + nt;
+            for (; t < end && ok; ++t) {
+                const int b = t % P::kScores, u = t / P::kScores;
+                if (u > 0) ok = wait(s_empty(b), (u - 1) & 1);
 #pragma unroll 1
                 for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
-                    const int s = it % P::kStages;
-                    ok = wait(kv_full(s), (it / P::kStages) & 1);
+                    const int s = it % P::kStagesK;
+                    ok = wait(kv_full(s), (it / P::kStagesK) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t d = tmem + P::kOcol + h * 64 * P::kStageBlocks, a = tmem + P::kPcol + (v & 1) * kPcols;
-                        const uint32_t low = v_low + s * (P::kStageBytes / 16);
 #pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
-                            if (k < steps)
-                                mma_f16_ts(d, a + 8 * k, kHighKv | (low + k * (2 * P::kGroupBytes / 16)), idesc_o,
-                                           jv > 0 || k > 0);
+                        for (int k = 0; k < 4 * P::kStageBlocks; ++k)
+                            mma_f16_ss(tmem + b * kKeys,
+                                       kHighQ | (q_low + h * (P::kStageBlocks * kRows * 128 / 16) +
+                                                 ((k >> 2) * (kRows * 128) + (k & 3) * 32) / 16),
+                                       kHighK | (k_low + s * (P::kStageBytes / 16) + ((k >> 2) * 1024 + (k & 3) * 32) / 16),
+                                       idesc, h > 0 || k > 0);
                         mma_commit(kv_empty(s));
                         if (h + 1 == P::kHalves) {
-                            mma_commit(pv_done(v & 1));
-                            mbar_arrive(pv_done(v & 1));     // passes the guard's findings on
+                            mma_commit(s_full(t & 1));       // by group: each waits for its own tiles alone
+                            if (t + 1 == end) mma_commit(q_empty);
                         }
                     }
                     __syncwarp();
                 }
             }
-            t += nt;
+        }
+        if (elect_one()) mma_commit(done_bar);
+        __syncwarp();
+        mbar_wait_bounded(done_bar, 0);
+        __syncwarp();
+    } else if (warp == kWarpOut) {
+        // O += P V, over the keys that some row sees
+        constexpr uint32_t idesc = idesc_f16_f32(kRows, 64 * P::kStageBlocks) | kIdescBMnMajor;
+        constexpr uint64_t kHighV = uint64_t(sdesc_high(P::kGroupBytes)) << 32;
+        const uint32_t v_low = sdesc_low(base + P::kQBytes + P::kStagesK * P::kStageBytes, 1024);
+        int it = 0, nq = 0, t = 0, looked = 0;               // stages, parts, tiles, guarded tiles so far
+        for (int i = 0; __any_sync(0xFFFFFFFFu, acquire(i)); ++i) {
+            const int nt = warp_uniform(part_of(i).nt), pos0 = warp_uniform(part_of(i).pos0);
+            const int key0 = warp_uniform(part_of(i).kt0 * kKeys), keys_end = warp_uniform(part_of(i).keys_end);
+            release(i);
+            if (nt == 0) continue;
+            for (int j = 0; j < nt && ok; ++j, ++t) {
+                const int key = key0 + j * kKeys;
+                const bool look = guarded(p, key, keys_end, pos0);
+                if (look && elect_one()) mbar_arrive(v_ask);
+                __syncwarp();
+                if (j == 0 && nq++ > 0) ok = wait(o_empty, nq & 1);          // the part before is read
+                ok = ok && wait(p_full(t & 1), (t >> 1) & 1);
+                if (ok && look) ok = wait(v_ready, (looked++) & 1);
+                const int steps = min((keys_end - key + 15) / 16, kKeys / 16);
+#pragma unroll 1
+                for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
+                    const int s = it % P::kStagesV;
+                    ok = wait(kv_full(P::kStagesK + s), (it / P::kStagesV) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t d = tmem + P::kOcol + h * 64 * P::kStageBlocks, a = tmem + P::kPcol + (t & 1) * kPcols;
+                        const uint32_t low = v_low + s * (P::kStageBytes / 16);
+#pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            if (k < steps)
+                                mma_f16_ts(d, a + 8 * k, kHighV | (low + k * (2 * P::kGroupBytes / 16)), idesc,
+                                           j > 0 || k > 0);
+                        mma_commit(kv_empty(P::kStagesK + s));
+                        if (h + 1 == P::kHalves) {
+                            mma_commit(pv_done(t));
+                            mbar_arrive(pv_done(t));         // passes the guard's findings on
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
         }
         if (elect_one()) mma_commit(done_bar);
         __syncwarp();
@@ -607,10 +660,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             if (g.nt == 0) continue;
             ++np;
             bool found = false;
-            for (int j = 0; j < g.nt + P::kScores && ok; ++j) {
-                if (j < g.nt) it += P::kHalves;              // K
-                if (j < P::kScores) continue;
-                const int key = (g.kt0 + j - P::kScores) * kKeys;
+            for (int j = 0; j < g.nt && ok; ++j) {
+                const int key = (g.kt0 + j) * kKeys;
                 if (!guarded(p, key, g.keys_end, g.pos0)) {
                     it += P::kHalves;
                     continue;
@@ -622,8 +673,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 const int below = p.window > 0 ? min(g.keys_end - p.window - key, above) : 0;
 #pragma unroll 1
                 for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
-                    const int s = it % P::kStages;
-                    ok = wait(kv_full(s), (it / P::kStages) & 1);
+                    const int s = P::kStagesK + it % P::kStagesV;
+                    ok = wait(kv_full(s), (it / P::kStagesV) & 1);
                     if (!ok) break;
                     uint8_t *st = smem + P::kQBytes + s * P::kStageBytes;
                     // a lane's 16-byte column, of every kStep'th token
@@ -691,7 +742,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     // and a second arrival within a phase would stand in for a
                     // warp that still works.
                     if (lane == 0) mbar_arrive(s_empty(sb));
-                    if (t > 1) ok = wait(pv_done(t & 1), ((t >> 1) - 1) & 1);
+                    if (t > 1) ok = wait(pv_done(t - 2), pv_phase(t - 2));
                     if (!ok) break;
                     if (lane == 0) mbar_arrive(p_full(t & 1));
                     continue;
@@ -746,11 +797,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     }
                     if (j == 0 || !__any_sync(0xFFFFFFFFu, raise)) break;
                     // O by the new reference, once the tile before is added in.
-                    // (The barrier's phase before that one, tile t - 3's, is
-                    // over: that product was issued before this tile's
-                    // scores.)  The scores are read again rather than held in
-                    // 128 registers meanwhile.
-                    ok = wait(pv_done((t - 1) & 1), ((t - 1) >> 1) & 1);
+                    // The scores are read again rather than held in 128
+                    // registers meanwhile.
+                    ok = wait(pv_done(t - 1), pv_phase(t - 1));
                     if (!ok) break;
                     tc_fence_after();
                     const float a = raise ? ex2((was - now) * c) : 1.f;
@@ -771,7 +820,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_empty(sb));     // the scores are in registers
                 // P's buffer: tile t - 2's product has read it
-                if (t > 1) ok = wait(pv_done(t & 1), ((t >> 1) - 1) & 1);
+                if (t > 1) ok = wait(pv_done(t - 2), pv_phase(t - 2));
                 if (!ok) break;
                 tc_fence_after();
                 const float off = m == -INFINITY ? 0.f : kShift - m * c;
@@ -803,32 +852,29 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             if (!ok) break;
             if (!busy) {
                 use -= nt;                                   // a pair that skips a part hands nothing on
-                if (nt > 0 && ((t - 1) & 1) == half) {       // for both of the pair, at the product's end
-                    ok = wait(pv_done((t - 1) & 1), ((t - 1) >> 1) & 1);
+                if (nt > 0) {
+                    ok = wait(pv_done(t - 1), pv_phase(t - 1));
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_n(o_empty, 2);
+                    if (lane == 0) mbar_arrive(o_empty);
                 }
                 release(i);
                 continue;
             }
             if (nt > 0) {
-                // the last tile's reference; its product, which the group that
-                // had the tile waits for (it has waited for tile t - 3's, the
-                // barrier's phase before), the other after it; and the row's
-                // sum by the last reference, the first group's share first
-                const uint32_t last_pv = pv_done((t - 1) & 1), last_phase = ((t - 1) >> 1) & 1;
-                ok = wait(turn(quad, (use - 1) & 1), ((use - 1) >> 1) & 1);
-                if (ok && ((t - 1) & 1) == half) ok = wait(last_pv, last_phase);
+                // The last tile's reference and its product (begun after both
+                // groups read the part before, so `sums` is free), then the
+                // row's sum by that reference, the first group's share first.
+                ok = wait(turn(quad, (use - 1) & 1), ((use - 1) >> 1) & 1) && wait(pv_done(t - 1), pv_phase(t - 1));
                 if (!ok) break;
+                tc_fence_after();
                 const float last = ref[row];
                 if (last != m) l *= ex2((m - last) * c);
                 m = last;
                 sums[half * kRows + row] = l;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pair(quad));
-                ok = wait(pair(quad), (pairs++) & 1) && wait(last_pv, last_phase);
+                ok = wait(pair(quad), (pairs++) & 1);
                 if (!ok) break;
-                tc_fence_after();
                 l = sums[row] + sums[kRows + row];
             }
             const bool fix = nt > 0 && spoilt[np & 1] == np;
@@ -908,116 +954,78 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
 
 // ---------------------------------------------------------- joining the parts
 constexpr int kJoinThreads = 256;
+// A share has at most rows / (n - 1) + 1 rows of n parts, and kJoinSplit CTAs.
+constexpr int kJoinSplit = 4;
+constexpr int kJoinWeights = 3 * kRows + 2 * kMaxCtas;
 
-// Rows [r0, r1) of a row tile from its parts, in order: slot(i), i < n.
-template <int D>
-__device__ __noinline__ void join_rows(const Args &p, const Part &g, int r0, int r1, int n, int slot0, float *weights) {
-    // the parts of ranges first .. first + n - 1, or batch-invariant ones in a row
-    auto slot = [&](int i) { return size_t(p.inv ? slot0 + i : i == 0 ? slot0 : slot0 - 1 + 2 * i); };
-    __syncthreads();                                         // weights may still be read
-    for (int r = r0 + int(threadIdx.x >> 5); r < r1; r += kJoinThreads / 32) {
-        const int lane = threadIdx.x & 31;
-        float top = -INFINITY, l = 0.f;
-        for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(&p.part_ml[slot(i) * p.slot_rows + r]).x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const int i = i0 + lane;
-            float w = 0.f, wl = 0.f;
-            if (i < n) {
-                const float2 ml = __ldcg(&p.part_ml[slot(i) * p.slot_rows + r]);
-                w = top == -INFINITY ? 0.f : ex2(ml.x - top);
-                wl = ml.y == 0.f ? 0.f : w * ml.y;
-            }
-            // in order, so that parts which add nothing change nothing
-            for (int k = 0; k < min(32, n - i0); ++k) l += __shfl_sync(0xFFFFFFFFu, wl, k);
-            if (i < n) weights[(r - r0) * n + i] = w;
-        }
-        const float inv = l != 0.f ? 1.f / l : 0.f;
-        if (lane == 0) {
-            weights[(r1 - r0) * n + (r - r0)] = inv;
-            if (p.lse != nullptr)
-                p.lse[size_t(g.row0 + r / p.group) * p.q_heads + g.kvh * p.group + r % p.group] =
-                    l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
-        }
-    }
-    __syncthreads();
-    constexpr int kLanes = D / 4;                            // threads per row, four columns each
-    for (int r = r0 + int(threadIdx.x) / kLanes; r < r1; r += kJoinThreads / kLanes) {
-        const int col = 4 * (int(threadIdx.x) % kLanes);
-        const float *w = weights + (r - r0) * n;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kAhead = 8;
-#pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += kAhead) {
-            float4 v[kAhead];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (i0 + k < n)
-                    v[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + (slot(i0 + k) * p.slot_rows + r) * D + col));
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (i0 + k < n && w[i0 + k] != 0.f) {
-                    o.x = fmaf(w[i0 + k], v[k].x, o.x);
-                    o.y = fmaf(w[i0 + k], v[k].y, o.y);
-                    o.z = fmaf(w[i0 + k], v[k].z, o.z);
-                    o.w = fmaf(w[i0 + k], v[k].w, o.w);
-                }
-        }
-        const float inv = weights[(r1 - r0) * n + (r - r0)];
-        const size_t orow = size_t(g.row0 + r / p.group) * p.q_heads + g.kvh * p.group + r % p.group;
-        uint2 h;
-        h.x = h2_as_u32(inv != 0.f ? __floats2half2_rn(o.x * inv, o.y * inv) : __floats2half2_rn(0.f, 0.f));
-        h.y = h2_as_u32(inv != 0.f ? __floats2half2_rn(o.z * inv, o.w * inv) : __floats2half2_rn(0.f, 0.f));
-        *reinterpret_cast<uint2 *>(p.out + orow * D + col) = h;
-    }
-}
-
-// One CTA per boundary between two ranges (batch invariance: the same ranges
-// of units), each a share of the rows of the tile that it cuts.
+// o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over a row's parts, M the
+// largest m_i.  Latency bounds it: the statistics of all rows and parts come
+// in one pass of loads, and o's parts several loads ahead.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
-paged_attn_join_kernel(const Args p, int ranges) {
-    // rows of a share times parts, and a factor per row: at most
-    // (rows / (n - 1) + 1) (n + 1) with n >= 2 parts
-    __shared__ float weights[3 * kRows + 3 + 2 * kMaxCtas];
-    __shared__ Cursor start;
-    __shared__ int total;
+paged_attn_join_kernel(const Args p) {
+    __shared__ float2 ml[kJoinWeights];          // m, l; then the part's weight in x
+    __shared__ float scale[kRows];
+    grid_dep_wait();
     grid_dep_launch();
-    // the sequences' sizes were final before the kernel in front of this one began
-    if (threadIdx.x < 32) {
-        const int all = all_units(p);
-        const Split split(all, ranges);
-        const int c = int(blockIdx.x) + (p.inv ? 0 : 1);
-        Cursor s{};
-        if (c < split.ranges) {
-            s.unit = split.begin(c);
-            s.left = split.begin(c + 1) - s.unit;
-            s.w = place_of(p, s.unit);
+    const int count = p.shares[0].count;
+    for (int e = blockIdx.x; e < count; e += gridDim.x) {
+        const Share g = p.shares[e];
+        const int n = g.n;
+        if (n == 0) continue;
+        const int s0 = g.share * g.rows / g.shares, s1 = (g.share + 1) * g.rows / g.shares;
+        const int r0 = s0 + int(blockIdx.y) * (s1 - s0) / kJoinSplit;
+        const int rows = s0 + int(blockIdx.y + 1) * (s1 - s0) / kJoinSplit - r0;
+        auto at = [&](int i, int r) {            // part i's row
+            const int slot = p.inv_bits >= 0 ? g.slot0 + i : i == 0 ? g.slot0 : g.slot0 - 1 + 2 * i;
+            return size_t(slot) * p.slot_rows + r0 + r;
+        };
+        auto row_out = [&](int r) {
+            return size_t(g.row0 + (r0 + r) / p.group) * p.q_heads + g.kvh * p.group + (r0 + r) % p.group;
+        };
+        __syncthreads();                         // the entry before is done with
+        for (int k = threadIdx.x; k < rows * n; k += kJoinThreads) ml[k] = __ldcg(&p.part_ml[at(k % n, k / n)]);
+        __syncthreads();
+        // a row per thread, its parts in order: parts that add nothing change nothing
+        for (int r = threadIdx.x; r < rows; r += kJoinThreads) {
+            float2 *x = ml + r * n;
+            float top = -INFINITY, l = 0.f;
+            for (int i = 0; i < n; ++i) top = fmaxf(top, x[i].x);
+            for (int i = 0; i < n; ++i) {
+                const float w = top == -INFINITY ? 0.f : ex2(x[i].x - top);
+                if (x[i].y != 0.f) l += w * x[i].y;
+                x[i].x = w;
+            }
+            scale[r] = l != 0.f ? 1.f / l : 0.f;
+            if (p.lse != nullptr) p.lse[row_out(r)] = l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
         }
-        if (threadIdx.x == 0) {
-            start = s;
-            total = all;
-        }
-    }
-    __syncthreads();
-    Cursor cur = start;
-    if (cur.left > 0) cur.load(p);
-    grid_dep_wait();                                         // every CTA: who waits for this grid waits for the one before
-    if (cur.left <= 0) return;
-    Part g;
-    if (p.inv == 0) {
-        const Split split(total, ranges);
-        const int at = cur.unit;
-        cur.next(p, 0, g);
-        if (g.u == 0) return;                                // the boundary lies between two tiles
-        const int first = split.owner(at - g.u), last = split.owner(at - g.u + g.units - 1);
-        const int m = last - first, i = int(blockIdx.x) + 1 - first - 1;
-        join_rows<D>(p, g, i * g.rows / m, (i + 1) * g.rows / m, m + 1, 2 * first + 1, weights);
-    } else {
-        while (cur.next(p, 0, g)) {
-            if (g.units == 1) continue;
-            join_rows<D>(p, g, g.u * g.rows / g.units, (g.u + 1) * g.rows / g.units, g.units, cur.unit - 1 - g.u, weights);
+        __syncthreads();
+        constexpr int kLanes = D / 4;            // threads per row, four columns each
+        const int col = 4 * (int(threadIdx.x) % kLanes);
+        for (int r = int(threadIdx.x) / kLanes; r < rows; r += kJoinThreads / kLanes) {
+            const float2 *x = ml + r * n;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            constexpr int kAhead = 8;
+#pragma unroll 1
+            for (int i0 = 0; i0 < n; i0 += kAhead) {
+                float4 v[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (i0 + k < n) v[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at(i0 + k, r) * D + col));
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (i0 + k < n && x[i0 + k].x != 0.f) {
+                        const float w = x[i0 + k].x;
+                        o = make_float4(fmaf(w, v[k].x, o.x), fmaf(w, v[k].y, o.y), fmaf(w, v[k].z, o.z), fmaf(w, v[k].w, o.w));
+                    }
+            }
+            const float inv = scale[r];
+            uint2 h = make_uint2(0u, 0u);
+            if (inv != 0.f) {
+                h.x = h2_as_u32(__floats2half2_rn(o.x * inv, o.y * inv));
+                h.y = h2_as_u32(__floats2half2_rn(o.z * inv, o.w * inv));
+            }
+            *reinterpret_cast<uint2 *>(p.out + row_out(r) * D + col) = h;
         }
     }
 }
@@ -1025,11 +1033,13 @@ paged_attn_join_kernel(const Args p, int ranges) {
 // -------------------------------------------------------------------- the host
 int tokens_per_tile(int q_heads, int kv_heads) { return kRows / (q_heads / kv_heads); }
 
-// Tiles of a batch-invariant part: by the table's width alone, so that it is
-// the same in every call on a cache.
-int inv_tiles(int max_context) {
-    const int tiles = (max_context + kKeys - 1) / kKeys;
-    return std::max(kInvTiles, (tiles + kInvParts - 1) / kInvParts);
+// Tiles of a batch-invariant part (2^this): by the table's width alone, so
+// that it is the same in every call on a cache.
+int inv_tile_bits(int max_context) {
+    const long long tiles = ((long long)max_context + kKeys - 1) / kKeys;
+    int bits = kInvBits;
+    while (tiles > (long long)kInvParts << bits) ++bits;
+    return bits;
 }
 
 struct Slots {
@@ -1044,7 +1054,7 @@ Slots slots_of(int n_tokens, int B, int q_heads, int kv_heads, int max_context, 
         s.count = 2 * size_t(kMaxCtas);
     } else {
         const size_t tiles = size_t(kv_heads) * (size_t(n_tokens) / tok + std::min(B, n_tokens) + 1);
-        const int keys = inv_tiles(max_context) * kKeys;
+        const size_t keys = size_t(kKeys) << inv_tile_bits(max_context);
         s.count = tiles * ((size_t(max_context) + keys - 1) / keys + 1);
     }
     return s;
@@ -1066,8 +1076,7 @@ w4v_status launch(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtens
     }
     if (launch_pdl(paged_attn_kernel<D>, dim3(grid), dim3(kThreads), Plan<D>::kBytes, stream, qmap, kmap, vmap, a) !=
             cudaSuccess ||
-        launch_pdl(paged_attn_join_kernel<D>, dim3(a.inv ? grid : std::max(grid - 1, 1)), dim3(kJoinThreads), 0,
-                   stream, a, grid) != cudaSuccess) {
+        launch_pdl(paged_attn_join_kernel<D>, dim3(grid, kJoinSplit), dim3(kJoinThreads), 0, stream, a) != cudaSuccess) {
         cudaGetLastError();
         return W4V_ERR_CUDA;
     }
@@ -1079,7 +1088,7 @@ w4v_status launch(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtens
 size_t paged_attn_ws_bytes(int n_tokens, int B, int q_heads, int kv_heads, int head_dim, int max_context,
                            bool invariant) {
     const Slots s = slots_of(n_tokens, B, q_heads, kv_heads, max_context, invariant);
-    return s.count * s.rows * (size_t(head_dim) * sizeof(float) + sizeof(float2)) + 256;
+    return s.count * (s.rows * (size_t(head_dim) * sizeof(float) + sizeof(float2)) + sizeof(Share)) + 256;
 }
 
 w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
@@ -1095,6 +1104,7 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     a.lse = lse;
     a.part_o = static_cast<float *>(ws);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + slots.count * slots.rows * D);
+    a.shares = reinterpret_cast<Share *>(a.part_ml + slots.count * slots.rows);
     a.v = reinterpret_cast<const __half *>(kv.v);
     a.table = kv.table;
     a.lengths = kv.lengths;
@@ -1112,7 +1122,7 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     while (1 << a.page_bits < kv.page) ++a.page_bits;
     a.window = window;
     a.slot_rows = slots.rows;
-    a.inv = invariant ? inv_tiles(kv.table_width * kv.page) : 0;
+    a.inv_bits = invariant ? inv_tile_bits(kv.table_width * kv.page) : -1;
     a.scale_log2 = scale * 1.4426950408889634f;
     // K and V as (64 elements, 8 tokens, blocks of a head, 8-token groups):
     // a box is a page's groups of one stage's blocks
