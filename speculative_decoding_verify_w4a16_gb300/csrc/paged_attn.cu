@@ -67,7 +67,7 @@ constexpr int kKeys = 128;                      // keys per tile
 constexpr int kRows = 128;                      // rows per tile
 constexpr int kThreads = 384;
 constexpr int kWarpProd = 0, kWarpScores = 1, kWarpOut = 2, kWarpGuard = 3, kWarpSoft = 4;
-constexpr int kParts = 4;                       // ring of parts
+constexpr int kParts = 2;                       // ring of parts (the softmax groups count on two)
 constexpr int kPartReaders = 11;                // every warp but the producer
 constexpr uint32_t kTmemCols = 512;
 // Tensor memory: S in one or two buffers of 128 columns, P in two of 64, O.
@@ -90,12 +90,12 @@ struct Plan {
     static constexpr int kBar = kQBytes + kStages * kStageBytes;
     static constexpr int kScores = D >= 256 ? 1 : 2;             // S buffers, and tiles that Q K^T runs ahead
     static constexpr uint32_t kPcol = kScores * kKeys, kOcol = kPcol + 2 * kPcols;
-    static constexpr int kNumBars = 2 + 2 * kStages + 10 + 4 + 8 + 4 + 2 * kParts;
+    static constexpr int kNumBars = 2 + 2 * kStages + 10 + 4 + 8 + 8 + 2 * kParts;
     static constexpr int kMisc = kBar + 8 * kNumBars;
     static constexpr int kRing = (kMisc + 16 + 15) & ~15;
     static constexpr int kRef = kRing + kParts * 48;             // float[kRows]: the rows' references
-    static constexpr int kSums = kRef + kRows * 4;               // float[2][kRows]: the groups' sums
-    static constexpr int kBytes = kSums + 2 * kRows * 4;
+    static constexpr int kSums = kRef + kRows * 4;               // float2[2][kRows]: a group's m and l, by part
+    static constexpr int kBytes = kSums + 2 * kRows * 8;
     static_assert(kOcol + D <= kTmemCols, "tensor memory plan");
     static_assert(kBytes <= 227 * 1024, "shared memory plan");
 };
@@ -383,13 +383,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     auto s_empty = [&](int i) { return rest + 64u + 8u * i; };
     const uint32_t v_ask = rest + 80u, v_ready = rest + 88u, o_empty = rest + 96u, done_bar = rest + 104u;
     auto turn = [&](int quad, int i) { return rest + 112u + 16u * quad + 8u * i; };
-    auto pair = [&](int quad) { return rest + 176u + 8u * quad; };
-    auto part_full = [&](int i) { return rest + 208u + 8u * i; };
-    auto part_empty = [&](int i) { return rest + 208u + 8u * (kParts + i); };
+    auto pair = [&](int quad, int i) { return rest + 176u + 16u * quad + 8u * i; };
+    auto part_full = [&](int i) { return rest + 240u + 8u * i; };
+    auto part_empty = [&](int i) { return rest + 240u + 8u * (kParts + i); };
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + P::kMisc);    // [0] tmem, [2..3] below
     volatile uint32_t *spoilt = misc + 2;                    // [i & 1]: part i (from 1) had values cleared
     Part *ring = reinterpret_cast<Part *>(smem + P::kRing);
-    float *ref = reinterpret_cast<float *>(smem + P::kRef), *sums = reinterpret_cast<float *>(smem + P::kSums);
+    float *ref = reinterpret_cast<float *>(smem + P::kRef);
+    float2 *sums = reinterpret_cast<float2 *>(smem + P::kSums);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -407,12 +408,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         for (int i = 0; i < 4; ++i) mbar_init(pv_done(i), 2);    // the MMAs, and the issuer's own arrival
         mbar_init(v_ask, 1);
         mbar_init(v_ready, 1);
-        mbar_init(o_empty, 8);                   // both softmax groups
+        mbar_init(o_empty, 4);                   // the group that ends a part
         mbar_init(done_bar, 2);                  // both issuers
         for (int q = 0; q < 4; ++q) {
             mbar_init(turn(q, 0), 1);
             mbar_init(turn(q, 1), 1);
-            mbar_init(pair(q), 2);               // the two warps that share 32 rows
+            mbar_init(pair(q, 0), 1);            // the group that does not end a part
+            mbar_init(pair(q, 1), 1);
         }
         for (int i = 0; i < kParts; ++i) {
             mbar_init(part_full(i), 1);
@@ -716,8 +718,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         const int half = (warp - kWarpSoft) >> 2, quad = warp & 3, row = 32 * quad + lane;
         const uint32_t lanes = uint32_t(32 * quad) << 16;
         const float c = p.scale_log2;
-        constexpr int kCols = D / 2;                         // this warp's columns of O in the epilogue
-        const uint32_t ocol = tmem + lanes + P::kOcol + half * kCols;
         int t = 0, np = 0;                                   // tiles and parts (with keys) so far
         int use = 0, pairs = 0;                              // references handed on, parts ended by this pair of warps
         for (int i = 0; acquire(i); ++i) {
@@ -750,55 +750,47 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 tc_fence_after();
                 uint32_t x[4][32];
                 const int key = (kt0 + j) * kKeys;
-                bool raise = false;
-                float was = 0.f;
-#pragma unroll 1
-                for (bool again = false;; again = true) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(tmem + lanes + sb * kKeys + 32 * k, x[k]);
+                for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(tmem + lanes + sb * kKeys + 32 * k, x[k]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tc_wait_ld_keep<32>(x[k]);
-                    if (key + kKeys - 1 > sure_hi || key < sure_lo) {
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const int hi = pos - key - 32 * b, lo = from - key - 32 * b;     // keys lo .. hi are seen
-                            const uint32_t seen = (hi < 0 ? 0u : 0xFFFFFFFFu >> (31 - min(hi, 31))) &
-                                                  (lo > 31 ? 0u : 0xFFFFFFFFu << max(lo, 0));
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if ((seen & (1u << k)) == 0u) x[b][k] = 0xFF800000u;         // -inf
-                        }
-                    }
-                    if (again) break;
-                    float top4[4];
+                for (int k = 0; k < 4; ++k) tc_wait_ld_keep<32>(x[k]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_empty(sb));     // the scores are in registers
+                if (key + kKeys - 1 > sure_hi || key < sure_lo) {
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
-                        top4[b] = __uint_as_float(x[b][0]);
+                        const int hi = pos - key - 32 * b, lo = from - key - 32 * b;         // keys lo .. hi are seen
+                        const uint32_t seen = (hi < 0 ? 0u : 0xFFFFFFFFu >> (31 - min(hi, 31))) &
+                                              (lo > 31 ? 0u : 0xFFFFFFFFu << max(lo, 0));
 #pragma unroll
-                        for (int k = 1; k < 31; k += 2)
-                            top4[b] = max3(top4[b], __uint_as_float(x[b][k]), __uint_as_float(x[b][k + 1]));
-                        top4[b] = fmaxf(top4[b], __uint_as_float(x[b][31]));
+                        for (int k = 0; k < 32; ++k)
+                            if ((seen & (1u << k)) == 0u) x[b][k] = 0xFF800000u;             // -inf
                     }
-                    const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-                    // the reference that the tile before left, raised if need be
-                    if (use > 0) {
-                        ok = wait(turn(quad, (use - 1) & 1), ((use - 1) >> 1) & 1);
-                        if (!ok) break;
-                    }
-                    was = j > 0 ? ref[row] : -INFINITY;
-                    raise = mine && top > was && (was == -INFINITY || (top - was) * c > kSlack);
-                    const float now = raise ? top : was;
-                    if (raise || j == 0) ref[row] = now;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(turn(quad, use & 1));
-                    if (now != m) {
-                        l *= ex2((m - now) * c);             // m = -inf: l is 0 and stays
-                        m = now;
-                    }
-                    if (j == 0 || !__any_sync(0xFFFFFFFFu, raise)) break;
-                    // O by the new reference, once the tile before is added in.
-                    // The scores are read again rather than held in 128
-                    // registers meanwhile.
+                }
+                float top4[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    top4[b] = __uint_as_float(x[b][0]);
+#pragma unroll
+                    for (int k = 1; k < 31; k += 2)
+                        top4[b] = max3(top4[b], __uint_as_float(x[b][k]), __uint_as_float(x[b][k + 1]));
+                    top4[b] = fmaxf(top4[b], __uint_as_float(x[b][31]));
+                }
+                const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+                // the reference that the tile before left, raised if need be
+                if (use > 0) ok = wait(turn(quad, (use - 1) & 1), ((use - 1) >> 1) & 1);
+                if (!ok) break;
+                const float was = j > 0 ? ref[row] : -INFINITY;
+                const bool raise = mine && top > was && (was == -INFINITY || (top - was) * c > kSlack);
+                const float now = raise ? top : was;
+                ref[row] = now;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(turn(quad, use & 1));
+                l *= now == m ? 1.f : ex2((m - now) * c);    // m = -inf: l is 0 and stays
+                m = now;
+                if (__any_sync(0xFFFFFFFFu, raise && j > 0)) {
+                    // O by the new reference, once the tile before is added in
                     ok = wait(pv_done(t - 1), pv_phase(t - 1));
                     if (!ok) break;
                     tc_fence_after();
@@ -814,11 +806,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                         tc_wait_st();
                         tc_keep_alive<32>(r);
                     }
+                    tc_fence_before();
                 }
-                if (!ok) break;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(s_empty(sb));     // the scores are in registers
                 // P's buffer: tile t - 2's product has read it
                 if (t > 1) ok = wait(pv_done(t - 2), pv_phase(t - 2));
                 if (!ok) break;
@@ -850,32 +839,37 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 if (lane == 0) mbar_arrive(p_full(t & 1));
             }
             if (!ok) break;
-            if (!busy) {
-                use -= nt;                                   // a pair that skips a part hands nothing on
-                if (nt > 0) {
-                    ok = wait(pv_done(t - 1), pv_phase(t - 1));
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive(o_empty);
+            // The group that had the part's last tile ends it (a part without
+            // keys: the first group); the other leaves its sums and goes on to
+            // the next part.
+            if (!busy) use -= nt;                            // a pair that skips a part hands nothing on
+            float2 *shared_sums = sums + (np & 1) * kRows + row;
+            if (nt > 0 ? ((t - 1) & 1) != half : half != 0) {
+                if (busy && nt > 0) {
+                    *shared_sums = make_float2(m, l);
+                    __syncwarp();
+                    // (it runs ahead by one part at most, for the ring holds two)
+                    if (lane == 0) mbar_arrive(pair(quad, pairs & 1));
+                    ++pairs;
                 }
                 release(i);
                 continue;
             }
+            if (nt > 0) ok = wait(pv_done(t - 1), pv_phase(t - 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (!busy) {
+                if (nt > 0 && lane == 0) mbar_arrive(o_empty);
+                release(i);
+                continue;
+            }
             if (nt > 0) {
-                // The last tile's reference and its product (begun after both
-                // groups read the part before, so `sums` is free), then the
-                // row's sum by that reference, the first group's share first.
-                ok = wait(turn(quad, (use - 1) & 1), ((use - 1) >> 1) & 1) && wait(pv_done(t - 1), pv_phase(t - 1));
+                ok = wait(pair(quad, pairs & 1), (pairs >> 1) & 1);
+                ++pairs;
                 if (!ok) break;
-                tc_fence_after();
-                const float last = ref[row];
-                if (last != m) l *= ex2((m - last) * c);
-                m = last;
-                sums[half * kRows + row] = l;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(pair(quad));
-                ok = wait(pair(quad), (pairs++) & 1);
-                if (!ok) break;
-                l = sums[row] + sums[kRows + row];
+                // the other group's sum, by this one's (the last) reference
+                const float2 other = *shared_sums;
+                l += other.x == m ? other.y : other.y * ex2((other.x - m) * c);
             }
             const bool fix = nt > 0 && spoilt[np & 1] == np;
             const Part g = part_of(i);
@@ -884,17 +878,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             const float m2 = m * c - kShift;
             const size_t orow = size_t(g.row0 + row / p.group) * p.q_heads + g.kvh * p.group + row % p.group;
             const size_t srow = size_t(whole ? 0 : g.slot) * p.slot_rows + row;
-            if (mine && half == 0) {
+            if (mine) {
                 if (!whole) p.part_ml[srow] = make_float2(m2, l);
                 else if (p.lse != nullptr) p.lse[orow] = nt > 0 ? (m2 + log2f(l)) * kLn2 : -INFINITY;
             }
             __syncwarp();
-            __half *out = p.out + orow * D + half * kCols;
-            float *part = p.part_o + srow * D + half * kCols;
+            __half *out = p.out + orow * D;
+            float *part = p.part_o + srow * D;
 #pragma unroll 1
-            for (int o = 0; o < kCols; o += 32) {
+            for (int o = 0; o < D; o += 32) {
                 uint32_t r[32];
-                tmem_ld_32x32b_x32(ocol + o, r);
+                tmem_ld_32x32b_x32(tmem + lanes + P::kOcol + o, r);
                 tc_wait_ld_keep<32>(r);
                 if (mine && whole) {
 #pragma unroll
@@ -929,9 +923,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     const int id = p.table[size_t(g.b) * p.width + (k >> p.page_bits)];
                     if (id < 0 || id >= p.n_pages) continue;
                     const size_t slot = ((size_t(id) * p.kv_heads + g.kvh) << p.page_bits) + (k & ((1 << p.page_bits) - 1));
-                    const __half *v = p.v + slot * D + half * kCols;
+                    const __half *v = p.v + slot * D;
 #pragma unroll 1
-                    for (int o = 0; o < kCols; ++o) {
+                    for (int o = 0; o < D; ++o) {
                         const float y = __half2float(v[o]);
                         if (isfinite(y)) continue;
                         if (whole) out[o] = __float2half_rn(__half2float(out[o]) + y);
