@@ -89,6 +89,7 @@ struct Plan {
     static constexpr int kStages = kStagesK + kStagesV;          // rings of their own, each with one reader
     static constexpr int kBar = kQBytes + kStages * kStageBytes;
     static constexpr int kScores = D >= 256 ? 1 : 2;             // S buffers, and tiles that Q K^T runs ahead
+    static constexpr bool kOwn = D <= 64;                        // an O for each softmax group
     static constexpr uint32_t kPcol = kScores * kKeys, kOcol = kPcol + 2 * kPcols;
     static constexpr int kNumBars = 2 + 2 * kStages + 10 + 4 + 8 + 8 + 2 * kParts;
     static constexpr int kMisc = kBar + 8 * kNumBars;
@@ -96,7 +97,7 @@ struct Plan {
     static constexpr int kRef = kRing + kParts * 48;             // float[kRows]: the rows' references
     static constexpr int kSums = kRef + kRows * 4;               // float2[2][kRows]: a group's m and l, by part
     static constexpr int kBytes = kSums + 2 * kRows * 8;
-    static_assert(kOcol + D <= kTmemCols, "tensor memory plan");
+    static_assert(kOcol + (kOwn ? 2 : 1) * D <= kTmemCols, "tensor memory plan");
     static_assert(kBytes <= 227 * 1024, "shared memory plan");
 };
 
@@ -629,13 +630,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t d = tmem + P::kOcol + h * 64 * P::kStageBlocks, a = tmem + P::kPcol + (t & 1) * kPcols;
+                        const uint32_t d = tmem + P::kOcol + (P::kOwn ? (t & 1) * D : 0) + h * 64 * P::kStageBlocks, a = tmem + P::kPcol + (t & 1) * kPcols;
                         const uint32_t low = v_low + s * (P::kStageBytes / 16);
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k)
                             if (k < steps)
                                 mma_f16_ts(d, a + 8 * k, kHighV | (low + k * (2 * P::kGroupBytes / 16)), idesc,
-                                           j > 0 || k > 0);
+                                           j > (P::kOwn ? 1 : 0) || k > 0);
                         mma_commit(kv_empty(P::kStagesK + s));
                         if (h + 1 == P::kHalves) {
                             mma_commit(pv_done(t));
@@ -778,46 +779,52 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     top4[b] = fmaxf(top4[b], __uint_as_float(x[b][31]));
                 }
                 const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-                // the reference that the tile before left, raised if need be
-                if (use > 0) ok = wait(turn(quad, (use - 1) & 1), ((use - 1) >> 1) & 1);
-                if (!ok) break;
-                const float was = j > 0 ? ref[row] : -INFINITY;
+                // The reference that the tile before left (of this group's own
+                // tiles, or with one O of all), raised if need be
+                float was = m;
+                if (!P::kOwn) {
+                    if (use > 0) ok = wait(turn(quad, (use - 1) & 1), ((use - 1) >> 1) & 1);
+                    if (!ok) break;
+                    was = j > 0 ? ref[row] : -INFINITY;
+                }
                 const bool raise = mine && top > was && (was == -INFINITY || (top - was) * c > kSlack);
                 const float now = raise ? top : was;
-                ref[row] = now;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(turn(quad, use & 1));
+                if (!P::kOwn) {
+                    ref[row] = now;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(turn(quad, use & 1));
+                }
                 l *= now == m ? 1.f : ex2((m - now) * c);    // m = -inf: l is 0 and stays
                 m = now;
-                if (__any_sync(0xFFFFFFFFu, raise && j > 0)) {
-                    // O by the new reference, once the tile before is added in
-                    ok = wait(pv_done(t - 1), pv_phase(t - 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const float a = raise ? ex2((was - now) * c) : 1.f;
-#pragma unroll 1
-                    for (int o = 0; o < D; o += 32) {
-                        uint32_t r[32];
-                        tmem_ld_32x32b_x32(tmem + lanes + P::kOcol + o, r);
-                        tc_wait_ld_keep<32>(r);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * a);
-                        tmem_st_32x32b_x32(tmem + lanes + P::kOcol + o, r);
-                        tc_wait_st();
-                        tc_keep_alive<32>(r);
-                    }
-                    tc_fence_before();
-                }
                 // P's buffer: tile t - 2's product has read it
                 if (t > 1) ok = wait(pv_done(t - 2), pv_phase(t - 2));
                 if (!ok) break;
                 tc_fence_after();
+                if (__any_sync(0xFFFFFFFFu, raise && j > (P::kOwn ? 1 : 0))) {
+                    // O by the new reference, once the tile before is added in
+                    if (!P::kOwn) ok = wait(pv_done(t - 1), pv_phase(t - 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float a = raise ? ex2((was - now) * c) : 1.f;
+                    const uint32_t ocol = tmem + lanes + P::kOcol + (P::kOwn ? half * D : 0);
+#pragma unroll 1
+                    for (int o = 0; o < D; o += 32) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(ocol + o, r);
+                        tc_wait_ld_keep<32>(r);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * a);
+                        tmem_st_32x32b_x32(ocol + o, r);
+                        tc_wait_st();
+                        tc_keep_alive<32>(r);
+                    }
+                }
                 const float off = m == -INFINITY ? 0.f : kShift - m * c;
                 const float2 cc = make_float2(c, c), oo = make_float2(off, off);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t w[2][32];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t w[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
                         const int e = 64 * h + 2 * k;
@@ -826,12 +833,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                         y.x = ex2(y.x);
                         y.y = ex2(y.y);
                         sum[k & 1] = __fadd2_rn(sum[k & 1], y);
-                        w[k] = h2_as_u32(__float22half2_rn(y));
+                        w[h][k] = h2_as_u32(__float22half2_rn(y));
                     }
-                    tmem_st_32x32b_x32(tmem + lanes + P::kPcol + (t & 1) * kPcols + 32 * h, w);
-                    tc_wait_st();
-                    tc_keep_alive<32>(w);
+                    tmem_st_32x32b_x32(tmem + lanes + P::kPcol + (t & 1) * kPcols + 32 * h, w[h]);
                 }
+                tc_wait_st();
+                tc_keep_alive<32>(w[0]);
+                tc_keep_alive<32>(w[1]);
                 const float2 all = __fadd2_rn(sum[0], sum[1]);
                 l += all.x + all.y;
                 tc_fence_before();
@@ -844,6 +852,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             // the next part.
             if (!busy) use -= nt;                            // a pair that skips a part hands nothing on
             float2 *shared_sums = sums + (np & 1) * kRows + row;
+            float weight = 1.f, weight2 = 0.f;
             if (nt > 0 ? ((t - 1) & 1) != half : half != 0) {
                 if (busy && nt > 0) {
                     *shared_sums = make_float2(m, l);
@@ -867,9 +876,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 ok = wait(pair(quad, pairs & 1), (pairs >> 1) & 1);
                 ++pairs;
                 if (!ok) break;
-                // the other group's sum, by this one's (the last) reference
+                // Both groups' sums.  With one O by this group's reference, the
+                // last; with two by the larger, and the O's with them (each
+                // product rounded by itself: which group has the even key
+                // tiles depends on what the CTA did before, the sum must not).
                 const float2 other = *shared_sums;
-                l += other.x == m ? other.y : other.y * ex2((other.x - m) * c);
+                if (P::kOwn) {
+                    const float both = fmaxf(m, other.x);
+                    weight = m == both ? 1.f : ex2((m - both) * c);
+                    weight2 = other.x == both ? 1.f : ex2((other.x - both) * c);
+                    l = __fadd_rn(__fmul_rn(l, weight), __fmul_rn(other.y, weight2));    // a group without keys: 0
+                    if (both == -INFINITY) weight = weight2 = 0.f;
+                    m = both;
+                } else {
+                    l += other.x == m ? other.y : other.y * ex2((other.x - m) * c);
+                }
             }
             const bool fix = nt > 0 && spoilt[np & 1] == np;
             const Part g = part_of(i);
@@ -888,8 +909,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
 #pragma unroll 1
             for (int o = 0; o < D; o += 32) {
                 uint32_t r[32];
-                tmem_ld_32x32b_x32(tmem + lanes + P::kOcol + o, r);
+                tmem_ld_32x32b_x32(tmem + lanes + P::kOcol + (P::kOwn ? half * D : 0) + o, r);
                 tc_wait_ld_keep<32>(r);
+                if (P::kOwn && nt > 1) {
+                    uint32_t q[32];
+                    tmem_ld_32x32b_x32(tmem + lanes + P::kOcol + (half ^ 1) * D + o, q);
+                    tc_wait_ld_keep<32>(q);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        r[k] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(r[k]), weight),
+                                                         __fmul_rn(__uint_as_float(q[k]), weight2)));
+                }
                 if (mine && whole) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
