@@ -83,6 +83,16 @@ def test_fused_rows_and_in_place(w4v_mod, gpu):
     check(w4v_mod, gpu, c, 50, True, None, *x, in_place=True)
 
 
+@pytest.mark.parametrize("D,rot,inter", [(64, 64, False), (128, 32, False), (256, 64, True), (64, 22, False), (256, 256, False)])
+def test_many_rows(w4v_mod, gpu, D, rot, inter):
+    """Enough rows for the kernel that takes a long prompt, more heads than its threads load at once, in place too."""
+    rng = np.random.default_rng([D, rot, 9])
+    c = cache(rng, [2500, 0, 100], [2600, 5, 100], 1, 3, D, 64)
+    x = rows(rng, 2600, 21, 3, D)
+    check(w4v_mod, gpu, c, rot, inter, None, *x)
+    check(w4v_mod, gpu, c, rot, inter, None, *x, in_place=True)
+
+
 def test_rows_without_a_place(w4v_mod, gpu):
     """Rows before position 0 and pages that are not there are not written; rows of no sequence are left alone."""
     rng = np.random.default_rng(5)
