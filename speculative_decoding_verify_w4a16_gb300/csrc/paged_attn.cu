@@ -109,7 +109,7 @@ struct Share {
     int row0, rows, kvh;
     int slot0, n;
     int share, shares;
-    int count;                  // entry 0: how many entries there are
+    int count;                  // batch-invariant, entry 0: how many entries there are (default: one per range)
 };
 
 struct Args {
@@ -121,6 +121,7 @@ struct Args {
     const int32_t *table, *lengths, *offsets;
     uint32_t *status;
     int n_tokens, q_heads, kv_heads, group, tok;   // query heads per key/value head, tokens per tile
+    int wide;                   // out is 32-byte aligned
     int B, width, n_pages, page_bits, window, slot_rows;   // 2^page_bits tokens a page
     int inv_bits;               // -1, or 2^inv_bits tiles per batch-invariant part
     struct Share *shares;       // what the second kernel joins
@@ -477,7 +478,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             const int unit = cur.unit;
             if (!cur.next(p, blockIdx.x, g)) g.nt = -1;
             // the share of this range's first row tile, or of every unit's
-            if (lane == 0 && (p.inv_bits < 0 ? i == 0 : g.nt >= 0 || all == 0)) {
+            auto share_out = [&]() {
+                if (lane != 0 || (p.inv_bits < 0 ? i > 0 : g.nt < 0 && all > 0)) return;
                 Share e{g.row0, g.rows, g.kvh, unit - g.u, 0, g.u, g.units, p.inv_bits < 0 ? int(gridDim.x) : all};
                 if (p.inv_bits >= 0) {
                     if (g.units > 1) e.n = g.units;
@@ -489,7 +491,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     e.shares = n - 1;
                 }
                 p.shares[p.inv_bits < 0 ? int(blockIdx.x) : unit] = e;
-            }
+            };
+            if (g.nt <= 0) share_out();                      // else after the first loads
             if (i >= kParts) ok = wait(part_empty(i % kParts), (i / kParts - 1) & 1);
             if (!ok) break;
             if (lane == 0) {
@@ -543,6 +546,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     }
                     (kv == 0 ? itk : itv) = it;
                 }
+                if (j == 0) share_out();
 #pragma unroll
                 for (int k = 0; k < P::kScores + 1; ++k) ids[k] = ids[k + 1];
                 ids[P::kScores + 1] = ahead;
@@ -921,6 +925,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                                                          __fmul_rn(__uint_as_float(q[k]), weight2)));
                 }
                 if (mine && whole) {
+                    uint32_t w[16];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t h[4];
@@ -929,12 +934,22 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                             const float2 y = make_float2(__uint_as_float(r[8 * k + 2 * e]), __uint_as_float(r[8 * k + 2 * e + 1]));
                             h[e] = inv != 0.f ? h2_as_u32(__floats2half2_rn(y.x * inv, y.y * inv)) : 0u;
                         }
-                        reinterpret_cast<uint4 *>(out + o)[k] = make_uint4(h[0], h[1], h[2], h[3]);
+                        w[4 * k] = h[0];
+                        w[4 * k + 1] = h[1];
+                        w[4 * k + 2] = h[2];
+                        w[4 * k + 3] = h[3];
+                    }
+                    if (p.wide) {
+                        stg_256(out + o, w);
+                        stg_256(out + o + 16, w + 8);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            reinterpret_cast<uint4 *>(out + o)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
                     }
                 } else if (mine) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        reinterpret_cast<uint4 *>(part + o)[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+                    for (int k = 0; k < 4; ++k) stg_256(part + o + 8 * k, r + 8 * k);
                 }
                 __syncwarp();
             }
@@ -992,7 +1007,7 @@ paged_attn_join_kernel(const Args p) {
     __shared__ float scale[kRows];
     grid_dep_wait();
     grid_dep_launch();
-    const int count = p.shares[0].count;
+    const int count = p.inv_bits < 0 ? gridDim.x : p.shares[0].count;
     for (int e = blockIdx.x; e < count; e += gridDim.x) {
         const Share g = p.shares[e];
         const int n = g.n;
@@ -1126,7 +1141,8 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     Args a;
     a.out = reinterpret_cast<__half *>(out);
     a.lse = lse;
-    a.part_o = static_cast<float *>(ws);
+    a.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0u;
+    a.part_o = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + 31u) & ~uintptr_t(31));
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + slots.count * slots.rows * D);
     a.shares = reinterpret_cast<Share *>(a.part_ml + slots.count * slots.rows);
     a.v = reinterpret_cast<const __half *>(kv.v);

@@ -553,6 +553,14 @@ __device__ __forceinline__ uint16_t lds_u16(uint32_t addr) {
     return v;
 }
 
+// 32 bytes to global memory in one instruction (sm_100 and later), a whole
+// sector where a thread writes a row of its own; 32-byte aligned.
+__device__ __forceinline__ void stg_256(void *p, const uint32_t *r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // ------------------------------------------------------- gpu-scope atomics
 // Release-only increment: publishes this CTA's earlier writes without making
 // later memory operations wait for the atomic to return.

@@ -127,6 +127,22 @@ def test_strided_rows_and_another_stream(w4v_mod, gpu):
     assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_results_at_16_byte_addresses(w4v_mod, gpu, D):
+    """out and the workspace at addresses that are multiples of 16 bytes and not of 32."""
+    rng = np.random.default_rng([11, D])
+    c = cache(rng, [9, 200], [100, 5000], 4, 2, D, 16)
+    want, _ = run(w4v_mod, gpu, c)
+    d = {x: to_dev(a, gpu) for x, a in c.items()}
+    size = c["q"].size
+    out = torch.zeros(size + 16, dtype=torch.float16, device=gpu)[8:8 + size].view(c["q"].shape)
+    nbytes = w4v_mod.paged_attn_workspace_bytes(209, 2, 4, 2, D, d["table"].shape[1] * 16)
+    ws = torch.zeros(nbytes + 16, dtype=torch.uint8, device=gpu)[16:]
+    assert out.data_ptr() % 32 == 16 and ws.data_ptr() % 32 == 16
+    w4v_mod.paged_attn(d["q"], d["k"], d["v"], d["table"], d["lengths"], d["offsets"], out=out, ws=ws)
+    assert np.array_equal(out.cpu().numpy(), want)
+
+
 def test_repeatable_and_graph_replay(w4v_mod, gpu):
     """The same bits on every call with one workspace; a captured call follows lengths that change."""
     rng = np.random.default_rng(12)
