@@ -468,11 +468,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             cur.w = place_of(p, cur.unit, last);
             cur.load(p);
         }
-        const int box_bits = min(p.page_bits, 7), box = 1 << box_bits;       // tokens per TMA box
-        const uint32_t box_bytes = uint32_t(box / 8) * P::kGroupBytes;
-        const int boxes = kKeys >> box_bits;
-        const int groups = 1 << (p.page_bits - 3);           // 8-token groups of a page
-        int itk = 0, itv = 0, nq = 0;
+        const int box_bits = min(p.page_bits, 7);            // 2^box_bits tokens per TMA box
+        const uint32_t box_bytes = P::kGroupBytes << (box_bits - 3);
+        const int boxes = kKeys >> box_bits;                 // of a key tile
+        const int group_bits = p.page_bits - 3;              // 8-token groups of a page
+        // this lane's box within a stage, and the stages to fill next
+        const uint32_t box_at = base + P::kQBytes + lane * box_bytes;
+        struct Stage {
+            int s;
+            uint32_t phase;
+        } sk{0, 0}, sv{0, 0};
+        int nq = 0;
         for (int i = 0; ok; ++i) {
             Part g{};
             const int unit = cur.unit;
@@ -501,22 +507,43 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             }
             if (g.nt < 0) break;
             if (g.nt == 0) continue;
-            // this lane's page (box) of key tile j: its first 8-token group, or
-            // one past the cache, which TMA fills with zeros
-            auto group_of = [&](int j) -> int {
-                const int key = (g.kt0 + j) * kKeys + (lane << box_bits);
-                if (j >= g.nt || lane >= boxes || key >= g.keys_end) return -1;
-                const int id = p.table[size_t(g.b) * p.width + (key >> p.page_bits)];
-                if (id < 0 || id >= p.n_pages) return p.n_pages * p.kv_heads * groups;
-                return (id * p.kv_heads + g.kvh) * groups + ((key >> 3) & (groups - 1));
+            // Page ids of the part's boxes, 32 at a time, one per lane: three
+            // such batches at hand, so that each is loaded long before its use
+            // and V's, which runs behind K's, is still there.
+            const int32_t *row = p.table + size_t(g.b) * p.width;
+            const int box0 = (g.kt0 * kKeys) >> box_bits;
+            const int all_boxes = ((g.keys_end - 1) >> box_bits) + 1;
+            auto batch = [&](int n) -> int {
+                const int at = box0 + 32 * n + lane;
+                return at < all_boxes ? row[at >> (p.page_bits - box_bits)] : -1;
             };
-            // K runs kScores tiles ahead of V, in the issuer's order: the ids
-            // of tiles j - kScores .. j + 1 are at hand
-            int ids[P::kScores + 2];
-#pragma unroll
-            for (int k = 0; k < P::kScores; ++k) ids[k] = -1;
-            ids[P::kScores] = group_of(0);
-            ids[P::kScores + 1] = group_of(1);
+            int ids0 = batch(0), ids1 = batch(1), ids2 = -1;
+            // this lane's box of key tile j: its first 8-token group (that of
+            // no page is one past the cache, which TMA fills with zeros)
+            auto group_of = [&](int j) -> int {
+                const int e = j * boxes, n = (e >> 5) % 3;
+                const int id = __shfl_sync(0xFFFFFFFFu, n == 0 ? ids0 : n == 1 ? ids1 : ids2, (e + lane) & 31);
+                const int at = id >= 0 && id < p.n_pages ? id * p.kv_heads + g.kvh : p.n_pages * p.kv_heads;
+                return (at << group_bits) + (((box0 + e + lane) << (box_bits - 3)) & ((1 << group_bits) - 1));
+            };
+            auto load = [&](const CUtensorMap *map, int j, int first, int depth, Stage &st) {
+                const int grp = group_of(j);
+                const int n = min(all_boxes - (box0 + j * boxes), boxes);
+#pragma unroll 1
+                for (int h = 0; h < P::kHalves && ok; ++h) {
+                    const int s = first + st.s;
+                    ok = wait(kv_empty(s), st.phase ^ 1);    // the first time round: passes
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(kv_full(s), n * box_bytes);
+                    __syncwarp();
+                    if (lane < n)
+                        tma_load_4d(box_at + s * P::kStageBytes, map, 0, 0, h * P::kStageBlocks, grp, kv_full(s));
+                    if (++st.s == depth) {
+                        st.s = 0;
+                        st.phase ^= 1;
+                    }
+                }
+            };
             if (nq > 0) ok = wait(q_empty, (nq - 1) & 1);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(q_full, P::kBlocks * p.tok * p.group * 128u);
@@ -524,39 +551,26 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             if (lane < P::kBlocks)
                 tma_load_4d(base + lane * kRows * 128, &qmap, 0, g.kvh * p.group, g.row0, lane, q_full);
             ++nq;
+            // K runs kScores tiles ahead of V, in the issuers' order
             for (int j = 0; j < g.nt + P::kScores && ok; ++j) {
-                const int ahead = group_of(j + 2);
-#pragma unroll 1
-                for (int kv = j < g.nt ? 0 : 1; kv < (j >= P::kScores ? 2 : 1) && ok; ++kv) {
-                    const CUtensorMap *map = kv == 0 ? &kmap : &vmap;
-                    const int grp = kv == 0 ? ids[P::kScores] : ids[0];
-                    const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, grp >= 0));
-                    const int depth = kv == 0 ? P::kStagesK : P::kStagesV, first = kv == 0 ? 0 : P::kStagesK;
-                    int it = kv == 0 ? itk : itv;
-#pragma unroll 1
-                    for (int h = 0; h < P::kHalves; ++h, ++it) {
-                        const int s = first + it % depth;
-                        if (it >= depth) ok = wait(kv_empty(s), (it / depth - 1) & 1);
-                        if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(kv_full(s), n * box_bytes);
-                        __syncwarp();
-                        if (grp >= 0)
-                            tma_load_4d(base + P::kQBytes + s * P::kStageBytes + lane * box_bytes, map, 0, 0,
-                                        h * P::kStageBlocks, grp, kv_full(s));
-                    }
-                    (kv == 0 ? itk : itv) = it;
+                const int e = j * boxes;
+                if ((e & 31) == 0 && e > 0) {                // K enters a batch: on its way, the next one
+                    const int n = (e >> 5) + 1;
+                    const int next = n % 3;
+                    if (next == 0) ids0 = batch(n);
+                    else if (next == 1) ids1 = batch(n);
+                    else ids2 = batch(n);
                 }
+                if (j < g.nt) load(&kmap, j, 0, P::kStagesK, sk);
                 if (j == 0) share_out();
-#pragma unroll
-                for (int k = 0; k < P::kScores + 1; ++k) ids[k] = ids[k + 1];
-                ids[P::kScores + 1] = ahead;
+                if (j >= P::kScores) load(&vmap, j - P::kScores, P::kStagesK, P::kStagesV, sv);
             }
         }
-        // every copy has landed before the CTA ends, also where its reader gave up
-        for (int i = max(0, itk - P::kStagesK); i < itk; ++i)
-            ok = mbar_wait_bounded(kv_full(i % P::kStagesK), (i / P::kStagesK) & 1) && ok;
-        for (int i = max(0, itv - P::kStagesV); i < itv; ++i)
-            ok = mbar_wait_bounded(kv_full(P::kStagesK + i % P::kStagesV), (i / P::kStagesV) & 1) && ok;
+        // Every copy has landed before the CTA ends, also where its reader gave
+        // up.  (A stage that was never filled passes, as the phase before the first.)
+        for (int s = 0; s < P::kStagesK; ++s) ok = mbar_wait_bounded(kv_full(s), sk.phase ^ (s < sk.s ? 0 : 1)) && ok;
+        for (int s = 0; s < P::kStagesV; ++s)
+            ok = mbar_wait_bounded(kv_full(P::kStagesK + s), sv.phase ^ (s < sv.s ? 0 : 1)) && ok;
         if (nq > 0) ok = mbar_wait_bounded(q_full, (nq - 1) & 1) && ok;
     } else if (warp == kWarpScores) {
         // S = Q K^T.  Descriptors: the high words are constants, and the low
