@@ -74,6 +74,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kPcols = kKeys / 2;
 constexpr float kShift = 8.f, kSlack = 6.f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kPartCost = 5;                    // what a row tile costs beside its keys, in key tiles
 constexpr int kInvBits = 2;                     // least tiles of a batch-invariant part (2^this)
 constexpr int kInvParts = 32;                   // most parts of a row tile
 
@@ -140,18 +141,20 @@ __device__ __forceinline__ Seq seq_of(const Args &p, int b) {
     return s;
 }
 
-// Key tiles that row tile qt reads, and its units.
+// Key tiles that row tile qt reads, and its units: one per key tile (one where
+// there are none), and in the default schedule kPartCost more, last, that
+// stand for the work beside the keys.
 struct Extent {
-    int lo, hi, units;          // tiles [lo, hi); a tile without keys is one unit
+    int lo, hi, units;          // tiles [lo, hi)
 };
 __device__ __forceinline__ Extent extent_of(const Args &p, const Seq &s, int qt) {
     const int t0 = qt * p.tok, t1 = min(s.n, t0 + p.tok) - 1;
     const int p0 = s.len - s.n + t0, p1 = s.len - s.n + t1;
-    Extent e{0, 0, 1};
+    Extent e{0, 0, p.inv_bits < 0 ? 1 + kPartCost : 1};
     if (p1 >= 0) {
         e.lo = p.window > 0 ? max(0, p0 - p.window + 1) / kKeys : 0;
         e.hi = p1 / kKeys + 1;
-        e.units = p.inv_bits < 0 ? e.hi - e.lo : ((e.hi - 1) >> p.inv_bits) - (e.lo >> p.inv_bits) + 1;
+        e.units = p.inv_bits < 0 ? e.hi - e.lo + kPartCost : ((e.hi - 1) >> p.inv_bits) - (e.lo >> p.inv_bits) + 1;
     }
     return e;
 }
@@ -268,7 +271,7 @@ struct Part {
     int pos0, keys_end;         // its position; keys that any of the rows sees end here
     int b, kvh;
     int slot;                   // where its partial result goes, -1: it is the whole
-    int u, units;               // its first unit, the row tile's units
+    int u, units;               // its first unit, the row tile's (without kPartCost)
 };
 static_assert(sizeof(Part) <= 48, "ring of parts");
 struct Cursor {
@@ -276,48 +279,55 @@ struct Cursor {
     int unit, left;             // index of the next unit, units left in the range
     Seq s;
     __device__ __forceinline__ void load(const Args &p) { s = seq_of(p, w.b); }
-    __device__ __forceinline__ bool next(const Args &p, int cta, Part &g) {
-        if (left <= 0) return false;
-        const Extent e = extent_of(p, s, w.qt);
-        const int t0 = w.qt * p.tok, toks = min(p.tok, s.n - t0);
-        g.row0 = s.first + t0;
-        g.rows = toks * p.group;
-        g.pos0 = s.len - s.n + t0;
-        g.keys_end = max(g.pos0 + toks, 0);
-        g.b = w.b;
-        g.kvh = w.kvh;
-        g.u = w.u;
-        g.units = e.units;
-        int take = 1;
-        if (p.inv_bits < 0) {
-            take = min(e.units - w.u, left);
-            g.kt0 = e.lo + w.u;
-            g.nt = e.hi > e.lo ? take : 0;
-            g.slot = 2 * cta + (w.u == 0);
-        } else {
-            const int c = ((e.lo >> p.inv_bits) + w.u) << p.inv_bits;
-            g.kt0 = max(e.lo, c);
-            g.nt = max(min(e.hi, c + (1 << p.inv_bits)) - g.kt0, 0);
-            g.slot = unit;
-        }
-        if (take == e.units) g.slot = -1;
-        w.u += take;
-        unit += take;
-        left -= take;
-        if (w.u == e.units) {
-            w.u = 0;
-            if ((w.qt + 1) * p.tok < s.n) {
-                ++w.qt;
+    // The next part, and the index of its first unit.
+    __device__ __forceinline__ bool next(const Args &p, int cta, Part &g, int &first) {
+        for (int take = 0; take == 0;) {
+            if (left <= 0) return false;
+            const Extent e = extent_of(p, s, w.qt);
+            const int t0 = w.qt * p.tok, toks = min(p.tok, s.n - t0);
+            g.row0 = s.first + t0;
+            g.rows = toks * p.group;
+            g.pos0 = s.len - s.n + t0;
+            g.keys_end = max(g.pos0 + toks, 0);
+            g.b = w.b;
+            g.kvh = w.kvh;
+            g.u = w.u;
+            g.units = e.units;
+            first = unit;
+            int step = 1;
+            if (p.inv_bits < 0) {
+                g.units -= kPartCost;
+                step = min(e.units - w.u, left);
+                take = max(min(g.units - w.u, left), 0);     // none: a range may begin past the keys
+                g.kt0 = e.lo + w.u;
+                g.nt = e.hi > e.lo ? take : 0;
+                g.slot = 2 * cta + (w.u == 0);
             } else {
-                w.qt = 0;
-                if (++w.kvh == p.kv_heads) {
-                    w.kvh = 0;
-                    if (left > 0)
+                take = 1;
+                const int c = ((e.lo >> p.inv_bits) + w.u) << p.inv_bits;
+                g.kt0 = max(e.lo, c);
+                g.nt = max(min(e.hi, c + (1 << p.inv_bits)) - g.kt0, 0);
+                g.slot = unit;
+            }
+            if (take == g.units) g.slot = -1;
+            w.u += step;
+            unit += step;
+            left -= step;
+            if (w.u == e.units) {
+                w.u = 0;
+                if ((w.qt + 1) * p.tok < s.n) {
+                    ++w.qt;
+                } else {
+                    w.qt = 0;
+                    if (++w.kvh == p.kv_heads) {
+                        w.kvh = 0;
+                        if (left > 0)
 #pragma unroll 1
-                    do {
-                        ++w.b;
-                        load(p);
-                    } while (s.n == 0 && w.b < p.B - 1);
+                        do {
+                            ++w.b;
+                            load(p);
+                        } while (s.n == 0 && w.b < p.B - 1);
+                    }
                 }
             }
         }
@@ -481,8 +491,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         int nq = 0;
         for (int i = 0; ok; ++i) {
             Part g{};
-            const int unit = cur.unit;
-            if (!cur.next(p, blockIdx.x, g)) g.nt = -1;
+            int unit = 0;
+            if (!cur.next(p, blockIdx.x, g, unit)) g.nt = -1;
             // the share of this range's first row tile, or of every unit's
             auto share_out = [&]() {
                 if (lane != 0 || (p.inv_bits < 0 ? i > 0 : g.nt < 0 && all > 0)) return;
