@@ -56,6 +56,7 @@
 // instructions and the schedule is worked out by one warp (from 138 KB of
 // code to 77 the 8192-token prompt went from 537 to 441 us).
 #include <algorithm>
+#include <climits>
 
 #include "runtime.h"
 #include "sm103_ptx.cuh"
@@ -63,7 +64,7 @@
 namespace w4v {
 namespace {
 
-constexpr int kKeys = 128;                      // keys per tile
+constexpr int kKeyBits = 7, kKeys = 1 << kKeyBits;       // keys per tile
 constexpr int kRows = 128;                      // rows per tile
 constexpr int kThreads = 384;
 constexpr int kWarpProd = 0, kWarpScores = 1, kWarpOut = 2, kWarpGuard = 3, kWarpSoft = 4;
@@ -122,9 +123,13 @@ struct Args {
     const int32_t *table, *lengths, *offsets;
     uint32_t *status;
     int n_tokens, q_heads, kv_heads, group, tok;   // query heads per key/value head, tokens per tile
+    uint64_t tok_mul;           // 2^tok_shift / tok, rounded up; 2^tok_shift is 2^31 times tok or more,
+    int tok_shift;              // so that x * tok_mul >> tok_shift is x / tok for 31-bit x
     int wide;                   // out is 32-byte aligned
-    int B, width, n_pages, page_bits, window, slot_rows;   // 2^page_bits tokens a page
-    int inv_bits;               // -1, or 2^inv_bits tiles per batch-invariant part
+    int B, width, n_pages, page_bits, slot_rows;   // 2^page_bits tokens a page
+    int back;                   // keys that a row sees before its own (INT_MAX: all)
+    int invariant;              // batch-invariant: a part is one unit
+    int unit_bits, part_cost;   // 2^unit_bits tiles per unit; units for the work beside a row tile's keys
     struct Share *shares;       // what the second kernel joins
     float scale_log2;
 };
@@ -143,20 +148,24 @@ __device__ __forceinline__ Seq seq_of(const Args &p, int b) {
 
 // Key tiles that row tile qt reads, and its units: one per key tile (one where
 // there are none), and in the default schedule kPartCost more, last, that
-// stand for the work beside the keys.
+// stand for the work beside the keys.  (Without branches on the mode: the
+// compiler makes a copy of a loop for each side of those.)
 struct Extent {
     int lo, hi, units;          // tiles [lo, hi)
 };
 __device__ __forceinline__ Extent extent_of(const Args &p, const Seq &s, int qt) {
     const int t0 = qt * p.tok, t1 = min(s.n, t0 + p.tok) - 1;
-    const int p0 = s.len - s.n + t0, p1 = s.len - s.n + t1;
-    Extent e{0, 0, p.inv_bits < 0 ? 1 + kPartCost : 1};
-    if (p1 >= 0) {
-        e.lo = p.window > 0 ? max(0, p0 - p.window + 1) / kKeys : 0;
-        e.hi = p1 / kKeys + 1;
-        e.units = p.inv_bits < 0 ? e.hi - e.lo + kPartCost : ((e.hi - 1) >> p.inv_bits) - (e.lo >> p.inv_bits) + 1;
-    }
+    const int p0 = max(s.len - s.n + t0, 0), p1 = max(s.len - s.n + t1, -1);
+    Extent e;
+    e.lo = max(p0 - p.back, 0) >> kKeyBits;
+    e.hi = (p1 >> kKeyBits) + 1;
+    e.units = max(((e.hi - 1) >> p.unit_bits) - (e.lo >> p.unit_bits) + 1, 1) + p.part_cost;
     return e;
+}
+
+// Row tiles of n new tokens: n / tok rounded up, by a multiplication.
+__device__ __forceinline__ int row_tiles(const Args &p, int n) {
+    return int(uint64_t(uint32_t(n + p.tok - 1)) * p.tok_mul >> p.tok_shift);
 }
 
 // Units of one key/value head of 32 sequences, one per lane (0 past the end).
@@ -167,20 +176,24 @@ __device__ __forceinline__ int lane_units(const Args &p, int b) {
     const int lane = threadIdx.x & 31;
     Seq s{0, 0, 0};
     if (b < p.B) s = seq_of(p, b);
-    const int tiles = (s.n + p.tok - 1) / p.tok;
-    int u = 0;
+    const int tiles = row_tiles(p, s.n);
+    uint32_t many = __ballot_sync(0xFFFFFFFFu, tiles > kFew);
+    Seq o = s;
+    int u = 0, src = lane, qt = 0, end = min(tiles, kFew), step = 1;
 #pragma unroll 1
-    for (int qt = 0; qt < min(tiles, kFew); ++qt) u += extent_of(p, s, qt).units;
-#pragma unroll 1
-    for (uint32_t many = __ballot_sync(0xFFFFFFFFu, tiles > kFew); many != 0; many &= many - 1) {
-        const int src = __ffs(many) - 1;
-        const Seq o{0, __shfl_sync(0xFFFFFFFFu, s.n, src), __shfl_sync(0xFFFFFFFFu, s.len, src)};
-        const int ot = __shfl_sync(0xFFFFFFFFu, tiles, src);
+    for (bool own = true;; own = false) {        // the loop's body is there once
         int sum = 0;
 #pragma unroll 1
-        for (int qt = kFew + lane; qt < ot; qt += 32) sum += extent_of(p, o, qt).units;
-        sum = __reduce_add_sync(0xFFFFFFFFu, sum);
+        for (; qt < end; qt += step) sum += extent_of(p, o, qt).units;
+        if (!own) sum = __reduce_add_sync(0xFFFFFFFFu, sum);
         if (lane == src) u += sum;
+        if (many == 0) break;
+        src = __ffs(many) - 1;
+        many &= many - 1;
+        o = Seq{0, __shfl_sync(0xFFFFFFFFu, s.n, src), __shfl_sync(0xFFFFFFFFu, s.len, src)};
+        qt = kFew + lane;
+        end = __shfl_sync(0xFFFFFFFFu, tiles, src);
+        step = 32;
     }
     return u;
 }
@@ -199,7 +212,8 @@ __device__ __forceinline__ int warp_scan(int x) {
 
 // An even split of `units` over at most `ctas` ranges, none of them empty.
 struct Split {
-    int ranges, each, more;     // the first `more` ranges hold one unit more than `each`
+    int ranges = 0, each = 0, more = 0;          // the first `more` ranges hold one unit more than `each`
+    __device__ __forceinline__ Split() {}
     __device__ __forceinline__ Split(int units, int ctas) {
         ranges = min(units, ctas);
         each = ranges > 0 ? units / ranges : 0;
@@ -207,59 +221,66 @@ struct Split {
     }
     __device__ __forceinline__ int begin(int c) const { return c * each + min(c, more); }
     __device__ __forceinline__ int owner(int u) const {
-        const int edge = more * (each + 1);
-        return u < edge ? u / (each + 1) : more + (u - edge) / each;
+        const int past = u - more * (each + 1);
+        return past < 0 ? u / (each + 1) : more + past / each;
     }
 };
 
 struct Place {
     int b, kvh, qt, u;          // unit u of a row tile
 };
-// All units (one warp), and the lane_units of the last 32 sequences.
-__device__ __forceinline__ int all_units(const Args &p, int &last) {
-    int sum = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        last = lane_units(p, b0 + (threadIdx.x & 31));
-        sum += last;
-    }
-    return __reduce_add_sync(0xFFFFFFFFu, sum) * p.kv_heads;
-}
-// The place of unit `at` (one warp; at < all_units, which left `last`).
-__device__ __forceinline__ Place place_of(const Args &p, int at, int last) {
+// All units, how they are split, and the place of the first one of range cta
+// (one warp).  Two passes over the sequences, 32 at a time; with 32 or fewer
+// the second one has the first one's counts.
+__device__ __forceinline__ Place schedule(const Args &p, int cta, int ctas, int &all, Split &split) {
     const int lane = threadIdx.x & 31;
     Place w{0, 0, 0, 0};
+    int u = 0, at = 0;
+    all = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int u = p.B <= 32 ? last : lane_units(p, b0 + lane);
-        const int upto = warp_scan(u * p.kv_heads);
-        const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > at);
-        if (past == 0) {
-            at -= __shfl_sync(0xFFFFFFFFu, upto, 31);
-            continue;
-        }
-        const int src = __ffs(past) - 1;
-        const int su = __shfl_sync(0xFFFFFFFFu, u, src);
-        at -= __shfl_sync(0xFFFFFFFFu, upto, src) - su * p.kv_heads;
-        w.b = b0 + src;
-        w.kvh = at / su;
-        int rest = at % su;
-        const Seq s = seq_of(p, w.b);
+    for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
-        for (int q0 = 0;; q0 += 32) {
-            const bool in = q0 + lane < (s.n + p.tok - 1) / p.tok;
-            const int mine = in ? extent_of(p, s, q0 + lane).units : 0;
-            const int sum = warp_scan(mine);
-            const uint32_t over = __ballot_sync(0xFFFFFFFFu, sum > rest);
-            if (over != 0 || q0 >= s.n) {
-                const int l = over != 0 ? __ffs(over) - 1 : 0;
-                w.qt = q0 + l;
-                w.u = rest - __shfl_sync(0xFFFFFFFFu, sum - mine, l);
-                break;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            if (pass == 0 || p.B > 32) u = lane_units(p, b0 + lane);
+            if (pass == 0) {
+                all += u;
+                continue;
             }
-            rest -= __shfl_sync(0xFFFFFFFFu, sum, 31);
+            const int upto = warp_scan(u * p.kv_heads);
+            const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > at);
+            if (past == 0) {
+                at -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+                continue;
+            }
+            const int src = __ffs(past) - 1;
+            const int su = __shfl_sync(0xFFFFFFFFu, u, src);
+            at -= __shfl_sync(0xFFFFFFFFu, upto, src) - su * p.kv_heads;
+            w.b = b0 + src;
+            w.kvh = at / su;
+            int rest = at - w.kvh * su;
+            const Seq s = seq_of(p, w.b);
+            const int tiles = row_tiles(p, s.n);
+#pragma unroll 1
+            for (int q0 = 0;; q0 += 32) {
+                const int mine = q0 + lane < tiles ? extent_of(p, s, q0 + lane).units : 0;
+                const int sum = warp_scan(mine);
+                const uint32_t over = __ballot_sync(0xFFFFFFFFu, sum > rest);
+                if (over != 0 || q0 >= tiles) {
+                    const int l = over != 0 ? __ffs(over) - 1 : 0;
+                    w.qt = q0 + l;
+                    w.u = rest - __shfl_sync(0xFFFFFFFFu, sum - mine, l);
+                    break;
+                }
+                rest -= __shfl_sync(0xFFFFFFFFu, sum, 31);
+            }
+            break;
         }
-        break;
+        if (pass == 0) {
+            all = __reduce_add_sync(0xFFFFFFFFu, all) * p.kv_heads;
+            split = Split(all, ctas);
+            if (cta >= split.ranges) break;
+            at = split.begin(cta);
+        }
     }
     return w;
 }
@@ -294,21 +315,13 @@ struct Cursor {
             g.u = w.u;
             g.units = e.units;
             first = unit;
-            int step = 1;
-            if (p.inv_bits < 0) {
-                g.units -= kPartCost;
-                step = min(e.units - w.u, left);
-                take = max(min(g.units - w.u, left), 0);     // none: a range may begin past the keys
-                g.kt0 = e.lo + w.u;
-                g.nt = e.hi > e.lo ? take : 0;
-                g.slot = 2 * cta + (w.u == 0);
-            } else {
-                take = 1;
-                const int c = ((e.lo >> p.inv_bits) + w.u) << p.inv_bits;
-                g.kt0 = max(e.lo, c);
-                g.nt = max(min(e.hi, c + (1 << p.inv_bits)) - g.kt0, 0);
-                g.slot = unit;
-            }
+            const int step = min(e.units - w.u, p.invariant ? 1 : left);
+            g.units -= p.part_cost;
+            take = max(min(g.units - w.u, step), 0);         // none: a range may begin past the keys
+            const int c = ((e.lo >> p.unit_bits) + w.u) << p.unit_bits;
+            g.kt0 = max(e.lo, c);
+            g.nt = max(min(e.hi, c + (take << p.unit_bits)) - g.kt0, 0);
+            g.slot = p.invariant ? unit : 2 * cta + (w.u == 0);
             if (take == g.units) g.slot = -1;
             w.u += step;
             unit += step;
@@ -356,21 +369,23 @@ __device__ __forceinline__ void clear_not_finite(uint4 &v) {
 // those from keys_end - window on), or its last step has spare keys.
 __device__ __forceinline__ bool guarded(const Args &p, int key, int keys_end, int pos0) {
     const int seen = min(keys_end - key, kKeys);
-    return seen % 16 != 0 || pos0 + 1 - key < seen || (p.window > 0 && keys_end - p.window > key);
+    return seen % 16 != 0 || pos0 + 1 - key < seen || (keys_end - 1 - p.back > key);
 }
 
 // A whole warp's wait for a phase, in as few instructions as it takes: they
-// are at two dozen places.  A role that gave up leaves; those that wait for
-// it give up in turn.
+// are at two dozen places (with a look at the clock in the loop the kernel was
+// 2-7% slower throughout).  A try suspends the warp for up to kSuspendHintNs,
+// so the limit is seconds.  A role that gave up leaves; those that wait for it
+// give up in turn.
+constexpr int kWaitTries = 1 << 17;
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
     bool done = mbar_test_wait(bar, parity);
-    if (!__all_sync(0xFFFFFFFFu, done)) {
-        const uint64_t t0 = global_timer_ns();
 #pragma unroll 1
-        while (!done && global_timer_ns() - t0 < kWaitLimitNs) done = mbar_try_wait(bar, parity);
-        done = __all_sync(0xFFFFFFFFu, done);
+    for (int n = 0; n < kWaitTries; ++n) {
+        if (__all_sync(0xFFFFFFFFu, done)) return true;
+        done = mbar_try_wait(bar, parity);
     }
-    return done;
+    return false;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -468,14 +483,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     // 256 x 208 of the 384 x 168 that the CTA was launched with
     if (warp < kWarpSoft) set_max_registers_down<88>();
     if (warp == kWarpProd) {
-        int last = 0;
-        const int all = all_units(p, last);
-        const Split split(all, gridDim.x);
+        int all = 0;
+        Split split;
         Cursor cur{};
+        cur.w = schedule(p, blockIdx.x, gridDim.x, all, split);
         if (int(blockIdx.x) < split.ranges) {
             cur.unit = split.begin(blockIdx.x);
             cur.left = split.begin(blockIdx.x + 1) - cur.unit;
-            cur.w = place_of(p, cur.unit, last);
             cur.load(p);
         }
         const int box_bits = min(p.page_bits, 7);            // 2^box_bits tokens per TMA box
@@ -493,11 +507,77 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             Part g{};
             int unit = 0;
             if (!cur.next(p, blockIdx.x, g, unit)) g.nt = -1;
+            if (i >= kParts) ok = wait(part_empty(i % kParts), (i / kParts - 1) & 1);
+            if (!ok) break;
+            if (lane == 0) {
+                ring[i % kParts] = g;
+                mbar_arrive(part_full(i % kParts));
+            }
+            if (g.nt > 0) {
+                // Page ids of the part's boxes, 32 at a time, one per lane: three
+                // such batches at hand, so that each is loaded long before its use
+                // and V's, which runs behind K's, is still there.
+                const int32_t *row = p.table + size_t(g.b) * p.width;
+                const int box0 = (g.kt0 * kKeys) >> box_bits;
+                const int all_boxes = ((g.keys_end - 1) >> box_bits) + 1;
+                auto batch = [&](int n) -> int {
+                    const int at = box0 + 32 * n + lane;
+                    return at < all_boxes ? row[at >> (p.page_bits - box_bits)] : -1;
+                };
+                int ids0 = batch(0), ids1 = batch(1), ids2 = -1;
+                // this lane's box of key tile j: its first 8-token group (that of
+                // no page is one past the cache, which TMA fills with zeros)
+                auto group_of = [&](int j) -> int {
+                    const int e = j * boxes, n = (e >> 5) % 3;
+                    const int id = __shfl_sync(0xFFFFFFFFu, n == 0 ? ids0 : n == 1 ? ids1 : ids2, (e + lane) & 31);
+                    const int at = id >= 0 && id < p.n_pages ? id * p.kv_heads + g.kvh : p.n_pages * p.kv_heads;
+                    return (at << group_bits) + (((box0 + e + lane) << (box_bits - 3)) & ((1 << group_bits) - 1));
+                };
+                auto load = [&](const CUtensorMap *map, int j, int first, int depth, Stage &st) {
+                    const int grp = group_of(j);
+                    const int n = min(all_boxes - (box0 + j * boxes), boxes);
+#pragma unroll 1
+                    for (int h = 0; h < P::kHalves && ok; ++h) {
+                        const int s = first + st.s;
+                        ok = wait(kv_empty(s), st.phase ^ 1);    // the first time round: passes
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(kv_full(s), n * box_bytes);
+                        __syncwarp();
+                        if (lane < n)
+                            tma_load_4d(box_at + s * P::kStageBytes, map, 0, 0, h * P::kStageBlocks, grp, kv_full(s));
+                        if (++st.s == depth) {
+                            st.s = 0;
+                            st.phase ^= 1;
+                        }
+                    }
+                };
+                if (nq > 0) ok = wait(q_empty, (nq - 1) & 1);
+                if (ok) {
+                    if (lane == 0) mbar_arrive_expect_tx(q_full, P::kBlocks * p.tok * p.group * 128u);
+                    __syncwarp();
+                    if (lane < P::kBlocks)
+                        tma_load_4d(base + lane * kRows * 128, &qmap, 0, g.kvh * p.group, g.row0, lane, q_full);
+                    ++nq;
+                }
+                // K runs kScores tiles ahead of V, in the issuers' order
+                for (int j = 0; j < g.nt + P::kScores && ok; ++j) {
+                    const int e = j * boxes;
+                    if ((e & 31) == 0 && e > 0) {                // K enters a batch: on its way, the next one
+                        const int n = (e >> 5) + 1;
+                        const int next = n % 3;
+                        if (next == 0) ids0 = batch(n);
+                        else if (next == 1) ids1 = batch(n);
+                        else ids2 = batch(n);
+                    }
+                    if (j < g.nt) load(&kmap, j, 0, P::kStagesK, sk);
+                    if (j >= P::kScores) load(&vmap, j - P::kScores, P::kStagesK, P::kStagesV, sv);
+                }
+            }
             // the share of this range's first row tile, or of every unit's
-            auto share_out = [&]() {
-                if (lane != 0 || (p.inv_bits < 0 ? i > 0 : g.nt < 0 && all > 0)) return;
-                Share e{g.row0, g.rows, g.kvh, unit - g.u, 0, g.u, g.units, p.inv_bits < 0 ? int(gridDim.x) : all};
-                if (p.inv_bits >= 0) {
+            // (here, behind the loads, for the second kernel alone reads it)
+            if (lane == 0 && (p.invariant ? g.nt >= 0 || all == 0 : i == 0)) {
+                Share e{g.row0, g.rows, g.kvh, unit - g.u, 0, g.u, g.units, p.invariant ? all : int(gridDim.x)};
+                if (p.invariant) {
                     if (g.units > 1) e.n = g.units;
                 } else if (g.nt >= 0 && g.u > 0) {
                     const int first = split.owner(unit - g.u), n = split.owner(unit - g.u + g.units - 1) - first + 1;
@@ -506,75 +586,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     e.share = int(blockIdx.x) - first - 1;
                     e.shares = n - 1;
                 }
-                p.shares[p.inv_bits < 0 ? int(blockIdx.x) : unit] = e;
-            };
-            if (g.nt <= 0) share_out();                      // else after the first loads
-            if (i >= kParts) ok = wait(part_empty(i % kParts), (i / kParts - 1) & 1);
-            if (!ok) break;
-            if (lane == 0) {
-                ring[i % kParts] = g;
-                mbar_arrive(part_full(i % kParts));
+                p.shares[p.invariant ? unit : int(blockIdx.x)] = e;
             }
             if (g.nt < 0) break;
-            if (g.nt == 0) continue;
-            // Page ids of the part's boxes, 32 at a time, one per lane: three
-            // such batches at hand, so that each is loaded long before its use
-            // and V's, which runs behind K's, is still there.
-            const int32_t *row = p.table + size_t(g.b) * p.width;
-            const int box0 = (g.kt0 * kKeys) >> box_bits;
-            const int all_boxes = ((g.keys_end - 1) >> box_bits) + 1;
-            auto batch = [&](int n) -> int {
-                const int at = box0 + 32 * n + lane;
-                return at < all_boxes ? row[at >> (p.page_bits - box_bits)] : -1;
-            };
-            int ids0 = batch(0), ids1 = batch(1), ids2 = -1;
-            // this lane's box of key tile j: its first 8-token group (that of
-            // no page is one past the cache, which TMA fills with zeros)
-            auto group_of = [&](int j) -> int {
-                const int e = j * boxes, n = (e >> 5) % 3;
-                const int id = __shfl_sync(0xFFFFFFFFu, n == 0 ? ids0 : n == 1 ? ids1 : ids2, (e + lane) & 31);
-                const int at = id >= 0 && id < p.n_pages ? id * p.kv_heads + g.kvh : p.n_pages * p.kv_heads;
-                return (at << group_bits) + (((box0 + e + lane) << (box_bits - 3)) & ((1 << group_bits) - 1));
-            };
-            auto load = [&](const CUtensorMap *map, int j, int first, int depth, Stage &st) {
-                const int grp = group_of(j);
-                const int n = min(all_boxes - (box0 + j * boxes), boxes);
-#pragma unroll 1
-                for (int h = 0; h < P::kHalves && ok; ++h) {
-                    const int s = first + st.s;
-                    ok = wait(kv_empty(s), st.phase ^ 1);    // the first time round: passes
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(kv_full(s), n * box_bytes);
-                    __syncwarp();
-                    if (lane < n)
-                        tma_load_4d(box_at + s * P::kStageBytes, map, 0, 0, h * P::kStageBlocks, grp, kv_full(s));
-                    if (++st.s == depth) {
-                        st.s = 0;
-                        st.phase ^= 1;
-                    }
-                }
-            };
-            if (nq > 0) ok = wait(q_empty, (nq - 1) & 1);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(q_full, P::kBlocks * p.tok * p.group * 128u);
-            __syncwarp();
-            if (lane < P::kBlocks)
-                tma_load_4d(base + lane * kRows * 128, &qmap, 0, g.kvh * p.group, g.row0, lane, q_full);
-            ++nq;
-            // K runs kScores tiles ahead of V, in the issuers' order
-            for (int j = 0; j < g.nt + P::kScores && ok; ++j) {
-                const int e = j * boxes;
-                if ((e & 31) == 0 && e > 0) {                // K enters a batch: on its way, the next one
-                    const int n = (e >> 5) + 1;
-                    const int next = n % 3;
-                    if (next == 0) ids0 = batch(n);
-                    else if (next == 1) ids1 = batch(n);
-                    else ids2 = batch(n);
-                }
-                if (j < g.nt) load(&kmap, j, 0, P::kStagesK, sk);
-                if (j == 0) share_out();
-                if (j >= P::kScores) load(&vmap, j - P::kScores, P::kStagesK, P::kStagesV, sv);
-            }
         }
         // Every copy has landed before the CTA ends, also where its reader gave
         // up.  (A stage that was never filled passes, as the phase before the first.)
@@ -701,7 +715,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 ok = wait(v_ask, (looked++) & 1);
                 const int seen = min(g.keys_end - key, kKeys), cleared = (seen + 15) / 16 * 16;
                 const int above = min(max(g.pos0 + 1 - key, 0), seen);
-                const int below = p.window > 0 ? min(g.keys_end - p.window - key, above) : 0;
+                const int below = min(max(g.keys_end - 1 - p.back, 0) - key, above);
 #pragma unroll 1
                 for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
                     const int s = P::kStagesK + it % P::kStagesV;
@@ -745,6 +759,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     } else {
         set_max_registers_up<208>();
         const int half = (warp - kWarpSoft) >> 2, quad = warp & 3, row = 32 * quad + lane;
+        const int row_tok = row / p.group, row_head = row - row_tok * p.group;
         const uint32_t lanes = uint32_t(32 * quad) << 16;
         const float c = p.scale_log2;
         int t = 0, np = 0;                                   // tiles and parts (with keys) so far
@@ -754,8 +769,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             np += nt > 0;
             const bool mine = row < rows;
             const bool busy = 32 * quad < rows;              // some row of this warp is in use
-            const int pos = part_of(i).pos0 + row / p.group;
-            const int from = p.window > 0 ? pos - p.window + 1 : 0;
+            const int pos = part_of(i).pos0 + row_tok;
+            const int from = max(max(pos, 0) - p.back, 0);
             // every key of [sure_lo, sure_hi] is seen by all of the warp's rows
             const int sure_hi = __reduce_min_sync(0xFFFFFFFFu, mine ? pos : 0x7FFFFFFF);
             const int sure_lo = __reduce_max_sync(0xFFFFFFFFu, mine ? from : 0);
@@ -925,7 +940,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             const bool whole = g.slot < 0;
             const float inv = nt > 0 && l != 0.f ? 1.f / l : 0.f;
             const float m2 = m * c - kShift;
-            const size_t orow = size_t(g.row0 + row / p.group) * p.q_heads + g.kvh * p.group + row % p.group;
+            const size_t orow = size_t(g.row0 + row_tok) * p.q_heads + g.kvh * p.group + row_head;
             const size_t srow = size_t(whole ? 0 : g.slot) * p.slot_rows + row;
             if (mine) {
                 if (!whole) p.part_ml[srow] = make_float2(m2, l);
@@ -983,7 +998,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             if (fix && mine) {
                 // the values that were cleared, for a row that sees them: the
                 // weight is above 0, so they make the sum what they are
-                const int below = p.window > 0 ? g.keys_end - p.window : 0;
+                const int below = max(g.keys_end - 1 - p.back, 0);
                 const int last = min((kt0 + nt) * kKeys - 1, pos);
 #pragma unroll 1
                 for (int k = max(kt0 * kKeys, from); k <= last; ++k) {
@@ -1031,29 +1046,34 @@ paged_attn_join_kernel(const Args p) {
     __shared__ float scale[kRows];
     grid_dep_wait();
     grid_dep_launch();
-    const int count = p.inv_bits < 0 ? gridDim.x : p.shares[0].count;
+    const bool gave_up = (__ldcg(p.status) & (1u << kStatusTimeout)) != 0u;      // shares may be missing
+    const int count = p.invariant ? p.shares[0].count : int(gridDim.x);
     for (int e = blockIdx.x; e < count; e += gridDim.x) {
         const Share g = p.shares[e];
         const int n = g.n;
-        if (n == 0) continue;
+        if (n == 0 || gave_up) continue;
         const int s0 = g.share * g.rows / g.shares, s1 = (g.share + 1) * g.rows / g.shares;
         const int r0 = s0 + int(blockIdx.y) * (s1 - s0) / kJoinSplit;
         const int rows = s0 + int(blockIdx.y + 1) * (s1 - s0) / kJoinSplit - r0;
         auto at = [&](int i, int r) {            // part i's row
-            const int slot = p.inv_bits >= 0 ? g.slot0 + i : i == 0 ? g.slot0 : g.slot0 - 1 + 2 * i;
+            const int slot = p.invariant ? g.slot0 + i : i == 0 ? g.slot0 : g.slot0 - 1 + 2 * i;
             return size_t(slot) * p.slot_rows + r0 + r;
         };
         auto row_out = [&](int r) {
             return size_t(g.row0 + (r0 + r) / p.group) * p.q_heads + g.kvh * p.group + (r0 + r) % p.group;
         };
         __syncthreads();                         // the entry before is done with
+#pragma unroll 2
         for (int k = threadIdx.x; k < rows * n; k += kJoinThreads) ml[k] = __ldcg(&p.part_ml[at(k % n, k / n)]);
         __syncthreads();
         // a row per thread, its parts in order: parts that add nothing change nothing
+#pragma unroll 1
         for (int r = threadIdx.x; r < rows; r += kJoinThreads) {
             float2 *x = ml + r * n;
             float top = -INFINITY, l = 0.f;
+#pragma unroll 4
             for (int i = 0; i < n; ++i) top = fmaxf(top, x[i].x);
+#pragma unroll 2
             for (int i = 0; i < n; ++i) {
                 const float w = top == -INFINITY ? 0.f : ex2(x[i].x - top);
                 if (x[i].y != 0.f) l += w * x[i].y;
@@ -1065,6 +1085,7 @@ paged_attn_join_kernel(const Args p) {
         __syncthreads();
         constexpr int kLanes = D / 4;            // threads per row, four columns each
         const int col = 4 * (int(threadIdx.x) % kLanes);
+#pragma unroll 1
         for (int r = int(threadIdx.x) / kLanes; r < rows; r += kJoinThreads / kLanes) {
             const float2 *x = ml + r * n;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1179,14 +1200,19 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     a.kv_heads = kv.kv_heads;
     a.group = group;
     a.tok = tokens_per_tile(q_heads, kv.kv_heads);
+    a.tok_shift = 31;
+    while (1 << (a.tok_shift - 31) < a.tok) ++a.tok_shift;
+    a.tok_mul = ((uint64_t(1) << a.tok_shift) + a.tok - 1) / a.tok;
     a.B = kv.B;
     a.width = kv.table_width;
     a.n_pages = kv.n_pages;
     a.page_bits = 0;
     while (1 << a.page_bits < kv.page) ++a.page_bits;
-    a.window = window;
+    a.back = window > 0 ? window - 1 : INT_MAX;
     a.slot_rows = slots.rows;
-    a.inv_bits = invariant ? inv_tile_bits(kv.table_width * kv.page) : -1;
+    a.invariant = invariant;
+    a.unit_bits = invariant ? inv_tile_bits(kv.table_width * kv.page) : 0;
+    a.part_cost = invariant ? 0 : kPartCost;
     a.scale_log2 = scale * 1.4426950408889634f;
     // K and V as (64 elements, 8 tokens, blocks of a head, 8-token groups):
     // a box is a page's groups of one stage's blocks
