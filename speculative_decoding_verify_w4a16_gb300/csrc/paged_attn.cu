@@ -93,7 +93,7 @@ struct Plan {
     static constexpr int kScores = D >= 256 ? 1 : 2;             // S buffers, and tiles that Q K^T runs ahead
     static constexpr bool kOwn = D <= 64;                        // an O for each softmax group
     static constexpr uint32_t kPcol = kScores * kKeys, kOcol = kPcol + 2 * kPcols;
-    static constexpr int kNumBars = 2 + 2 * kStages + 10 + 4 + 8 + 8 + 2 * kParts;
+    static constexpr int kNumBars = 2 + 2 * kStages + 12 + 4 + 8 + 8 + 2 * kParts;
     static constexpr int kMisc = kBar + 8 * kNumBars;
     static constexpr int kRing = (kMisc + 16 + 15) & ~15;
     static constexpr int kRef = kRing + kParts * 48;             // float[kRows]: the rows' references
@@ -408,11 +408,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     auto pv_done = [&](int tile) { return rest + 32u + 8u * (tile & 3); };
     auto pv_phase = [&](int tile) { return uint32_t(tile >> 2) & 1u; };
     auto s_empty = [&](int i) { return rest + 64u + 8u * i; };
-    const uint32_t v_ask = rest + 80u, v_ready = rest + 88u, o_empty = rest + 96u, done_bar = rest + 104u;
-    auto turn = [&](int quad, int i) { return rest + 112u + 16u * quad + 8u * i; };
-    auto pair = [&](int quad, int i) { return rest + 176u + 16u * quad + 8u * i; };
-    auto part_full = [&](int i) { return rest + 240u + 8u * i; };
-    auto part_empty = [&](int i) { return rest + 240u + 8u * (kParts + i); };
+    auto v_ask = [&](int n) { return rest + 80u + 8u * (n & 1); };          // by guarded tile
+    auto v_ready = [&](int n) { return rest + 96u + 8u * (n & 1); };
+    const uint32_t o_empty = rest + 112u, done_bar = rest + 120u;
+    auto turn = [&](int quad, int i) { return rest + 128u + 16u * quad + 8u * i; };
+    auto pair = [&](int quad, int i) { return rest + 192u + 16u * quad + 8u * i; };
+    auto part_full = [&](int i) { return rest + 256u + 8u * i; };
+    auto part_empty = [&](int i) { return rest + 256u + 8u * (kParts + i); };
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + P::kMisc);    // [0] tmem, [2..3] below
     volatile uint32_t *spoilt = misc + 2;                    // [i & 1]: part i (from 1) had values cleared
     Part *ring = reinterpret_cast<Part *>(smem + P::kRing);
@@ -433,8 +435,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             mbar_init(s_empty(i), 4);
         }
         for (int i = 0; i < 4; ++i) mbar_init(pv_done(i), 2);    // the MMAs, and the issuer's own arrival
-        mbar_init(v_ask, 1);
-        mbar_init(v_ready, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(v_ask(i), 1);
+            mbar_init(v_ready(i), 1);
+        }
         mbar_init(o_empty, 4);                   // the group that ends a part
         mbar_init(done_bar, 2);                  // both issuers
         for (int q = 0; q < 4; ++q) {
@@ -650,20 +654,34 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         constexpr uint32_t idesc = idesc_f16_f32(kRows, 64 * P::kStageBlocks) | kIdescBMnMajor;
         constexpr uint64_t kHighV = uint64_t(sdesc_high(P::kGroupBytes)) << 32;
         const uint32_t v_low = sdesc_low(base + P::kQBytes + P::kStagesK * P::kStageBytes, 1024);
-        int it = 0, nq = 0, t = 0, looked = 0;               // stages, parts, tiles, guarded tiles so far
+        int it = 0, nq = 0, t = 0;                           // stages, parts, tiles so far
+        int asked = 0, looked = 0;                           // guarded tiles that the guard was asked for, and has done
+        auto ask = [&](bool look) {
+            if (look && elect_one()) mbar_arrive(v_ask(asked));
+            asked += look;
+            __syncwarp();
+        };
         for (int i = 0; __any_sync(0xFFFFFFFFu, acquire(i)); ++i) {
             const int nt = warp_uniform(part_of(i).nt), pos0 = warp_uniform(part_of(i).pos0);
             const int key0 = warp_uniform(part_of(i).kt0 * kKeys), keys_end = warp_uniform(part_of(i).keys_end);
             release(i);
             if (nt == 0) continue;
+            bool look = guarded(p, key0, keys_end, pos0);
+            ask(look);
             for (int j = 0; j < nt && ok; ++j, ++t) {
                 const int key = key0 + j * kKeys;
-                const bool look = guarded(p, key, keys_end, pos0);
-                if (look && elect_one()) mbar_arrive(v_ask);
-                __syncwarp();
+                // The guard works one tile ahead where that tile's stages were
+                // last filled before this one's: waiting for their next fill
+                // it then cannot take the one before for it.
+                const bool next = j + 1 < nt && guarded(p, key + kKeys, keys_end, pos0);
+                if (P::kStagesV >= 2 * P::kHalves) ask(next);
                 if (j == 0 && nq++ > 0) ok = wait(o_empty, nq & 1);          // the part before is read
                 ok = ok && wait(p_full(t & 1), (t >> 1) & 1);
-                if (ok && look) ok = wait(v_ready, (looked++) & 1);
+                if (ok && look) {
+                    ok = wait(v_ready(looked), (looked >> 1) & 1);
+                    ++looked;
+                }
+                look = next;
                 const int steps = min((keys_end - key + 15) / 16, kKeys / 16);
 #pragma unroll 1
                 for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
@@ -687,6 +705,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     }
                     __syncwarp();
                 }
+                if (P::kStagesV < 2 * P::kHalves) ask(ok && next);
             }
         }
         if (elect_one()) mma_commit(done_bar);
@@ -711,8 +730,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     it += P::kHalves;
                     continue;
                 }
-                // the issuer is at this tile: its stages are this fill or the one before
-                ok = wait(v_ask, (looked++) & 1);
+                // the issuer has seen the stages' fill before this one
+                ok = wait(v_ask(looked), (looked >> 1) & 1);
                 const int seen = min(g.keys_end - key, kKeys), cleared = (seen + 15) / 16 * 16;
                 const int above = min(max(g.pos0 + 1 - key, 0), seen);
                 const int below = min(max(g.keys_end - 1 - p.back, 0) - key, above);
@@ -722,30 +741,41 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     ok = wait(kv_full(s), (it / P::kStagesV) & 1);
                     if (!ok) break;
                     uint8_t *st = smem + P::kQBytes + s * P::kStageBytes;
+                    // A first look at the 8-token groups that hold such keys, in
+                    // the order of the addresses: 0 x v is 0 or, if v is not
+                    // finite, NaN, and a NaN stays in the sum.
+                    constexpr int kLoads = 8;                                // 512 bytes each
+                    static_assert(kLoads * 512 % P::kGroupBytes == 0 && P::kStageBytes % (kLoads * 512) == 0, "whole groups");
+                    __half2 sum[2] = {__float2half2_rn(0.f), __float2half2_rn(0.f)};
+                    const int end = (seen + 7) / 8 * P::kGroupBytes;
+#pragma unroll 1
+                    for (int a = below > 0 ? 0 : above / 8 * P::kGroupBytes & ~(kLoads * 512 - 1); a < end; a += kLoads * 512) {
+                        uint4 v[kLoads];
+#pragma unroll
+                        for (int k = 0; k < kLoads; ++k) v[k] = *reinterpret_cast<const uint4 *>(st + a + 512 * k + 16 * lane);
+#pragma unroll
+                        for (int k = 0; k < kLoads; ++k) {
+                            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                sum[e & 1] = __hfma2(*reinterpret_cast<const __half2 *>(&w[e]), __float2half2_rn(0.f), sum[e & 1]);
+                        }
+                    }
+                    const bool some = __any_sync(0xFFFFFFFFu, ((h2_as_u32(sum[0]) | h2_as_u32(sum[1])) & 0x7FFF7FFFu) != 0u);
                     // a lane's 16-byte column, of every kStep'th token
-                    constexpr int kStep = 32 / kPieces, kAhead = 4;          // loads in flight
+                    constexpr int kStep = 32 / kPieces;
                     uint8_t *col = st + (lane % kPieces / 8) * 1024 + (lane % 8) * 16;
                     const int first = lane / kPieces;
                     auto piece = [&](int tok) {
                         return reinterpret_cast<uint4 *>(col + (tok / 8) * P::kGroupBytes + (tok % 8) * 128);
                     };
 #pragma unroll 1
-                    for (int side = 0; side < 2; ++side) {
-                        const int end = side == 0 ? seen : below;
-#pragma unroll 1
-                        for (int k0 = (side == 0 ? above : 0) + first; k0 < end; k0 += kStep * kAhead) {
-                            uint32_t bad = 0;
-#pragma unroll
-                            for (int k = 0; k < kAhead; ++k) bad |= not_finite(*piece(min(k0 + kStep * k, end - 1)));
-                            if (bad == 0) continue;
-                            found = true;
-#pragma unroll 1
-                            for (int k = k0; k < min(k0 + kStep * kAhead, end); k += kStep) {
-                                uint4 v = *piece(k);
-                                clear_not_finite(v);
-                                *piece(k) = v;
-                            }
-                        }
+                    for (int k = first; some && k < seen; k += kStep) {
+                        uint4 v = *piece(k);
+                        if ((k >= below && k < above) || not_finite(v) == 0u) continue;
+                        found = true;
+                        clear_not_finite(v);
+                        *piece(k) = v;
                     }
 #pragma unroll 1
                     for (int k = seen + first; k < cleared; k += kStep) *piece(k) = make_uint4(0, 0, 0, 0);
@@ -753,7 +783,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 }
                 if (found) spoilt[np & 1] = np;
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive(v_ready);
+                if (ok && lane == 0) mbar_arrive(v_ready(looked));
+                ++looked;
             }
         }
     } else {
