@@ -75,7 +75,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kPcols = kKeys / 2;
 constexpr float kShift = 8.f, kSlack = 6.f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kPartCost = 5;                    // what a row tile costs beside its keys, in key tiles
+constexpr int kPartCost = 3;                    // what a row tile costs beside its keys, in key tiles
 constexpr int kInvBits = 2;                     // least tiles of a batch-invariant part (2^this)
 constexpr int kInvParts = 32;                   // most parts of a row tile
 
@@ -596,10 +596,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         }
         // Every copy has landed before the CTA ends, also where its reader gave
         // up.  (A stage that was never filled passes, as the phase before the first.)
-        for (int s = 0; s < P::kStagesK; ++s) ok = mbar_wait_bounded(kv_full(s), sk.phase ^ (s < sk.s ? 0 : 1)) && ok;
-        for (int s = 0; s < P::kStagesV; ++s)
-            ok = mbar_wait_bounded(kv_full(P::kStagesK + s), sv.phase ^ (s < sv.s ? 0 : 1)) && ok;
-        if (nq > 0) ok = mbar_wait_bounded(q_full, (nq - 1) & 1) && ok;
+#pragma unroll 1
+        for (int s = 0; s < P::kStages; ++s) {
+            const Stage st = s < P::kStagesK ? sk : Stage{P::kStagesK + sv.s, sv.phase};
+            ok = wait(kv_full(s), st.phase ^ (s < st.s ? 0 : 1)) && ok;
+        }
+        if (nq > 0) ok = wait(q_full, (nq - 1) & 1) && ok;
     } else if (warp == kWarpScores) {
         // S = Q K^T.  Descriptors: the high words are constants, and the low
         // ones (address / 16) grow by constants from one per operand.  (Put
