@@ -103,16 +103,20 @@ struct Plan {
     static_assert(kBytes <= 227 * 1024, "shared memory plan");
 };
 
-// Rows of a row tile that one CTA of the second kernel joins: the share-th of
-// `shares` equal shares, from n parts (n = 0: nothing).  Default: entry c is
-// for the tile that range c begins inside of, from slot 2 first + 1 and then
-// slots 2 (first + i); batch-invariant: entry u for unit u, from slots in a row.
-struct Share {
-    int row0, rows, kvh;
+// Rows [r0, r1) of a row tile that an entry's CTAs of the second kernel join
+// from n parts (n = 0: nothing).  Default: entry c is for the tile that range c
+// begins inside of, its parts in slot 2 first + 1 and then 2 (first + i);
+// batch-invariant: entry u for unit u, slots in a row.  What needs a division
+// is worked out here, where there is time.
+struct __align__(16) Share {
+    int row0, kvh;              // the tile's first token
+    int rows;                   // r0, and in the upper half r1
     int slot0, n;
-    int share, shares;
+    int n_mul;                  // 2^20 / n, rounded up: k * n_mul >> 20 is k / n for k < 1024
+    int block;                  // rows that are fetched at a time
     int count;                  // batch-invariant, entry 0: how many entries there are (default: one per range)
 };
+constexpr int kJoinBytes = 24 * 1024;           // of parts at a time
 
 struct Args {
     __half *out;
@@ -124,6 +128,7 @@ struct Args {
     uint32_t *status;
     int n_tokens, q_heads, kv_heads, group, tok;   // query heads per key/value head, tokens per tile
     uint64_t tok_mul;           // 2^tok_shift / tok, rounded up; 2^tok_shift is 2^31 times tok or more,
+    int group_mul;              // 2^16 / group, rounded up: row * group_mul >> 16 is row / group for rows of a tile
     int tok_shift;              // so that x * tok_mul >> tok_shift is x / tok for 31-bit x
     int wide;                   // out is 32-byte aligned
     int B, width, n_pages, page_bits, slot_rows;   // 2^page_bits tokens a page
@@ -580,15 +585,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             // the share of this range's first row tile, or of every unit's
             // (here, behind the loads, for the second kernel alone reads it)
             if (lane == 0 && (p.invariant ? g.nt >= 0 || all == 0 : i == 0)) {
-                Share e{g.row0, g.rows, g.kvh, unit - g.u, 0, g.u, g.units, p.invariant ? all : int(gridDim.x)};
+                Share e{g.row0, g.kvh, 0, unit - g.u, 0, 0, 1, p.invariant ? all : int(gridDim.x)};
+                int share = g.u, shares = g.units;
                 if (p.invariant) {
-                    if (g.units > 1) e.n = g.units;
+                    e.n = g.units > 1 ? g.units : 0;
                 } else if (g.nt >= 0 && g.u > 0) {
-                    const int first = split.owner(unit - g.u), n = split.owner(unit - g.u + g.units - 1) - first + 1;
+                    const int first = split.owner(unit - g.u);
+                    e.n = split.owner(unit - g.u + g.units - 1) - first + 1;
                     e.slot0 = 2 * first + 1;
-                    e.n = n;
-                    e.share = int(blockIdx.x) - first - 1;
-                    e.shares = n - 1;
+                    share = int(blockIdx.x) - first - 1;
+                    shares = e.n - 1;
+                }
+                if (e.n > 0) {
+                    e.rows = share * g.rows / shares | (share + 1) * g.rows / shares << 16;
+                    e.n_mul = (1 << 20) / e.n + 1;
+                    e.block = max(kJoinBytes / (4 * D) / e.n, 1);
                 }
                 p.shares[p.invariant ? unit : int(blockIdx.x)] = e;
             }
@@ -1070,22 +1081,30 @@ constexpr int kJoinSplit = 4;
 constexpr int kJoinWeights = 3 * kRows + 2 * kMaxCtas;
 
 // o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over a row's parts, M the
-// largest m_i.  Latency bounds it: the statistics of all rows and parts come
-// in one pass of loads, and o's parts several loads ahead.
+// largest m_i.  Latency bounds it: a warp fetches its rows' statistics and all
+// fetch o's parts, both to shared memory, before anything is waited for, and
+// the weights are worked out while the latter come in.  Sums run over the
+// parts in order, so that parts that add nothing change nothing.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_attn_join_kernel(const Args p) {
-    __shared__ float2 ml[kJoinWeights];          // m, l; then the part's weight in x
+    __shared__ float2 ml[kJoinWeights];          // m, l; then the part's weight, its share of the sum
     __shared__ float scale[kRows];
+    __shared__ __align__(16) float4 parts[kJoinBytes / 16];
+    constexpr int kLanes = D / 4, kLines = kJoinThreads / kLanes;    // threads per row, four columns each
+    constexpr int kHeld = kJoinBytes / (4 * D);  // rows of parts that fit
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = int(threadIdx.x) % kLanes, line = int(threadIdx.x) / kLanes;
     grid_dep_wait();
     grid_dep_launch();
     const bool gave_up = (__ldcg(p.status) & (1u << kStatusTimeout)) != 0u;      // shares may be missing
     const int count = p.invariant ? p.shares[0].count : int(gridDim.x);
+#pragma unroll 1
     for (int e = blockIdx.x; e < count; e += gridDim.x) {
         const Share g = p.shares[e];
         const int n = g.n;
         if (n == 0 || gave_up) continue;
-        const int s0 = g.share * g.rows / g.shares, s1 = (g.share + 1) * g.rows / g.shares;
+        const int s0 = g.rows & 0xFFFF, s1 = g.rows >> 16;
         const int r0 = s0 + int(blockIdx.y) * (s1 - s0) / kJoinSplit;
         const int rows = s0 + int(blockIdx.y + 1) * (s1 - s0) / kJoinSplit - r0;
         auto at = [&](int i, int r) {            // part i's row
@@ -1093,56 +1112,83 @@ paged_attn_join_kernel(const Args p) {
             return size_t(slot) * p.slot_rows + r0 + r;
         };
         auto row_out = [&](int r) {
-            return size_t(g.row0 + (r0 + r) / p.group) * p.q_heads + g.kvh * p.group + (r0 + r) % p.group;
+            const int tok = (r0 + r) * p.group_mul >> 16;
+            return size_t(g.row0 + tok) * p.q_heads + g.kvh * p.group + (r0 + r - tok * p.group);
         };
+        const int held = min(n, kHeld);          // parts at a time (all of them, or those of one row)
         __syncthreads();                         // the entry before is done with
-#pragma unroll 2
-        for (int k = threadIdx.x; k < rows * n; k += kJoinThreads) ml[k] = __ldcg(&p.part_ml[at(k % n, k / n)]);
-        __syncthreads();
-        // a row per thread, its parts in order: parts that add nothing change nothing
+        // rows to warps: of a few parts a row is a lane's, else a warp's
+        const int wide = n <= 4 ? 0 : 31;        // lanes per row - 1
+        const int first = wide != 0 ? warp : int(threadIdx.x), step = wide != 0 ? kJoinThreads / 32 : kJoinThreads;
 #pragma unroll 1
-        for (int r = threadIdx.x; r < rows; r += kJoinThreads) {
-            float2 *x = ml + r * n;
-            float top = -INFINITY, l = 0.f;
+        for (int r = first; r < rows; r += step)
+#pragma unroll 1
+            for (int i = lane & wide; i < n; i += wide + 1) cp_async<8>(smem_u32(&ml[r * n + i]), &p.part_ml[at(i, r)], 8);
+        cp_async_commit();
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int b = 0; b < rows; b += g.block) {
+            const int here = min(g.block, rows - b);
+#pragma unroll 1
+            for (int i0 = 0; i0 < n; i0 += held) {
+                const int m = min(held, n - i0);
+                if (b + i0 > 0) __syncthreads(); // what was there before is done with
+#pragma unroll 2
+                for (int k = line; k < here * m; k += kLines) {
+                    const int r = m == n ? k * g.n_mul >> 20 : 0, i = k - r * m;
+                    cp_async_16(smem_u32(&parts[k * kLanes + col]), p.part_o + at(i0 + i, b + r) * D + 4 * col);
+                }
+                cp_async_commit();
+                if (b + i0 == 0) {
+                    cp_async_wait<1>();
+                    __syncwarp();
+#pragma unroll 1
+                    for (int r = first; r < rows; r += step) {
+                        float2 *x = ml + r * n;
+                        float top = -INFINITY, l = 0.f;
+#pragma unroll 1
+                        for (int i = lane & wide; i < n; i += wide + 1) top = fmaxf(top, x[i].x);
+                        if (wide != 0)
+#pragma unroll
+                            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+#pragma unroll 1
+                        for (int i = lane & wide; i < n; i += wide + 1) {
+                            const float2 y = x[i];
+                            const float w = top == -INFINITY ? 0.f : ex2(y.x - top);
+                            x[i] = make_float2(w, y.y != 0.f ? w * y.y : 0.f);
+                        }
+                        if (wide != 0) __syncwarp();
 #pragma unroll 4
-            for (int i = 0; i < n; ++i) top = fmaxf(top, x[i].x);
-#pragma unroll 2
-            for (int i = 0; i < n; ++i) {
-                const float w = top == -INFINITY ? 0.f : ex2(x[i].x - top);
-                if (x[i].y != 0.f) l += w * x[i].y;
-                x[i].x = w;
-            }
-            scale[r] = l != 0.f ? 1.f / l : 0.f;
-            if (p.lse != nullptr) p.lse[row_out(r)] = l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
-        }
-        __syncthreads();
-        constexpr int kLanes = D / 4;            // threads per row, four columns each
-        const int col = 4 * (int(threadIdx.x) % kLanes);
-#pragma unroll 1
-        for (int r = int(threadIdx.x) / kLanes; r < rows; r += kJoinThreads / kLanes) {
-            const float2 *x = ml + r * n;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int kAhead = 8;
-#pragma unroll 1
-            for (int i0 = 0; i0 < n; i0 += kAhead) {
-                float4 v[kAhead];
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    if (i0 + k < n) v[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at(i0 + k, r) * D + col));
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    if (i0 + k < n && x[i0 + k].x != 0.f) {
-                        const float w = x[i0 + k].x;
-                        o = make_float4(fmaf(w, v[k].x, o.x), fmaf(w, v[k].y, o.y), fmaf(w, v[k].z, o.z), fmaf(w, v[k].w, o.w));
+                        for (int i = 0; i < n; ++i) l += x[i].y;
+                        if ((lane & wide) == 0) {
+                            scale[r] = l != 0.f ? 1.f / l : 0.f;
+                            if (p.lse != nullptr) p.lse[row_out(r)] = l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
+                        }
                     }
+                }
+                cp_async_wait<0>();
+                __syncthreads();
+#pragma unroll 1
+                for (int r = line; r < here; r += kLines) {
+                    if (i0 == 0) o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float2 *x = ml + (b + r) * n + i0;
+                    const float4 *v = parts + r * m * kLanes + col;
+#pragma unroll 4
+                    for (int i = 0; i < m; ++i) {
+                        const float w = x[i].x;
+                        const float4 y = v[i * kLanes];
+                        if (w != 0.f) o = make_float4(fmaf(w, y.x, o.x), fmaf(w, y.y, o.y), fmaf(w, y.z, o.z), fmaf(w, y.w, o.w));
+                    }
+                    if (i0 + m < n) continue;
+                    const float inv = scale[b + r];
+                    uint2 h = make_uint2(0u, 0u);
+                    if (inv != 0.f) {
+                        h.x = h2_as_u32(__floats2half2_rn(o.x * inv, o.y * inv));
+                        h.y = h2_as_u32(__floats2half2_rn(o.z * inv, o.w * inv));
+                    }
+                    *reinterpret_cast<uint2 *>(p.out + row_out(b + r) * D + 4 * col) = h;
+                }
             }
-            const float inv = scale[r];
-            uint2 h = make_uint2(0u, 0u);
-            if (inv != 0.f) {
-                h.x = h2_as_u32(__floats2half2_rn(o.x * inv, o.y * inv));
-                h.y = h2_as_u32(__floats2half2_rn(o.z * inv, o.w * inv));
-            }
-            *reinterpret_cast<uint2 *>(p.out + row_out(r) * D + col) = h;
         }
     }
 }
@@ -1222,7 +1268,7 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     a.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0u;
     a.part_o = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + 31u) & ~uintptr_t(31));
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + slots.count * slots.rows * D);
-    a.shares = reinterpret_cast<Share *>(a.part_ml + slots.count * slots.rows);
+    a.shares = reinterpret_cast<Share *>((reinterpret_cast<uintptr_t>(a.part_ml + slots.count * slots.rows) + 15u) & ~uintptr_t(15));
     a.v = reinterpret_cast<const __half *>(kv.v);
     a.table = kv.table;
     a.lengths = kv.lengths;
@@ -1233,6 +1279,7 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     a.kv_heads = kv.kv_heads;
     a.group = group;
     a.tok = tokens_per_tile(q_heads, kv.kv_heads);
+    a.group_mul = 65536 / group + 1;
     a.tok_shift = 31;
     while (1 << (a.tok_shift - 31) < a.tok) ++a.tok_shift;
     a.tok_mul = ((uint64_t(1) << a.tok_shift) + a.tok - 1) / a.tok;

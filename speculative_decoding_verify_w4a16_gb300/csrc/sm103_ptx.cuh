@@ -226,6 +226,10 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, uint32_t
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(bytes), "r"(src_bytes)
                  : "memory");
 }
+// Sixteen bytes past the L1, not kept for other readers.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most n of this thread's most recent commit groups are pending.
 template <int n>
