@@ -605,6 +605,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             }
             if (g.nt < 0) break;
         }
+        // A range that was given up leaves nothing to join.
+        if (!ok)
+            for (int e = (p.invariant ? split.begin(blockIdx.x) : int(blockIdx.x)) + lane;
+                 e < (p.invariant ? min(split.begin(blockIdx.x + 1), max(all, 1)) : int(blockIdx.x) + 1); e += 32) {
+                p.shares[e].n = 0;
+                p.shares[e].count = all;
+            }
         // Every copy has landed before the CTA ends, also where its reader gave
         // up.  (A stage that was never filled passes, as the phase before the first.)
 #pragma unroll 1
@@ -1097,13 +1104,12 @@ paged_attn_join_kernel(const Args p) {
     const int col = int(threadIdx.x) % kLanes, line = int(threadIdx.x) / kLanes;
     grid_dep_wait();
     grid_dep_launch();
-    const bool gave_up = (__ldcg(p.status) & (1u << kStatusTimeout)) != 0u;      // shares may be missing
     const int count = p.invariant ? p.shares[0].count : int(gridDim.x);
 #pragma unroll 1
     for (int e = blockIdx.x; e < count; e += gridDim.x) {
         const Share g = p.shares[e];
         const int n = g.n;
-        if (n == 0 || gave_up) continue;
+        if (n == 0) continue;
         const int s0 = g.rows & 0xFFFF, s1 = g.rows >> 16;
         const int r0 = s0 + int(blockIdx.y) * (s1 - s0) / kJoinSplit;
         const int rows = s0 + int(blockIdx.y + 1) * (s1 - s0) / kJoinSplit - r0;
