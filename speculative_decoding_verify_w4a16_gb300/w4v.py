@@ -431,58 +431,75 @@ class Rope:
         self.phases = torch.from_numpy(phases.view(np.int64)).to(device)
 
 
+# What these calls check of their tensors costs as much as their smallest
+# kernels run, so the types are looked up once and nothing is imported per call.
+_HALF = _INT32 = _FLOAT = None
+
+
+def _types():
+    import torch
+    global _HALF, _INT32, _FLOAT
+    _HALF, _INT32, _FLOAT = torch.float16, torch.int32, torch.float32
+
+
 def _i32(t, where, shape):
     """A dense int32 tensor of that shape: its address (0 for None)."""
-    import torch
     if t is None:
         return 0
     if t.shape != shape:
         raise W4VError(ERR_SHAPE, where)
-    if t.dtype is not torch.int32 or not t.is_contiguous():
+    if t.dtype is not _INT32 or not t.is_contiguous():
         raise W4VError(ERR_ARG, where)
     return t.data_ptr()
 
 
 def _rows(t, where, n, heads, head_dim):
     """Rows of dense heads: the row stride of a fp16 [n][heads][head_dim] tensor."""
-    import torch
     if t.shape != (n, heads, head_dim):
         raise W4VError(ERR_SHAPE, where)
-    if t.dtype is not torch.float16:
+    if t.dtype is not _HALF:
         raise W4VError(ERR_ARG, where)
-    stride = t.stride()
-    if n and (stride[2] != 1 or (heads > 1 and stride[1] != head_dim)):
+    rows, head, step = t.stride()
+    if n and (step != 1 or (heads > 1 and head != head_dim)):
         raise W4VError(ERR_ARG, where)
-    return stride[0] if n > 1 else heads * head_dim
+    return rows if n > 1 else heads * head_dim
 
 
-def _dense_out(t, where, like, dtype):
-    """The result tensor: t, or a new one of that type and shape."""
-    import torch
+def _dense_out(t, where, like):
+    """The fp16 result tensor: t, or a new one of that shape."""
     if t is None:
-        return torch.empty(like.shape, dtype=dtype, device=like.device)
+        import torch
+        return torch.empty(like.shape, dtype=_HALF, device=like.device)
     if t.shape != like.shape:
         raise W4VError(ERR_SHAPE, where)
-    if t.dtype is not dtype or not t.is_contiguous():
+    if t.dtype is not _HALF or not t.is_contiguous():
         raise W4VError(ERR_ARG, where)
     return t
 
 
 def _kv(where, k_cache, v_cache, table, lengths, offsets):
     """(packed w4v_kv_t, sequences, table width, kv heads, page, head_dim)."""
-    import torch
-    shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape or table.dim() != 2:
+    if _HALF is None:
+        _types()
+    shape, seqs = k_cache.shape, table.shape
+    if len(shape) != 4 or v_cache.shape != shape or len(seqs) != 2:
         raise W4VError(ERR_SHAPE, where)
-    half = torch.float16
-    if k_cache.dtype is not half or v_cache.dtype is not half or not k_cache.is_contiguous() or \
-            not v_cache.is_contiguous():
+    if k_cache.dtype is not _HALF or v_cache.dtype is not _HALF or not k_cache.is_contiguous() or \
+            not v_cache.is_contiguous() or table.dtype is not _INT32 or not table.is_contiguous():
         raise W4VError(ERR_ARG, where)
     n_pages, heads, page, D = shape
-    B, width = table.shape
-    return (_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), _i32(table, where, (B, width)),
-                     _i32(lengths, where, (B,)), _i32(offsets, where, (B + 1,)), B, width, n_pages, heads, page, D),
+    B, width = seqs
+    return (_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), _i32(lengths, where, (B,)),
+                     _i32(offsets, where, (B + 1,)), B, width, n_pages, heads, page, D),
             B, width, heads, page, D)
+
+
+def _tokens(q, where):
+    """(tokens, heads) of a [n][heads][head_dim] tensor."""
+    shape = q.shape
+    if len(shape) != 3:
+        raise W4VError(ERR_SHAPE, where)
+    return shape[0], shape[1]
 
 
 def rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: Rope, q_out=None, positions=None,
@@ -491,13 +508,12 @@ def rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: Rope, 
     into their pages of k_cache, v_cache [n_pages][Hkv][page][D] and return the rotated q.  q, k, v may
     be slices of one projection's rows; lengths count the new tokens.  positions: int32 [n], where the
     rotation's position is not the cache position."""
-    import torch
     where = "rope_append"
     kv, _, _, heads, _, D = _kv(where, k_cache, v_cache, table, lengths, offsets)
-    n, Hq = q.shape[:2]
-    strides = _rows(q, where, n, Hq, D), _rows(k, where, n, heads, D), _rows(v, where, n, heads, D)
-    q_out = _dense_out(q_out, where, q, torch.float16)
-    code = load().rope_append(kv, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, n, Hq,
+    n, Hq = _tokens(q, where)
+    q_out = _dense_out(q_out, where, q)
+    code = load().rope_append(kv, q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, where, n, Hq, D),
+                              _rows(k, where, n, heads, D), _rows(v, where, n, heads, D), n, Hq,
                               _i32(positions, where, (n,)), rope.phases.data_ptr(), rope.rot, rope.mul,
                               ROPE_INTERLEAVED if rope.interleaved else 0, q_out.data_ptr(), _stream(stream))
     if code != OK:
@@ -517,13 +533,12 @@ def paged_attn(q, k_cache, v_cache, table, lengths, offsets, scale=None, window:
     1/sqrt(D) unless given; window > 0: the last `window` tokens only).  Returns out [n][Hq][D].
     lse: float [n][Hq] to fill with the rows' log-sum-exp.
     batch_invariant: each row's result does not depend on what shares the call (W4V_BATCH_INVARIANT)."""
-    import torch
     where = "paged_attn"
     kv, B, width, heads, page, D = _kv(where, k_cache, v_cache, table, lengths, offsets)
-    n, Hq = q.shape[:2]
+    n, Hq = _tokens(q, where)
     stride = _rows(q, where, n, Hq, D)
-    out = _dense_out(out, where, q, torch.float16)
-    if lse is not None and (lse.shape != (n, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous()):
+    out = _dense_out(out, where, q)
+    if lse is not None and (lse.shape != (n, Hq) or lse.dtype is not _FLOAT or not lse.is_contiguous()):
         raise W4VError(ERR_SHAPE if lse.shape != (n, Hq) else ERR_ARG, where)
     if ws is None:
         ws = workspace(paged_attn_workspace_bytes(n, B, Hq, heads, D, width * page, batch_invariant), q.device)
@@ -545,14 +560,17 @@ def _plane(pool):
     if len(shape) < 5:
         raise W4VError(ERR_SHAPE, "pool")
     nbytes = shape[-3] * shape[-2] * shape[-1] * pool.element_size()
-    return math.prod(shape[:-4]), shape[-4], shape[-2], nbytes
+    return shape[0] if len(shape) == 5 else math.prod(shape[:-4]), shape[-4], shape[-2], nbytes
 
 
 def _pages(where, pool, refs, table, lengths, page=None):
     """(packed w4v_pages_t, n_pages, S, table width)."""
-    if refs.dim() != 1 or table.dim() != 2:
+    if _HALF is None:
+        _types()
+    seqs = table.shape
+    if refs.dim() != 1 or len(seqs) != 2:
         raise W4VError(ERR_SHAPE, where)
-    n_pages, (S, width) = refs.shape[0], table.shape
+    n_pages, (S, width) = refs.shape[0], seqs
     planes, nbytes, at = 0, 0, 0
     if pool is not None:
         planes, pool_pages, page, nbytes = _plane(pool)
@@ -566,8 +584,8 @@ def _pages(where, pool, refs, table, lengths, page=None):
 
 
 def _short(short, where, device):
-    import torch
     if short is None:
+        import torch
         short = torch.zeros(1, dtype=torch.int32, device=device)
     return short, _i32(short, where, (1,))
 
@@ -630,6 +648,8 @@ def kv_compact(pool, refs, table, lengths, refs_out=None, table_out=None, ws=Non
 def kv_copy(pool, src, dst, stream=None):
     """Contents of pages src[i] to pages dst[i] (int32 [n]) in every plane of pool [..., n_pages][Hkv][page][D]."""
     where = "kv_copy"
+    if _HALF is None:
+        _types()
     planes, n_pages, _, nbytes = _plane(pool)
     if not pool.is_contiguous():
         raise W4VError(ERR_ARG, where)
