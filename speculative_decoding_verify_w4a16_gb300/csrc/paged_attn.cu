@@ -116,7 +116,8 @@ struct __align__(16) Share {
     int block;                  // rows that are fetched at a time
     int count;                  // batch-invariant, entry 0: how many entries there are (default: one per range)
 };
-constexpr int kJoinBytes = 24 * 1024;           // of parts at a time
+template <int D>
+constexpr int kHeld = D == 256 ? 40 : 12288 / (2 * D);      // rows of parts that it holds at a time
 
 struct Args {
     __half *out;
@@ -599,7 +600,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 if (e.n > 0) {
                     e.rows = share * g.rows / shares | (share + 1) * g.rows / shares << 16;
                     e.n_mul = (1 << 20) / e.n + 1;
-                    e.block = max(kJoinBytes / (4 * D) / e.n, 1);
+                    e.block = max(kHeld<D> / e.n, 1);
                 }
                 p.shares[p.invariant ? unit : int(blockIdx.x)] = e;
             }
@@ -1097,9 +1098,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 paged_attn_join_kernel(const Args p) {
     __shared__ float2 ml[kJoinWeights];          // m, l; then the part's weight, its share of the sum
     __shared__ float scale[kRows];
-    __shared__ __align__(16) float4 parts[kJoinBytes / 16];
     constexpr int kLanes = D / 4, kLines = kJoinThreads / kLanes;    // threads per row, four columns each
-    constexpr int kHeld = kJoinBytes / (4 * D);  // rows of parts that fit
+    __shared__ __align__(16) float4 parts[kHeld<D> * kLanes];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = int(threadIdx.x) % kLanes, line = int(threadIdx.x) / kLanes;
     grid_dep_wait();
@@ -1121,7 +1121,7 @@ paged_attn_join_kernel(const Args p) {
             const int tok = (r0 + r) * p.group_mul >> 16;
             return size_t(g.row0 + tok) * p.q_heads + g.kvh * p.group + (r0 + r - tok * p.group);
         };
-        const int held = min(n, kHeld);          // parts at a time (all of them, or those of one row)
+        const int held = min(n, kHeld<D>);          // parts at a time (all of them, or those of one row)
         __syncthreads();                         // the entry before is done with
         // rows to warps: of a few parts a row is a lane's, else a warp's
         const int wide = n <= 4 ? 0 : 31;        // lanes per row - 1
