@@ -23,38 +23,57 @@
 // apart as groups of one page, so a tile gathered from up to 16 pages is one
 // operand of one descriptor, K-major for K and N-major for V.
 //
-// Work: the unit is one tile's 128 keys.  All units in order (sequence,
-// key/value head, row tile, keys) are dealt out evenly to one CTA per SM, so
-// a long context at one row tile and a causal triangle of many both fill the
-// GPU.  A CTA's range may begin and end inside a tile; such a part leaves o,
-// m and l in the workspace (at most two parts a CTA), and a second kernel
-// joins them, each boundary's CTA a share of the tile's rows.  The lengths
-// are on the device, so each CTA finds its own range by a scan over the
-// sequences.  With batch invariance the unit is a fixed range of keys, every
-// one a part of its own: which keys meet in one running sum then depends on
-// the row alone.
+// Work: the unit is one tile's 128 keys; a row tile counts kPartCost more for
+// what it costs beside its keys (its epilogue, its first scores).  All units
+// in order (sequence, key/value head, row tile, keys) are dealt out evenly to
+// one CTA per SM, so a long context at one row tile and a causal triangle of
+// many both fill the GPU.  A CTA's range may begin and end inside a tile; such
+// a part leaves o, m and l in the workspace (at most two parts a CTA), and a
+// second kernel joins them, each boundary's CTAs a share of the tile's rows.
+// The lengths are on the device, so each CTA finds its own range by a scan
+// over the sequences.  With batch invariance the unit is a fixed range of
+// keys, every one a part of its own: which keys meet in one running sum then
+// depends on the row alone.
 //
 // A weight of 0 does not hide a value that is not finite (0 x inf is NaN),
 // and within a tile some rows see keys that others must not.  Where a tile
-// holds such keys, the issuer looks their values over before the product and
+// holds such keys, a warp looks their values over before the product and
 // clears what is not finite; the rows that do see it add it in the epilogue.
 // A drafted token that overflowed thus spoils no position before it.
 //
 // Roles (12 warps): 0 producer (the CTA's parts, which it hands on through a
 // ring in shared memory, page ids, TMA), 1 issuer of Q K^T, 2 issuer of P V,
-// 3 guard (the looking over) and tensor-memory owner, 4-7 and 8-11 softmax.
-// S and P have buffers of their own, so Q K^T runs ahead (two tiles; one for
-// heads of 256, whose O leaves room for one S) and waits only until the
-// scores are in registers.  An issuer is held up by its MMAs' execution and
-// in between by its own waits and loop; with two, one's MMAs run meanwhile.
-// The two softmax groups take alternate key tiles, a thread a whole row; what
-// passes between them is the rows' reference.
+// 3 guard (the looking over, a tile ahead of the issuer) and tensor-memory
+// owner, 4-7 and 8-11 softmax.  S and P have buffers of their own, so Q K^T
+// runs ahead (two tiles; one for heads of 256, whose O leaves room for one S)
+// and waits only until the scores are in registers.  An issuer is held up by
+// its MMAs' execution and in between by its own waits and loop; with two,
+// one's MMAs run meanwhile (with one issuer for both, the 8192-token prompt
+// took a fifth longer).  The two softmax groups take alternate key tiles, a
+// thread a whole row; what passes between them is the rows' reference.
 //
-// Code size is part of the design: between them the roles run through their
-// loops once per tile, and what falls out of the instruction caches is
-// fetched again.  So each loop body is there once, waits are a few
-// instructions and the schedule is worked out by one warp (from 138 KB of
-// code to 77 the 8192-token prompt went from 537 to 441 us).
+// Code size is part of the design: the roles run through most of the code
+// once per tile or once per part, and what falls out of the instruction
+// caches is fetched again.  So each loop body is there once, conditions that
+// hold for a whole call are arithmetic instead of branches (the compiler
+// copies a loop for either side of those), waits are a few instructions and
+// the schedule is worked out by one warp.  The 8192-token prompt went from
+// 537 to 441 us with 138 -> 77 KB of code, and when the kernel had grown
+// again from 272 to 257 with 94 -> 78.
+//
+// Measured (one GB300, device time of a call; bound: the cached keys' and
+// values' bytes at 6.67 TB/s or the products at 1905 TFLOP/s):
+//   1 token over 1000, 20 heads on 4 of 128              9.8 us (bound 0.3: latency)
+//   16 tokens over 32,781, 16 heads on 4 of 256         34.8 us (bound 20.2: bytes)
+//   8 x 21 tokens over up to 9000, 20 heads of 128      70.3 us (bound 60.8: bytes; 5.8 TB/s)
+//   32 x up to 40 tokens, window 1000, 20 on 4 of 64    23.6 us (bound 3.9: bytes)
+//   4 x up to 1500 tokens over 12,000, 16 on 4 of 256    225 us (bound 173: 1465 TFLOP/s)
+//   8192 tokens, 20 heads of 128                         254 us (bound 180: 1352 TFLOP/s)
+// The short ones are a chain of latencies (lengths -> table -> K -> scores ->
+// softmax -> product -> parts -> join, about 9 us before the first and after
+// the last byte); prompts are bound by a row's softmax between its two
+// products (maximum 340 cycles, powers 910, loads and stores 350 of 1500 a
+// tile and group, the tensor pipe 61-71% active).
 #include <algorithm>
 #include <climits>
 
@@ -68,14 +87,19 @@ constexpr int kKeyBits = 7, kKeys = 1 << kKeyBits;       // keys per tile
 constexpr int kRows = 128;                      // rows per tile
 constexpr int kThreads = 384;
 constexpr int kWarpProd = 0, kWarpScores = 1, kWarpOut = 2, kWarpGuard = 3, kWarpSoft = 4;
-constexpr int kParts = 2;                       // ring of parts (the softmax groups count on two)
+// Ring of parts (three, with room for it made, changed nothing; the softmax
+// groups count on two).
+constexpr int kParts = 2;
 constexpr int kPartReaders = 11;                // every warp but the producer
 constexpr uint32_t kTmemCols = 512;
 // Tensor memory: S in one or two buffers of 128 columns, P in two of 64, O.
 constexpr uint32_t kPcols = kKeys / 2;
 constexpr float kShift = 8.f, kSlack = 6.f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kPartCost = 3;                    // what a row tile costs beside its keys, in key tiles
+// What a row tile costs beside its keys, in key tiles.  The time of 3; with 0
+// the CTAs that hold the short rows of prompts end last: 272 -> 314 us for
+// 8192 tokens, 245 -> 338 for prompts in chunks; 6 costs up to 2% more.
+constexpr int kPartCost = 3;
 constexpr int kInvBits = 2;                     // least tiles of a batch-invariant part (2^this)
 constexpr int kInvParts = 32;                   // most parts of a row tile
 
