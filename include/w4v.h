@@ -498,7 +498,7 @@ w4v_status rope_phases(int rot, double base, int scaling, const double *params, 
  * Sizes: n_tokens >= 0 (0 is a no-op), q_heads a multiple of kv_heads and at
  * most 128 times as many, scale > 0 and finite, window >= 0, and
  * (n_tokens / tok + min(B, n_tokens)) * kv_heads * (table_width * page / 128
- * + 2) < 2^31 with tok = 128 / (q_heads / kv_heads).
+ * + 5) < 2^31 with tok = 128 / (q_heads / kv_heads).
  * W4V_BATCH_INVARIANT: each row's result is bit for bit the same whatever
  * rows and sequences share the call and however many new tokens come with
  * it, so verified positions equal the one-token steps they stand for.

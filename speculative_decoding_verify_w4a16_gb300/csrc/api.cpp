@@ -480,10 +480,11 @@ w4v_status paged_attn(const w4v_kv_t *kv, const uint16_t *q, long long q_stride,
     if (q_heads % kv->kv_heads != 0 || q_heads / kv->kv_heads > w4v::kAttnMaxGroup || window < 0 ||
         !stride_ok(q_stride, q_heads, kv->head_dim))
         return W4V_ERR_SHAPE;
-    // row tiles times key tiles of a whole table row: counted in 32 bits
+    // row tiles times key tiles of a whole table row (and the units that stand
+    // for a row tile's other work): counted in 32 bits
     const int tok = w4v::kAttnMaxGroup / (q_heads / kv->kv_heads);
     const double tiles = double(n_tokens / tok + std::min(kv->B, n_tokens)) * kv->kv_heads;
-    if (tiles * (double(kv->table_width) * kv->page / 128 + 2) >= 2147483648.0) return W4V_ERR_SHAPE;
+    if (tiles * (double(kv->table_width) * kv->page / 128 + 5) >= 2147483648.0) return W4V_ERR_SHAPE;
     if (!(scale > 0.f) || !std::isfinite(scale)) return W4V_ERR_ARG;
     if (n_tokens == 0 || kv->B == 0) return W4V_OK;
     if (q == nullptr || out == nullptr) return W4V_ERR_ARG;

@@ -58,6 +58,16 @@ def test_attention_refusals(w4v_mod):
     assert call(n=0, q=None, out=None, ws=None) == call(kv=_kv(w, B=0), q=None, ws=None) == w.OK
 
 
+@pytest.mark.parametrize("row_tiles,code", [((1 << 31) // (133 * 64), "SHAPE"), ((1 << 31) // (133 * 64) - 1, "WORKSPACE")])
+def test_attention_work_fits_32_bits(w4v_mod, row_tiles, code):
+    # row tiles of 128 tokens, 64 heads, 128 key tiles and 5 units more a row tile: from 2^31 units on refused
+    w = w4v_mod
+    kv = _kv(w, B=1, table_width=128, page=128, kv_heads=64)
+    n = 128 * row_tiles + (0 if code == "SHAPE" else -128)
+    assert ((n // 128 + 1) * 64 * 133 >= 1 << 31) == (code == "SHAPE")
+    assert w.load().paged_attn(kv, FAKE, 64 * 128, n, 64, 0.1, 0, FAKE, None, FAKE, 16, 0, None) == getattr(w, "ERR_" + code)
+
+
 def test_attention_workspace_sizes(w4v_mod):
     size = w4v_mod.paged_attn_workspace_bytes
     assert size(16, 1, 20, 4, 128, 4096) > 0 and size(16, 1, 20, 4, 128, 4096, True) > 0
