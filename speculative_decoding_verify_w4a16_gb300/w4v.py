@@ -156,9 +156,16 @@ def _check(code: int, where: str) -> None:
         raise W4VError(code, where)
 
 
+_torch = None
+
+
 def _stream(stream=None) -> Optional[int]:
     if stream is None:
-        import torch
+        global _torch
+        if _torch is None:
+            import torch
+            _torch = torch
+        torch = _torch
         if torch.cuda.is_initialized():          # the raw handle: a Stream object costs more than a small call's checks
             return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
@@ -465,12 +472,12 @@ def _rows(t, where, n, heads, head_dim):
     return rows if n > 1 else heads * head_dim
 
 
-def _dense_out(t, where, like):
+def _dense_out(t, where, like, shape):
     """The fp16 result tensor: t, or a new one of that shape."""
     if t is None:
         import torch
-        return torch.empty(like.shape, dtype=_HALF, device=like.device)
-    if t.shape != like.shape:
+        return torch.empty(shape, dtype=_HALF, device=like.device)
+    if t.shape != shape:
         raise W4VError(ERR_SHAPE, where)
     if t.dtype is not _HALF or not t.is_contiguous():
         raise W4VError(ERR_ARG, where)
@@ -484,22 +491,17 @@ def _kv(where, k_cache, v_cache, table, lengths, offsets):
     shape, seqs = k_cache.shape, table.shape
     if len(shape) != 4 or v_cache.shape != shape or len(seqs) != 2:
         raise W4VError(ERR_SHAPE, where)
-    if k_cache.dtype is not _HALF or v_cache.dtype is not _HALF or not k_cache.is_contiguous() or \
-            not v_cache.is_contiguous() or table.dtype is not _INT32 or not table.is_contiguous():
-        raise W4VError(ERR_ARG, where)
     n_pages, heads, page, D = shape
     B, width = seqs
-    return (_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), _i32(lengths, where, (B,)),
-                     _i32(offsets, where, (B + 1,)), B, width, n_pages, heads, page, D),
-            B, width, heads, page, D)
-
-
-def _tokens(q, where):
-    """(tokens, heads) of a [n][heads][head_dim] tensor."""
-    shape = q.shape
-    if len(shape) != 3:
+    if not (k_cache.dtype is v_cache.dtype is _HALF and k_cache.is_contiguous() and v_cache.is_contiguous() and
+            table.dtype is _INT32 and table.is_contiguous()):
+        raise W4VError(ERR_ARG, where)
+    if lengths.shape != (B,) or offsets.shape != (B + 1,):
         raise W4VError(ERR_SHAPE, where)
-    return shape[0], shape[1]
+    if not (lengths.dtype is offsets.dtype is _INT32 and lengths.is_contiguous() and offsets.is_contiguous()):
+        raise W4VError(ERR_ARG, where)
+    return (_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(), offsets.data_ptr(),
+                     B, width, n_pages, heads, page, D), B, width, heads, page, D)
 
 
 def rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: Rope, q_out=None, positions=None,
@@ -510,8 +512,11 @@ def rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: Rope, 
     rotation's position is not the cache position."""
     where = "rope_append"
     kv, _, _, heads, _, D = _kv(where, k_cache, v_cache, table, lengths, offsets)
-    n, Hq = _tokens(q, where)
-    q_out = _dense_out(q_out, where, q)
+    shape = q.shape
+    if len(shape) != 3:
+        raise W4VError(ERR_SHAPE, where)
+    n, Hq, _ = shape
+    q_out = _dense_out(q_out, where, q, shape)
     code = load().rope_append(kv, q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, where, n, Hq, D),
                               _rows(k, where, n, heads, D), _rows(v, where, n, heads, D), n, Hq,
                               _i32(positions, where, (n,)), rope.phases.data_ptr(), rope.rot, rope.mul,
@@ -535,9 +540,12 @@ def paged_attn(q, k_cache, v_cache, table, lengths, offsets, scale=None, window:
     batch_invariant: each row's result does not depend on what shares the call (W4V_BATCH_INVARIANT)."""
     where = "paged_attn"
     kv, B, width, heads, page, D = _kv(where, k_cache, v_cache, table, lengths, offsets)
-    n, Hq = _tokens(q, where)
+    shape = q.shape
+    if len(shape) != 3:
+        raise W4VError(ERR_SHAPE, where)
+    n, Hq, _ = shape
     stride = _rows(q, where, n, Hq, D)
-    out = _dense_out(out, where, q)
+    out = _dense_out(out, where, q, shape)
     if lse is not None and (lse.shape != (n, Hq) or lse.dtype is not _FLOAT or not lse.is_contiguous()):
         raise W4VError(ERR_SHAPE if lse.shape != (n, Hq) else ERR_ARG, where)
     if ws is None:
