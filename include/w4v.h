@@ -526,7 +526,8 @@ w4v_status paged_attn(const w4v_kv_t *kv, const uint16_t *q, long long q_stride,
  *   lengths  device, int32 [S]
  * Sizes: 1 <= n_pages <= 2^24, 0 <= S <= 65535 (0 is a no-op),
  * table_width >= 1, page a power of two, 8 to 256, table_width * page < 2^31.
- * Workspace: kv_workspace_bytes(n_pages, S), zero-filled before first use. */
+ * Workspace: kv_workspace_bytes(n_pages, S), or more; it needs no clearing, and
+ * one may serve pools and batches of different sizes in turn. */
 typedef struct {
     void *pool;
     int32_t *refs, *table, *lengths;

@@ -32,7 +32,8 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kCopyThreads = 256;
 constexpr uint32_t kCopyPiece = 16384;          // bytes of one plane's page that a CTA takes at a time
 
-// Workspace: header, then ints.
+// Workspace: header, then ints.  Every call writes what it reads of it, so one
+// workspace may serve pools of different sizes, whose arrays lie elsewhere.
 struct Header {
     int copies;                                  // pairs in src/dst
     int ok;                                      // whether the second kernel has anything to apply
@@ -41,8 +42,9 @@ struct Work {
     Header *head;
     int32_t *list;        // [n_pages] free pages, lowest first; compact: new id of every page
     int32_t *src, *dst;   // [n_pages] copies
-    int32_t *need;        // [S] pages a sequence needs (kv_extend), rank of a partial page (kv_fork)
-    int32_t *base;        // [S] first of them in list; kv_fork: marks of named children (zero between calls)
+    int32_t *need;        // [S] kv_extend: pages a sequence needs
+    int32_t *base;        // [S] kv_extend: first of them in list; kv_fork: rank of a fork's partial page, or -1
+    int32_t *marks;       // [S] kv_extend: the last page is replaced by a copy; kv_fork: named as a child
 };
 __host__ __device__ inline size_t work_ints(int n_pages, int S) { return 4 + 3 * size_t(n_pages) + 3 * size_t(S); }
 
@@ -57,7 +59,6 @@ struct Args {
     int32_t *short_out;
     int32_t *refs_out, *table_out;
     Work w;
-    int32_t *marks;                              // [S], zero between calls
 };
 
 // Sum over the block of one value a thread, and the sum of the threads before.
@@ -126,7 +127,7 @@ kv_extend_kernel(const Args p) {
     if (threadIdx.x == 0) shared_last = bad = copies = 0;
     __syncthreads();
     // What each sequence needs: whole new pages, and one in place of a partly
-    // filled last page that others hold too (marks[s]).
+    // filled last page that others hold too (marks).
     for (int s = threadIdx.x; s < p.S; s += kPlanThreads) {
         const int len = length_of(s, p), want = p.want[s];
         int need = 0, mark = 0;
@@ -142,7 +143,7 @@ kv_extend_kernel(const Args p) {
             }
         }
         p.w.need[s] = need;
-        if (mark) p.marks[s] = 1;
+        p.w.marks[s] = mark;
     }
     __syncthreads();
     if (shared_last && threadIdx.x == 0) {
@@ -150,13 +151,13 @@ kv_extend_kernel(const Args p) {
         // order until one holder is left, which keeps the page: in turn,
         // since each decides on what the ones before it left.
         for (int s = 0; s < p.S; ++s) {
-            if (!p.marks[s]) continue;
+            if (!p.w.marks[s]) continue;
             const int id = p.table[size_t(s) * p.width + length_of(s, p) / p.page];
             if (p.refs[id] > 1) {
                 p.refs[id] -= 1;
                 p.w.need[s] += 1;
             } else {
-                p.marks[s] = 0;
+                p.w.marks[s] = 0;
             }
         }
     }
@@ -180,7 +181,7 @@ kv_extend_kernel(const Args p) {
                 const int len = length_of(s, p);
                 int32_t *row = p.table + size_t(s) * p.width;
                 int from = p.w.base[s], at = pages_of(len, p);
-                if (shared_last && p.marks[s]) {
+                if (shared_last && p.w.marks[s]) {
                     if (lane == 0) {
                         const int id = p.w.list[from], c = atomicAdd(&copies, 1);
                         p.w.src[c] = row[len / p.page];
@@ -204,11 +205,9 @@ kv_extend_kernel(const Args p) {
         __syncthreads();
         if (threadIdx.x == 0)
             for (int s = 0; s < p.S; ++s)
-                if (p.marks[s]) p.refs[p.table[size_t(s) * p.width + length_of(s, p) / p.page]] += 1;
+                if (p.w.marks[s]) p.refs[p.table[size_t(s) * p.width + length_of(s, p) / p.page]] += 1;
     }
     __syncthreads();
-    if (shared_last)
-        for (int s = threadIdx.x; s < p.S; s += kPlanThreads) p.marks[s] = 0;
     if (threadIdx.x == 0) {
         p.w.head->copies = ok ? copies : 0;
         *p.short_out = ok ? 0 : bad ? -1 : int(min(lack, 0x7FFFFFFFll));
@@ -242,18 +241,21 @@ kv_fork_kernel(const Args p) {
     grid_dep_wait();
     grid_dep_launch();
     if (threadIdx.x == 0) bad = 0;
+    for (int i = threadIdx.x; i < p.n; i += kPlanThreads) {
+        const int a = p.parents[i], c = p.children[i];
+        if (a >= 0 && a < p.S) p.w.marks[a] = 0;
+        if (c >= 0 && c < p.S) p.w.marks[c] = 0;
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < p.n; i += kPlanThreads) {
         const int a = p.parents[i], c = p.children[i];
-        if (a < 0 || a >= p.S || c < 0 || c >= p.S || p.lengths[c] > 0 || atomicExch(p.marks + c, 1) != 0) bad = 1;
+        if (a < 0 || a >= p.S || c < 0 || c >= p.S || p.lengths[c] > 0 || atomicExch(p.w.marks + c, 1) != 0) bad = 1;
     }
     __syncthreads();
     // a child that is a parent too would be read while it is written
     for (int i = threadIdx.x; i < p.n; i += kPlanThreads)
-        if (p.parents[i] >= 0 && p.parents[i] < p.S && p.marks[p.parents[i]] != 0) bad = 1;
+        if (p.parents[i] >= 0 && p.parents[i] < p.S && p.w.marks[p.parents[i]] != 0) bad = 1;
     __syncthreads();
-    for (int i = threadIdx.x; i < p.n; i += kPlanThreads)
-        if (p.children[i] >= 0 && p.children[i] < p.S) p.marks[p.children[i]] = 0;
     int total = 0, lack = 0;
     if (!bad) {
         // base: forks with a partly filled last page, in order (a child may
@@ -443,7 +445,7 @@ Args make_args(const w4v_pages_t &g, void *ws) {
         a.w.dst = a.w.src + g.n_pages;
         a.w.need = a.w.dst + g.n_pages;
         a.w.base = a.w.need + g.S;
-        a.marks = a.w.base + g.S;
+        a.w.marks = a.w.base + g.S;
     }
     return a;
 }

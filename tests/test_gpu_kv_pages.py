@@ -154,3 +154,32 @@ def test_no_pool(w4v_mod, gpu):
     w4v_mod.kv_copy(pool, torch.tensor([n - 1, 7], dtype=torch.int32, device=gpu),
                     torch.tensor([0, n - 2], dtype=torch.int32, device=gpu))
     assert torch.all(pool[0, 0] == 2.0) and torch.all(pool[0, n - 2] == 3.0) and not torch.any(pool[0, 1:7])
+
+
+@pytest.mark.parametrize("fill", [0, 0x45])
+def test_one_workspace_for_caches_of_different_sizes(w4v_mod, gpu, fill):
+    """Two pools of other sizes, and calls on the first sequences of a batch alone, through one workspace
+    that nothing clears: what a call leaves in it never looks like a mark to the next."""
+    r = np.random.default_rng(20)
+    a = Both(w4v_mod, gpu, 100, 64, 6, 16)
+    b = Both(w4v_mod, gpu, 20, 4, 6, 16)
+    c = Both(w4v_mod, gpu, 100, 32, 6, 16)
+    ws = torch.full((w4v_mod.kv_workspace_bytes(100, 64),), fill, dtype=torch.uint8, device=gpu)
+    for x in (a, b, c):
+        x.ws = ws
+    for _ in range(3):
+        a.extend(r.integers(1, 24, 64))                # base holds page ranks where c has its marks
+        c.extend([16 * 5, 16 + 7, *[0] * 30])
+        c.fork([0, 1], [5, 31])
+        a.compact()                                    # list holds page ids where b has its marks
+        b.extend([20, 33, 0, 0])
+        b.fork([0, 1], [2, 3])
+        a.extend(np.where(r.random(64) < 0.5, 30, 0))
+        b.truncate([10, 20, 10, 20])                   # last pages shared, partly filled
+        b.extend([10, 25, 12, 20])                     # only two of the holders grow
+        c.truncate([0, 16 + 3, *[0] * 3, 16 * 5 - 9, *[0] * 25, 16 + 3])
+        a.fork([], [])
+        c.extend([3, 16 + 3, *[0] * 3, 16 * 5, *[0] * 25, 16 + 7])
+        for x in (a, b, c):
+            x.truncate([0] * len(x.o.lengths))
+            assert not x.o.refs.any()
