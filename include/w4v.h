@@ -76,8 +76,9 @@ const char *w4v_status_string(w4v_status status);
 w4v_status w4v_init(void);
 
 /* Synchronizes `stream`, then returns and clears the device status word of
- * the current device: W4V_OK, or W4V_ERR_TIMEOUT if a kernel gave up a wait
- * since the last call. */
+ * the current device: W4V_OK, or what happened since the last call:
+ * W4V_ERR_TIMEOUT if a kernel gave up a wait, else W4V_ERR_SHAPE if the arrays
+ * that paged_attn found on the device ask for more than its arguments allow. */
 w4v_status w4v_get_status(w4v_stream_t stream);
 
 /* ------------------------------------------------------- int4 weight packing
@@ -424,7 +425,8 @@ w4v_status gdn_step(float *state, const uint16_t *k_prev, const uint16_t *v_prev
  *   - The device arrays are read as they are: a length is clamped to
  *     [0, table_width * page], an offset to [0, n_tokens], and a page id
  *     outside [0, n_pages) is never followed (a read gives zeros, a write is
- *     dropped).
+ *     dropped).  Offsets should not decrease: a row that several sequences
+ *     name gets the result of one of them.
  *   - table, lengths and offsets are int32 on the device, so a captured
  *     graph can be replayed while they change. */
 typedef struct {
@@ -498,7 +500,9 @@ w4v_status rope_phases(int rot, double base, int scaling, const double *params, 
  * Sizes: n_tokens >= 0 (0 is a no-op), q_heads a multiple of kv_heads and at
  * most 128 times as many, scale > 0 and finite, window >= 0, and
  * (n_tokens / tok + min(B, n_tokens)) * kv_heads * (table_width * page / 128
- * + 5) < 2^31 with tok = 128 / (q_heads / kv_heads).
+ * + 5) < 2^31 with tok = 128 / (q_heads / kv_heads).  Offsets on the device
+ * that name rows again and again, for more work than that or than the workspace
+ * holds: nothing is written, and w4v_get_status returns W4V_ERR_SHAPE.
  * W4V_BATCH_INVARIANT: each row's result is bit for bit the same whatever
  * rows and sequences share the call and however many new tokens come with
  * it, so verified positions equal the one-token steps they stand for.

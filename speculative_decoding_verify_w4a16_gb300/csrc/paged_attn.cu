@@ -160,6 +160,7 @@ struct Args {
     int back;                   // keys that a row sees before its own (INT_MAX: all)
     int invariant;              // batch-invariant: a part is one unit
     int unit_bits, part_cost;   // 2^unit_bits tiles per unit; units for the work beside a row tile's keys
+    uint32_t max_units;         // of one key/value head: what the workspace (batch-invariant) and 32 bits hold
     struct Share *shares;       // what the second kernel joins
     float scale_log2;
 };
@@ -261,11 +262,13 @@ struct Place {
 };
 // All units, how they are split, and the place of the first one of range cta
 // (one warp).  Two passes over the sequences, 32 at a time; with 32 or fewer
-// the second one has the first one's counts.
-__device__ __forceinline__ Place schedule(const Args &p, int cta, int ctas, int &all, Split &split) {
+// the second one has the first one's counts.  The host has seen that rows
+// counted once fit; offsets that go up and down count rows again and again, so
+// the sum is looked at here, and too large a one leaves nothing to do (false).
+__device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place &w, int &all, Split &split) {
     const int lane = threadIdx.x & 31;
-    Place w{0, 0, 0, 0};
     int u = 0, at = 0;
+    uint32_t mine = 0;                           // this lane's sequences, no further than 2^31 - 1
     all = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
@@ -273,7 +276,7 @@ __device__ __forceinline__ Place schedule(const Args &p, int cta, int ctas, int 
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             if (pass == 0 || p.B > 32) u = lane_units(p, b0 + lane);
             if (pass == 0) {
-                all += u;
+                mine = min(mine + uint32_t(u), 0x7FFFFFFFu);
                 continue;
             }
             const int upto = warp_scan(u * p.kv_heads);
@@ -292,13 +295,13 @@ __device__ __forceinline__ Place schedule(const Args &p, int cta, int ctas, int 
             const int tiles = row_tiles(p, s.n);
 #pragma unroll 1
             for (int q0 = 0;; q0 += 32) {
-                const int mine = q0 + lane < tiles ? extent_of(p, s, q0 + lane).units : 0;
-                const int sum = warp_scan(mine);
+                const int tile = q0 + lane < tiles ? extent_of(p, s, q0 + lane).units : 0;
+                const int sum = warp_scan(tile);
                 const uint32_t over = __ballot_sync(0xFFFFFFFFu, sum > rest);
                 if (over != 0 || q0 >= tiles) {
                     const int l = over != 0 ? __ffs(over) - 1 : 0;
                     w.qt = q0 + l;
-                    w.u = rest - __shfl_sync(0xFFFFFFFFu, sum - mine, l);
+                    w.u = rest - __shfl_sync(0xFFFFFFFFu, sum - tile, l);
                     break;
                 }
                 rest -= __shfl_sync(0xFFFFFFFFu, sum, 31);
@@ -306,13 +309,16 @@ __device__ __forceinline__ Place schedule(const Args &p, int cta, int ctas, int 
             break;
         }
         if (pass == 0) {
-            all = __reduce_add_sync(0xFFFFFFFFu, all) * p.kv_heads;
+            const uint64_t sum = (uint64_t(__reduce_add_sync(0xFFFFFFFFu, mine >> 16)) << 16) +
+                                 __reduce_add_sync(0xFFFFFFFFu, mine & 0xFFFFu);
+            if (sum > p.max_units) return false;
+            all = int(sum) * p.kv_heads;
             split = Split(all, ctas);
             if (cta >= split.ranges) break;
             at = split.begin(cta);
         }
     }
-    return w;
+    return true;
 }
 
 // A run of units of one row tile.
@@ -520,7 +526,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         int all = 0;
         Split split;
         Cursor cur{};
-        cur.w = schedule(p, blockIdx.x, gridDim.x, all, split);
+        if (!schedule(p, blockIdx.x, gridDim.x, cur.w, all, split) && blockIdx.x == 0 && lane == 0)
+            atomicOr(p.status, 1u << kStatusShape);
         if (int(blockIdx.x) < split.ranges) {
             cur.unit = split.begin(blockIdx.x);
             cur.left = split.begin(blockIdx.x + 1) - cur.unit;
@@ -1323,6 +1330,7 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     a.invariant = invariant;
     a.unit_bits = invariant ? inv_tile_bits(kv.table_width * kv.page) : 0;
     a.part_cost = invariant ? 0 : kPartCost;
+    a.max_units = uint32_t(std::min(invariant ? slots.count : size_t(INT_MAX), size_t(INT_MAX)) / kv.kv_heads);
     a.scale_log2 = scale * 1.4426950408889634f;
     // K and V as (64 elements, 8 tokens, blocks of a head, 8-token groups):
     // a box is a page's groups of one stage's blocks

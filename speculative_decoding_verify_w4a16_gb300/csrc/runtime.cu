@@ -7,7 +7,8 @@
 
 namespace w4v {
 
-// Bit (1 << code) is set by a kernel that abandons a bounded wait.
+// Bit (1 << code) is set by a kernel that abandons a bounded wait, or that finds
+// on the device what no host check could see.
 __device__ uint32_t g_status_word;
 
 namespace {
@@ -162,5 +163,6 @@ extern "C" w4v_status w4v_get_status(w4v_stream_t stream) {
         return W4V_ERR_CUDA;
     }
     if (v & (1u << W4V_ERR_TIMEOUT)) return W4V_ERR_TIMEOUT;
+    if (v & (1u << W4V_ERR_SHAPE)) return W4V_ERR_SHAPE;
     return v ? W4V_ERR_CUDA : W4V_OK;
 }

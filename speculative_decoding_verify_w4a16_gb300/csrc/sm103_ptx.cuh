@@ -13,7 +13,7 @@ namespace w4v {
 // A wait that has not completed after this long is abandoned: the kernel
 // records W4V_ERR_TIMEOUT in the device status word and winds down.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr uint32_t kStatusTimeout = 7u;
+constexpr uint32_t kStatusShape = 2u, kStatusTimeout = 7u;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -218,3 +218,29 @@ def test_a_token_that_is_not_finite_touches_only_rows_that_see_it(w4v_mod, gpu, 
             assert not np.isfinite(got[4:8, 2:, 3]).any()
             rest = np.arange(D) != 3
             assert np.array_equal(got[4:8, 2:][..., rest], clean[4:8, 2:][..., rest])
+
+
+@pytest.mark.parametrize("invariant", [True, False])
+def test_offsets_that_count_rows_again_and_again(w4v_mod, gpu, invariant):
+    """Offsets that go up and down ask for more than the workspace (batch-invariant) or 32 bits of work hold:
+    nothing is written, neither results nor past the workspace, the status says so, and the next call is as ever."""
+    w, rng = w4v_mod, np.random.default_rng(16)
+    n, Hq, Hkv, page, length = (3200, 16, 4, 16, 3200) if invariant else (32768, 128, 1, 256, 1 << 21)
+    width = length // page
+    i32 = lambda a: to_dev(np.asarray(a, np.int32), gpu)  # noqa: E731
+    lengths, offsets = i32([length] * 9), i32([0, n] * 5)
+    table = torch.full((9, width), -1, dtype=torch.int32, device=gpu)
+    k = torch.zeros((4, Hkv, page, 64), dtype=torch.float16, device=gpu)
+    q = torch.zeros((n, Hq, 64), dtype=torch.float16, device=gpu)
+    out = torch.full_like(q, 9.0)
+    nbytes = w.paged_attn_workspace_bytes(n, 9, Hq, Hkv, 64, length, invariant)
+    around = torch.full((nbytes + (1 << 20),), 0x5A, dtype=torch.uint8, device=gpu)
+    w.paged_attn(q, k, k, table, lengths, offsets, out=out, ws=around[:nbytes], batch_invariant=invariant)
+    assert w.get_status() == w.ERR_SHAPE and w.get_status() == w.OK
+    assert torch.all(out == 9.0) and torch.all(around[nbytes:] == 0x5A)
+    if invariant:                                      # ascending offsets that need every row tile there is
+        c = cache(rng, [1] * 8 + [25], [3190] * 8 + [25], Hq, Hkv, 64, page)
+        ws = around[:w.paged_attn_workspace_bytes(33, 9, Hq, Hkv, 64, c["table"].shape[1] * page, True)]
+        check(w, gpu, c, invariant=True)
+        want, got = run(w, gpu, c, invariant=True), run(w, gpu, c, invariant=True, ws=ws.zero_())
+        assert np.array_equal(want[0], got[0])

@@ -193,3 +193,19 @@ def test_binding_refuses_wrong_tensors(w4v_mod):
     assert code(w.kv_fork, pool, refs, table, lens, lens, lens[:1]) == w.ERR_SHAPE
     assert code(w.kv_compact, pool, refs, table, lens, refs_out=refs[:2]) == w.ERR_SHAPE
     assert code(w.kv_copy, pool[0], refs, refs) == w.ERR_SHAPE
+
+
+@pytest.mark.parametrize("group", [1, 3, 5, 128])
+def test_invariant_workspace_holds_every_part(w4v_mod, group):
+    """One slot per row tile and 512 keys of its context (tables up to 16,384 tokens): enough for all ascending
+    offsets, the fullest ones (a sequence for every row, full contexts) included."""
+    import random
+    rng = random.Random(group)
+    tok = 128 // group
+    for _ in range(300):
+        B, Hkv, width = rng.randint(1, 40), rng.randint(1, 5), rng.randint(1, 16384)
+        news = [rng.choice([0, 1, tok, tok + 1, rng.randint(0, 4 * tok)]) for _ in range(B)]
+        n = sum(news) + rng.choice([0, 0, 3])
+        slot = min(tok, max(n, 1)) * group * (64 * 4 + 8) + 16
+        slots = (w4v_mod.paged_attn_workspace_bytes(n, B, Hkv * group, Hkv, 64, width, True) - 256) // slot
+        assert Hkv * sum(-(-m // tok) for m in news) * -(-width // 512) <= slots
