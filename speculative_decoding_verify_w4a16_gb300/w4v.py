@@ -4,6 +4,11 @@ Every step of the verify path runs in the library's CUDA kernels; this
 module passes device pointers from torch tensors, the current stream, and
 turns status codes into exceptions.  There is no fallback: if the library is
 missing or the GPU is not sm_103, calls raise.
+
+`stream=` takes a torch stream or a raw handle (default: the current stream).
+Results and workspaces that the caller does not pass are then that stream's;
+ordering the call after its inputs, and what reads its results after it, is
+the caller's part.
 """
 from __future__ import annotations
 
@@ -176,6 +181,32 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _torch_stream(stream=None):
+    """The torch stream of a call's `stream`: a torch stream, a raw handle, or None (the current one)."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream()
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    handle = (stream.value if isinstance(stream, ctypes.c_void_p) else int(stream)) or 0
+    # 0 and 1 (cudaStreamLegacy) both name the default stream
+    return torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+
+
+def _new(shape, dtype, device, stream=None, zero=False):
+    """A result tensor of a call on `stream`.  Where one is given the tensor is that stream's own, so
+    that its memory is not still in use by another stream's earlier work (and cleared in order); the
+    current stream, where the caller is likely to read it, counts as a user too."""
+    import torch
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def init() -> None:
     _check(load().w4v_init(), "w4v_init")
 
@@ -217,9 +248,13 @@ def w8_lmhead_argmax_workspace_bytes(M: int, V: int) -> int:
     return load().w8_lmhead_argmax_workspace_bytes(M, V)
 
 
-def workspace(nbytes: int, device="cuda"):
-    """A zero-filled device workspace (the library leaves it zeroed after each call)."""
+def workspace(nbytes: int, device="cuda", stream=None):
+    """A zero-filled device workspace (the library leaves it zeroed after each call), allocated and
+    cleared on `stream` (default: the current one), in whose order it may be used and given up."""
     import torch
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return workspace(nbytes, device)
     return torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
@@ -239,9 +274,9 @@ def w4a16_gemm(A, Bq, scales, N: int, zeros=None, out=None, ws=None, stream=None
     import torch
     M, K = A.shape
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        out = _new((M, N), torch.float16, A.device, stream)
     if ws is None:
-        ws = workspace(w4a16_workspace_bytes(M, N, K), A.device)
+        ws = workspace(w4a16_workspace_bytes(M, N, K), A.device, stream)
     flags = (STATIC_WEIGHTS if static_weights else 0) | (BATCH_INVARIANT if batch_invariant else 0)
     code = load().w4a16_gemm_ex(_ptr(A), _ptr(Bq), _ptr(scales), _ptr(zeros), int(group), _ptr(out), M, N, K,
                                 _ptr(ws), ws.numel(), flags, _stream(stream))
@@ -268,12 +303,13 @@ class GroupedGemm:
             arr[i] = Problem(_ptr(A), _ptr(Bq), _ptr(sc), _ptr(z), _ptr(C), int(C.shape[1]), int(A.shape[1]))
         nbytes = lib.w4a16_grouped_plan_bytes(n)
         # torch's allocations start on 512-byte boundaries (the plan needs 64)
-        self.plan = torch.empty(max(int(nbytes), 64), dtype=torch.uint8, device=dev)
+        self.plan = _new(max(int(nbytes), 64), torch.uint8, dev, stream)
         self.handle = GroupedHandle()
         code = lib.w4a16_grouped_plan(arr, n, int(M), int(group), _ptr(self.plan), self.plan.numel(),
                                       ctypes.byref(self.handle), _stream(stream))
         _check(code, "w4a16_grouped_plan")
-        self.ws = workspace(lib.w4a16_grouped_workspace_bytes(ctypes.byref(self.handle)), dev)
+        self.ws = workspace(lib.w4a16_grouped_workspace_bytes(ctypes.byref(self.handle)), dev, stream)
+        _torch_stream(stream).synchronize()                    # cleared: calls may run on any stream
 
     def __call__(self, stream=None, static_weights: bool = False, ws=None):
         ws = self.ws if ws is None else ws
@@ -292,9 +328,9 @@ def w8_lmhead_argmax(X, W, scale, out=None, maxlogit=None, logits=None, ws=None,
     M, K = X.shape
     V = W.shape[0]
     if out is None:
-        out = torch.empty(M, dtype=torch.int32, device=X.device)
+        out = _new(M, torch.int32, X.device, stream)
     if ws is None:
-        ws = workspace(w8_lmhead_argmax_workspace_bytes(M, V), X.device)
+        ws = workspace(w8_lmhead_argmax_workspace_bytes(M, V), X.device, stream)
     code = load().w8_lmhead_argmax_ex(_ptr(X), _ptr(W), _ptr(scale), M, K, V, _ptr(out), _ptr(maxlogit),
                                       _ptr(logits), _ptr(ws), ws.numel(), BATCH_INVARIANT if batch_invariant else 0,
                                       _stream(stream))
@@ -308,9 +344,9 @@ def spec_accept(target, draft, n_out=None, tok_out=None, stream=None):
     B, K1 = target.shape
     K = K1 - 1
     if n_out is None:
-        n_out = torch.empty(B, dtype=torch.int32, device=target.device)
+        n_out = _new(B, torch.int32, target.device, stream)
     if tok_out is None:
-        tok_out = torch.empty((B, K1), dtype=torch.int32, device=target.device)
+        tok_out = _new((B, K1), torch.int32, target.device, stream)
     code = load().spec_accept(_ptr(target), _ptr(draft) if K > 0 else None, B, K, _ptr(n_out),
                               _ptr(tok_out), _stream(stream))
     _check(code, "spec_accept")
@@ -326,15 +362,15 @@ def w8_lmhead_argmax_accept(X, W, scale, draft, out=None, n_out=None, tok_out=No
     V = W.shape[0]
     B, nd = draft.shape
     if out is None:
-        out = torch.empty(M, dtype=torch.int32, device=X.device)
+        out = _new(M, torch.int32, X.device, stream)
     if n_out is None:
-        n_out = torch.empty(B, dtype=torch.int32, device=X.device)
+        n_out = _new(B, torch.int32, X.device, stream)
     if tok_out is None:
-        tok_out = torch.empty((B, nd + 1), dtype=torch.int32, device=X.device)
+        tok_out = _new((B, nd + 1), torch.int32, X.device, stream)
     if M != B * (nd + 1):
         raise W4VError(ERR_SHAPE, "w8_lmhead_argmax_accept")
     if ws is None:
-        ws = workspace(w8_lmhead_argmax_workspace_bytes(M, V), X.device)
+        ws = workspace(w8_lmhead_argmax_workspace_bytes(M, V), X.device, stream)
     code = load().w8_lmhead_argmax_accept_ex(_ptr(X), _ptr(W), _ptr(scale), B, nd, K, V,
                                              _ptr(draft) if nd > 0 else None, _ptr(out), _ptr(n_out),
                                              _ptr(tok_out), _ptr(maxlogit), _ptr(ws), ws.numel(),
@@ -349,11 +385,11 @@ def ngram_draft(context, lengths, n_min: int, n_max: int, K: int, out=None, matc
     import torch
     B, ld = context.shape
     if out is None:
-        out = torch.empty((B, K), dtype=torch.int32, device=context.device)
+        out = _new((B, K), torch.int32, context.device, stream)
     if match is None:
-        match = torch.empty(B, dtype=torch.int32, device=context.device)
+        match = _new(B, torch.int32, context.device, stream)
     if ws is None:
-        ws = workspace(load().ngram_draft_workspace_bytes(B), context.device)
+        ws = workspace(load().ngram_draft_workspace_bytes(B), context.device, stream)
     code = load().ngram_draft(_ptr(context), _ptr(lengths), B, ld, int(n_min), int(n_max), int(K),
                               _ptr(out) if K > 0 else None, _ptr(match), _ptr(ws), ws.numel(), _stream(stream))
     _check(code, "ngram_draft")
@@ -367,7 +403,7 @@ def gdn_verify(state, q, k, v, alpha, beta, out=None, stream=None):
     B, H, dv, dk = state.shape
     T = q.shape[1]
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=torch.float16, device=state.device)
+        out = _new((B, T, H, dv), torch.float16, state.device, stream)
     code = load().gdn_verify(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), B, T, H, dk, dv,
                              _ptr(out), _stream(stream))
     _check(code, "gdn_verify")
@@ -382,7 +418,7 @@ def gdn_step(state, prev, q, k, v, alpha, beta, out=None, stream=None):
     B, H, dv, dk = state.shape
     T = q.shape[1]
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=torch.float16, device=state.device)
+        out = _new((B, T, H, dv), torch.float16, state.device, stream)
     if prev is None:
         kp = vp = ap = bp = n = None
         T_prev = 0
@@ -472,11 +508,10 @@ def _rows(t, where, n, heads, head_dim):
     return rows if n > 1 else heads * head_dim
 
 
-def _dense_out(t, where, like, shape):
+def _dense_out(t, where, like, shape, stream):
     """The fp16 result tensor: t, or a new one of that shape."""
     if t is None:
-        import torch
-        return torch.empty(shape, dtype=_HALF, device=like.device)
+        return _new(shape, _HALF, like.device, stream)
     if t.shape != shape:
         raise W4VError(ERR_SHAPE, where)
     if t.dtype is not _HALF or not t.is_contiguous():
@@ -516,7 +551,7 @@ def rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: Rope, 
     if len(shape) != 3:
         raise W4VError(ERR_SHAPE, where)
     n, Hq, _ = shape
-    q_out = _dense_out(q_out, where, q, shape)
+    q_out = _dense_out(q_out, where, q, shape, stream)
     code = load().rope_append(kv, q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, where, n, Hq, D),
                               _rows(k, where, n, heads, D), _rows(v, where, n, heads, D), n, Hq,
                               _i32(positions, where, (n,)), rope.phases.data_ptr(), rope.rot, rope.mul,
@@ -545,11 +580,11 @@ def paged_attn(q, k_cache, v_cache, table, lengths, offsets, scale=None, window:
         raise W4VError(ERR_SHAPE, where)
     n, Hq, _ = shape
     stride = _rows(q, where, n, Hq, D)
-    out = _dense_out(out, where, q, shape)
+    out = _dense_out(out, where, q, shape, stream)
     if lse is not None and (lse.shape != (n, Hq) or lse.dtype is not _FLOAT or not lse.is_contiguous()):
         raise W4VError(ERR_SHAPE if lse.shape != (n, Hq) else ERR_ARG, where)
     if ws is None:
-        ws = workspace(paged_attn_workspace_bytes(n, B, Hq, heads, D, width * page, batch_invariant), q.device)
+        ws = workspace(paged_attn_workspace_bytes(n, B, Hq, heads, D, width * page, batch_invariant), q.device, stream)
     code = load().paged_attn(kv, q.data_ptr(), stride, n, Hq, D ** -0.5 if scale is None else scale, int(window),
                              out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
                              BATCH_INVARIANT if batch_invariant else 0, _stream(stream))
@@ -591,10 +626,9 @@ def _pages(where, pool, refs, table, lengths, page=None):
                         nbytes, planes, n_pages, S, width, page), n_pages, S, width)
 
 
-def _short(short, where, device):
+def _short(short, where, device, stream):
     if short is None:
-        import torch
-        short = torch.zeros(1, dtype=torch.int32, device=device)
+        short = _new(1, _INT32, device, stream, zero=True)
     return short, _i32(short, where, (1,))
 
 
@@ -605,9 +639,9 @@ def kv_extend(pool, refs, table, lengths, new_lengths, short=None, ws=None, stre
     where = "kv_extend"
     pages, n_pages, S, _ = _pages(where, pool, refs, table, lengths)
     want = _i32(new_lengths, where, (S,))
-    short, at = _short(short, where, refs.device)
+    short, at = _short(short, where, refs.device, stream)
     if ws is None:
-        ws = workspace(kv_workspace_bytes(n_pages, S), refs.device)
+        ws = workspace(kv_workspace_bytes(n_pages, S), refs.device, stream)
     code = load().kv_extend(pages, want, at, ws.data_ptr(), ws.numel(), _stream(stream))
     if code != OK:
         raise W4VError(code, where)
@@ -630,9 +664,9 @@ def kv_fork(pool, refs, table, lengths, parents, children, short=None, ws=None, 
     pages, n_pages, S, _ = _pages(where, pool, refs, table, lengths)
     n = parents.numel()
     a, c = _i32(parents, where, (n,)), _i32(children, where, (n,))
-    short, at = _short(short, where, refs.device)
+    short, at = _short(short, where, refs.device, stream)
     if ws is None:
-        ws = workspace(kv_workspace_bytes(n_pages, S), refs.device)
+        ws = workspace(kv_workspace_bytes(n_pages, S), refs.device, stream)
     code = load().kv_fork(pages, a, c, n, at, ws.data_ptr(), ws.numel(), _stream(stream))
     if code != OK:
         raise W4VError(code, where)
@@ -646,7 +680,7 @@ def kv_compact(pool, refs, table, lengths, refs_out=None, table_out=None, ws=Non
     refs_out, table_out = refs if refs_out is None else refs_out, table if table_out is None else table_out
     r, t = _i32(refs_out, where, (n_pages,)), _i32(table_out, where, (S, width))
     if ws is None:
-        ws = workspace(kv_workspace_bytes(n_pages, S), refs.device)
+        ws = workspace(kv_workspace_bytes(n_pages, S), refs.device, stream)
     code = load().kv_compact(pages, r, t, ws.data_ptr(), ws.numel(), _stream(stream))
     if code != OK:
         raise W4VError(code, where)
