@@ -920,7 +920,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     __syncwarp();
                     if (lane == 0) mbar_arrive(turn(quad, use & 1));
                 }
-                l *= now == m ? 1.f : ex2((m - now) * c);    // m = -inf: l is 0 and stays
+                l = __fmul_rn(l, now == m ? 1.f : ex2((m - now) * c));   // m = -inf: l is 0 and stays
                 m = now;
                 // P's buffer: tile t - 2's product has read it
                 if (t > 1) ok = wait(pv_done(t - 2), pv_phase(t - 2));
@@ -967,7 +967,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 tc_keep_alive<32>(w[0]);
                 tc_keep_alive<32>(w[1]);
                 const float2 all = __fadd2_rn(sum[0], sum[1]);
-                l += all.x + all.y;
+                l = __fadd_rn(l, __fadd_rn(all.x, all.y));
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full(t & 1));
@@ -1003,9 +1003,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 ++pairs;
                 if (!ok) break;
                 // Both groups' sums.  With one O by this group's reference, the
-                // last; with two by the larger, and the O's with them (each
-                // product rounded by itself: which group has the even key
-                // tiles depends on what the CTA did before, the sum must not).
+                // last; with two by the larger, and the O's with them.  Each
+                // product is rounded by itself, here and in the loop above:
+                // which group has the even key tiles, and which the last one,
+                // depends on the CTA's work before and on the tile's other
+                // rows, and a row's sum must not.
                 const float2 other = *shared_sums;
                 if (P::kOwn) {
                     const float both = fmaxf(m, other.x);
@@ -1015,7 +1017,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     if (both == -INFINITY) weight = weight2 = 0.f;
                     m = both;
                 } else {
-                    l += other.x == m ? other.y : other.y * ex2((other.x - m) * c);
+                    l = __fadd_rn(l, other.x == m ? other.y : __fmul_rn(other.y, ex2((other.x - m) * c)));
                 }
             }
             const bool fix = nt > 0 && spoilt[np & 1] == np;

@@ -244,3 +244,33 @@ def test_offsets_that_count_rows_again_and_again(w4v_mod, gpu, invariant):
         check(w, gpu, c, invariant=True)
         want, got = run(w, gpu, c, invariant=True), run(w, gpu, c, invariant=True, ws=ws.zero_())
         assert np.array_equal(want[0], got[0])
+
+
+def same_as_alone(w, gpu, c, rows, window=0, **kw):
+    """Rows (sequence, index among its new tokens) of a batch-invariant call, bit for bit as one-token calls."""
+    got, lse = run(w, gpu, c, window=window, invariant=True, **kw)
+    for b, i in rows:
+        t, n = c["offsets"][b] + i, c["offsets"][b + 1] - c["offsets"][b]
+        one = dict(c, q=c["q"][t:t + 1], table=c["table"][b:b + 1], offsets=np.array([0, 1], np.int32),
+                   lengths=np.array([c["lengths"][b] - n + i + 1], np.int32))
+        o1, l1 = run(w, gpu, one, window=window, invariant=True, **kw)
+        assert np.array_equal(o1[0], got[t]) and np.array_equal(l1[0], lse[t]), (b, i)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_batch_invariance_where_a_key_tile_ends_inside_a_part(w4v_mod, gpu, D):
+    """Rows whose last key tile is not the last one of their part, because later tokens of the block see more:
+    which group of warps joins the two groups' sums then differs from the one-token call."""
+    rng = np.random.default_rng(17)
+    c = cache(rng, [16, 16, 16], [650, 901, 135], 10, 2, D, 16)
+    same_as_alone(w4v_mod, gpu, c, [(b, i) for b in range(3) for i in range(16)])
+    # Sums of equal size: 128 keys from 512 on, then one that raises the maximum by 6.5 to 7.2 powers of two,
+    # so that whether their joining rounds once or twice shows (in a fifth of the sums).
+    c = cache(rng, [128], [773], 8, 8, D, 16)
+    c["q"][:] = 0
+    c["q"][:, :, 0] = 8 * rng.uniform(0.95, 1.05, (128, 8))
+    level = np.full(c["table"].shape[1] * 16, -40.0)
+    level[512:640], level[517], level[640] = rng.uniform(-2, 0, 128), 0.0, 4.75
+    for p in range(-(-773 // 16)):
+        c["k"][c["table"][0, p], :, :, 0] = level[16 * p:16 * p + 16]
+    same_as_alone(w4v_mod, gpu, c, [(0, i) for i in range(128)], scale=0.125)
