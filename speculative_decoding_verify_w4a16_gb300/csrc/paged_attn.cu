@@ -1140,7 +1140,9 @@ constexpr int kJoinWeights = 3 * kRows + 2 * kMaxCtas;
 // largest m_i.  Latency bounds it: a warp fetches its rows' statistics and all
 // fetch o's parts, both to shared memory, before anything is waited for, and
 // the weights are worked out while the latter come in.  Sums run over the
-// parts in order, so that parts that add nothing change nothing.
+// parts in order, so that parts of which a row sees no key (o = 0) change
+// nothing.  A weight too small for fp32 still multiplies, so that it does not
+// hide what is not finite.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_attn_join_kernel(const Args p) {
@@ -1231,7 +1233,7 @@ paged_attn_join_kernel(const Args p) {
                     for (int i = 0; i < m; ++i) {
                         const float w = x[i].x;
                         const float4 y = v[i * kLanes];
-                        if (w != 0.f) o = make_float4(fmaf(w, y.x, o.x), fmaf(w, y.y, o.y), fmaf(w, y.z, o.z), fmaf(w, y.w, o.w));
+                        o = make_float4(fmaf(w, y.x, o.x), fmaf(w, y.y, o.y), fmaf(w, y.z, o.z), fmaf(w, y.w, o.w));
                     }
                     if (i0 + m < n) continue;
                     const float inv = scale[b + r];

@@ -297,3 +297,26 @@ def test_batch_invariance_does_not_see_the_table(w4v_mod, gpu, D):
     ids = np.where(c["table"][:, :, None] < 0, -1, c["table"][:, :, None] * 8 + np.arange(8, dtype=np.int32))
     eight = run(w4v_mod, gpu, dict(c, k=k, v=v, table=ids.reshape(1, -1)), invariant=True)
     assert np.array_equal(got[0], eight[0]) and np.array_equal(got[1], eight[1])
+
+
+@pytest.mark.parametrize("invariant", [False, True])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_value_that_is_not_finite_shows_whatever_its_weight(w4v_mod, gpu, value, D, invariant):
+    """An early token's value that overflowed, in a context cut into parts whose weights run over 290 powers of
+    two: rows that see the token are not finite there, as where the context is one part."""
+    rng = np.random.default_rng(19)
+    for length in (300, 5000):
+        c = cache(rng, [3], [length], 2, 1, D, 16)
+        c["q"][:] = 0
+        c["q"][:, :, 0] = 8.0
+        ramp = (np.arange(c["table"].shape[1] * 16) / length * 100.0).astype(np.float16)
+        for p in range(-(-length // 16)):
+            c["k"][c["table"][0, p], 0, :, 0] = ramp[16 * p:16 * p + 16]
+        clean, _ = run(w4v_mod, gpu, c, scale=0.25, invariant=invariant)
+        bad = dict(c, v=c["v"].copy())
+        bad["v"][c["table"][0, 0], 0, 5, 3] = value
+        got, lse = run(w4v_mod, gpu, bad, scale=0.25, invariant=invariant)
+        rest = np.arange(D) != 3
+        assert not np.isfinite(got[..., 3]).any() and np.isfinite(lse).all()
+        assert np.array_equal(got[..., rest], clean[..., rest])
