@@ -489,10 +489,10 @@ w4v_status rope_phases(int rot, double base, int scaling, const double *params, 
  *     o_t = sum_j softmax_j(scale q_t . k_j) v_j   over p_t - window < j <= p_t
  * (window 0: every j <= p_t), p_t the row's position, query head h reading
  * key/value head h / (q_heads / kv_heads).  Scores, softmax statistics and
- * sums are fp32; the weights enter the product with v as fp16 (11 significant
- * bits, scaled by up to 2^14 so that none above 2^-38 of the largest is
- * lost).  A row that sees no token gives zeros and lse = -inf.  What the
- * cache holds past a sequence's length is never used.
+ * sums are fp32; the weights enter the product with v as fp16, scaled by 2^8
+ * or more: each is off by at most 2^-11 of itself (from 2^-22 of the largest
+ * on) or 2^-33 of the largest.  A row that sees no token gives zeros and
+ * lse = -inf.  What the cache holds past a sequence's length is never used.
  *   q      device, fp16 rows of q_heads heads, q_stride elements apart
  *   out    device, fp16 [n_tokens][q_heads][head_dim] (written, never read)
  *   lse    device, float [n_tokens][q_heads] or NULL:

@@ -320,3 +320,23 @@ def test_a_value_that_is_not_finite_shows_whatever_its_weight(w4v_mod, gpu, valu
         rest = np.arange(D) != 3
         assert not np.isfinite(got[..., 3]).any() and np.isfinite(lse).all()
         assert np.array_equal(got[..., rest], clean[..., rest])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("power", [-20.0, -22.5, -30.0, -32.0, -32.875])
+def test_small_weights(w4v_mod, gpu, D, power):
+    """A weight 2^power of the largest is off by at most 2^-11 of itself or 2^-33 of the largest, and not lost
+    above that.  Its value is 2^15 and all others are 0, so the result is that weight.  (The power itself is a
+    score in fp32, good to 2^-18; the result is rounded to fp16, of 2^-24 at the least.)"""
+    rng = np.random.default_rng(20)
+    for first, small in ((0, 77), (77, 0), (3, 200)):              # in one key tile, in either order, and in two
+        c = cache(rng, [1], [260], 2, 1, D, 16)
+        c["q"][:], c["k"][:], c["v"][:] = 0, 0, 0
+        c["q"][:, :, 0] = 1.0
+        at = lambda a, j: a[c["table"][0, j // 16], 0, j % 16]  # noqa: E731
+        c["k"][:, :, :, 0] = -200.0
+        at(c["k"], first)[0], at(c["k"], small)[0], at(c["v"], small)[:] = 0.0, power, 2.0 ** 15
+        got, _ = run(w4v_mod, gpu, c, scale=float(np.log(2.0)))
+        want = 2.0 ** (power + 15)
+        tol = max(2.0 ** -11 * want, 2.0 ** (15 - 33)) + 2.0 ** -17 * want + max(2.0 ** -11 * want, 2.0 ** -25)
+        assert np.all(np.abs(got.astype(np.float64) - want) <= tol) and np.all(got > 0)
