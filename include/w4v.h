@@ -492,7 +492,8 @@ w4v_status rope_phases(int rot, double base, int scaling, const double *params, 
  * sums are fp32; the weights enter the product with v as fp16, scaled by 2^8
  * or more: each is off by at most 2^-11 of itself (from 2^-22 of the largest
  * on) or 2^-33 of the largest.  A row that sees no token gives zeros and
- * lse = -inf.  What the cache holds past a sequence's length is never used.
+ * lse = -inf; a row that no sequence's offsets cover is left alone, in out and
+ * in lse.  What the cache holds past a sequence's length is never used.
  *   q      device, fp16 rows of q_heads heads, q_stride elements apart
  *   out    device, fp16 [n_tokens][q_heads][head_dim] (written, never read)
  *   lse    device, float [n_tokens][q_heads] or NULL:

@@ -61,7 +61,7 @@ def token_places(lengths, offsets):
 def attention(q, k_cache, v_cache, table, lengths, offsets, scale, window=0):
     """(out, lse, mag, absdot) of every new row in double; what error bounds go by: mag is
     sum_j p_j |v_j|, absdot the largest scale sum_d |q_d k_jd| of a row's keys.  A row without a
-    visible key: zeros and -inf."""
+    visible key, or of no sequence (which paged_attn leaves alone): zeros and -inf."""
     n, Hq, D = q.shape
     Hkv, page = k_cache.shape[1], k_cache.shape[2]
     out, mag = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))

@@ -544,7 +544,8 @@ def rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: Rope, 
     """Rotate the new tokens' q [n][Hq][D] and k [n][Hkv][D] by their positions, write k and v [n][Hkv][D]
     into their pages of k_cache, v_cache [n_pages][Hkv][page][D] and return the rotated q.  q, k, v may
     be slices of one projection's rows; lengths count the new tokens.  positions: int32 [n], where the
-    rotation's position is not the cache position."""
+    rotation's position is not the cache position.  Rows that no sequence's offsets cover are left alone:
+    in a new q_out they hold anything."""
     where = "rope_append"
     kv, _, _, heads, _, D = _kv(where, k_cache, v_cache, table, lengths, offsets)
     shape = q.shape
@@ -572,6 +573,7 @@ def paged_attn(q, k_cache, v_cache, table, lengths, offsets, scale=None, window:
     """Causal attention of the new tokens' q [n][Hq][D] over the paged cache that holds them (scale
     1/sqrt(D) unless given; window > 0: the last `window` tokens only).  Returns out [n][Hq][D].
     lse: float [n][Hq] to fill with the rows' log-sum-exp.
+    Rows that no sequence's offsets cover are not written: in a new `out` they hold anything.
     batch_invariant: each row's result does not depend on what shares the call (W4V_BATCH_INVARIANT)."""
     where = "paged_attn"
     kv, B, width, heads, page, D = _kv(where, k_cache, v_cache, table, lengths, offsets)

@@ -340,3 +340,15 @@ def test_small_weights(w4v_mod, gpu, D, power):
         want = 2.0 ** (power + 15)
         tol = max(2.0 ** -11 * want, 2.0 ** (15 - 33)) + 2.0 ** -17 * want + max(2.0 ** -11 * want, 2.0 ** -25)
         assert np.all(np.abs(got.astype(np.float64) - want) <= tol) and np.all(got > 0)
+
+
+@pytest.mark.parametrize("invariant", [False, True])
+def test_rows_of_no_sequence_are_left_alone(w4v_mod, gpu, invariant):
+    """Rows before the first offset and from the last one on (a batch padded to a fixed size)."""
+    rng = np.random.default_rng(21)
+    c = cache(rng, [3, 0, 16], [500, 40, 2000], 4, 2, 64, 16)
+    want, lse = run(w4v_mod, gpu, c, invariant=invariant)
+    pad = dict(c, offsets=c["offsets"] + 5, q=np.concatenate([c["q"][:5], c["q"], np.full((9, 4, 64), np.nan, np.float16)]))
+    got, l = run(w4v_mod, gpu, pad, invariant=invariant)
+    assert np.all(got[:5] == 9) and np.all(got[24:] == 9) and np.all(l[:5] == 7) and np.all(l[24:] == 7)
+    assert np.array_equal(l[5:24], lse) and np.array_equal(got[5:24], want)      # the same work, split in the same way
