@@ -505,15 +505,13 @@ w4v_status rope_phases(int rot, double base, int scaling, const double *params, 
  * that name rows again and again, for more work than that or than the workspace
  * holds: nothing is written, and w4v_get_status returns W4V_ERR_SHAPE.
  * W4V_BATCH_INVARIANT: each row's result is bit for bit the same whatever
- * rows and sequences share the call, however many new tokens come with it and
- * however wide the table or large the pages are, so verified positions equal
- * the one-token steps they stand for.
+ * rows and sequences share the call and however many new tokens come with
+ * it, so verified positions equal the one-token steps they stand for.
  * Without it the contexts are cut where that balances the GPU.
  * Workspace: paged_attn_workspace_bytes(...) with the call's own n_tokens and
  * B or larger ones, max_context = table_width * page; zero-filled before
  * first use.  With W4V_BATCH_INVARIANT it grows with the number of rows times
- * the pieces of max_context (of 512 tokens up to 16,384, then 16 more in every
- * doubling), so a long prompt goes through in chunks. */
+ * up to 32 pieces of the context, so a long prompt goes through in chunks. */
 size_t paged_attn_workspace_bytes(int n_tokens, int B, int q_heads, int kv_heads, int head_dim, int max_context,
                                   unsigned flags);
 w4v_status paged_attn(const w4v_kv_t *kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,

@@ -39,7 +39,7 @@
 // The lengths are on the device, so each CTA finds its own range by a scan
 // over the sequences.  With batch invariance the unit is a fixed range of
 // keys, every one a part of its own: which keys meet in one running sum then
-// depends on their positions and the row alone.
+// depends on the row alone.
 //
 // A weight of 0 does not hide a value that is not finite (0 x inf is NaN),
 // and within a tile some rows see keys that others must not.  Where a tile
@@ -106,12 +106,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // the CTAs that hold the short rows of prompts end last: 272 -> 314 us for
 // 8192 tokens, 245 -> 338 for prompts in chunks; 6 costs up to 2% more.
 constexpr int kPartCost = 3;
-// Batch-invariant parts: 2^kInvBits key tiles each (512 keys) up to tile
-// 2^(kInvBits + kInvLog + 1) (16,384 keys), and from there on 2^kInvLog parts in
-// every doubling.  A key's part follows from its position alone, the longest
-// part of a context is a 16th to a 32nd of it, and the longest context of all
-// has 304 parts.
-constexpr int kInvBits = 2, kInvLog = 4;
+constexpr int kInvBits = 2;                     // least tiles of a batch-invariant part (2^this)
+constexpr int kInvParts = 32;                   // most parts of a row tile
 
 template <int D>
 struct Plan {
@@ -168,8 +164,8 @@ struct Args {
     int wide;                   // out is 32-byte aligned
     int B, width, n_pages, page_bits, slot_rows;   // 2^page_bits tokens a page
     int back;                   // keys that a row sees before its own (INT_MAX: all)
-    int invariant;              // -1: batch-invariant, a part is one unit and a unit several tiles; 0: a unit is a tile
-    int part_cost;              // units for the work beside a row tile's keys
+    int invariant;              // batch-invariant: a part is one unit
+    int unit_bits, part_cost;   // 2^unit_bits tiles per unit; units for the work beside a row tile's keys
     uint32_t max_units;         // of one key/value head: what the workspace (batch-invariant) and 32 bits hold
     struct Share *shares;       // what the second kernel joins
     float scale_log2;
@@ -187,21 +183,10 @@ __device__ __forceinline__ Seq seq_of(const Args &p, int b) {
     return s;
 }
 
-// The unit of a key tile, and the first key tile of a unit.  (Masks instead of
-// branches on the mode: the compiler makes a copy of a loop for each side of
-// those.)
-__device__ __forceinline__ int unit_of(const Args &p, int tile) {
-    const int more = (max(31 - kInvLog - __clz(tile), kInvBits) - kInvBits) & p.invariant;
-    return (tile >> (more + (kInvBits & p.invariant))) + (more << kInvLog);
-}
-__device__ __forceinline__ int unit_begin(const Args &p, int unit) {
-    const int more = (max(unit >> kInvLog, 1) - 1) & p.invariant;
-    return (unit - (more << kInvLog)) << (more + (kInvBits & p.invariant));
-}
-
-// Key tiles that row tile qt reads, and its units: those of its tiles (one where
+// Key tiles that row tile qt reads, and its units: one per key tile (one where
 // there are none), and in the default schedule kPartCost more, last, that
-// stand for the work beside the keys.
+// stand for the work beside the keys.  (Without branches on the mode: the
+// compiler makes a copy of a loop for each side of those.)
 struct Extent {
     int lo, hi, units;          // tiles [lo, hi)
 };
@@ -211,7 +196,7 @@ __device__ __forceinline__ Extent extent_of(const Args &p, const Seq &s, int qt)
     Extent e;
     e.lo = max(p0 - p.back, 0) >> kKeyBits;
     e.hi = (p1 >> kKeyBits) + 1;
-    e.units = unit_of(p, max(e.hi - 1, e.lo)) - unit_of(p, e.lo) + 1 + p.part_cost;
+    e.units = max(((e.hi - 1) >> p.unit_bits) - (e.lo >> p.unit_bits) + 1, 1) + p.part_cost;
     return e;
 }
 
@@ -375,9 +360,9 @@ struct Cursor {
             const int step = min(e.units - w.u, p.invariant ? 1 : left);
             g.units -= p.part_cost;
             take = max(min(g.units - w.u, step), 0);         // none: a range may begin past the keys
-            const int c = unit_of(p, e.lo) + w.u;
-            g.kt0 = max(e.lo, unit_begin(p, c));
-            g.nt = max(min(e.hi, unit_begin(p, c + take)) - g.kt0, 0);
+            const int c = ((e.lo >> p.unit_bits) + w.u) << p.unit_bits;
+            g.kt0 = max(e.lo, c);
+            g.nt = max(min(e.hi, c + (take << p.unit_bits)) - g.kt0, 0);
             g.slot = p.invariant ? unit : 2 * cta + (w.u == 0);
             if (take == g.units) g.slot = -1;
             w.u += step;
@@ -1258,12 +1243,13 @@ paged_attn_join_kernel(const Args p) {
 // -------------------------------------------------------------------- the host
 int tokens_per_tile(int q_heads, int kv_heads) { return kRows / (q_heads / kv_heads); }
 
-// Batch-invariant parts of a context: the last key's, as unit_of counts.
-int inv_parts(int max_context) {
-    const int last = std::max(max_context - 1, 0) >> kKeyBits;
-    int more = 0;
-    while (last >> (kInvBits + more) >= 2 << kInvLog) ++more;
-    return (last >> (kInvBits + more)) + (more << kInvLog) + 1;
+// Tiles of a batch-invariant part (2^this): by the table's width alone, so
+// that it is the same in every call on a cache.
+int inv_tile_bits(int max_context) {
+    const long long tiles = ((long long)max_context + kKeys - 1) / kKeys;
+    int bits = kInvBits;
+    while (tiles > (long long)kInvParts << bits) ++bits;
+    return bits;
 }
 
 struct Slots {
@@ -1278,7 +1264,8 @@ Slots slots_of(int n_tokens, int B, int q_heads, int kv_heads, int max_context, 
         s.count = 2 * size_t(kMaxCtas);
     } else {
         const size_t tiles = size_t(kv_heads) * (size_t(n_tokens) / tok + std::min(B, n_tokens) + 1);
-        s.count = tiles * inv_parts(max_context);
+        const size_t keys = size_t(kKeys) << inv_tile_bits(max_context);
+        s.count = tiles * ((size_t(max_context) + keys - 1) / keys + 1);
     }
     return s;
 }
@@ -1350,7 +1337,8 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     while (1 << a.page_bits < kv.page) ++a.page_bits;
     a.back = window > 0 ? window - 1 : INT_MAX;
     a.slot_rows = slots.rows;
-    a.invariant = invariant ? -1 : 0;
+    a.invariant = invariant;
+    a.unit_bits = invariant ? inv_tile_bits(kv.table_width * kv.page) : 0;
     a.part_cost = invariant ? 0 : kPartCost;
     a.max_units = uint32_t(std::min(invariant ? slots.count : size_t(INT_MAX), size_t(INT_MAX)) / kv.kv_heads);
     a.scale_log2 = scale * 1.4426950408889634f;

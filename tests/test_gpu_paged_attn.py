@@ -276,29 +276,6 @@ def test_batch_invariance_where_a_key_tile_ends_inside_a_part(w4v_mod, gpu, D):
     same_as_alone(w4v_mod, gpu, c, [(0, i) for i in range(128)], scale=0.125)
 
 
-@pytest.mark.parametrize("D", [64, 128, 256])
-def test_batch_invariance_does_not_see_the_table(w4v_mod, gpu, D):
-    """A table trimmed to the batch's longest context, one with room for more, and other pages give the same bits;
-    contexts of more than 16,384 tokens, whose later parts are longer, among them."""
-    rng = np.random.default_rng(18)
-    c = cache(rng, [4, 1, 7], [2100, 530, 1029], 6, 2, D, 16)
-    want = run(w4v_mod, gpu, c, invariant=True)
-    for width in (132, 1100, 5000, 70000):
-        wide = np.full((3, width), -1, np.int32)
-        wide[:, :132] = c["table"][:, :132]
-        got = run(w4v_mod, gpu, dict(c, table=wide), invariant=True)
-        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]), width
-    c = cache(rng, [5], [34900], 2, 1, D, 64)
-    check(w4v_mod, gpu, c, invariant=True)
-    got = run(w4v_mod, gpu, c, invariant=True)
-    same_as_alone(w4v_mod, gpu, c, [(0, 0), (0, 3)])
-    same_as_alone(w4v_mod, gpu, c, [(0, 2)], window=19000)
-    k, v = (x.reshape(x.shape[0], 1, 8, 8, D).swapaxes(1, 2).reshape(-1, 1, 8, D) for x in (c["k"], c["v"]))
-    ids = np.where(c["table"][:, :, None] < 0, -1, c["table"][:, :, None] * 8 + np.arange(8, dtype=np.int32))
-    eight = run(w4v_mod, gpu, dict(c, k=k, v=v, table=ids.reshape(1, -1)), invariant=True)
-    assert np.array_equal(got[0], eight[0]) and np.array_equal(got[1], eight[1])
-
-
 @pytest.mark.parametrize("invariant", [False, True])
 @pytest.mark.parametrize("value", [np.nan, np.inf])
 @pytest.mark.parametrize("D", [64, 128, 256])

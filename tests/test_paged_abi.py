@@ -209,12 +209,3 @@ def test_invariant_workspace_holds_every_part(w4v_mod, group):
         slot = min(tok, max(n, 1)) * group * (64 * 4 + 8) + 16
         slots = (w4v_mod.paged_attn_workspace_bytes(n, B, Hkv * group, Hkv, 64, width, True) - 256) // slot
         assert Hkv * sum(-(-m // tok) for m in news) * -(-width // 512) <= slots
-
-
-def test_invariant_parts_of_long_contexts(w4v_mod):
-    """Workspaces for tables past 16,384 tokens: 16 parts more in every doubling, rounded up to whole parts."""
-    size = lambda c: w4v_mod.paged_attn_workspace_bytes(1, 1, 1, 1, 64, c, True)  # noqa: E731
-    part = size(1) - 256
-    for c, parts in ((0, 1), (512, 1), (513, 2), (16384, 32), (16385, 33), (16384 + 1024, 33), (16384 + 1025, 34),
-                     (32768, 48), (32769, 49), (65536, 64), (131072, 80), (1 << 30, 288), ((1 << 31) - 1, 304)):
-        assert size(c) - 256 == parts * part, c
