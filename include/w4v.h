@@ -506,7 +506,11 @@ w4v_status rope_phases(int rot, double base, int scaling, const double *params, 
  * holds: nothing is written, and w4v_get_status returns W4V_ERR_SHAPE.
  * W4V_BATCH_INVARIANT: each row's result is bit for bit the same whatever
  * rows and sequences share the call and however many new tokens come with
- * it, so verified positions equal the one-token steps they stand for.
+ * it, so verified positions equal the one-token steps they stand for.  The
+ * table's size does count: a context is summed in parts of 512 tokens where
+ * table_width * page is at most 16,384, of 1024 up to 32,768, and so on in
+ * doublings.  Calls that are to agree need tables of one such class: keep one
+ * width rather than trimming it to each batch.
  * Without it the contexts are cut where that balances the GPU.
  * Workspace: paged_attn_workspace_bytes(...) with the call's own n_tokens and
  * B or larger ones, max_context = table_width * page; zero-filled before

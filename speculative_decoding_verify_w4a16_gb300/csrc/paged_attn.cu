@@ -1243,8 +1243,11 @@ paged_attn_join_kernel(const Args p) {
 // -------------------------------------------------------------------- the host
 int tokens_per_tile(int q_heads, int kv_heads) { return kRows / (q_heads / kv_heads); }
 
-// Tiles of a batch-invariant part (2^this): by the table's width alone, so
-// that it is the same in every call on a cache.
+// Tiles of a batch-invariant part (2^this): by the table's size alone, so that
+// it is the same in every call on a cache.  (By the keys' positions, 16 parts
+// in every doubling, it would not depend on the table either, but parts of
+// unequal length are dealt out unevenly: 16 tokens over 32,781 took 54.5 us
+// against 41.5.)
 int inv_tile_bits(int max_context) {
     const long long tiles = ((long long)max_context + kKeys - 1) / kKeys;
     int bits = kInvBits;

@@ -574,7 +574,8 @@ def paged_attn(q, k_cache, v_cache, table, lengths, offsets, scale=None, window:
     1/sqrt(D) unless given; window > 0: the last `window` tokens only).  Returns out [n][Hq][D].
     lse: float [n][Hq] to fill with the rows' log-sum-exp.
     Rows that no sequence's offsets cover are not written: in a new `out` they hold anything.
-    batch_invariant: each row's result does not depend on what shares the call (W4V_BATCH_INVARIANT)."""
+    batch_invariant: each row's result does not depend on what shares the call (W4V_BATCH_INVARIANT), as
+    long as the table's size width * page stays up to 16,384, or between the same two powers of two."""
     where = "paged_attn"
     kv, B, width, heads, page, D = _kv(where, k_cache, v_cache, table, lengths, offsets)
     shape = q.shape

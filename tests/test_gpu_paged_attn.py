@@ -329,3 +329,29 @@ def test_rows_of_no_sequence_are_left_alone(w4v_mod, gpu, invariant):
     got, l = run(w4v_mod, gpu, pad, invariant=invariant)
     assert np.all(got[:5] == 9) and np.all(got[24:] == 9) and np.all(l[:5] == 7) and np.all(l[24:] == 7)
     assert np.array_equal(l[5:24], lse) and np.array_equal(got[5:24], want)      # the same work, split in the same way
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_batch_invariance_over_tables_of_one_class(w4v_mod, gpu, D):
+    """A table trimmed to the batch's longest context and one with room for more give the same bits while both
+    hold up to 16,384 tokens, or lie between the same powers of two; and so do pages of another size."""
+    rng = np.random.default_rng(18)
+    c = cache(rng, [4, 1, 7], [2100, 530, 1029], 6, 2, D, 16)
+
+    def at(width):
+        wide = np.full((3, width), -1, np.int32)
+        wide[:, :132] = c["table"][:, :132]
+        return run(w4v_mod, gpu, dict(c, table=wide), invariant=True)
+    for widths in ((132, 500, 1024), (1025, 1500, 2048), (40000, 65536)):
+        results = [at(width) for width in widths]
+        for got in results[1:]:
+            assert np.array_equal(got[0], results[0][0]) and np.array_equal(got[1], results[0][1]), widths
+    c = cache(rng, [5], [34900], 2, 1, D, 64)
+    check(w4v_mod, gpu, c, invariant=True)
+    same_as_alone(w4v_mod, gpu, c, [(0, 0), (0, 3)])
+    same_as_alone(w4v_mod, gpu, c, [(0, 2)], window=19000)
+    got = run(w4v_mod, gpu, c, invariant=True)
+    k, v = (x.reshape(x.shape[0], 1, 8, 8, D).swapaxes(1, 2).reshape(-1, 1, 8, D) for x in (c["k"], c["v"]))
+    ids = np.where(c["table"][:, :, None] < 0, -1, c["table"][:, :, None] * 8 + np.arange(8, dtype=np.int32))
+    eight = run(w4v_mod, gpu, dict(c, k=k, v=v, table=ids.reshape(1, -1)), invariant=True)
+    assert np.array_equal(got[0], eight[0]) and np.array_equal(got[1], eight[1])
