@@ -67,19 +67,25 @@
 // 537 to 441 us with 138 -> 77 KB of code, and when the kernel had grown
 // again from 272 to 257 with 94 -> 78.
 //
-// Measured (one GB300, device time of a call; bound: the cached keys' and
-// values' bytes at 6.67 TB/s or the products at 1905 TFLOP/s):
-//   1 token over 1000, 20 heads on 4 of 128              9.8 us (bound 0.3: latency)
-//   16 tokens over 32,781, 16 heads on 4 of 256         34.8 us (bound 20.2: bytes)
-//   8 x 21 tokens over up to 9000, 20 heads of 128      70.3 us (bound 60.8: bytes; 5.8 TB/s)
-//   32 x up to 40 tokens, window 1000, 20 on 4 of 64    23.6 us (bound 3.9: bytes)
-//   4 x up to 1500 tokens over 12,000, 16 on 4 of 256    225 us (bound 173: 1465 TFLOP/s)
-//   8192 tokens, 20 heads of 128                         254 us (bound 180: 1352 TFLOP/s)
-// The short ones are a chain of latencies (lengths -> table -> K -> scores ->
-// softmax -> product -> parts -> join, about 9 us before the first and after
-// the last byte); prompts are bound by a row's softmax between its two
-// products (maximum 340 cycles, powers 910, loads and stores 350 of 1500 a
-// tile and group, the tensor pipe 61-71% active).
+// Measured (one GB300, device time of a call; in brackets first the
+// batch-invariant form's, which writes and reads back a part for every 512 keys
+// or more of a row tile; bound: the cached keys' and values' bytes at 6.67 TB/s
+// or the products at 1905 TFLOP/s):
+//   1 token over 1000, 20 heads on 4 of 128              9.9 us (11.6; bound 0.3: latency)
+//   16 tokens over 32,781, 16 heads on 4 of 256         34.4 us (41.6; bound 20.2: bytes)
+//   8 x 21 tokens over up to 9000, 20 heads of 128      70.4 us (97; bound 60.8: bytes; 5.8 TB/s)
+//   32 x up to 40 tokens, window 1000, 20 on 4 of 64    23.6 us (31; bound 3.9: bytes)
+//   4 x up to 1500 tokens over 12,000, 16 on 4 of 256    225 us (534; bound 173: 1465 TFLOP/s)
+//   8192 tokens, 20 heads of 128                         253 us (672; bound 180: 1357 TFLOP/s)
+// The short ones are a chain of latencies.  By the clock, us from the end of
+// the kernel before, one token over 1000: place found 1.0, page ids 1.9, first
+// scores 3.2, weights 4.4, product 5.0, part stored 5.5, CTAs ended 6.4, second
+// kernel under way 7.2, joined 9.0.  16 tokens over 32,781: 1.8, 2.1, 5.6, 6.5,
+// the last product 26.1 (so 24 us from the first load to the last product, 5.6
+// TB/s), part stored 28.2, ended 28.4, second kernel 29.2, joined 34.3.
+// Prompts are bound by a row's softmax between its two products (maximum 340
+// cycles, powers 910, loads and stores 350 of 1500 a tile and group, the
+// tensor pipe 61-71% active).
 #include <algorithm>
 #include <climits>
 

@@ -44,8 +44,11 @@ union Piece {
 constexpr int kAhead = 3;                       // heads of a thread whose pieces are loaded together
 
 // kVec: rot is a multiple of 16 (half layout) or 8 (interleaved), so pairs
-// and copied elements fall into whole 16-byte pieces.  Otherwise elements
-// are moved pair by pair (twice the instructions, the same bytes).
+// and copied elements fall into whole 16-byte pieces.  Otherwise elements are
+// moved pair by pair, with a division each: the same bytes, but 88 us instead of
+// 35 for 8192 rows of 24 x 256 (rot 242), 31 instead of 16 for 28 x 64 (rot 50),
+// 6.0 instead of 3.1 for 16 rows.  The bound is 48 registers, 40 warps an SM;
+// the half layout spills 44 bytes under it.
 template <bool kInter, bool kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1280 / kThreads)
 rope_append_kernel(const Args p) {
@@ -162,7 +165,7 @@ rope_append_kernel(const Args p) {
 // CTAs of 256 threads for a few tokens, of 128 for many, where twice as many
 // tokens side by side count for more than each one's own time (one GB300: 16
 // rows of 28 x 128 2.8 against 3.1 us, 8192 rows of 24 x 256 39.7 against
-// 34.8 us, 5.8 TB/s).
+// 34.8 us, 5.8 TB/s; measured at these two ends, not where they cross).
 template <bool kInter, bool kVec>
 w4v_status launch(const Args &a, int sms, cudaStream_t stream) {
     const bool many = a.n_tokens >= 16 * sms;
