@@ -355,3 +355,17 @@ def test_batch_invariance_over_tables_of_one_class(w4v_mod, gpu, D):
     ids = np.where(c["table"][:, :, None] < 0, -1, c["table"][:, :, None] * 8 + np.arange(8, dtype=np.int32))
     eight = run(w4v_mod, gpu, dict(c, k=k, v=v, table=ids.reshape(1, -1)), invariant=True)
     assert np.array_equal(got[0], eight[0]) and np.array_equal(got[1], eight[1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long_contexts_to_the_weights_rounding(w4v_mod, gpu, D):
+    """The bound of attention_bounds charges every key a step of one running sum.  Dealt out over at least 148
+    CTAs, 20,011 keys are at most two tiles (256 keys) to a part and 157 parts to join: with these steps instead, what
+    is left is little more than the weights' and the result's roundings."""
+    rng = np.random.default_rng([22, D])
+    c = cache(rng, [2], [20011], 3, 1, D, 16)
+    got, _ = run(w4v_mod, gpu, c)
+    o, _, mag, absdot = paged.attention(c["q"], c["k"], c["v"], c["table"], c["lengths"], c["offsets"], D ** -0.5)
+    eps = (D + 8) * 2.0 ** -23 * absdot + 2.0 ** -20
+    rel = 2.0 ** -11 + 2 * eps + 2 * (256 + 157) * 2.0 ** -23
+    assert np.all(np.abs(got - o) <= 2.0 ** -11 * np.abs(o) + rel[..., None] * (1 + 2.0 ** -10) * mag + 2.0 ** -24)
