@@ -466,6 +466,22 @@ w4v_status rope_append(const w4v_kv_t *kv, const uint16_t *q, const uint16_t *k,
                        const int32_t *positions, const uint64_t *phases, int rot, float mul, unsigned flags,
                        uint16_t *q_out, w4v_stream_t stream);
 
+/* rope_append for targets that norm their queries and keys: every query and
+ * key head x (all head_dim elements) first becomes
+ *     x / sqrt(mean(x^2) + eps) * (w + c),
+ * w = q_weight or k_weight (device, fp16 [head_dim]; NULL: all factors 1),
+ * c = 0, or 1 with W4V_NORM_ZERO_CENTRED (weights kept around zero; no
+ * meaning where the weights are NULL), and is then rotated and written as
+ * above; nothing is rounded in between.  eps >= 0 and finite; with eps = 0 a
+ * head of zeros gives NaN.  Values are not normed.  Everything else as
+ * rope_append. */
+#define W4V_NORM_ZERO_CENTRED 8u
+w4v_status norm_rope_append(const w4v_kv_t *kv, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                            long long q_stride, long long k_stride, long long v_stride, int n_tokens, int q_heads,
+                            const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+                            const int32_t *positions, const uint64_t *phases, int rot, float mul, unsigned flags,
+                            uint16_t *q_out, w4v_stream_t stream);
+
 /* Host only: phases and mul of a base and a scaling for long contexts.
  * f_i = base^(-2i/rot), then
  *   W4V_ROPE_PLAIN    as it is;

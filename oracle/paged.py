@@ -49,6 +49,15 @@ def rotate(x, positions, freqs, mul, interleaved):
     return y
 
 
+def head_norm(x, weight=None, eps=1e-6, centre=0.0):
+    """Every head of x [n][heads][D] over its root mean square, times weight + centre (weight None: as it is)."""
+    y = x.astype(np.float64)
+    for t in range(y.shape[0]):
+        for h in range(y.shape[1]):
+            y[t, h] /= math.sqrt(float(np.dot(y[t, h], y[t, h])) / y.shape[2] + eps)
+    return y if weight is None else y * (np.asarray(weight, np.float64) + centre)
+
+
 def token_places(lengths, offsets):
     """(sequence, position) of every new row, (-1, 0) for one that no sequence covers."""
     places = [(-1, 0)] * int(max(offsets))

@@ -394,17 +394,19 @@ bool stride_ok(long long stride, int heads, int head_dim) {
 }
 }  // namespace
 
-w4v_status rope_append(const w4v_kv_t *kv, const uint16_t *q, const uint16_t *k, const uint16_t *v,
-                       long long q_stride, long long k_stride, long long v_stride, int n_tokens, int q_heads,
-                       const int32_t *positions, const uint64_t *phases, int rot, float mul, unsigned flags,
-                       uint16_t *q_out, w4v_stream_t stream) {
-    if ((flags & ~unsigned(W4V_ROPE_INTERLEAVED)) != 0u) return W4V_ERR_ARG;
+namespace {
+// rope_append and, with norms, norm_rope_append.
+w4v_status append(const w4v_kv_t *kv, const uint16_t *q, const uint16_t *k, const uint16_t *v, long long q_stride,
+                  long long k_stride, long long v_stride, int n_tokens, int q_heads, const w4v::HeadNorm *norm,
+                  const int32_t *positions, const uint64_t *phases, int rot, float mul, bool interleaved,
+                  uint16_t *q_out, w4v_stream_t stream) {
     const w4v_status st = kv_check(kv, n_tokens, q_heads);
     if (st != W4V_OK) return st;
     const int D = kv->head_dim, Hk = kv->kv_heads;
     if (rot < 0 || rot > D || rot % 2 != 0 || !stride_ok(q_stride, q_heads, D) || !stride_ok(k_stride, Hk, D) ||
         !stride_ok(v_stride, Hk, D))
         return W4V_ERR_SHAPE;
+    if (norm != nullptr && (!(norm->eps >= 0.f) || !std::isfinite(norm->eps))) return W4V_ERR_ARG;
     if (n_tokens == 0 || kv->B == 0) return W4V_OK;
     if (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr || (rot > 0 && phases == nullptr))
         return W4V_ERR_ARG;
@@ -412,9 +414,30 @@ w4v_status rope_append(const w4v_kv_t *kv, const uint16_t *q, const uint16_t *k,
     if (!w4v::aligned16(q) || !w4v::aligned16(k) || !w4v::aligned16(v) || !w4v::aligned16(q_out) ||
         !aligned4(positions) || (reinterpret_cast<uintptr_t>(phases) & 7u) != 0u)
         return W4V_ERR_ALIGN;
+    if (norm != nullptr && (!w4v::aligned16(norm->q_weight) || !w4v::aligned16(norm->k_weight))) return W4V_ERR_ALIGN;
     return w4v::launch_rope_append(*kv, q, k, v, q_stride, k_stride, v_stride, n_tokens, q_heads, positions, phases,
-                                   rot, mul, (flags & W4V_ROPE_INTERLEAVED) != 0u, q_out,
-                                   reinterpret_cast<cudaStream_t>(stream));
+                                   rot, mul, interleaved, norm, q_out, reinterpret_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+w4v_status rope_append(const w4v_kv_t *kv, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                       long long q_stride, long long k_stride, long long v_stride, int n_tokens, int q_heads,
+                       const int32_t *positions, const uint64_t *phases, int rot, float mul, unsigned flags,
+                       uint16_t *q_out, w4v_stream_t stream) {
+    if ((flags & ~unsigned(W4V_ROPE_INTERLEAVED)) != 0u) return W4V_ERR_ARG;
+    return append(kv, q, k, v, q_stride, k_stride, v_stride, n_tokens, q_heads, nullptr, positions, phases, rot, mul,
+                  (flags & W4V_ROPE_INTERLEAVED) != 0u, q_out, stream);
+}
+
+w4v_status norm_rope_append(const w4v_kv_t *kv, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                            long long q_stride, long long k_stride, long long v_stride, int n_tokens, int q_heads,
+                            const uint16_t *q_weight, const uint16_t *k_weight, float eps, const int32_t *positions,
+                            const uint64_t *phases, int rot, float mul, unsigned flags, uint16_t *q_out,
+                            w4v_stream_t stream) {
+    if ((flags & ~unsigned(W4V_ROPE_INTERLEAVED | W4V_NORM_ZERO_CENTRED)) != 0u) return W4V_ERR_ARG;
+    const w4v::HeadNorm norm{q_weight, k_weight, eps, (flags & W4V_NORM_ZERO_CENTRED) != 0u};
+    return append(kv, q, k, v, q_stride, k_stride, v_stride, n_tokens, q_heads, &norm, positions, phases, rot, mul,
+                  (flags & W4V_ROPE_INTERLEAVED) != 0u, q_out, stream);
 }
 
 w4v_status rope_phases(int rot, double base, int scaling, const double *params, uint64_t *phases, float *mul_out) {

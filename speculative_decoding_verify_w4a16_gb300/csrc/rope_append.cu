@@ -17,6 +17,14 @@
 // writes its own alone.  The first heads' pieces are on the way while the CTA
 // finds the token's sequence and slot.  (With pairs as items, numbered over
 // the heads, 8192 rows of 24 x 256 took 48.6 us, half of it in divisions.)
+//
+// With norms (norm_rope_append) every head of q and k is first divided by its
+// root mean square and weighted: y = x w / sqrt(mean x^2 + eps).  The pieces of
+// a head lie in neighbouring lanes, so its sum of squares is one butterfly of
+// log2(D / 8) shuffles.  Weight and rotation are both linear in x, so element i
+// becomes r (x_i (w_i c_i) + x_j (w_j s_i)), j its partner: the products in
+// brackets are worked out once per CTA and lie in shared memory by piece, and
+// r, the head's factor, multiplies last.
 #include <algorithm>
 
 #include "runtime.h"
@@ -34,6 +42,8 @@ struct Args {
     int n_tokens, q_heads, kv_heads, head_dim, rot;
     int B, table_width, n_pages, page_bits;      // 2^page_bits tokens a page
     float mul;
+    const __half *q_weight, *k_weight;           // norms: [head_dim] or null (all ones)
+    float eps, centre;                           // centre: added to the weights
 };
 
 union Piece {
@@ -162,15 +172,195 @@ rope_append_kernel(const Args p) {
     }
 }
 
+// The sums of a head's squares, lane by lane in, in every lane of the head out
+// (`lanes` neighbouring lanes, a power of two).
+template <int n>
+__device__ __forceinline__ void head_sums(float (&x)[n], int lanes) {
+#pragma unroll 1
+    for (int d = 1; d < lanes; d <<= 1)
+#pragma unroll
+        for (int u = 0; u < n; ++u) x[u] += __shfl_xor_sync(0xFFFFFFFFu, x[u], d);
+}
+
+// The same with norms.  kVec as above; without it a warp takes a head, pair by pair.
+template <bool kInter, bool kVec, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+norm_rope_append_kernel(const Args p) {
+    // Element i of q (0) or k (1) is r (x_i coef.x + x_partner coef.y); elements
+    // 2j and 2j + 1 of piece c lie in coef[.][j][c].
+    __shared__ float4 coef[2][4][32];
+    __shared__ int seq;
+    const int t = blockIdx.x, D = p.head_dim, tid = threadIdx.x;
+    if (tid == 0) seq = -1;
+    grid_dep_wait();
+    grid_dep_launch();
+    const __half *qs = p.q + t * p.q_stride, *ks = p.k + t * p.k_stride, *vs = p.v + t * p.v_stride;
+    const int e = 8 * (tid & (D / 8 - 1)), first = tid / (D / 8), step = kThreads / (D / 8);
+    const int turned = p.q_heads + p.kv_heads, heads = turned + p.kv_heads;
+    const bool turn = e < p.rot;
+    const int partner = e >= p.rot / 2 ? -p.rot / 2 : p.rot / 2;
+    Piece a[kAhead], z[kAhead];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int h = h0 + u * step;
+            a[u].u = z[u].u = make_uint4(0u, 0u, 0u, 0u);
+            if (h >= heads) continue;
+            const __half *src = (h < p.q_heads ? qs + h * D : h < turned ? ks + (h - p.q_heads) * D : vs + (h - turned) * D) + e;
+            a[u].u = *reinterpret_cast<const uint4 *>(src);
+            if (!kInter && turn && h < turned) z[u].u = *reinterpret_cast<const uint4 *>(src + partner);
+        }
+    };
+    if (kVec) load(first);
+
+    // This thread's pairs (then single elements) f, g and their weights of q and k
+    constexpr int kItems = 256 / kThreads;
+    const int pairs = p.rot / 2, items = D - pairs;
+    auto places = [&](int i, int &f, int &g) {
+        f = i >= pairs ? pairs + i : kInter ? 2 * i : i;
+        g = i >= pairs ? f : kInter ? f + 1 : f + pairs;
+    };
+    float w[kItems][2][2];
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+        int f, g;
+        places(min(tid + n * kThreads, items - 1), f, g);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const __half *src = x == 0 ? p.q_weight : p.k_weight;
+            w[n][x][0] = src != nullptr ? __half2float(src[f]) + p.centre : 1.f;
+            w[n][x][1] = src != nullptr ? __half2float(src[g]) + p.centre : 1.f;
+        }
+    }
+    __syncthreads();
+    for (int b = tid; b < p.B; b += kThreads)
+        if (p.offsets[b] <= t && t < p.offsets[b + 1]) seq = b;
+    __syncthreads();
+    const int b = seq;
+    if (b < 0) return;
+    const int end = min(p.offsets[b + 1], p.n_tokens);
+    const int cap = p.table_width << p.page_bits, last = (1 << p.page_bits) - 1;
+    const int at = min(max(p.lengths[b], 0), cap) - end + t;      // may be negative: the row has no slot
+    const int pos = p.positions != nullptr ? p.positions[t] : at;
+    auto at_element = [&](int x, int i) -> float2 & {
+        return reinterpret_cast<float2 *>(&coef[x][i / 2 & 3][i / 8])[i & 1];
+    };
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+        const int i = tid + n * kThreads;
+        if (i >= items) continue;
+        int f, g;
+        places(i, f, g);
+        float s = 0.f, c = 1.f;
+        if (i < pairs) {
+            const uint32_t part = uint32_t((uint64_t(int64_t(pos)) * p.phases[i]) >> 32);
+            sincospif(float(int32_t(part)) * (1.f / 2147483648.f), &s, &c);   // 2 pi part / 2^32
+            s *= p.mul;
+            c *= p.mul;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (i < pairs) at_element(x, g) = make_float2(w[n][x][1] * c, w[n][x][0] * s);
+            at_element(x, f) = make_float2(w[n][x][0] * c, -w[n][x][1] * s);
+        }
+    }
+    long long slot = -1;                                         // head 0's elements of this token
+    if (at >= 0) {
+        const int id = p.table[size_t(b) * p.table_width + (at >> p.page_bits)];
+        if (id >= 0 && id < p.n_pages) slot = (((long long)id * p.kv_heads << p.page_bits) + (at & last)) * D;
+    }
+    const long long hop = (long long)D << p.page_bits;           // from head to head within a page
+    __half *qd = p.q_out + size_t(t) * p.q_heads * D;
+    const float mean = 1.f / float(D);                           // D is a power of two
+    __syncthreads();
+
+    if (kVec) {
+        for (int h0 = first, pass = 0; pass * kAhead * step < heads; h0 += kAhead * step, ++pass) {
+            if (pass > 0) {
+                load(h0);
+                __syncthreads();                                 // q_out may be q: both partners read before either is written
+            }
+            float sum[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                sum[u] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 x = __half22float2(a[u].h[i]);
+                    sum[u] = fmaf(x.x, x.x, fmaf(x.y, x.y, sum[u]));
+                }
+            }
+            head_sums(sum, D / 8);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int h = h0 + u * step;
+                if (h >= heads || (h >= p.q_heads && slot < 0)) continue;
+                __half *dst = (h < p.q_heads ? qd + h * D
+                                             : h < turned ? p.k_cache + slot + (h - p.q_heads) * hop
+                                                          : p.v_cache + slot + (h - turned) * hop) + e;
+                if (h < turned) {
+                    const float r = rsqrtf(sum[u] * mean + p.eps);
+                    Piece o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 m = coef[h < p.q_heads ? 0 : 1][i][e / 8];
+                        const float2 x = __half22float2(a[u].h[i]);
+                        const float2 y = kInter ? make_float2(x.y, x.x) : __half22float2(z[u].h[i]);
+                        // (elements from rot on have no partner: its factor 0 must not meet an infinity of its own)
+                        o.h[i] = turn ? __floats2half2_rn((x.x * m.x + y.x * m.y) * r, (x.y * m.z + y.y * m.w) * r)
+                                      : __floats2half2_rn(x.x * m.x * r, x.y * m.z * r);
+                    }
+                    a[u].u = o.u;
+                }
+                *reinterpret_cast<uint4 *>(dst) = a[u].u;
+            }
+        }
+    } else {
+        const int warp = tid / 32, lane = tid & 31;
+        for (int h = warp; h < p.q_heads + (slot >= 0 ? p.kv_heads : 0); h += kThreads / 32) {
+            const bool isq = h < p.q_heads;
+            const __half *src = isq ? qs + h * D : ks + (h - p.q_heads) * D;
+            __half *dst = isq ? qd + h * D : p.k_cache + slot + (h - p.q_heads) * hop;
+            float sum[1] = {0.f};
+            if (lane < D / 8) {
+                Piece x;
+                x.u = *reinterpret_cast<const uint4 *>(src + 8 * lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 y = __half22float2(x.h[i]);
+                    sum[0] = fmaf(y.x, y.x, fmaf(y.y, y.y, sum[0]));
+                }
+            }
+            head_sums(sum, 32);
+            const float r = rsqrtf(sum[0] * mean + p.eps);
+            for (int i = lane; i < items; i += 32) {
+                int f, g;
+                places(i, f, g);
+                const float2 m = at_element(isq ? 0 : 1, f);
+                const float x = __half2float(src[f]), y = __half2float(src[g]);
+                if (i < pairs) {
+                    const float2 l = at_element(isq ? 0 : 1, g);
+                    dst[g] = __float2half_rn((y * l.x + x * l.y) * r);
+                }
+                dst[f] = __float2half_rn(i < pairs ? (x * m.x + y * m.y) * r : x * m.x * r);
+            }
+        }
+        if (slot >= 0)
+            for (int h = first; h < p.kv_heads; h += step)
+                *reinterpret_cast<uint4 *>(p.v_cache + slot + h * hop + e) = *reinterpret_cast<const uint4 *>(vs + h * D + e);
+    }
+}
+
 // CTAs of 256 threads for a few tokens, of 128 for many, where twice as many
 // tokens side by side count for more than each one's own time (one GB300: 16
 // rows of 28 x 128 2.8 against 3.1 us, 8192 rows of 24 x 256 39.7 against
 // 34.8 us, 5.8 TB/s; measured at these two ends, not where they cross).
 template <bool kInter, bool kVec>
-w4v_status launch(const Args &a, int sms, cudaStream_t stream) {
+w4v_status launch(const Args &a, bool norm, int sms, cudaStream_t stream) {
     const bool many = a.n_tokens >= 16 * sms;
-    if (launch_pdl(many ? rope_append_kernel<kInter, kVec, 128> : rope_append_kernel<kInter, kVec, 256>,
-                   dim3(a.n_tokens), dim3(many ? 128 : 256), 0, stream, a) != cudaSuccess) {
+    const auto kernel = norm ? many ? norm_rope_append_kernel<kInter, kVec, 128> : norm_rope_append_kernel<kInter, kVec, 256>
+                             : many ? rope_append_kernel<kInter, kVec, 128> : rope_append_kernel<kInter, kVec, 256>;
+    if (launch_pdl(kernel, dim3(a.n_tokens), dim3(many ? 128 : 256), 0, stream, a) != cudaSuccess) {
         cudaGetLastError();
         return W4V_ERR_CUDA;
     }
@@ -182,7 +372,7 @@ w4v_status launch(const Args &a, int sms, cudaStream_t stream) {
 w4v_status launch_rope_append(const w4v_kv_t &kv, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                               long long q_stride, long long k_stride, long long v_stride, int n_tokens, int q_heads,
                               const int32_t *positions, const uint64_t *phases, int rot, float mul, bool interleaved,
-                              uint16_t *q_out, cudaStream_t stream) {
+                              const HeadNorm *norm, uint16_t *q_out, cudaStream_t stream) {
     const DeviceInfo *info = nullptr;
     w4v_status st = device_info(&info);
     if (st != W4V_OK) return st;
@@ -212,8 +402,14 @@ w4v_status launch_rope_append(const w4v_kv_t &kv, const uint16_t *q, const uint1
     a.page_bits = 0;
     while (1 << a.page_bits < kv.page) ++a.page_bits;
     a.mul = mul;
-    if (interleaved) return rot % 8 == 0 ? launch<true, true>(a, info->sm_count, stream) : launch<true, false>(a, info->sm_count, stream);
-    return rot % 16 == 0 ? launch<false, true>(a, info->sm_count, stream) : launch<false, false>(a, info->sm_count, stream);
+    a.q_weight = norm != nullptr ? reinterpret_cast<const __half *>(norm->q_weight) : nullptr;
+    a.k_weight = norm != nullptr ? reinterpret_cast<const __half *>(norm->k_weight) : nullptr;
+    a.eps = norm != nullptr ? norm->eps : 0.f;
+    a.centre = norm != nullptr && norm->zero_centred ? 1.f : 0.f;
+    const bool whole = rot % (interleaved ? 8 : 16) == 0, n = norm != nullptr;
+    const int sms = info->sm_count;
+    if (interleaved) return whole ? launch<true, true>(a, n, sms, stream) : launch<true, false>(a, n, sms, stream);
+    return whole ? launch<false, true>(a, n, sms, stream) : launch<false, false>(a, n, sms, stream);
 }
 
 }  // namespace w4v

@@ -149,10 +149,16 @@ w4v_status launch_spec_accept(const int32_t *target, const int32_t *draft, int B
                               int32_t *n_accepted, int32_t *out_tokens, cudaStream_t stream);
 
 // Paged key/value cache: rotary positions and appending, attention, pages.
+// Norms of q's and k's heads (weights [head_dim], null: all ones).
+struct HeadNorm {
+    const uint16_t *q_weight, *k_weight;
+    float eps;
+    bool zero_centred;         // 1 is added to the weights
+};
 w4v_status launch_rope_append(const w4v_kv_t &kv, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                               long long q_stride, long long k_stride, long long v_stride, int n_tokens, int q_heads,
                               const int32_t *positions, const uint64_t *phases, int rot, float mul, bool interleaved,
-                              uint16_t *q_out, cudaStream_t stream);
+                              const HeadNorm *norm, uint16_t *q_out, cudaStream_t stream);
 // Largest query heads per key/value head (a tile's 128 rows hold one token's).
 constexpr int kAttnMaxGroup = 128;
 size_t paged_attn_ws_bytes(int n_tokens, int B, int q_heads, int kv_heads, int head_dim, int max_context,

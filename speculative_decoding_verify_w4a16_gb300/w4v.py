@@ -119,6 +119,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             L, F, U = ctypes.c_longlong, ctypes.c_float, ctypes.c_uint
             lib.rope_append.argtypes = [P, P, P, P, L, L, L, I, I, P, P, I, F, U, P, P]
             lib.rope_append.restype = I
+            lib.norm_rope_append.argtypes = [P, P, P, P, L, L, L, I, I, P, P, F, P, P, I, F, U, P, P]
+            lib.norm_rope_append.restype = I
             lib.rope_phases.argtypes = [I, ctypes.c_double, I, P, P, P]
             lib.rope_phases.restype = I
             lib.paged_attn_workspace_bytes.argtypes = [I, I, I, I, I, I, U]
@@ -443,6 +445,7 @@ def gdn_commit(state, k, v, alpha, beta, n_accepted, stream=None):
 
 # ---------------------------------------------------------------- paged cache --
 ROPE_INTERLEAVED = 4
+NORM_ZERO_CENTRED = 8
 ROPE_SCALINGS = {"linear": (1, 1), "ntk": (2, 1), "yarn": (3, 4), "banded": (4, 4)}
 
 
@@ -474,6 +477,24 @@ class Rope:
         self.phases = torch.from_numpy(phases.view(np.int64)).to(device)
 
 
+class HeadNorm:
+    """Norms of every query and key head (norm_rope_append): fp16 [head_dim] weights on the device (None: no
+    weights), eps, and whether 1 is to be added to the weights."""
+
+    def __init__(self, q_weight=None, k_weight=None, eps: float = 1e-6, zero_centred: bool = False):
+        import torch
+        if not (eps >= 0 and math.isfinite(eps)):
+            raise W4VError(ERR_ARG, "HeadNorm")
+        for w in (q_weight, k_weight):
+            if w is None:
+                continue
+            if w.dim() != 1:
+                raise W4VError(ERR_SHAPE, "HeadNorm")
+            if w.dtype is not torch.float16 or not w.is_contiguous():
+                raise W4VError(ERR_ARG, "HeadNorm")
+        self.q_weight, self.k_weight, self.eps, self.zero_centred = q_weight, k_weight, float(eps), bool(zero_centred)
+
+
 # What these calls check of their tensors costs as much as their smallest
 # kernels run, so the types are looked up once and nothing is imported per call.
 _HALF = _INT32 = _FLOAT = None
@@ -481,7 +502,8 @@ _HALF = _INT32 = _FLOAT = None
 
 def _types():
     import torch
-    global _HALF, _INT32, _FLOAT
+    global _HALF, _INT32, _FLOAT, _torch
+    _torch = torch
     _HALF, _INT32, _FLOAT = torch.float16, torch.int32, torch.float32
 
 
@@ -494,6 +516,21 @@ def _i32(t, where, shape):
     if t.dtype is not _INT32 or not t.is_contiguous():
         raise W4VError(ERR_ARG, where)
     return t.data_ptr()
+
+
+def _same_device(where, first, *others):
+    """Everything on the GPU that is current (the library launches there)."""
+    at = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != at:
+            raise W4VError(ERR_ARG, where)
+    if at < 0 or at != _torch_device():
+        raise W4VError(ERR_ARG, where)
+
+
+def _torch_device():
+    cuda = _torch.cuda
+    return _torch._C._cuda_getDevice() if cuda.is_initialized() else cuda.current_device()
 
 
 def _rows(t, where, n, heads, head_dim):
@@ -557,6 +594,33 @@ def rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: Rope, 
                               _rows(k, where, n, heads, D), _rows(v, where, n, heads, D), n, Hq,
                               _i32(positions, where, (n,)), rope.phases.data_ptr(), rope.rot, rope.mul,
                               ROPE_INTERLEAVED if rope.interleaved else 0, q_out.data_ptr(), _stream(stream))
+    if code != OK:
+        raise W4VError(code, where)
+    return q_out
+
+
+def norm_rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: Rope, norm: HeadNorm, q_out=None,
+                     positions=None, stream=None):
+    """rope_append with every query and key head normed first (root mean square, weights of `norm`), in the
+    same pass: nothing is rounded between the norm and the rotation."""
+    where = "norm_rope_append"
+    kv, _, _, heads, _, D = _kv(where, k_cache, v_cache, table, lengths, offsets)
+    shape = q.shape
+    if len(shape) != 3:
+        raise W4VError(ERR_SHAPE, where)
+    n, Hq, _ = shape
+    wq, wk = norm.q_weight, norm.k_weight
+    if (wq is not None and wq.shape[0] != D) or (wk is not None and wk.shape[0] != D):
+        raise W4VError(ERR_SHAPE, where)
+    strides = _rows(q, where, n, Hq, D), _rows(k, where, n, heads, D), _rows(v, where, n, heads, D)
+    pos = _i32(positions, where, (n,))
+    _same_device(where, q, k, v, k_cache, v_cache, table, lengths, offsets, rope.phases, wq, wk, q_out, positions)
+    q_out = _dense_out(q_out, where, q, shape, stream)
+    code = load().norm_rope_append(kv, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, n, Hq,
+                                   None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(),
+                                   norm.eps, pos, rope.phases.data_ptr(), rope.rot, rope.mul,
+                                   (ROPE_INTERLEAVED if rope.interleaved else 0) |
+                                   (NORM_ZERO_CENTRED if norm.zero_centred else 0), q_out.data_ptr(), _stream(stream))
     if code != OK:
         raise W4VError(code, where)
     return q_out

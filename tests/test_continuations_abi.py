@@ -1,0 +1,77 @@
+"""What the entry points for continuations of one prompt refuse, before anything is launched (no GPU: every
+call here with fake pointers fails validation or is a no-op), and the binding's own checks of tensors."""
+import pytest
+import torch
+
+FAKE = 0x10000
+BIG = 1 << 40
+
+
+def _kv(w, **kw):
+    d = dict(k=FAKE, v=FAKE, table=FAKE, lengths=FAKE, offsets=FAKE, B=2, table_width=10, n_pages=40, kv_heads=4,
+             page=16, head_dim=128)
+    d.update(kw)
+    return w._KV.pack(*(x or 0 for x in d.values()))
+
+
+KV_FAULTS = [(dict(page=12), "SHAPE"), (dict(head_dim=96), "SHAPE"), (dict(B=-1), "SHAPE"), (dict(table_width=0), "SHAPE"),
+             (dict(n_pages=0), "SHAPE"), (dict(kv_heads=0), "SHAPE"), (dict(table_width=1 << 27), "SHAPE"),
+             (dict(n_pages=1 << 30), "SHAPE"), (dict(k=None), "ARG"), (dict(v=None), "ARG"), (dict(table=None), "ARG"),
+             (dict(lengths=None), "ARG"), (dict(offsets=None), "ARG"), (dict(k=FAKE + 8), "ALIGN"),
+             (dict(v=FAKE + 2), "ALIGN"), (dict(table=FAKE + 2), "ALIGN"), (dict(offsets=FAKE + 1), "ALIGN")]
+
+
+def norm_rope(w, kv=None, q=FAKE, k=FAKE, v=FAKE, qs=2560, ks=512, vs=512, n=8, heads=20, wq=FAKE, wk=None, eps=1e-6,
+              pos=None, ph=FAKE, rot=128, flags=0, out=FAKE + 4096):
+    return w.load().norm_rope_append(_kv(w) if kv is None else kv, q, k, v, qs, ks, vs, n, heads, wq, wk, eps, pos, ph,
+                                     rot, 1.0, flags, out, None)
+
+
+@pytest.mark.parametrize("kw,code", KV_FAULTS)
+def test_cache_refusals(w4v_mod, kw, code):
+    assert norm_rope(w4v_mod, kv=_kv(w4v_mod, **kw)) == getattr(w4v_mod, "ERR_" + code)
+
+
+def test_norm_rope_refusals(w4v_mod):
+    w = w4v_mod
+    call = lambda **kw: norm_rope(w, **kw)  # noqa: E731
+    assert w.load().norm_rope_append(None, FAKE, FAKE, FAKE, 2560, 512, 512, 8, 20, FAKE, FAKE, 1e-6, None, FAKE, 128,
+                                     1.0, 0, FAKE, None) == w.ERR_ARG
+    assert call(rot=129) == call(rot=130) == call(rot=-2) == call(n=-1) == call(heads=0) == w.ERR_SHAPE
+    assert call(qs=2558) == call(ks=504) == call(vs=516) == w.ERR_SHAPE
+    assert call(flags=2) == call(flags=1) == call(flags=16) == w.ERR_ARG
+    assert call(q=None) == call(k=None) == call(v=None) == call(out=None) == call(ph=None) == w.ERR_ARG
+    assert call(eps=-1e-6) == call(eps=float("nan")) == call(eps=float("inf")) == w.ERR_ARG
+    assert call(qs=5120, out=FAKE) == w.ERR_ARG                       # in place needs dense rows
+    assert call(q=FAKE + 2) == call(v=FAKE + 8) == call(ph=FAKE + 4) == call(pos=FAKE + 2) == w.ERR_ALIGN
+    assert call(wq=FAKE + 2) == call(wk=FAKE + 8) == w.ERR_ALIGN
+    assert call(n=0, q=None, out=None) == call(kv=_kv(w, B=0), q=None) == w.OK
+
+
+def _tensors():
+    h, i = torch.float16, torch.int32
+    return dict(k=torch.zeros(4, 2, 16, 64, dtype=h), table=torch.zeros(2, 3, dtype=i), lens=torch.zeros(2, dtype=i),
+                offs=torch.zeros(3, dtype=i), q=torch.zeros(5, 4, 64, dtype=h), kn=torch.zeros(5, 2, 64, dtype=h))
+
+
+def _code(w, f, *a, **kw):
+    with pytest.raises(w.W4VError) as e:
+        f(*a, **kw)
+    return e.value.code
+
+
+def test_binding_refuses_norm_tensors(w4v_mod):
+    w, t = w4v_mod, _tensors()
+    rope, norm, cache = w.Rope(64, device="cpu"), w.HeadNorm(), (t["k"], t["k"], t["table"], t["lens"], t["offs"])
+    code = lambda *a, **kw: _code(w, w.norm_rope_append, *a, **kw)  # noqa: E731
+    q, kn = t["q"], t["kn"]
+    assert code(q, kn, kn[:4], *cache, rope, norm) == code(q[0], kn, kn, *cache, rope, norm) == w.ERR_SHAPE
+    assert code(q, kn.float(), kn, *cache, rope, norm) == w.ERR_ARG
+    assert code(q, kn, kn, *cache, rope, norm, positions=torch.zeros(5)) == w.ERR_ARG
+    assert code(q, kn, kn, *cache, rope, w.HeadNorm(torch.zeros(32, dtype=torch.float16))) == w.ERR_SHAPE
+    assert code(q, kn, kn, *cache, rope, w.HeadNorm(None, torch.zeros(128, dtype=torch.float16))) == w.ERR_SHAPE
+    assert code(q, kn, kn, *cache, rope, norm) == w.ERR_ARG            # tensors of the host
+    assert _code(w, w.HeadNorm, torch.zeros(64)) == _code(w, w.HeadNorm, eps=-1.0) == w.ERR_ARG
+    assert _code(w, w.HeadNorm, eps=float("nan")) == w.ERR_ARG
+    assert _code(w, w.HeadNorm, torch.zeros(1, 64, dtype=torch.float16)) == w.ERR_SHAPE
+    assert _code(w, w.HeadNorm, None, torch.zeros(128, dtype=torch.float16)[::2]) == w.ERR_ARG

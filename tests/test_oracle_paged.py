@@ -82,3 +82,12 @@ def test_pool_by_hand():
     p.compact()                                                      # three live: page 3 -> 2
     assert p.table[2].tolist() == [0, 2, -1, -1] and p.refs.tolist() == [1, 1, 1, 0, 0, 0] and p.pool[0, 2, 0] == 1
     assert p.fork([0, 0], [1, 1]) == -1 and p.fork([0], [2]) == -1 and p.fork([0], [3]) == -1
+
+
+def test_head_norm_by_hand():
+    """3 and 4 of a head of four: mean square 25 / 4; weights and what is added to them multiply; zeros stay."""
+    x = np.zeros((1, 2, 4), np.float16)
+    x[0, 0, :2] = 3, 4
+    assert np.allclose(paged.head_norm(x, eps=0.0 + 1e-300)[0, 0], [1.2, 1.6, 0, 0])
+    assert np.allclose(paged.head_norm(x, [1, 0.5, 1, 1], 1e-300, 1.0)[0, 0], [2.4, 2.4, 0, 0])
+    assert np.allclose(paged.head_norm(x, None, 6.25 * 3)[0, 0], [0.6, 0.8, 0, 0]) and not paged.head_norm(x)[0, 1].any()
