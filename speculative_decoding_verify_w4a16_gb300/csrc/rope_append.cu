@@ -182,9 +182,15 @@ __device__ __forceinline__ void head_sums(float (&x)[n], int lanes) {
         for (int u = 0; u < n; ++u) x[u] += __shfl_xor_sync(0xFFFFFFFFu, x[u], d);
 }
 
-// The same with norms.  kVec as above; without it a warp takes a head, pair by pair.
+// The same with norms.  kVec as above; without it a warp takes a head, pair by
+// pair.  Partner pieces come from their lanes by shuffles: read again from L1
+// they held 12 registers more across the waits, 49.7 us against 44.8 for 8192
+// rows of 24 x 256.  Two heads a thread ahead: 630 rows of 60 x 128 6.9 us
+// (three 7.7, with registers spilled), 16 rows of 28 x 128 2.9 (3.2), 8192 rows
+// 45.2 (44.8).
+constexpr int kNormAhead = 2;
 template <bool kInter, bool kVec, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+__global__ void __launch_bounds__(kThreads, 1280 / kThreads)
 norm_rope_append_kernel(const Args p) {
     // Element i of q (0) or k (1) is r (x_i coef.x + x_partner coef.y); elements
     // 2j and 2j + 1 of piece c lie in coef[.][j][c].
@@ -197,18 +203,17 @@ norm_rope_append_kernel(const Args p) {
     const __half *qs = p.q + t * p.q_stride, *ks = p.k + t * p.k_stride, *vs = p.v + t * p.v_stride;
     const int e = 8 * (tid & (D / 8 - 1)), first = tid / (D / 8), step = kThreads / (D / 8);
     const int turned = p.q_heads + p.kv_heads, heads = turned + p.kv_heads;
-    const bool turn = e < p.rot;
-    const int partner = e >= p.rot / 2 ? -p.rot / 2 : p.rot / 2;
-    Piece a[kAhead], z[kAhead];
+    // The lane that holds the partner piece (half layout), or this one.
+    const int partner = kInter || e >= p.rot ? int(threadIdx.x & 31) : int(threadIdx.x & 31) + (e >= p.rot / 2 ? -p.rot / 16 : p.rot / 16);
+    Piece a[kNormAhead];
     auto load = [&](int h0) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < kNormAhead; ++u) {
             const int h = h0 + u * step;
-            a[u].u = z[u].u = make_uint4(0u, 0u, 0u, 0u);
-            if (h >= heads) continue;
-            const __half *src = (h < p.q_heads ? qs + h * D : h < turned ? ks + (h - p.q_heads) * D : vs + (h - turned) * D) + e;
-            a[u].u = *reinterpret_cast<const uint4 *>(src);
-            if (!kInter && turn && h < turned) z[u].u = *reinterpret_cast<const uint4 *>(src + partner);
+            a[u].u = make_uint4(0u, 0u, 0u, 0u);
+            if (h < heads)
+                a[u].u = *reinterpret_cast<const uint4 *>((h < p.q_heads ? qs + h * D : h < turned ? ks + (h - p.q_heads) * D
+                                                                                                   : vs + (h - turned) * D) + e);
         }
     };
     if (kVec) load(first);
@@ -275,14 +280,11 @@ norm_rope_append_kernel(const Args p) {
     __syncthreads();
 
     if (kVec) {
-        for (int h0 = first, pass = 0; pass * kAhead * step < heads; h0 += kAhead * step, ++pass) {
-            if (pass > 0) {
-                load(h0);
-                __syncthreads();                                 // q_out may be q: both partners read before either is written
-            }
-            float sum[kAhead];
+        for (int h0 = first, pass = 0; pass * kNormAhead * step < heads; h0 += kNormAhead * step, ++pass) {
+            if (pass > 0) load(h0);
+            float sum[kNormAhead];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
+            for (int u = 0; u < kNormAhead; ++u) {
                 sum[u] = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -292,8 +294,14 @@ norm_rope_append_kernel(const Args p) {
             }
             head_sums(sum, D / 8);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
+            for (int u = 0; u < kNormAhead; ++u) {
                 const int h = h0 + u * step;
+                Piece z;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w = h2_as_u32(a[u].h[i]);
+                    z.h[i] = kInter ? __lowhigh2highlow(a[u].h[i]) : u32_as_h2(__shfl_sync(0xFFFFFFFFu, w, partner));
+                }
                 if (h >= heads || (h >= p.q_heads && slot < 0)) continue;
                 __half *dst = (h < p.q_heads ? qd + h * D
                                              : h < turned ? p.k_cache + slot + (h - p.q_heads) * hop
@@ -305,10 +313,8 @@ norm_rope_append_kernel(const Args p) {
                     for (int i = 0; i < 4; ++i) {
                         const float4 m = coef[h < p.q_heads ? 0 : 1][i][e / 8];
                         const float2 x = __half22float2(a[u].h[i]);
-                        const float2 y = kInter ? make_float2(x.y, x.x) : __half22float2(z[u].h[i]);
-                        // (elements from rot on have no partner: its factor 0 must not meet an infinity of its own)
-                        o.h[i] = turn ? __floats2half2_rn((x.x * m.x + y.x * m.y) * r, (x.y * m.z + y.y * m.w) * r)
-                                      : __floats2half2_rn(x.x * m.x * r, x.y * m.z * r);
+                        const float2 y = __half22float2(z.h[i]);
+                        o.h[i] = __floats2half2_rn((x.x * m.x + y.x * m.y) * r, (x.y * m.z + y.y * m.w) * r);
                     }
                     a[u].u = o.u;
                 }
