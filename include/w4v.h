@@ -286,6 +286,36 @@ w4v_status w8_lmhead_argmax_noalloc(const uint16_t *X, const int8_t *W, const ui
                                     int M, int K, int V, int32_t *argmax_out, float *maxlogit,
                                     float *logits_debug, w4v_stream_t stream);
 
+/* --------------------------------------------------------- token_logprobs
+ * What the target thinks of given tokens, from its logits (for instance those
+ * that w8_lmhead_argmax writes): drafts and prompts are scored, continuations
+ * ranked by it.  With z_v = x_v / temperature over a row of V logits x and
+ * lse = ln sum_v exp(z_v),
+ *     logprobs[r][i]     = z_t - lse, t = tokens[r][i] (-inf for a token
+ *                          outside [0, V), such as the -1 of a padded draft);
+ *     entropy[r]         = lse - sum_v p_v z_v, p_v = exp(z_v - lse);
+ *     top_ids[r][j],     = the j-th largest logit's token and its log
+ *     top_logprobs[r][j]   probability, of equal logits the lower token first.
+ * Arithmetic is fp32.  Logits of -inf are tokens that cannot follow (p = 0); a
+ * row of nothing else gives logprobs of -inf and an entropy of 0.  A row that
+ * holds a NaN or +inf gives NaN for every token in [0, V) and for the entropy;
+ * its top_ids count NaN as -inf, as the argmax does.
+ *   logits        device, float rows of V logits (fp16 with W4V_LOGITS_FP16),
+ *                 row_stride >= V elements apart; any address that is a
+ *                 multiple of the element's size
+ *   tokens        device, int32 [M][n] (may be NULL when n == 0)
+ *   logprobs      device, float [M][n] (may be NULL when n == 0)
+ *   entropy       device, float [M] or NULL
+ *   top_ids       device, int32 [M][top] (may be NULL when top == 0)
+ *   top_logprobs  device, float [M][top] (may be NULL when top == 0)
+ * Sizes: 0 <= M <= 2^24 (0 is a no-op), 1 <= V <= 2^28, 0 <= n <= 2^20,
+ * 0 <= top <= 32 and at most V, temperature > 0 and finite (as is its
+ * reciprocal times log2 e).  No workspace. */
+#define W4V_LOGITS_FP16 16u
+w4v_status token_logprobs(const void *logits, long long row_stride, int M, int V, const int32_t *tokens, int n,
+                          float temperature, float *logprobs, float *entropy, int top, int32_t *top_ids,
+                          float *top_logprobs, unsigned flags, w4v_stream_t stream);
+
 /* ----------------------------------------------------------- spec_accept
  * Longest-prefix greedy acceptance for B sequences:
  *   n[b] = the largest j <= K with draft[b][i] == target[b][i] for all i < j,

@@ -20,7 +20,7 @@ OBJ = os.path.join(ROOT, "_build", "w4v")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libw4v.so")
 SOURCES = ("runtime.cu", "api.cpp", "spec_accept.cu", "w4a16_gemm.cu", "w4a16_prefill.cu",
-           "w8_lmhead_argmax.cu", "lmhead_noalloc.cu",
+           "w8_lmhead_argmax.cu", "lmhead_noalloc.cu", "token_logprobs.cu",
            "ngram_draft.cu", "gdn_state.cu",
            "rope_append.cu", "paged_attn.cu", "kv_pages.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -369,6 +369,29 @@ w4v_status spec_accept(const int32_t *target, const int32_t *draft, int B, int K
 
 namespace {
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+}  // namespace
+
+w4v_status token_logprobs(const void *logits, long long row_stride, int M, int V, const int32_t *tokens, int n,
+                          float temperature, float *logprobs, float *entropy, int top, int32_t *top_ids,
+                          float *top_logprobs, unsigned flags, w4v_stream_t stream) {
+    if ((flags & ~unsigned(W4V_LOGITS_FP16)) != 0u) return W4V_ERR_ARG;
+    const bool half = (flags & W4V_LOGITS_FP16) != 0u;
+    if (M < 0 || M > 1 << 24 || V < 1 || V > 1 << 28 || n < 0 || n > 1 << 20 || top < 0 || top > w4v::kLogprobsMaxTop ||
+        top > V || row_stride < V || row_stride >= 1ll << 38)
+        return W4V_ERR_SHAPE;
+    if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.4426951f / temperature)) return W4V_ERR_ARG;
+    if (M == 0) return W4V_OK;
+    if (logits == nullptr || (n > 0 && (tokens == nullptr || logprobs == nullptr)) ||
+        (top > 0 && (top_ids == nullptr || top_logprobs == nullptr)))
+        return W4V_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(logits) & (half ? 1u : 3u)) != 0u || !aligned4(tokens) || !aligned4(logprobs) ||
+        !aligned4(entropy) || !aligned4(top_ids) || !aligned4(top_logprobs))
+        return W4V_ERR_ALIGN;
+    return w4v::launch_token_logprobs(logits, half, row_stride, M, V, tokens, n, temperature, logprobs, entropy, top,
+                                      top_ids, top_logprobs, reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
 bool page_ok(int page) { return page >= 8 && page <= 256 && (page & (page - 1)) == 0; }
 
 // The cache, and the rows that go with it (after n_tokens == 0 returned).

@@ -148,6 +148,12 @@ size_t w8_lmhead_ws_bytes(int M, int V);
 w4v_status launch_spec_accept(const int32_t *target, const int32_t *draft, int B, int K,
                               int32_t *n_accepted, int32_t *out_tokens, cudaStream_t stream);
 
+// Log probabilities: most alternatives a row.
+constexpr int kLogprobsMaxTop = 32;
+w4v_status launch_token_logprobs(const void *logits, bool half, long long stride, int M, int V, const int32_t *tokens,
+                                 int n, float temperature, float *logprobs, float *entropy, int top, int32_t *top_ids,
+                                 float *top_logprobs, cudaStream_t stream);
+
 // Paged key/value cache: rotary positions and appending, attention, pages.
 // Norms of q's and k's heads (weights [head_dim], null: all ones).
 struct HeadNorm {

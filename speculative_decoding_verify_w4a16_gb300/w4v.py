@@ -117,6 +117,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.gdn_step.argtypes = [P, P, P, P, P, P, I, P, P, P, P, P, I, I, I, I, I, P, P]
             lib.gdn_step.restype = I
             L, F, U = ctypes.c_longlong, ctypes.c_float, ctypes.c_uint
+            lib.token_logprobs.argtypes = [P, L, I, I, P, I, F, P, P, I, P, P, U, P]
+            lib.token_logprobs.restype = I
             lib.rope_append.argtypes = [P, P, P, P, L, L, L, I, I, P, P, I, F, U, P, P]
             lib.rope_append.restype = I
             lib.norm_rope_append.argtypes = [P, P, P, P, L, L, L, I, I, P, P, F, P, P, I, F, U, P, P]
@@ -655,6 +657,46 @@ def paged_attn(q, k_cache, v_cache, table, lengths, offsets, scale=None, window:
     code = load().paged_attn(kv, q.data_ptr(), stride, n, Hq, D ** -0.5 if scale is None else scale, int(window),
                              out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
                              BATCH_INVARIANT if batch_invariant else 0, _stream(stream))
+    if code != OK:
+        raise W4VError(code, where)
+    return out
+
+
+LOGITS_FP16 = 16
+
+
+def token_logprobs(logits, tokens=None, top: int = 0, temperature: float = 1.0, out=None, stream=None):
+    """Log probabilities of `tokens` (int32 [M] or [M][n]; -1: none) under softmax(logits / temperature), logits
+    float or fp16 [M][V] (rows may be part of longer ones).  Returns (logprobs as `tokens`, entropy [M],
+    top_ids [M][top], top_logprobs [M][top]), the last two the `top` <= 32 most likely tokens in order.
+    out: the four tensors to fill."""
+    where = "token_logprobs"
+    if _HALF is None:
+        _types()
+    if logits.dim() != 2 or not 0 <= top <= 32:
+        raise W4VError(ERR_SHAPE, where)
+    M, V = logits.shape
+    half = logits.dtype is _HALF
+    if not (half or logits.dtype is _FLOAT) or (M and V > 1 and logits.stride(1) != 1):
+        raise W4VError(ERR_ARG, where)
+    shape = (M, 0) if tokens is None else tuple(tokens.shape)
+    if len(shape) not in (1, 2) or shape[0] != M:
+        raise W4VError(ERR_SHAPE, where)
+    at, n = _i32(tokens, where, shape), shape[1] if len(shape) == 2 else 1
+    if out is None:
+        _same_device(where, logits, tokens)
+        new = lambda shape, dtype: _new(shape, dtype, logits.device, stream)  # noqa: E731
+        out = new(shape, _FLOAT), new(M, _FLOAT), new((M, top), _INT32), new((M, top), _FLOAT)
+    lp, entropy, ids, tops = out
+    for t, s, dtype in ((lp, shape, _FLOAT), (entropy, (M,), _FLOAT), (ids, (M, top), _INT32), (tops, (M, top), _FLOAT)):
+        if t.shape != s:
+            raise W4VError(ERR_SHAPE, where)
+        if t.dtype is not dtype or not t.is_contiguous():
+            raise W4VError(ERR_ARG, where)
+    _same_device(where, logits, tokens, *out)
+    code = load().token_logprobs(logits.data_ptr(), logits.stride(0) if M > 1 else V, M, V, at, n, temperature,
+                                 lp.data_ptr(), entropy.data_ptr(), top, ids.data_ptr(), tops.data_ptr(),
+                                 LOGITS_FP16 if half else 0, _stream(stream))
     if code != OK:
         raise W4VError(code, where)
     return out

@@ -75,3 +75,32 @@ def test_binding_refuses_norm_tensors(w4v_mod):
     assert _code(w, w.HeadNorm, eps=float("nan")) == w.ERR_ARG
     assert _code(w, w.HeadNorm, torch.zeros(1, 64, dtype=torch.float16)) == w.ERR_SHAPE
     assert _code(w, w.HeadNorm, None, torch.zeros(128, dtype=torch.float16)[::2]) == w.ERR_ARG
+
+
+def test_logprob_refusals(w4v_mod):
+    w = w4v_mod
+
+    def call(x=FAKE, stride=1000, M=2, V=1000, t=FAKE, n=1, heat=1.0, lp=FAKE, h=None, top=3, ids=FAKE, tops=FAKE, flags=0):
+        return w.load().token_logprobs(x, stride, M, V, t, n, heat, lp, h, top, ids, tops, flags, None)
+    assert call(M=-1) == call(M=(1 << 24) + 1) == call(V=0) == call(V=(1 << 28) + 1, stride=1 << 30) == w.ERR_SHAPE
+    assert call(n=-1) == call(n=(1 << 20) + 1) == call(top=-1) == call(top=33) == call(top=3, V=2) == w.ERR_SHAPE
+    assert call(stride=999) == call(stride=0) == call(stride=1 << 38) == w.ERR_SHAPE
+    for heat in (0.0, -1.0, float("nan"), float("inf"), 1e-39):
+        assert call(heat=heat) == w.ERR_ARG
+    assert call(flags=1) == call(flags=8) == call(flags=32) == w.ERR_ARG
+    assert call(x=None) == call(t=None) == call(lp=None) == call(ids=None) == call(tops=None) == w.ERR_ARG
+    assert call(x=FAKE + 2) == call(x=FAKE + 1, flags=16) == call(t=FAKE + 2) == call(lp=FAKE + 1) == w.ERR_ALIGN
+    assert call(h=FAKE + 2) == call(ids=FAKE + 2) == call(tops=FAKE + 3) == w.ERR_ALIGN
+    assert call(M=0, x=None, t=None, lp=None, ids=None, tops=None) == w.OK
+
+
+def test_binding_refuses_logprob_tensors(w4v_mod):
+    w, i = w4v_mod, torch.int32
+    x, t = torch.zeros(3, 50), torch.zeros(3, 2, dtype=i)
+    code = lambda *a, **kw: _code(w, w.token_logprobs, *a, **kw)  # noqa: E731
+    out = lambda top: (torch.zeros(3, 2), torch.zeros(3), torch.zeros(3, top, dtype=i), torch.zeros(3, top))  # noqa: E731
+    assert code(x[0], t) == code(x, t[:2]) == code(x, t[None]) == code(x, t, top=33) == code(x, t, top=-1) == w.ERR_SHAPE
+    assert code(x.double(), t) == code(x.t().contiguous().t(), t) == code(x, t.long()) == code(x, t.t().contiguous().t()) == w.ERR_ARG
+    assert code(x, t, top=4, out=out(3)) == w.ERR_SHAPE
+    assert code(x, t, top=3, out=out(3)[:2] + (torch.zeros(3, 3), torch.zeros(3, 3))) == w.ERR_ARG
+    assert code(x, t) == code(x, t, top=3, out=out(3)) == w.ERR_ARG      # tensors of the host

@@ -1,0 +1,200 @@
+"""token_logprobs on the GPU against the oracle (double precision)."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import to_dev
+from oracle import scores
+
+pytestmark = pytest.mark.gpu
+
+
+def logits(rng, M, V, half=False, size=2.0):
+    x = (rng.standard_normal((M, V)) * size).astype(np.float32)
+    x[::2, rng.integers(0, V)] += 9
+    return x.astype(np.float16) if half else x
+
+
+def given(rng, M, V, n):
+    t = rng.integers(0, V, (M, n)).astype(np.int32)
+    if n > 1:
+        t[:, -1] = -1
+    if n > 2:
+        t[:, 1] = V
+    return t
+
+
+def compare(x, tokens, top, temperature, got):
+    lp, h, ids, tops = (t.cpu().numpy() for t in got)
+    lp = lp.reshape(len(x), -1)
+    for r in range(len(x)):
+        want = scores.row(x[r], tokens[r], top, temperature)
+        per, eh = scores.bounds(x[r], temperature)
+        xr = x[r].astype(np.float64)
+        high = np.nanmax(np.where(np.isneginf(xr), np.nan, xr)) if np.isfinite(xr).any() else 0.0
+
+        def near(a, b, logit):
+            b, logit = np.asarray(b, np.float64), np.asarray(logit, np.float64)
+            fin = np.isfinite(b)
+            assert np.array_equal(np.isnan(a), np.isnan(b)) and np.array_equal(a[~fin & ~np.isnan(b)], b[~fin & ~np.isnan(b)])
+            tol = per + 2.0 ** -21 * np.abs(logit[fin] - high) / temperature
+            assert np.all(np.abs(a[fin] - b[fin]) <= tol), (r, float(np.max(np.abs(a[fin] - b[fin]) / tol)))
+        near(lp[r], want[0], [xr[t] if 0 <= t < len(xr) else 0.0 for t in tokens[r]])
+        assert np.array_equal(ids[r], want[2]), (r, ids[r], want[2])
+        near(tops[r], want[3], xr[ids[r]])
+        assert (np.isnan(h[r]) and np.isnan(want[1])) or abs(h[r] - want[1]) <= eh, (r, h[r], want[1], eh)
+
+
+def check(w, gpu, x, tokens, top=5, temperature=1.0, **kw):
+    got = w.token_logprobs(to_dev(x, gpu), to_dev(tokens, gpu), top=top, temperature=temperature, **kw)
+    torch.cuda.synchronize()
+    assert w.get_status() == w.OK
+    compare(x, tokens.reshape(len(x), -1), top, temperature, got)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("V", [1, 2, 3, 4, 5, 7, 8, 9, 31, 100, 127, 128, 129, 511, 1000, 2047, 2048, 2049, 4095, 4096,
+                               4097, 8193, 16385, 20479, 20480, 20481])
+def test_vocabularies_around_vectors_and_pieces(w4v_mod, gpu, half, V):
+    rng = np.random.default_rng([V, half])
+    check(w4v_mod, gpu, logits(rng, 3, V, half), given(rng, 3, V, 3), top=min(V, 20))
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("V", [40961, 81923, 151936, 163840, 163841, 200003, 400001])
+def test_large_vocabularies(w4v_mod, gpu, half, V):
+    """Clusters of every size, and pieces that a CTA takes in turn."""
+    rng = np.random.default_rng([V, half])
+    check(w4v_mod, gpu, logits(rng, 2, V, half), given(rng, 2, V, 4), top=32, temperature=0.7)
+
+
+@pytest.mark.parametrize("M,V", [(400, 1000), (40, 30011), (20, 50257), (160, 21000)])
+def test_many_rows(w4v_mod, gpu, M, V):
+    rng = np.random.default_rng([M, V])
+    check(w4v_mod, gpu, logits(rng, M, V), given(rng, M, V, 1), top=7)
+
+
+@pytest.mark.parametrize("top", [0, 1, 2, 19, 31, 32])
+@pytest.mark.parametrize("temperature", [0.05, 0.5, 1.0, 3.0])
+def test_alternatives_and_temperatures(w4v_mod, gpu, top, temperature):
+    rng = np.random.default_rng(top)
+    check(w4v_mod, gpu, logits(rng, 3, 9001), given(rng, 3, 9001, 2), top=top, temperature=temperature)
+
+
+def shaped_rows(V, half):
+    i = np.arange(V, dtype=np.float64)
+    few = np.full(V, -np.inf)
+    few[[V // 3, V - 1]] = 1.5, 1.5
+    rows = [np.zeros(V), i / V * 30, -i / V * 30, np.where(i % 2 == 0, 1.0, 2.0), np.where(i < V - 3, 1.0, 0.5),
+            np.full(V, -7.0), np.where(i == V - 1, 3.0, -np.inf), few, np.floor(i / V * 10), np.where(i % 97 == 3, 4.0, -1.0),
+            np.where(i % 3 == 0, -0.0, 0.0), np.where(i < 40, 2.0, -np.inf), np.where(i >= V - 40, 2.0, -np.inf),
+            np.where(i % 16 < 4, 20.0 + i / V, 0.0)]
+    return np.stack(rows).astype(np.float16 if half else np.float32)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("V", [50, 700, 5000, 21000, 170001])
+@pytest.mark.parametrize("top", [3, 32])
+def test_ties_orders_and_masks(w4v_mod, gpu, half, V, top):
+    """Rows of one value, of two, in order up and down, with few tokens above -inf, alternatives in a few threads' hands."""
+    x = shaped_rows(V, half)
+    check(w4v_mod, gpu, x, given(np.random.default_rng(1), len(x), V, 2), top=top)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("V", [64, 3001, 25000])
+def test_what_is_not_finite(w4v_mod, gpu, half, V):
+    rng = np.random.default_rng(2)
+    x = logits(rng, 8, V, half)
+    x[0] = -np.inf
+    x[1, V // 2] = np.nan
+    x[2, V - 1] = np.inf
+    x[3] = np.nan
+    x[4, :V - 2] = -np.inf
+    x[5, ::3] = -np.inf
+    x[6, 0], x[6, 1] = np.nan, -np.inf
+    x[7, 1:] = -np.inf
+    check(w4v_mod, gpu, x, given(rng, 8, V, 4), top=32)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e4, 3e37])
+def test_sizes(w4v_mod, gpu, size):
+    """Logits that differ by nothing, by thousands, and by more than fp32 holds."""
+    rng = np.random.default_rng(3)
+    x = np.clip(rng.standard_normal((4, 6001)) * size, -3e38, 3e38).astype(np.float32)
+    check(w4v_mod, gpu, x, given(rng, 4, 6001, 3), top=9)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("off,pad", [(0, 1), (1, 0), (2, 3), (3, 2), (5, 7), (7, 8)])
+def test_rows_anywhere(w4v_mod, gpu, half, off, pad):
+    """Rows that begin on no boundary, of a longer matrix whose other elements are NaN."""
+    rng, M, V = np.random.default_rng([off, pad]), 5, 4501
+    x, t = logits(rng, M, V, half), given(rng, M, V, 2)
+    wide = torch.full((M * (V + pad) + off + 8,), float("nan"), dtype=torch.float16 if half else torch.float32, device=gpu)
+    view = wide[off:off + M * (V + pad)].view(M, V + pad)[:, :V]
+    view.copy_(to_dev(x, gpu))
+    got = w4v_mod.token_logprobs(view, to_dev(t, gpu), top=20)
+    compare(x, t, 20, 1.0, got)
+
+
+def test_rows_past_32_bits(w4v_mod, gpu):
+    """Rows 2^30 elements apart."""
+    rng = np.random.default_rng(4)
+    x, t = logits(rng, 3, 2000, True), given(rng, 3, 2000, 1)
+    big = torch.empty((2 << 30) + 2000, dtype=torch.float16, device=gpu)
+    view = torch.as_strided(big, (3, 2000), (1 << 30, 1))
+    view.copy_(to_dev(x, gpu))
+    compare(x, t, 4, 1.0, w4v_mod.token_logprobs(view, to_dev(t, gpu), top=4))
+
+
+def test_forms_of_a_call(w4v_mod, gpu):
+    """Tokens as a vector, none at all, results into given tensors, no rows; the same bits every time."""
+    rng, w = np.random.default_rng(5), w4v_mod
+    x = logits(rng, 6, 30000)
+    d, t = to_dev(x, gpu), to_dev(given(rng, 6, 30000, 1), gpu)
+    a = w.token_logprobs(d, t[:, 0].contiguous(), top=8)
+    assert a[0].shape == (6,) and a[2].shape == (6, 8)
+    b = w.token_logprobs(d, t, top=8)
+    for _ in range(5):
+        out = tuple(torch.full_like(y, 3) for y in b)
+        assert w.token_logprobs(d, t, top=8, out=out) is out
+        assert all(torch.equal(p, q) for p, q in zip(b, out))
+    assert torch.equal(a[0], b[0][:, 0]) and all(torch.equal(p, q) for p, q in zip(a[1:], b[1:]))
+    none = w.token_logprobs(d)
+    assert none[0].shape == (6, 0) and none[2].shape == (6, 0) and torch.equal(none[1], b[1])
+    empty = w.token_logprobs(d[:0], t[:0], top=8)
+    assert [tuple(y.shape) for y in empty] == [(0, 1), (0,), (0, 8), (0, 8)]
+
+
+def test_another_stream_and_graph_replay(w4v_mod, gpu):
+    rng, w = np.random.default_rng(6), w4v_mod
+    x, t = logits(rng, 4, 12345), given(rng, 4, 12345, 2)
+    d, dt = to_dev(x, gpu), to_dev(t, gpu)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = w.token_logprobs(d, dt, top=5, stream=s)
+    s.synchronize()
+    compare(x, t, 5, 1.0, got)
+    out = tuple(torch.empty_like(y) for y in got)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w.token_logprobs(d, dt, top=5, out=out)
+    x2 = logits(rng, 4, 12345)
+    d.copy_(to_dev(x2, gpu))
+    g.replay()
+    torch.cuda.synchronize()
+    compare(x2, t, 5, 1.0, out)
+
+
+def test_scores_of_the_lm_head(w4v_mod, gpu):
+    """The verify step's own logits: the argmax is the first alternative."""
+    rng, w = np.random.default_rng(7), w4v_mod
+    X = to_dev(rng.standard_normal((16, 256)).astype(np.float16), gpu)
+    W8 = to_dev(rng.integers(-127, 128, (4096, 256)).astype(np.int8), gpu)
+    s8 = to_dev((rng.random(4096) * 0.002).astype(np.float16), gpu)
+    x = torch.empty((16, 4096), dtype=torch.float32, device=gpu)
+    best = w.w8_lmhead_argmax(X, W8, s8, logits=x)
+    got = w.token_logprobs(x, best, top=3)
+    assert torch.equal(got[2][:, 0], best) and torch.equal(got[3][:, 0], got[0])
+    compare(x.cpu().numpy(), best.cpu().numpy()[:, None], 3, 1.0, got)
