@@ -1,25 +1,34 @@
 // token_logprobs.cu -- log probabilities of given tokens, the rows' entropy
 // and their most likely tokens, from the lm_head's logits.
 //
-// With d_v = x_v - m, m a row's largest logit, and h = 1 / temperature,
+// With d_v = x_v - m, m a reference near a row's largest logit, and h = 1 /
+// temperature,
 //     s = sum_v e^(h d_v),  t = sum_v d_v e^(h d_v):
-//     log p_v = h d_v - ln s,   entropy = ln s - h t / s
-// (both terms of the entropy are positive, so nothing cancels).  One pass:
-// the logits are read once, into registers, 40 a thread.  A thread takes its
-// own largest one as reference, so the powers need no wait; s and t are brought
-// to a common reference by 2^(h (m_thread - m)), t as w (t + (m_thread - m) s).
+//     log p_v = h d_v - ln s,   entropy = ln s - h t / s.
+// One pass: each logit is read once.  A thread has its own reference, the
+// largest of its first 16 logits, which it raises (s and t rescaled) when a
+// logit is more than a factor 2^kSlack above it, so nothing waits for a
+// maximum, and ln s stays so small that log probabilities near 0 keep their
+// digits.  The references meet at the end: t becomes w (t + (m - m') s).
 //
-// A row is cut over the CTAs of a cluster, each of which holds its piece whole
-// (up to 20,480 logits), and joined by the first one through distributed shared
-// memory: no workspace, no second launch, no atomics between CTAs.
+// A row is one CTA's, or with few rows cut over the CTAs of a cluster, joined
+// by the first of them through distributed shared memory: no workspace, no
+// second launch, no atomics between CTAs.
 //
-// The `top` largest, ties to the lower index, without sorting: 128 groups of
-// four threads have a largest logit each, and the top-th largest of those is a
-// bound that at least `top` logits reach and few exceed (31 groups' at most:
-// 4960, but some 25 where logits lie without order).  Those are collected and
-// each counts how many are above it.  Logits equal to the bound that are too many to
-// collect, and those of a row that has fewer than `top` tokens above -inf, are
-// taken in order of their index by a scan.
+// The `top` largest, ties to the lower index, without sorting.  The CTA's first
+// 8192 logits: 128 groups of four threads have a largest logit each, and the
+// top-th largest of those is a bound that at least `top` logits reach and few
+// exceed (31 groups' at most, 1984; some 25 where logits lie without order).
+// From then on a thread looks whether its 16 next logits' largest, which it has
+// anyway, is above the bound, and collects those that are (a logit equal to the
+// bound comes too late, by its index).  In no order they are some 20 times
+// `top` of 151,936; the same groups' bound thins them out, and what is left
+// counts how many are above it.  Where more come than there is room for (a row
+// in ascending order), the row is gone through once more, 8192 logits at a time.
+//
+// What bounds it: the bytes.  Per 16 logits 8 maxima, 16 powers, 56 other
+// operations, and the powers at 16 a clock and SM take a third of the time
+// that 4-byte logits take from HBM.
 #include <climits>
 
 #include "runtime.h"
@@ -29,13 +38,15 @@ namespace w4v {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kHeldLogits = 40;                 // of a thread
-constexpr int kPiece = kThreads * kHeldLogits;  // of a CTA at a time
+constexpr int kBatch = 16;                      // logits of a thread that are looked at together
+constexpr int kLoads = 8;                       // 16-byte loads of a thread in flight
+constexpr float kSlack = 2.f;
 constexpr int kGroups = 128, kGroupLanes = kThreads / kGroups;
 constexpr int kMost = kLogprobsMaxTop;
-constexpr int kAbove = 4960, kTies = 512;       // keys that are collected: above the bound, equal to it
-static_assert((kMost - 1) * kGroupLanes * kHeldLogits <= kAbove, "every logit of the groups above the bound fits");
-static_assert(kMost <= kGroups, "the bound is a group's largest logit");
+constexpr int kList = 4096, kTies = 512, kFew = 1024;
+static_assert((kMost - 1) * kGroupLanes * kBatch + kTies + kMost <= kList, "what a batch adds to the list fits");
+static_assert(kMost * kGroupLanes * (kList / kThreads) <= kFew, "what the groups' bound leaves of a list fits");
+static_assert(kMost <= kGroups, "the bound is a group's largest");
 constexpr int kMaxCluster = 8;
 
 struct Args {
@@ -46,6 +57,7 @@ struct Args {
     int32_t *top_ids;
     int V, n, top, cluster_bits;
     float heat, heat_log2;                      // 1 / temperature, and times log2(e)
+    float slack;                                // kSlack in units of the logits
 };
 
 // Larger for a larger logit, then for a lower index; NaN counts as -inf and -0
@@ -88,20 +100,23 @@ __device__ __forceinline__ Sums join(const Sums &a, const Sums &b, float heat_lo
 }
 
 struct __align__(8) Shared {
-    uint64_t above[kAbove], ties[kTies + kMost];
-    uint64_t best[kMost];                       // the CTA's largest, in order
-    float group[kGroups];
+    uint64_t list[kList], ties[kTies];
+    uint64_t few[kFew];
+    uint64_t best[kMost];                       // the CTA's largest, in order (0: none)
+    uint64_t group_key[kGroups], bound_key;
+    float group[kGroups], bound;
     Sums warp[kWarps], all;
-    float bound;
-    int n_above, n_ties;
+    int n, n_ties, n_few;
     int scan[kWarps];
 };
+static_assert(sizeof(Shared) <= 48 * 1024, "static shared memory");
 
 template <typename T>
 struct Vec;                                     // 16 bytes of logits
 template <>
 struct Vec<float> {
     static constexpr int kCount = 4;
+    static constexpr uint32_t kLowest = 0xFF800000u;             // -inf
     static __device__ __forceinline__ void get(const uint4 &w, float *x) {
         x[0] = __uint_as_float(w.x);
         x[1] = __uint_as_float(w.y);
@@ -109,10 +124,18 @@ struct Vec<float> {
         x[3] = __uint_as_float(w.w);
     }
     static __device__ __forceinline__ float one(const float *p) { return *p; }
+    // The logits [first, first + 4) of a row of V as far as there are, else -inf.
+    static __device__ __forceinline__ uint4 some(const float *row, int first, int V) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = first + j >= 0 && first + j < V ? __float_as_uint(row[first + j]) : kLowest;
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
 };
 template <>
 struct Vec<__half> {
     static constexpr int kCount = 8;
+    static constexpr uint32_t kLowest = 0xFC00FC00u;
     static __device__ __forceinline__ void get(const uint4 &w, float *x) {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -123,13 +146,158 @@ struct Vec<__half> {
         }
     }
     static __device__ __forceinline__ float one(const __half *p) { return __half2float(*p); }
+    static __device__ __forceinline__ uint4 some(const __half *row, int first, int V) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = first + 2 * j;
+            const uint32_t lo = k >= 0 && k < V ? __half_as_ushort(row[k]) : 0xFC00u;
+            const uint32_t hi = k + 1 >= 0 && k + 1 < V ? __half_as_ushort(row[k + 1]) : 0xFC00u;
+            w[j] = lo | hi << 16;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
 };
+
+// How many groups have a larger value than this thread's group, or the same
+// and a lower number (the four lanes of a group share the work).
+template <typename K>
+__device__ __forceinline__ int groups_above(const K *group, K mine) {
+    const int g = int(threadIdx.x) / kGroupLanes, l = int(threadIdx.x) % kGroupLanes;
+    int above = 0;
+#pragma unroll 8
+    for (int k = 0; k < kGroups; k += kGroupLanes) {
+        const K o = group[k + l];
+        above += o > mine || (o == mine && k + l < g);
+    }
+#pragma unroll
+    for (int d = 1; d < kGroupLanes; d <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, d);
+    return above;
+}
+
+// sh.best: the `top` largest of sh.list[0 .. n), in order; n < top: all, then 0.
+// Begins and ends with a barrier.
+__device__ __noinline__ void best_of_list(Shared &sh, int top, int n) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    const uint64_t *list = sh.list;
+    if (n > 2 * kMost) {
+        uint64_t g = 0;
+        for (int i = tid; i < n; i += kThreads) g = max(g, sh.list[i]);
+#pragma unroll
+        for (int d = 1; d < kGroupLanes; d <<= 1) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
+        if (tid % kGroupLanes == 0) sh.group_key[tid / kGroupLanes] = g;
+        if (tid == 0) sh.n_few = 0;
+        __syncthreads();
+        const int above = groups_above(sh.group_key, g);
+        if (above == top - 1 && tid % kGroupLanes == 0) sh.bound_key = g;
+        __syncthreads();
+        const uint64_t bound = sh.bound_key;
+        if (g >= bound)
+            for (int i = tid; i < n; i += kThreads) {
+                const uint64_t key = sh.list[i];
+                if (key >= bound && key != 0) sh.few[atomicAdd(&sh.n_few, 1)] = key;
+            }
+        __syncthreads();
+        list = sh.few;
+        n = sh.n_few;
+    }
+    if (tid < kMost) sh.best[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+        const uint64_t key = list[i];
+        int place = 0;
+        for (int o = 0; o < n; ++o) place += list[o] > key;
+        if (place < top) sh.best[place] = key;
+    }
+    __syncthreads();
+}
+
+// A batch of the CTA: thread's logit k has index first + k / W * kThreads * W + k % W,
+// and is there at all where that is in [0, limit) (else it reads -inf).  Those that may be among the `top` largest go to the end of sh.list, at most
+// 31 groups' and kTies; sh.bound is what the others of the row have to exceed.
+// Every thread calls it; begins and ends with a barrier.
+template <int W>
+__device__ __noinline__ void collect(Shared &sh, const float (&x)[kBatch], float most, int first, int limit, int top) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto index_of_logit = [&](int k) { return first + k / W * (kThreads * W) + k % W; };
+    float g = most;
+#pragma unroll
+    for (int d = 1; d < kGroupLanes; d <<= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
+    __syncthreads();
+    if (tid % kGroupLanes == 0) sh.group[tid / kGroupLanes] = g;
+    if (tid == 0) sh.n_ties = 0;
+    __syncthreads();
+    const int above = groups_above(sh.group, g);
+    if (above == top - 1 && tid % kGroupLanes == 0) sh.bound = g;
+    const int before = sh.n;
+    __syncthreads();
+    const float bound = sh.bound;
+    if (most >= bound && most > -INFINITY)
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (!(x[k] >= bound) || !(x[k] > -INFINITY)) continue;
+            const uint64_t key = key_of(x[k], index_of_logit(k));
+            if (x[k] > bound) {
+                sh.list[atomicAdd(&sh.n, 1)] = key;
+            } else {
+                const int at = atomicAdd(&sh.n_ties, 1);
+                if (at < kTies) sh.ties[at] = key;
+            }
+        }
+    __syncthreads();
+    const int n = sh.n, ties = sh.n_ties;
+    int add = ties;
+    if (ties <= kTies && bound > -INFINITY) {
+        if (tid < ties) sh.list[n + tid] = sh.ties[tid];
+    } else {
+        // as many as may be wanted of those equal to the bound, in order of their index
+        const int want = max(top - (n - before), 0);
+        auto equal = [&](int k) {
+            const int i = index_of_logit(k);
+            return i >= 0 && i < limit && (bound == -INFINITY ? !(x[k] > -INFINITY) : x[k] == bound);
+        };
+        add = 0;
+#pragma unroll
+        for (int r = 0; r < kBatch; r += W) {
+            if (add >= want) continue;                           // the same for all threads
+            int mine = 0;
+#pragma unroll
+            for (int j = 0; j < W; ++j) mine += equal(r + j);
+            int upto = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+                if (lane >= d) upto += y;
+            }
+            __syncthreads();
+            if (lane == 31) sh.scan[warp] = upto;
+            __syncthreads();
+            int at = add + upto - mine, all = 0;
+            for (int o = 0; o < kWarps; ++o) {
+                if (o < warp) at += sh.scan[o];
+                all += sh.scan[o];
+            }
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                if (equal(r + j)) {
+                    if (at < want) sh.list[n + at] = key_of(x[r + j], index_of_logit(r + j));
+                    ++at;
+                }
+            add += all;
+        }
+        add = min(add, want);
+    }
+    __syncthreads();
+    if (tid == 0) sh.n = n + add;
+    __syncthreads();
+}
 
 template <typename T, bool kTop>
 __global__ void __launch_bounds__(kThreads, 2)
 token_logprobs_kernel(const Args p) {
     __shared__ Shared sh;
-    constexpr int W = Vec<T>::kCount, kVecs = kHeldLogits / W;
+    constexpr int W = Vec<T>::kCount, kRows = kBatch / W;        // vectors of a batch
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cluster = 1 << p.cluster_bits, rank = int(blockIdx.x) & (cluster - 1), row = int(blockIdx.x) >> p.cluster_bits;
     grid_dep_wait();
@@ -138,166 +306,95 @@ token_logprobs_kernel(const Args p) {
     // logit: vector v holds logits v W - shift ...
     const T *x0 = static_cast<const T *>(p.logits) + row * p.stride;
     const int shift = int(reinterpret_cast<uintptr_t>(x0) & 15u) / int(sizeof(T));
-    const T *base = x0 - shift;
+    const uint4 *base = reinterpret_cast<const uint4 *>(x0 - shift);
     const int vecs = int((unsigned(p.V) + shift + W - 1) / W);
     const int each = (vecs + cluster - 1) >> p.cluster_bits;
     const int begin = min(rank * each, vecs), end = min(begin + each, vecs);
+    const int whole0 = shift > 0, whole1 = min(int((unsigned(p.V) + shift) / W), end);       // whole vectors: [whole0, whole1)
 
     Sums mine{-INFINITY, 0.f, 0.f};
-    int carried = 0;
-    for (int v0 = begin; v0 == begin || v0 < end; v0 += kThreads * kVecs) {
-        float x[kHeldLogits];
-        uint4 w[kVecs];
-        // whole vectors all at once; what lies at the row's ends one by one
+    float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
+    float bound = -INFINITY;
+    bool again = false;                          // the row once more, every batch collected by all
+    if (kTop) {
+        if (tid == 0) sh.n = 0;
+        __syncthreads();
+    }
+    for (;;) {
+        for (int v0 = begin; v0 == begin || v0 < end; v0 += kThreads * kLoads) {
+            uint4 w[kLoads];
+            if (v0 >= whole0 && v0 + kThreads * kLoads <= whole1) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int v = v0 + i * kThreads + tid, first = v * W - shift;
-            if (v < end && first >= 0 && first <= p.V - W) w[i] = *reinterpret_cast<const uint4 *>(base + size_t(v) * W);
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int v = v0 + i * kThreads + tid, first = v * W - shift;
-            if (v >= end) continue;
-            if (first >= 0 && first <= p.V - W) {
-                Vec<T>::get(w[i], x + i * W);
+                for (int i = 0; i < kLoads; ++i) w[i] = base[v0 + i * kThreads + tid];
             } else {
 #pragma unroll
-                for (int j = 0; j < W; ++j)
-                    x[i * W + j] = first + j >= 0 && first + j < p.V ? Vec<T>::one(x0 + (first + j)) : -INFINITY;
-            }
-#pragma unroll
-            for (int j = 0; j < W; j += 2) top = max3(top, x[i * W + j], x[i * W + j + 1]);
-        }
-        // s and t by this thread's largest
-        const float ref = top == -INFINITY ? 0.f : top;
-        float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
-        const float2 minus = make_float2(-ref, -ref), by = make_float2(p.heat_log2, p.heat_log2);
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            if (v0 + i * kThreads + tid >= end) continue;
-#pragma unroll
-            for (int j = 0; j < W; j += 2) {
-                const float2 d = __fadd2_rn(make_float2(x[i * W + j], x[i * W + j + 1]), minus);
-                float2 e = __fmul2_rn(d, by);
-                e.x = ex2(e.x);
-                e.y = ex2(e.y);
-                s2 = __fadd2_rn(s2, e);
-                t2 = __ffma2_rn(e, d, t2);
-            }
-        }
-        Sums here{top, s2.x + s2.y, t2.x + t2.y};
-        if (here.t != here.t && here.s == here.s) {              // 0 times -inf: a logit of -inf
-            here.t = 0.f;
-#pragma unroll
-            for (int k = 0; k < kHeldLogits; ++k)
-                if (v0 + k / W * kThreads + tid < end) {
-                    const float d = x[k] - ref;
-                    if (d > -INFINITY) here.t = fmaf(ex2(d * p.heat_log2), d, here.t);
-                }
-        }
-        mine = join(mine, here, p.heat_log2);
-
-        if (kTop) {
-            float g = top;
-#pragma unroll
-            for (int d = 1; d < kGroupLanes; d <<= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
-            if (tid % kGroupLanes == 0) sh.group[tid / kGroupLanes] = g;
-            if (tid == 0) {
-                sh.n_above = 0;
-                sh.n_ties = carried;
-            }
-            if (tid < carried) sh.ties[tid] = sh.best[tid];
-            __syncthreads();
-            // the groups' largest: how many are above this one (a part for each lane)
-            constexpr int kShare = kGroups / kGroupLanes;
-            int above = 0;
-#pragma unroll 8
-            for (int k = 0; k < kShare; ++k) {
-                const int o = k * kGroupLanes + tid % kGroupLanes;
-                above += sh.group[o] > g || (sh.group[o] == g && o < tid / kGroupLanes);
-            }
-#pragma unroll
-            for (int d = 1; d < kGroupLanes; d <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, d);
-            if (above == p.top - 1 && tid % kGroupLanes == 0) sh.bound = g;
-            __syncthreads();
-            const float bound = sh.bound;
-            if (top >= bound && top > -INFINITY) {
-#pragma unroll
-                for (int k = 0; k < kHeldLogits; ++k) {
-                    const int v = v0 + k / W * kThreads + tid;
-                    if (v >= end || !(x[k] >= bound) || !(x[k] > -INFINITY)) continue;
-                    const uint64_t key = key_of(x[k], v * W - shift + k % W);
-                    if (x[k] > bound) {
-                        sh.above[atomicAdd(&sh.n_above, 1)] = key;
-                    } else {
-                        const int at = atomicAdd(&sh.n_ties, 1);
-                        if (at < kTies + kMost) sh.ties[at] = key;
-                    }
-                }
-            }
-            __syncthreads();
-            int n_above = sh.n_above, n_ties = sh.n_ties;
-            if (n_ties > kTies + kMost || bound == -INFINITY) {
-                // those equal to the bound in order of their index (the first
-                // vectors of all threads, then the second ones ...)
-                const int want = p.top - n_above;
-                int found = 0;
-#pragma unroll
-                for (int i = 0; i < kVecs; ++i) {
+                for (int i = 0; i < kLoads; ++i) {
                     const int v = v0 + i * kThreads + tid;
-                    if (found >= want || v0 + i * kThreads >= end) continue;             // the same for all
-                    int here_n = 0;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        const int index = v * W - shift + j;
-                        const bool is = v < end && index >= 0 && index < p.V &&
-                                        (bound == -INFINITY ? !(x[i * W + j] > -INFINITY) : x[i * W + j] == bound);
-                        here_n += is;
-                    }
-                    int upto = here_n;
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const int y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-                        if (lane >= d) upto += y;
-                    }
-                    __syncthreads();
-                    if (lane == 31) sh.scan[warp] = upto;
-                    __syncthreads();
-                    int at = found + upto - here_n, all = 0;
-#pragma unroll
-                    for (int o = 0; o < kWarps; ++o) {
-                        if (o < warp) at += sh.scan[o];
-                        all += sh.scan[o];
-                    }
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        const int index = v * W - shift + j;
-                        const bool is = v < end && index >= 0 && index < p.V &&
-                                        (bound == -INFINITY ? !(x[i * W + j] > -INFINITY) : x[i * W + j] == bound);
-                        if (is && at < want) sh.ties[carried + at] = key_of(x[i * W + j], index);
-                        at += is;
-                    }
-                    found += all;
+                    if (v >= whole0 && v < whole1) w[i] = base[v];
+                    else if (v < end) w[i] = Vec<T>::some(x0, v * W - shift, p.V);
+                    else w[i] = make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
                 }
-                n_ties = carried + min(found, max(want, 0));
-                __syncthreads();
             }
-            // in order: each key counts those above it
-            if (tid < kMost) sh.best[tid] = 0;
-            __syncthreads();
-            const int n = n_above + n_ties;
-            for (int i = tid; i < n; i += kThreads) {
-                const uint64_t key = i < n_above ? sh.above[i] : sh.ties[i - n_above];
-                int place = 0;
-                for (int o = 0; o < n_above; ++o) place += sh.above[o] > key;
-                for (int o = 0; o < n_ties; ++o) place += sh.ties[o] > key;
-                if (place < p.top) sh.best[place] = key;
+#pragma unroll
+            for (int b = 0; b < kLoads; b += kRows) {
+                if (b > 0 && v0 + b * kThreads >= end) break;
+                float x[kBatch];
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) Vec<T>::get(w[b + i], x + i * W);
+                float top = x[0];
+#pragma unroll
+                for (int k = 1; k < kBatch - 1; k += 2) top = max3(top, x[k], x[k + 1]);
+                top = max3(top, x[kBatch - 1], -INFINITY);
+                const int first = (v0 + b * kThreads + tid) * W - shift;
+                if (kTop && (again || (b == 0 && v0 == begin))) {
+                    collect<W>(sh, x, top, first, min(end * W - shift, p.V), p.top);
+                    bound = sh.bound;
+                    if (again) {
+                        best_of_list(sh, p.top, sh.n);
+                        if (tid < p.top) sh.list[tid] = sh.best[tid];
+                        if (tid == 0) sh.n = p.top;
+                        continue;
+                    }
+                } else if (kTop && top > bound) {
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        if (x[k] > bound) {
+                            const int at = atomicAdd(&sh.n, 1);
+                            if (at < kList) sh.list[at] = key_of(x[k], first + k / W * (kThreads * W) + k % W);
+                        }
+                }
+                if (top > mine.m + p.slack || (mine.m == -INFINITY && top > -INFINITY)) {
+                    const float d = mine.m - top, a = mine.m == -INFINITY ? 1.f : ex2(d * p.heat_log2);
+                    if (mine.m > -INFINITY)
+                        t = a == 0.f ? make_float2(0.f, 0.f) : make_float2(a * (t.x + d * s.x), a * (t.y + d * s.y));
+                    s = make_float2(a * s.x, a * s.y);
+                    mine.m = top;
+                }
+                const float ref = mine.m == -INFINITY ? 0.f : mine.m;
+                const float2 minus = make_float2(-ref, -ref), by = make_float2(p.heat_log2, p.heat_log2);
+#pragma unroll
+                for (int k = 0; k < kBatch; k += 2) {
+                    float2 d = __fadd2_rn(make_float2(x[k], x[k + 1]), minus);
+                    float2 e = __fmul2_rn(d, by);
+                    e.x = ex2(e.x);
+                    e.y = ex2(e.y);
+                    s = __fadd2_rn(s, e);
+                    d.x = fmaxf(d.x, -3e38f);                    // 0 times -inf is 0 (a NaN is in s already)
+                    d.y = fmaxf(d.y, -3e38f);
+                    t = __ffma2_rn(e, d, t);
+                }
             }
-            __syncthreads();
-            carried = p.top;
         }
+        if (!kTop) break;
+        __syncthreads();
+        if (again || sh.n <= kList) break;
+        __syncthreads();
+        if (tid == 0) sh.n = 0;
+        again = true;
     }
+    if (kTop) best_of_list(sh, p.top, sh.n);
+    mine.s = s.x + s.y;
+    mine.t = t.x + t.y;
 
     // the CTA's sums, then the cluster's
 #pragma unroll
@@ -334,18 +431,18 @@ token_logprobs_kernel(const Args p) {
             p.logprobs[size_t(row) * p.n + i] = at >= 0 && at < p.V ? logprob(Vec<T>::one(x0 + at)) : -INFINITY;
         }
         if (kTop) {
-            const int n = p.top << p.cluster_bits;
-            for (int i = tid; i < n; i += kThreads)
-                sh.above[i] = ld_cluster_u64(mapa_shared(smem_u32(&sh.best[i >> p.cluster_bits]), i & (cluster - 1)));
-            __syncthreads();
-            for (int i = tid; i < n; i += kThreads) {
-                const uint64_t key = sh.above[i];
-                int place = 0;
-                for (int o = 0; o < n; ++o) place += sh.above[o] > key;
-                if (place < p.top && key != 0) {
-                    p.top_ids[size_t(row) * p.top + place] = index_of(key);
-                    p.top_logprobs[size_t(row) * p.top + place] = logprob(logit_of(key));
-                }
+            if (cluster > 1) {
+                const int n = p.top << p.cluster_bits;
+                uint64_t key = 0;
+                if (tid < n) key = ld_cluster_u64(mapa_shared(smem_u32(&sh.best[tid >> p.cluster_bits]), tid & (cluster - 1)));
+                __syncthreads();
+                if (tid < n) sh.list[tid] = key;
+                best_of_list(sh, p.top, n);
+            }
+            if (tid < p.top) {
+                const uint64_t key = sh.best[tid];
+                p.top_ids[size_t(row) * p.top + tid] = index_of(key);
+                p.top_logprobs[size_t(row) * p.top + tid] = logprob(logit_of(key));
             }
         }
     }
@@ -383,11 +480,12 @@ w4v_status launch_token_logprobs(const void *logits, bool half, long long stride
     a.top = top;
     a.heat = 1.f / temperature;
     a.heat_log2 = 1.4426950408889634f / temperature;
-    // A row in one piece a CTA, as far as a cluster goes; few rows in smaller ones.
+    a.slack = kSlack / a.heat_log2;
+    // Rows are cut while there are fewer CTAs than the GPU holds at a time and a
+    // piece has more logits than its threads take at once.
     a.cluster_bits = 0;
-    while (1 << a.cluster_bits < kMaxCluster &&
-           (V > (long long)kPiece << a.cluster_bits ||
-            ((long long)M << a.cluster_bits < info->sm_count && V > 4096 << a.cluster_bits)))
+    while (1 << a.cluster_bits < kMaxCluster && (long long)M << a.cluster_bits <= info->sm_count &&
+           V > kThreads * kBatch << a.cluster_bits)
         ++a.cluster_bits;
     if (half) return top > 0 ? launch<__half, true>(a, M, stream) : launch<__half, false>(a, M, stream);
     return top > 0 ? launch<float, true>(a, M, stream) : launch<float, false>(a, M, stream);
