@@ -20,15 +20,17 @@
 // top-th largest of those is a bound that at least `top` logits reach and few
 // exceed (31 groups' at most, 1984; some 25 where logits lie without order).
 // From then on a thread looks whether its 16 next logits' largest, which it has
-// anyway, is above the bound, and collects those that are (a logit equal to the
-// bound comes too late, by its index).  In no order they are some 20 times
-// `top` of 151,936; the same groups' bound thins them out, and what is left
-// counts how many are above it.  Where more come than there is room for (a row
-// in ascending order), the row is gone through once more, 8192 logits at a time.
+// anyway, is above the bound (a logit equal to the bound comes too late, by its
+// index), and if so notes where they are: some 18 times `top` batches of
+// 151,936 logits in no order.  At the end the noted batches are read once more
+// (collecting their logits on the way cost 100 instructions a batch: 287 us
+// against 229 for 2048 rows with five alternatives), the same groups' bound
+// thins out what exceeds the first one, and what is left counts how many are
+// above it.  Where more come than there is room for (a row in ascending order),
+// the row is gone through once more, 8192 logits at a time.
 //
-// What bounds it: the bytes.  Per 16 logits 8 maxima, 16 powers, 56 other
-// operations, and the powers at 16 a clock and SM take a third of the time
-// that 4-byte logits take from HBM.
+// What bounds it: the bytes.  The powers, at 16 a clock and SM, take a third of
+// the time that 4-byte logits take from HBM.
 #include <climits>
 
 #include "runtime.h"
@@ -43,7 +45,7 @@ constexpr int kLoads = 8;                       // 16-byte loads of a thread in 
 constexpr float kSlack = 2.f;
 constexpr int kGroups = 128, kGroupLanes = kThreads / kGroups;
 constexpr int kMost = kLogprobsMaxTop;
-constexpr int kList = 4096, kTies = 512, kFew = 1024;
+constexpr int kList = 3072, kTies = 512, kFew = 768, kNotes = 2048;
 static_assert((kMost - 1) * kGroupLanes * kBatch + kTies + kMost <= kList, "what a batch adds to the list fits");
 static_assert(kMost * kGroupLanes * (kList / kThreads) <= kFew, "what the groups' bound leaves of a list fits");
 static_assert(kMost <= kGroups, "the bound is a group's largest");
@@ -105,8 +107,9 @@ struct __align__(8) Shared {
     uint64_t best[kMost];                       // the CTA's largest, in order (0: none)
     uint64_t group_key[kGroups], bound_key;
     float group[kGroups], bound;
+    int notes[kNotes];                          // first indexes of a thread's batches
     Sums warp[kWarps], all;
-    int n, n_ties, n_few;
+    int n, n_ties, n_few, n_notes;
     int scan[kWarps];
 };
 static_assert(sizeof(Shared) <= 48 * 1024, "static shared memory");
@@ -159,20 +162,73 @@ struct Vec<__half> {
     }
 };
 
-// How many groups have a larger value than this thread's group, or the same
-// and a lower number (the four lanes of a group share the work).
-template <typename K>
-__device__ __forceinline__ int groups_above(const K *group, K mine) {
-    const int g = int(threadIdx.x) / kGroupLanes, l = int(threadIdx.x) % kGroupLanes;
-    int above = 0;
-#pragma unroll 8
-    for (int k = 0; k < kGroups; k += kGroupLanes) {
-        const K o = group[k + l];
-        above += o > mine || (o == mine && k + l < g);
-    }
+// The n-th largest of the groups' values, by one warp (in n steps that take one
+// away each: a block's count of the larger ones would be shorter, and 40 times
+// the instructions).
+__device__ __forceinline__ uint64_t warp_max(uint64_t x) {
+    const uint32_t high = __reduce_max_sync(0xFFFFFFFFu, uint32_t(x >> 32));
+    return uint64_t(high) << 32 | __reduce_max_sync(0xFFFFFFFFu, uint32_t(x >> 32) == high ? uint32_t(x) : 0u);
+}
+__device__ __forceinline__ uint64_t nth_largest(const uint64_t *group, int n) {
+    const int lane = threadIdx.x & 31;
+    uint64_t x[kGroups / 32], top = 0;
 #pragma unroll
-    for (int d = 1; d < kGroupLanes; d <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, d);
-    return above;
+    for (int i = 0; i < kGroups / 32; ++i) x[i] = group[32 * i + lane];
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+        uint64_t mine = x[0];
+#pragma unroll
+        for (int i = 1; i < kGroups / 32; ++i) mine = max(mine, x[i]);
+        top = warp_max(mine);
+        bool taken = lane != __ffs(__ballot_sync(0xFFFFFFFFu, mine == top)) - 1;
+#pragma unroll
+        for (int i = 0; i < kGroups / 32; ++i)
+            if (!taken && x[i] == top) {
+                x[i] = 0;
+                taken = true;
+            }
+    }
+    return top;
+}
+// The same of floats that are not NaN (ordered as signed integers).
+__device__ __forceinline__ float nth_largest(const float *group, int n) {
+    const int lane = threadIdx.x & 31;
+    int x[kGroups / 32], top = 0;
+#pragma unroll
+    for (int i = 0; i < kGroups / 32; ++i) {
+        const int b = __float_as_int(group[32 * i + lane]);
+        x[i] = b < 0 ? b ^ 0x7FFFFFFF : b;
+    }
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+        int mine = x[0];
+#pragma unroll
+        for (int i = 1; i < kGroups / 32; ++i) mine = max(mine, x[i]);
+        top = __reduce_max_sync(0xFFFFFFFFu, mine);
+        bool taken = lane != __ffs(__ballot_sync(0xFFFFFFFFu, mine == top)) - 1;
+#pragma unroll
+        for (int i = 0; i < kGroups / 32; ++i)
+            if (!taken && x[i] == top) {
+                x[i] = INT_MIN;
+                taken = true;
+            }
+    }
+    return __int_as_float(top < 0 ? top ^ 0x7FFFFFFF : top);
+}
+
+// sh.bound: the top-th largest of the groups' largest logits, `most` this
+// thread's.  Every thread calls it; begins and ends with a barrier.
+__device__ __forceinline__ void bound_of_groups(Shared &sh, float most, int top) {
+#pragma unroll
+    for (int d = 1; d < kGroupLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+    __syncthreads();
+    if (threadIdx.x % kGroupLanes == 0) sh.group[threadIdx.x / kGroupLanes] = most;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const float bound = nth_largest(sh.group, top);
+        if (threadIdx.x == 0) sh.bound = bound;
+    }
+    __syncthreads();
 }
 
 // sh.best: the `top` largest of sh.list[0 .. n), in order; n < top: all, then 0.
@@ -181,7 +237,7 @@ __device__ __noinline__ void best_of_list(Shared &sh, int top, int n) {
     const int tid = threadIdx.x;
     __syncthreads();
     const uint64_t *list = sh.list;
-    if (n > 2 * kMost) {
+    if (n > 4 * kMost) {
         uint64_t g = 0;
         for (int i = tid; i < n; i += kThreads) g = max(g, sh.list[i]);
 #pragma unroll
@@ -189,8 +245,10 @@ __device__ __noinline__ void best_of_list(Shared &sh, int top, int n) {
         if (tid % kGroupLanes == 0) sh.group_key[tid / kGroupLanes] = g;
         if (tid == 0) sh.n_few = 0;
         __syncthreads();
-        const int above = groups_above(sh.group_key, g);
-        if (above == top - 1 && tid % kGroupLanes == 0) sh.bound_key = g;
+        if (tid < 32) {
+            const uint64_t bound = nth_largest(sh.group_key, top);
+            if (tid == 0) sh.bound_key = bound;
+        }
         __syncthreads();
         const uint64_t bound = sh.bound_key;
         if (g >= bound)
@@ -221,18 +279,11 @@ template <int W>
 __device__ __noinline__ void collect(Shared &sh, const float (&x)[kBatch], float most, int first, int limit, int top) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto index_of_logit = [&](int k) { return first + k / W * (kThreads * W) + k % W; };
-    float g = most;
-#pragma unroll
-    for (int d = 1; d < kGroupLanes; d <<= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
-    __syncthreads();
-    if (tid % kGroupLanes == 0) sh.group[tid / kGroupLanes] = g;
     if (tid == 0) sh.n_ties = 0;
-    __syncthreads();
-    const int above = groups_above(sh.group, g);
-    if (above == top - 1 && tid % kGroupLanes == 0) sh.bound = g;
+    bound_of_groups(sh, most, top);
     const int before = sh.n;
-    __syncthreads();
     const float bound = sh.bound;
+    __syncthreads();
     if (most >= bound && most > -INFINITY)
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
@@ -317,9 +368,10 @@ token_logprobs_kernel(const Args p) {
     float bound = -INFINITY;
     bool again = false;                          // the row once more, every batch collected by all
     if (kTop) {
-        if (tid == 0) sh.n = 0;
+        if (tid == 0) sh.n = sh.n_ties = sh.n_notes = 0;
         __syncthreads();
     }
+    const int first_end = (begin + kThreads * kLoads) * W - shift;       // a note of the first loads is below
     for (;;) {
         for (int v0 = begin; v0 == begin || v0 < end; v0 += kThreads * kLoads) {
             uint4 w[kLoads];
@@ -335,6 +387,17 @@ token_logprobs_kernel(const Args p) {
                     else w[i] = make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
                 }
             }
+            if (kTop && !again && v0 == begin) {
+                float top = -INFINITY, x[W];
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    Vec<T>::get(w[i], x);
+#pragma unroll
+                    for (int k = 0; k < W; k += 2) top = max3(top, x[k], x[k + 1]);
+                }
+                bound_of_groups(sh, top, p.top);
+                bound = sh.bound;
+            }
 #pragma unroll
             for (int b = 0; b < kLoads; b += kRows) {
                 if (b > 0 && v0 + b * kThreads >= end) break;
@@ -346,22 +409,31 @@ token_logprobs_kernel(const Args p) {
                 for (int k = 1; k < kBatch - 1; k += 2) top = max3(top, x[k], x[k + 1]);
                 top = max3(top, x[kBatch - 1], -INFINITY);
                 const int first = (v0 + b * kThreads + tid) * W - shift;
-                if (kTop && (again || (b == 0 && v0 == begin))) {
-                    collect<W>(sh, x, top, first, min(end * W - shift, p.V), p.top);
-                    bound = sh.bound;
-                    if (again) {
-                        best_of_list(sh, p.top, sh.n);
-                        if (tid < p.top) sh.list[tid] = sh.best[tid];
-                        if (tid == 0) sh.n = p.top;
-                        continue;
-                    }
-                } else if (kTop && top > bound) {
+                auto collect_all = [&] {                         // (a copy, so that x itself stays in registers)
+                    float y[kBatch];
 #pragma unroll
-                    for (int k = 0; k < kBatch; ++k)
-                        if (x[k] > bound) {
-                            const int at = atomicAdd(&sh.n, 1);
-                            if (at < kList) sh.list[at] = key_of(x[k], first + k / W * (kThreads * W) + k % W);
-                        }
+                    for (int k = 0; k < kBatch; ++k) y[k] = x[k];
+                    collect<W>(sh, y, top, first, min(end * W - shift, p.V), p.top);
+                };
+                if (kTop && again) {
+                    collect_all();
+                    best_of_list(sh, p.top, sh.n);
+                    if (tid < p.top) sh.list[tid] = sh.best[tid];
+                    if (tid == 0) sh.n = p.top;
+                    continue;
+                }
+                if (kTop) {
+                    bool note = top > bound || (v0 == begin && top == bound && bound > -INFINITY);
+                    if (b == 0 && v0 == begin && bound == -INFINITY) {
+                        // Few groups hold a token above -inf, so the first batch has
+                        // all those of -inf that may be wanted (or it is all there is).
+                        collect_all();
+                        note = false;
+                    }
+                    if (note) {
+                        const int at = atomicAdd(&sh.n_notes, 1);
+                        if (at < kNotes) sh.notes[at] = first;
+                    }
                 }
                 if (top > mine.m + p.slack || (mine.m == -INFINITY && top > -INFINITY)) {
                     const float d = mine.m - top, a = mine.m == -INFINITY ? 1.f : ex2(d * p.heat_log2);
@@ -387,7 +459,35 @@ token_logprobs_kernel(const Args p) {
         }
         if (!kTop) break;
         __syncthreads();
-        if (again || sh.n <= kList) break;
+        if (again) break;
+        const int notes = sh.n_notes;
+        if (notes <= kNotes) {
+            for (int i = tid; i < notes * kRows; i += kThreads) {
+                const int first = sh.notes[i / kRows] + i % kRows * (kThreads * W), v = (first + shift) / W;
+                if (v >= end) continue;
+                float x[W];
+                Vec<T>::get(v >= whole0 && v < whole1 ? base[v] : Vec<T>::some(x0, first, p.V), x);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    if (x[j] > bound) {
+                        const int at = atomicAdd(&sh.n, 1);
+                        if (at < kList) sh.list[at] = key_of(x[j], first + j);
+                    } else if (x[j] == bound && sh.notes[i / kRows] < first_end) {
+                        const int at = atomicAdd(&sh.n_ties, 1);
+                        if (at < kTies) sh.ties[at] = key_of(x[j], first + j);
+                    }
+                }
+            }
+            __syncthreads();
+            const int n = sh.n, ties = bound > -INFINITY ? sh.n_ties : 0;
+            if (n + ties <= kList && ties <= kTies) {
+                if (tid < ties) sh.list[n + tid] = sh.ties[tid];
+                __syncthreads();
+                if (tid == 0) sh.n = n + ties;
+                __syncthreads();
+                break;
+            }
+        }
         __syncthreads();
         if (tid == 0) sh.n = 0;
         again = true;
@@ -396,12 +496,17 @@ token_logprobs_kernel(const Args p) {
     mine.s = s.x + s.y;
     mine.t = t.x + t.y;
 
-    // the CTA's sums, then the cluster's
+    // the warp's sums by its largest reference, the CTA's, then the cluster's
+    {
+        float m = mine.m;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const Sums o{__shfl_xor_sync(0xFFFFFFFFu, mine.m, d), __shfl_xor_sync(0xFFFFFFFFu, mine.s, d),
-                     __shfl_xor_sync(0xFFFFFFFFu, mine.t, d)};
-        mine = join(mine, o, p.heat_log2);
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        mine = join(mine, Sums{m, 0.f, 0.f}, p.heat_log2);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            mine.s += __shfl_xor_sync(0xFFFFFFFFu, mine.s, d);
+            mine.t += __shfl_xor_sync(0xFFFFFFFFu, mine.t, d);
+        }
     }
     if (lane == 0) sh.warp[warp] = mine;
     __syncthreads();
