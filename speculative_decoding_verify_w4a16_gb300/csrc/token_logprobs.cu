@@ -15,19 +15,18 @@
 // by the first of them through distributed shared memory: no workspace, no
 // second launch, no atomics between CTAs.
 //
-// The `top` largest, ties to the lower index, without sorting.  The CTA's first
-// 8192 logits: 128 groups of four threads have a largest logit each, and the
-// top-th largest of those is a bound that at least `top` logits reach and few
-// exceed (31 groups' at most, 1984; some 25 where logits lie without order).
-// From then on a thread looks whether its 16 next logits' largest, which it has
-// anyway, is above the bound (a logit equal to the bound comes too late, by its
-// index), and if so notes where they are: some 18 times `top` batches of
-// 151,936 logits in no order.  At the end the noted batches are read once more
-// (collecting their logits on the way cost 100 instructions a batch: 287 us
-// against 229 for 2048 rows with five alternatives), the same groups' bound
-// thins out what exceeds the first one, and what is left counts how many are
-// above it.  Where more come than there is room for (a row in ascending order),
-// the row is gone through once more, 8192 logits at a time.
+// The `top` largest, ties to the lower index, without sorting.  The threads in
+// 64 groups: the top-th largest of the groups' largest logits is a bound that
+// at least `top` logits reach, and few exceed where they lie without order.
+// The first 16,384 logits give such a bound.  From then on a thread looks
+// whether its 16 next logits' largest, which it has anyway, is above it (a logit
+// equal to it comes too late, by its index), and if so notes the batch.  At the
+// end the groups' largest of all logits give a second, closer bound; the noted
+// batches that reach it, some 25, are read once more, and the logits that reach
+// it count how many are above them.  (Collecting logits on the way instead of
+// notes cost 100 instructions a batch.)  Where more come than there is room for
+// (a row in ascending order, one of few different values), the row is gone
+// through once more, a batch of every thread at a time.
 //
 // What bounds it: the bytes.  The powers, at 16 a clock and SM, take a third of
 // the time that 4-byte logits take from HBM.
@@ -39,17 +38,15 @@
 namespace w4v {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBatch = 16;                      // logits of a thread that are looked at together
 constexpr int kLoads = 8;                       // 16-byte loads of a thread in flight
 constexpr float kSlack = 2.f;
-constexpr int kGroups = 128, kGroupLanes = kThreads / kGroups;
+constexpr int kGroups = 64;
 constexpr int kMost = kLogprobsMaxTop;
-constexpr int kList = 3072, kTies = 512, kFew = 768, kNotes = 2048;
-static_assert((kMost - 1) * kGroupLanes * kBatch + kTies + kMost <= kList, "what a batch adds to the list fits");
-static_assert(kMost * kGroupLanes * (kList / kThreads) <= kFew, "what the groups' bound leaves of a list fits");
 static_assert(kMost <= kGroups, "the bound is a group's largest");
 constexpr int kMaxCluster = 8;
+// Vocabularies up to this size: CTAs of 128 threads.
+constexpr int kSmall = 8192;
 
 struct Args {
     const void *logits;
@@ -101,19 +98,6 @@ __device__ __forceinline__ Sums join(const Sums &a, const Sums &b, float heat_lo
     return r;
 }
 
-struct __align__(8) Shared {
-    uint64_t list[kList], ties[kTies];
-    uint64_t few[kFew];
-    uint64_t best[kMost];                       // the CTA's largest, in order (0: none)
-    uint64_t group_key[kGroups], bound_key;
-    float group[kGroups], bound;
-    int notes[kNotes];                          // first indexes of a thread's batches
-    Sums warp[kWarps], all;
-    int n, n_ties, n_few, n_notes;
-    int scan[kWarps];
-};
-static_assert(sizeof(Shared) <= 48 * 1024, "static shared memory");
-
 template <typename T>
 struct Vec;                                     // 16 bytes of logits
 template <>
@@ -162,193 +146,207 @@ struct Vec<__half> {
     }
 };
 
-// The n-th largest of the groups' values, by one warp (in n steps that take one
-// away each: a block's count of the larger ones would be shorter, and 40 times
-// the instructions).
-__device__ __forceinline__ uint64_t warp_max(uint64_t x) {
-    const uint32_t high = __reduce_max_sync(0xFFFFFFFFu, uint32_t(x >> 32));
-    return uint64_t(high) << 32 | __reduce_max_sync(0xFFFFFFFFu, uint32_t(x >> 32) == high ? uint32_t(x) : 0u);
-}
-__device__ __forceinline__ uint64_t nth_largest(const uint64_t *group, int n) {
-    const int lane = threadIdx.x & 31;
-    uint64_t x[kGroups / 32], top = 0;
+// A batch whose largest logit may be among the row's `top`.
+struct Note {
+    float most;
+    int first;                                  // see collect()
+};
+template <int kThreads>
+struct __align__(8) Shared {
+    static constexpr int kLanes = kThreads / kGroups, kWarps = kThreads / 32;
+    static constexpr int kTies = kThreads;
+    // What a batch of every thread may add: all of 31 groups, what is equal to
+    // the bound, what was there.
+    static constexpr int kList = ((kMost - 1) * kLanes * kBatch + kTies + kMost + 127) / 128 * 128;
+    static constexpr int kKeys = 2 * kThreads, kNotes = kList - kKeys;
+    union {
+        uint64_t list[kList];
+        struct {
+            uint64_t keys[kKeys];               // (the list's begin)
+            Note notes[kNotes];
+        };
+    };
+    uint64_t ties[kTies];
+    uint64_t best[kMost];                       // the CTA's largest, in order (0: none)
+    uint64_t group_key[kGroups], bound_key;
+    float group[kGroups], bound;
+    Sums warp[kWarps], all;
+    int n, n_ties, n_notes;
+    int scan[kWarps];
+};
+static_assert(sizeof(Shared<512>) <= 48 * 1024 && sizeof(Note) == sizeof(uint64_t), "static shared memory");
+
+// Of the groups' values, how many are larger than this thread's group's, and
+// how many as large (the lanes of a group share the work).
+template <int kLanes, typename K>
+__device__ __forceinline__ int2 groups_above(const K *group, K mine) {
+    int2 n = make_int2(0, 0);
 #pragma unroll
-    for (int i = 0; i < kGroups / 32; ++i) x[i] = group[32 * i + lane];
-#pragma unroll 1
-    for (int k = 0; k < n; ++k) {
-        uint64_t mine = x[0];
-#pragma unroll
-        for (int i = 1; i < kGroups / 32; ++i) mine = max(mine, x[i]);
-        top = warp_max(mine);
-        bool taken = lane != __ffs(__ballot_sync(0xFFFFFFFFu, mine == top)) - 1;
-#pragma unroll
-        for (int i = 0; i < kGroups / 32; ++i)
-            if (!taken && x[i] == top) {
-                x[i] = 0;
-                taken = true;
-            }
+    for (int k = 0; k < kGroups; k += kLanes) {
+        const K o = group[k + int(threadIdx.x) % kLanes];
+        n.x += o > mine;
+        n.y += o >= mine;
     }
-    return top;
-}
-// The same of floats that are not NaN (ordered as signed integers).
-__device__ __forceinline__ float nth_largest(const float *group, int n) {
-    const int lane = threadIdx.x & 31;
-    int x[kGroups / 32], top = 0;
 #pragma unroll
-    for (int i = 0; i < kGroups / 32; ++i) {
-        const int b = __float_as_int(group[32 * i + lane]);
-        x[i] = b < 0 ? b ^ 0x7FFFFFFF : b;
+    for (int d = 1; d < kLanes; d <<= 1) {
+        n.x += __shfl_xor_sync(0xFFFFFFFFu, n.x, d);
+        n.y += __shfl_xor_sync(0xFFFFFFFFu, n.y, d);
     }
-#pragma unroll 1
-    for (int k = 0; k < n; ++k) {
-        int mine = x[0];
-#pragma unroll
-        for (int i = 1; i < kGroups / 32; ++i) mine = max(mine, x[i]);
-        top = __reduce_max_sync(0xFFFFFFFFu, mine);
-        bool taken = lane != __ffs(__ballot_sync(0xFFFFFFFFu, mine == top)) - 1;
-#pragma unroll
-        for (int i = 0; i < kGroups / 32; ++i)
-            if (!taken && x[i] == top) {
-                x[i] = INT_MIN;
-                taken = true;
-            }
-    }
-    return __int_as_float(top < 0 ? top ^ 0x7FFFFFFF : top);
+    return n;
 }
 
-// sh.bound: the top-th largest of the groups' largest logits, `most` this
-// thread's.  Every thread calls it; begins and ends with a barrier.
-__device__ __forceinline__ void bound_of_groups(Shared &sh, float most, int top) {
+// The top-th largest of the groups' largest logits, `most` this thread's.
+// Every thread calls it; begins and ends with a barrier.
+template <int kThreads>
+__device__ __forceinline__ float bound_of_groups(Shared<kThreads> &sh, float most, int top) {
+    constexpr int kLanes = Shared<kThreads>::kLanes;
 #pragma unroll
-    for (int d = 1; d < kGroupLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+    for (int d = 1; d < kLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
     __syncthreads();
-    if (threadIdx.x % kGroupLanes == 0) sh.group[threadIdx.x / kGroupLanes] = most;
+    if (threadIdx.x % kLanes == 0) sh.group[threadIdx.x / kLanes] = most;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const float bound = nth_largest(sh.group, top);
-        if (threadIdx.x == 0) sh.bound = bound;
-    }
+    const int2 n = groups_above<kLanes>(sh.group, most);
+    if (n.x < top && top <= n.y) sh.bound = most;                // (several groups: the same value)
     __syncthreads();
+    return sh.bound;
 }
 
 // sh.best: the `top` largest of sh.list[0 .. n), in order; n < top: all, then 0.
 // Begins and ends with a barrier.
-__device__ __noinline__ void best_of_list(Shared &sh, int top, int n) {
+template <int kThreads>
+__device__ __noinline__ void best_of_list(Shared<kThreads> &sh, int top, int n) {
+    constexpr int kLanes = Shared<kThreads>::kLanes;
     const int tid = threadIdx.x;
     __syncthreads();
     const uint64_t *list = sh.list;
     if (n > 4 * kMost) {
+        // those that reach the top-th of the groups' largest
         uint64_t g = 0;
         for (int i = tid; i < n; i += kThreads) g = max(g, sh.list[i]);
 #pragma unroll
-        for (int d = 1; d < kGroupLanes; d <<= 1) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
-        if (tid % kGroupLanes == 0) sh.group_key[tid / kGroupLanes] = g;
-        if (tid == 0) sh.n_few = 0;
+        for (int d = 1; d < kLanes; d <<= 1) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
+        if (tid % kLanes == 0) sh.group_key[tid / kLanes] = g;
+        if (tid == 0) sh.n_ties = 0;
         __syncthreads();
-        if (tid < 32) {
-            const uint64_t bound = nth_largest(sh.group_key, top);
-            if (tid == 0) sh.bound_key = bound;
-        }
+        const int2 above = groups_above<kLanes>(sh.group_key, g);
+        if (above.x < top && top <= above.y) sh.bound_key = g;
         __syncthreads();
         const uint64_t bound = sh.bound_key;
         if (g >= bound)
             for (int i = tid; i < n; i += kThreads) {
                 const uint64_t key = sh.list[i];
-                if (key >= bound && key != 0) sh.few[atomicAdd(&sh.n_few, 1)] = key;
+                if (key < bound || key == 0) continue;
+                const int at = atomicAdd(&sh.n_ties, 1);
+                if (at < Shared<kThreads>::kTies) sh.ties[at] = key;
             }
         __syncthreads();
-        list = sh.few;
-        n = sh.n_few;
+        if (sh.n_ties <= Shared<kThreads>::kTies) {
+            list = sh.ties;
+            n = sh.n_ties;
+        }
     }
     if (tid < kMost) sh.best[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-        const uint64_t key = list[i];
+    // each counts those above it, two threads a key
+    for (int i = tid / 2; i < (n + 15) / 16 * 16; i += kThreads / 2) {       // (whole warps)
+        const uint64_t key = i < n ? list[i] : 0;
         int place = 0;
-        for (int o = 0; o < n; ++o) place += list[o] > key;
-        if (place < top) sh.best[place] = key;
+        for (int o = tid & 1; o < n; o += 2) place += list[o] > key;
+        place += __shfl_xor_sync(0xFFFFFFFFu, place, 1);
+        if (i < n && (tid & 1) == 0 && place < top) sh.best[place] = key;
     }
     __syncthreads();
 }
 
-// A batch of the CTA: thread's logit k has index first + k / W * kThreads * W + k % W,
-// and is there at all where that is in [0, limit) (else it reads -inf).  Those that may be among the `top` largest go to the end of sh.list, at most
-// 31 groups' and kTies; sh.bound is what the others of the row have to exceed.
-// Every thread calls it; begins and ends with a barrier.
-template <int W>
-__device__ __noinline__ void collect(Shared &sh, const float (&x)[kBatch], float most, int first, int limit, int top) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// The first `want` of the batch's logits that equal `value`, in order of their
+// index, to sh.list[n ...]; returns how many (x, first, limit: see collect()).
+// Every thread calls it; ends with a barrier.
+template <int W, int kThreads>
+__device__ __forceinline__ int in_order(Shared<kThreads> &sh, const float (&x)[kBatch], float value, int first, int limit,
+                                        int n, int want) {
+    constexpr int kWarps = Shared<kThreads>::kWarps;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto index_of_logit = [&](int k) { return first + k / W * (kThreads * W) + k % W; };
+    auto equal = [&](int k) {
+        const int i = index_of_logit(k);
+        return i >= 0 && i < limit && (value == -INFINITY ? !(x[k] > -INFINITY) : x[k] == value);
+    };
+    int found = 0;
+#pragma unroll
+    for (int r = 0; r < kBatch; r += W) {
+        if (found >= want) continue;                             // the same for all threads
+        int mine = 0;
+#pragma unroll
+        for (int j = 0; j < W; ++j) mine += equal(r + j);
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d) upto += y;
+        }
+        __syncthreads();
+        if (lane == 31) sh.scan[warp] = upto;
+        __syncthreads();
+        int at = found + upto - mine, all = 0;
+        for (int o = 0; o < kWarps; ++o) {
+            if (o < warp) at += sh.scan[o];
+            all += sh.scan[o];
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (equal(r + j)) {
+                if (at < want) sh.list[n + at] = key_of(x[r + j], index_of_logit(r + j));
+                ++at;
+            }
+        found += all;
+    }
+    __syncthreads();
+    return min(found, want);
+}
+
+// A batch of every thread: logit k of a thread has index first + k / W * kThreads
+// * W + k % W, and is there at all where that is in [0, limit) (else it reads
+// -inf).  Those that may be among the `top` largest go to the end of sh.list.
+// Every thread calls it; begins and ends with a barrier.
+template <int W, int kThreads>
+__device__ __noinline__ void collect(Shared<kThreads> &sh, const float (&x)[kBatch], float most, int first, int limit, int top) {
+    const int tid = threadIdx.x;
     if (tid == 0) sh.n_ties = 0;
-    bound_of_groups(sh, most, top);
+    const float bound = bound_of_groups(sh, most, top);
     const int before = sh.n;
-    const float bound = sh.bound;
     __syncthreads();
     if (most >= bound && most > -INFINITY)
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             if (!(x[k] >= bound) || !(x[k] > -INFINITY)) continue;
-            const uint64_t key = key_of(x[k], index_of_logit(k));
+            const uint64_t key = key_of(x[k], first + k / W * (kThreads * W) + k % W);
             if (x[k] > bound) {
                 sh.list[atomicAdd(&sh.n, 1)] = key;
             } else {
                 const int at = atomicAdd(&sh.n_ties, 1);
-                if (at < kTies) sh.ties[at] = key;
+                if (at < Shared<kThreads>::kTies) sh.ties[at] = key;
             }
         }
     __syncthreads();
-    const int n = sh.n, ties = sh.n_ties;
-    int add = ties;
-    if (ties <= kTies && bound > -INFINITY) {
-        if (tid < ties) sh.list[n + tid] = sh.ties[tid];
+    const int n = sh.n;
+    int add = sh.n_ties;
+    if (add <= Shared<kThreads>::kTies && bound > -INFINITY) {
+        if (tid < add) sh.list[n + tid] = sh.ties[tid];
     } else {
-        // as many as may be wanted of those equal to the bound, in order of their index
-        const int want = max(top - (n - before), 0);
-        auto equal = [&](int k) {
-            const int i = index_of_logit(k);
-            return i >= 0 && i < limit && (bound == -INFINITY ? !(x[k] > -INFINITY) : x[k] == bound);
-        };
-        add = 0;
-#pragma unroll
-        for (int r = 0; r < kBatch; r += W) {
-            if (add >= want) continue;                           // the same for all threads
-            int mine = 0;
-#pragma unroll
-            for (int j = 0; j < W; ++j) mine += equal(r + j);
-            int upto = mine;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-                if (lane >= d) upto += y;
-            }
-            __syncthreads();
-            if (lane == 31) sh.scan[warp] = upto;
-            __syncthreads();
-            int at = add + upto - mine, all = 0;
-            for (int o = 0; o < kWarps; ++o) {
-                if (o < warp) at += sh.scan[o];
-                all += sh.scan[o];
-            }
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                if (equal(r + j)) {
-                    if (at < want) sh.list[n + at] = key_of(x[r + j], index_of_logit(r + j));
-                    ++at;
-                }
-            add += all;
-        }
-        add = min(add, want);
+        add = in_order<W>(sh, x, bound, first, limit, n, max(top - (n - before), 0));
     }
     __syncthreads();
     if (tid == 0) sh.n = n + add;
     __syncthreads();
 }
 
-template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, bool kTop, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 token_logprobs_kernel(const Args p) {
-    __shared__ Shared sh;
+    using Sh = Shared<kThreads>;
+    __shared__ Sh sh;
     constexpr int W = Vec<T>::kCount, kRows = kBatch / W;        // vectors of a batch
+    constexpr int kWarps = Sh::kWarps;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cluster = 1 << p.cluster_bits, rank = int(blockIdx.x) & (cluster - 1), row = int(blockIdx.x) >> p.cluster_bits;
     grid_dep_wait();
@@ -362,16 +360,16 @@ token_logprobs_kernel(const Args p) {
     const int each = (vecs + cluster - 1) >> p.cluster_bits;
     const int begin = min(rank * each, vecs), end = min(begin + each, vecs);
     const int whole0 = shift > 0, whole1 = min(int((unsigned(p.V) + shift) / W), end);       // whole vectors: [whole0, whole1)
+    const int limit = min(end * W - shift, p.V);                 // this CTA's logits end here
 
     Sums mine{-INFINITY, 0.f, 0.f};
     float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
-    float bound = -INFINITY;
+    float bound = -INFINITY, most = -INFINITY;
     bool again = false;                          // the row once more, every batch collected by all
     if (kTop) {
-        if (tid == 0) sh.n = sh.n_ties = sh.n_notes = 0;
+        if (tid == 0) sh.n = sh.n_notes = 0;
         __syncthreads();
     }
-    const int first_end = (begin + kThreads * kLoads) * W - shift;       // a note of the first loads is below
     for (;;) {
         for (int v0 = begin; v0 == begin || v0 < end; v0 += kThreads * kLoads) {
             uint4 w[kLoads];
@@ -387,16 +385,16 @@ token_logprobs_kernel(const Args p) {
                     else w[i] = make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
                 }
             }
-            if (kTop && !again && v0 == begin) {
-                float top = -INFINITY, x[W];
+            const bool opening = kTop && !again && v0 == begin;
+            if (opening) {
+                float x[W];
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i) {
                     Vec<T>::get(w[i], x);
 #pragma unroll
-                    for (int k = 0; k < W; k += 2) top = max3(top, x[k], x[k + 1]);
+                    for (int k = 0; k < W; k += 2) most = max3(most, x[k], x[k + 1]);
                 }
-                bound_of_groups(sh, top, p.top);
-                bound = sh.bound;
+                bound = bound_of_groups(sh, most, p.top);
             }
 #pragma unroll
             for (int b = 0; b < kLoads; b += kRows) {
@@ -409,30 +407,27 @@ token_logprobs_kernel(const Args p) {
                 for (int k = 1; k < kBatch - 1; k += 2) top = max3(top, x[k], x[k + 1]);
                 top = max3(top, x[kBatch - 1], -INFINITY);
                 const int first = (v0 + b * kThreads + tid) * W - shift;
-                auto collect_all = [&] {                         // (a copy, so that x itself stays in registers)
-                    float y[kBatch];
+                if (kTop && (again || (opening && b == 0 && bound == -INFINITY))) {
+                    float y[kBatch];                             // (a copy, so that x itself stays in registers)
 #pragma unroll
                     for (int k = 0; k < kBatch; ++k) y[k] = x[k];
-                    collect<W>(sh, y, top, first, min(end * W - shift, p.V), p.top);
-                };
-                if (kTop && again) {
-                    collect_all();
-                    best_of_list(sh, p.top, sh.n);
-                    if (tid < p.top) sh.list[tid] = sh.best[tid];
-                    if (tid == 0) sh.n = p.top;
-                    continue;
+                    if (again) {
+                        collect<W>(sh, y, top, first, limit, p.top);
+                        best_of_list(sh, p.top, sh.n);
+                        if (tid < p.top) sh.list[tid] = sh.best[tid];
+                        if (tid == 0) sh.n = p.top;
+                        continue;
+                    }
+                    // Few groups hold a token above -inf, so the first batch has
+                    // all those of -inf that may be wanted (or it is all there is).
+                    const int n = in_order<W>(sh, y, -INFINITY, first, limit, 0, p.top);
+                    if (tid == 0) sh.n = n;
                 }
                 if (kTop) {
-                    bool note = top > bound || (v0 == begin && top == bound && bound > -INFINITY);
-                    if (b == 0 && v0 == begin && bound == -INFINITY) {
-                        // Few groups hold a token above -inf, so the first batch has
-                        // all those of -inf that may be wanted (or it is all there is).
-                        collect_all();
-                        note = false;
-                    }
-                    if (note) {
+                    most = fmaxf(most, top);
+                    if (top > bound || (opening && top == bound && bound > -INFINITY)) {
                         const int at = atomicAdd(&sh.n_notes, 1);
-                        if (at < kNotes) sh.notes[at] = first;
+                        if (at < Sh::kNotes) sh.notes[at] = Note{top, first};
                     }
                 }
                 if (top > mine.m + p.slack || (mine.m == -INFINITY && top > -INFINITY)) {
@@ -457,36 +452,25 @@ token_logprobs_kernel(const Args p) {
                 }
             }
         }
-        if (!kTop) break;
-        __syncthreads();
-        if (again) break;
+        if (!kTop || again) break;
+        const float second = bound_of_groups(sh, most, p.top);
         const int notes = sh.n_notes;
-        if (notes <= kNotes) {
+        if (notes <= Sh::kNotes) {
             for (int i = tid; i < notes * kRows; i += kThreads) {
-                const int first = sh.notes[i / kRows] + i % kRows * (kThreads * W), v = (first + shift) / W;
-                if (v >= end) continue;
+                const Note note = sh.notes[i / kRows];
+                const int first = note.first + i % kRows * (kThreads * W), v = (first + shift) / W;
+                if (note.most < second || v >= end) continue;
                 float x[W];
                 Vec<T>::get(v >= whole0 && v < whole1 ? base[v] : Vec<T>::some(x0, first, p.V), x);
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    if (x[j] > bound) {
+                for (int j = 0; j < W; ++j)
+                    if (x[j] >= second && x[j] > -INFINITY) {
                         const int at = atomicAdd(&sh.n, 1);
-                        if (at < kList) sh.list[at] = key_of(x[j], first + j);
-                    } else if (x[j] == bound && sh.notes[i / kRows] < first_end) {
-                        const int at = atomicAdd(&sh.n_ties, 1);
-                        if (at < kTies) sh.ties[at] = key_of(x[j], first + j);
+                        if (at < Sh::kKeys) sh.keys[at] = key_of(x[j], first + j);
                     }
-                }
             }
             __syncthreads();
-            const int n = sh.n, ties = bound > -INFINITY ? sh.n_ties : 0;
-            if (n + ties <= kList && ties <= kTies) {
-                if (tid < ties) sh.list[n + tid] = sh.ties[tid];
-                __syncthreads();
-                if (tid == 0) sh.n = n + ties;
-                __syncthreads();
-                break;
-            }
+            if (sh.n <= Sh::kKeys) break;
         }
         __syncthreads();
         if (tid == 0) sh.n = 0;
@@ -554,14 +538,19 @@ token_logprobs_kernel(const Args p) {
     cluster_sync_all();                          // no CTA leaves while its shared memory is read
 }
 
-template <typename T, bool kTop>
+template <typename T, bool kTop, int kThreads>
 w4v_status launch(const Args &a, int M, cudaStream_t stream) {
-    if (launch_pdl_cluster(token_logprobs_kernel<T, kTop>, dim3(unsigned(M) << a.cluster_bits), dim3(kThreads), 0, stream,
-                           1 << a.cluster_bits, a) != cudaSuccess) {
+    if (launch_pdl_cluster(token_logprobs_kernel<T, kTop, kThreads>, dim3(unsigned(M) << a.cluster_bits), dim3(kThreads),
+                           0, stream, 1 << a.cluster_bits, a) != cudaSuccess) {
         cudaGetLastError();
         return W4V_ERR_CUDA;
     }
     return W4V_OK;
+}
+
+template <typename T, bool kTop>
+w4v_status launch(const Args &a, int M, bool small, cudaStream_t stream) {
+    return small ? launch<T, kTop, 128>(a, M, stream) : launch<T, kTop, 512>(a, M, stream);
 }
 
 }  // namespace
@@ -586,14 +575,15 @@ w4v_status launch_token_logprobs(const void *logits, bool half, long long stride
     a.heat = 1.f / temperature;
     a.heat_log2 = 1.4426950408889634f / temperature;
     a.slack = kSlack / a.heat_log2;
+    const bool small = V <= kSmall;
     // Rows are cut while there are fewer CTAs than the GPU holds at a time and a
     // piece has more logits than its threads take at once.
     a.cluster_bits = 0;
     while (1 << a.cluster_bits < kMaxCluster && (long long)M << a.cluster_bits <= info->sm_count &&
-           V > kThreads * kBatch << a.cluster_bits)
+           V > (small ? 128 : 512) * kBatch << a.cluster_bits)
         ++a.cluster_bits;
-    if (half) return top > 0 ? launch<__half, true>(a, M, stream) : launch<__half, false>(a, M, stream);
-    return top > 0 ? launch<float, true>(a, M, stream) : launch<float, false>(a, M, stream);
+    if (half) return top > 0 ? launch<__half, true>(a, M, small, stream) : launch<__half, false>(a, M, small, stream);
+    return top > 0 ? launch<float, true>(a, M, small, stream) : launch<float, false>(a, M, small, stream);
 }
 
 }  // namespace w4v
