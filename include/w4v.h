@@ -568,6 +568,18 @@ w4v_status paged_attn(const w4v_kv_t *kv, const uint16_t *q, long long q_stride,
                       float scale, int window, uint16_t *out, float *lse, void *workspace,
                       size_t workspace_bytes, unsigned flags, w4v_stream_t stream);
 
+/* paged_attn with a window and a few first tokens of every sequence that
+ * stay visible (the system's prompt, or the tokens that a model lets idle
+ * attention rest on): row t sees the keys j <= p_t with
+ *     j > p_t - window  or  j < sinks.
+ * What lies between is not read.  Keys are attended as they lie in the cache,
+ * so positions are those that rope_append wrote them with.  sinks >= 0; with
+ * sinks == 0 or window == 0 (every token visible) this is paged_attn.  All
+ * else, W4V_BATCH_INVARIANT and the workspace among it, as paged_attn. */
+w4v_status paged_attn_sinks(const w4v_kv_t *kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
+                            float scale, int window, int sinks, uint16_t *out, float *lse, void *workspace,
+                            size_t workspace_bytes, unsigned flags, w4v_stream_t stream);
+
 /* ------------------------------------------------------------ kv_* pages --
  * Bookkeeping of the pages, on the device (the accepted lengths that drive
  * it are there).  A page id stands for that page of every plane: pool is

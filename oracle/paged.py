@@ -67,19 +67,20 @@ def token_places(lengths, offsets):
     return places
 
 
-def attention(q, k_cache, v_cache, table, lengths, offsets, scale, window=0):
+def attention(q, k_cache, v_cache, table, lengths, offsets, scale, window=0, sinks=0):
     """(out, lse, mag, absdot) of every new row in double; what error bounds go by: mag is
-    sum_j p_j |v_j|, absdot the largest scale sum_d |q_d k_jd| of a row's keys.  A row without a
-    visible key, or of no sequence (which paged_attn leaves alone): zeros and -inf."""
+    sum_j p_j |v_j|, absdot the largest scale sum_d |q_d k_jd| of a row's keys.  With a window the
+    `sinks` first keys are visible too.  A row without a visible key, or of no sequence (which
+    paged_attn leaves alone): zeros and -inf."""
     n, Hq, D = q.shape
     Hkv, page = k_cache.shape[1], k_cache.shape[2]
     out, mag = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
     lse, absdot = np.full((n, Hq), -np.inf), np.zeros((n, Hq))
     for t, (b, pos) in enumerate(token_places(lengths, offsets)):
         lo = max(0, pos - window + 1) if window else 0
-        if b < 0 or pos < lo:
+        if b < 0 or pos < lo or pos < 0:
             continue
-        js = np.arange(lo, pos + 1)
+        js = np.concatenate([np.arange(min(sinks, lo)), np.arange(lo, pos + 1)])
         ids = table[b][js // page]
         K = k_cache[ids, :, js % page].astype(np.float64)        # [keys][Hkv][D]
         V = v_cache[ids, :, js % page].astype(np.float64)

@@ -520,10 +520,16 @@ size_t paged_attn_workspace_bytes(int n_tokens, int B, int q_heads, int kv_heads
 w4v_status paged_attn(const w4v_kv_t *kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
                       float scale, int window, uint16_t *out, float *lse, void *ws, size_t ws_bytes, unsigned flags,
                       w4v_stream_t stream) {
+    return paged_attn_sinks(kv, q, q_stride, n_tokens, q_heads, scale, window, 0, out, lse, ws, ws_bytes, flags, stream);
+}
+
+w4v_status paged_attn_sinks(const w4v_kv_t *kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
+                            float scale, int window, int sinks, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
+                            unsigned flags, w4v_stream_t stream) {
     if ((flags & ~unsigned(W4V_BATCH_INVARIANT)) != 0u) return W4V_ERR_ARG;
     const w4v_status st = kv_check(kv, n_tokens, q_heads);
     if (st != W4V_OK) return st;
-    if (q_heads % kv->kv_heads != 0 || q_heads / kv->kv_heads > w4v::kAttnMaxGroup || window < 0 ||
+    if (q_heads % kv->kv_heads != 0 || q_heads / kv->kv_heads > w4v::kAttnMaxGroup || window < 0 || sinks < 0 ||
         !stride_ok(q_stride, q_heads, kv->head_dim))
         return W4V_ERR_SHAPE;
     // row tiles times key tiles of a whole table row (and the units that stand
@@ -540,7 +546,9 @@ w4v_status paged_attn(const w4v_kv_t *kv, const uint16_t *q, long long q_stride,
                                                              kv->table_width * kv->page, inv))
         return W4V_ERR_WORKSPACE;
     if (!w4v::aligned16(ws)) return W4V_ERR_ALIGN;
-    return w4v::launch_paged_attn(*kv, q, q_stride, n_tokens, q_heads, scale, window, out, lse, ws, inv,
+    // (first tokens past the table's are all that a row can see)
+    return w4v::launch_paged_attn(*kv, q, q_stride, n_tokens, q_heads, scale, window,
+                                  std::min(sinks, kv->table_width * kv->page), out, lse, ws, inv,
                                   reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -115,6 +115,10 @@ constexpr int kPartCost = 3;
 constexpr int kInvBits = 2;                     // least tiles of a batch-invariant part (2^this)
 constexpr int kInvParts = 32;                   // most parts of a row tile
 
+// What a row sees beside its own position and the window: nothing (kPlain), or
+// the sequence's first tokens (kSinks).
+enum Form { kPlain, kSinks };
+
 template <int D>
 struct Plan {
     static constexpr int kBlocks = D / 64;                       // 64-element blocks of a head
@@ -170,6 +174,8 @@ struct Args {
     int wide;                   // out is 32-byte aligned
     int B, width, n_pages, page_bits, slot_rows;   // 2^page_bits tokens a page
     int back;                   // keys that a row sees before its own (INT_MAX: all)
+    int sinks;                  // first keys that every row sees (kSinks)
+    int gap_mask;               // batch-invariant: -2 (a gap is an even number of tiles), else -1
     int invariant;              // batch-invariant: a part is one unit
     int unit_bits, part_cost;   // 2^unit_bits tiles per unit; units for the work beside a row tile's keys
     uint32_t max_units;         // of one key/value head: what the workspace (batch-invariant) and 32 bits hold
@@ -195,14 +201,30 @@ __device__ __forceinline__ Seq seq_of(const Args &p, int b) {
 // compiler makes a copy of a loop for each side of those.)
 struct Extent {
     int lo, hi, units;          // tiles [lo, hi)
+    int gap;                    // tiles left out between those of the first tokens and lo (kSinks)
 };
+// Tiles are numbered without the gap where one is left out: tile v is the
+// sequence's tile_of(v).
+__device__ __forceinline__ int sink_tiles(const Args &p) { return (p.sinks + kKeys - 1) >> kKeyBits; }
+template <int F>
+__device__ __forceinline__ int tile_of(const Args &p, int gap, int v) {
+    return F == kSinks && v >= sink_tiles(p) ? v + gap : v;
+}
+template <int F>
 __device__ __forceinline__ Extent extent_of(const Args &p, const Seq &s, int qt) {
     const int t0 = qt * p.tok, t1 = min(s.n, t0 + p.tok) - 1;
     const int p0 = max(s.len - s.n + t0, 0), p1 = max(s.len - s.n + t1, -1);
     Extent e;
     e.lo = max(p0 - p.back, 0) >> kKeyBits;
     e.hi = (p1 >> kKeyBits) + 1;
-    e.units = max(((e.hi - 1) >> p.unit_bits) - (e.lo >> p.unit_bits) + 1, 1) + p.part_cost;
+    e.gap = 0;
+    int left_out = 0;           // units that lie in the gap
+    if (F == kSinks) {
+        e.gap = max(e.lo - sink_tiles(p), 0) & p.gap_mask;
+        if (e.gap > 0) left_out = max(((sink_tiles(p) + e.gap) >> p.unit_bits) - ((sink_tiles(p) - 1) >> p.unit_bits) - 1, 0);
+        e.lo = 0;
+    }
+    e.units = max(((e.hi - 1) >> p.unit_bits) - (e.lo >> p.unit_bits) + 1 - left_out, 1) + p.part_cost;
     return e;
 }
 
@@ -214,6 +236,7 @@ __device__ __forceinline__ int row_tiles(const Args &p, int n) {
 // Units of one key/value head of 32 sequences, one per lane (0 past the end).
 // A lane counts a few row tiles by itself; the warp together those of a
 // sequence with more.
+template <int F>
 __device__ __forceinline__ int lane_units(const Args &p, int b) {
     constexpr int kFew = 4;
     const int lane = threadIdx.x & 31;
@@ -227,7 +250,7 @@ __device__ __forceinline__ int lane_units(const Args &p, int b) {
     for (bool own = true;; own = false) {        // the loop's body is there once
         int sum = 0;
 #pragma unroll 1
-        for (; qt < end; qt += step) sum += extent_of(p, o, qt).units;
+        for (; qt < end; qt += step) sum += extent_of<F>(p, o, qt).units;
         if (!own) sum = __reduce_add_sync(0xFFFFFFFFu, sum);
         if (lane == src) u += sum;
         if (many == 0) break;
@@ -277,6 +300,7 @@ struct Place {
 // the second one has the first one's counts.  The host has seen that rows
 // counted once fit; offsets that go up and down count rows again and again, so
 // the sum is looked at here, and too large a one leaves nothing to do (false).
+template <int F>
 __device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place &w, int &all, Split &split) {
     const int lane = threadIdx.x & 31;
     int u = 0, at = 0;
@@ -286,7 +310,7 @@ __device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            if (pass == 0 || p.B > 32) u = lane_units(p, b0 + lane);
+            if (pass == 0 || p.B > 32) u = lane_units<F>(p, b0 + lane);
             if (pass == 0) {
                 mine = min(mine + uint32_t(u), 0x7FFFFFFFu);
                 continue;
@@ -307,7 +331,7 @@ __device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place
             const int tiles = row_tiles(p, s.n);
 #pragma unroll 1
             for (int q0 = 0;; q0 += 32) {
-                const int tile = q0 + lane < tiles ? extent_of(p, s, q0 + lane).units : 0;
+                const int tile = q0 + lane < tiles ? extent_of<F>(p, s, q0 + lane).units : 0;
                 const int sum = warp_scan(tile);
                 const uint32_t over = __ballot_sync(0xFFFFFFFFu, sum > rest);
                 if (over != 0 || q0 >= tiles) {
@@ -341,6 +365,7 @@ struct Part {
     int b, kvh;
     int slot;                   // where its partial result goes, -1: it is the whole
     int u, units;               // its first unit, the row tile's (without kPartCost)
+    int gap;                    // tiles left out (kSinks; else not set)
 };
 static_assert(sizeof(Part) <= 48, "ring of parts");
 struct Cursor {
@@ -349,10 +374,11 @@ struct Cursor {
     Seq s;
     __device__ __forceinline__ void load(const Args &p) { s = seq_of(p, w.b); }
     // The next part, and the index of its first unit.
+    template <int F>
     __device__ __forceinline__ bool next(const Args &p, int cta, Part &g, int &first) {
         for (int take = 0; take == 0;) {
             if (left <= 0) return false;
-            const Extent e = extent_of(p, s, w.qt);
+            const Extent e = extent_of<F>(p, s, w.qt);
             const int t0 = w.qt * p.tok, toks = min(p.tok, s.n - t0);
             g.row0 = s.first + t0;
             g.rows = toks * p.group;
@@ -366,9 +392,23 @@ struct Cursor {
             const int step = min(e.units - w.u, p.invariant ? 1 : left);
             g.units -= p.part_cost;
             take = max(min(g.units - w.u, step), 0);         // none: a range may begin past the keys
-            const int c = ((e.lo >> p.unit_bits) + w.u) << p.unit_bits;
-            g.kt0 = max(e.lo, c);
-            g.nt = max(min(e.hi, c + (take << p.unit_bits)) - g.kt0, 0);
+            if (F == kSinks) {
+                // Unit u lies past the gap's units from the first one on that
+                // the first tokens do not reach; c and end are the sequence's
+                // tiles, kt0 and nt without the gap.
+                const int st = sink_tiles(p), past = ((st - 1) >> p.unit_bits) + 1;
+                const int left_out = e.gap > 0 ? max(((st + e.gap) >> p.unit_bits) - past, 0) : 0;
+                auto unit_at = [&](int u) { return (u >= past ? u + left_out : u) << p.unit_bits; };
+                auto without_gap = [&](int tile) { return min(tile, st) + max(tile - st - e.gap, 0); };
+                const int c = unit_at(w.u), end = min(e.hi, unit_at(w.u + max(take, 1) - 1) + (1 << p.unit_bits));
+                g.gap = e.gap;
+                g.kt0 = without_gap(c);
+                g.nt = take > 0 ? max(without_gap(end) - g.kt0, 0) : 0;
+            } else {
+                const int c = ((e.lo >> p.unit_bits) + w.u) << p.unit_bits;
+                g.kt0 = max(e.lo, c);
+                g.nt = max(min(e.hi, c + (take << p.unit_bits)) - g.kt0, 0);
+            }
             g.slot = p.invariant ? unit : 2 * cta + (w.u == 0);
             if (take == g.units) g.slot = -1;
             w.u += step;
@@ -415,8 +455,11 @@ __device__ __forceinline__ void clear_not_finite(uint4 &v) {
 // Whether a tile's values are looked over before the product: some row does
 // not see some key of it (the first row sees those up to pos0, the last one
 // those from keys_end - window on), or its last step has spare keys.
+template <int F>
 __device__ __forceinline__ bool guarded(const Args &p, int key, int keys_end, int pos0) {
     const int seen = min(keys_end - key, kKeys);
+    if (F == kSinks)                             // of the keys before the last row's window, the first ones are seen by all
+        return seen % 16 != 0 || pos0 + 1 - key < seen || (keys_end - 1 - p.back > max(key, p.sinks) && p.sinks < key + seen);
     return seen % 16 != 0 || pos0 + 1 - key < seen || (keys_end - 1 - p.back > key);
 }
 
@@ -437,7 +480,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
 }
 
 // ---------------------------------------------------------------- the kernel
-template <int D>
+template <int D, int F>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const Args p) {
@@ -538,7 +581,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         int all = 0;
         Split split;
         Cursor cur{};
-        if (!schedule(p, blockIdx.x, gridDim.x, cur.w, all, split) && blockIdx.x == 0 && lane == 0)
+        if (!schedule<F>(p, blockIdx.x, gridDim.x, cur.w, all, split) && blockIdx.x == 0 && lane == 0)
             atomicOr(p.status, 1u << kStatusShape);
         if (int(blockIdx.x) < split.ranges) {
             cur.unit = split.begin(blockIdx.x);
@@ -559,7 +602,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         for (int i = 0; ok; ++i) {
             Part g{};
             int unit = 0;
-            if (!cur.next(p, blockIdx.x, g, unit)) g.nt = -1;
+            if (!cur.next<F>(p, blockIdx.x, g, unit)) g.nt = -1;
             if (i >= kParts) ok = wait(part_empty(i % kParts), (i / kParts - 1) & 1);
             if (!ok) break;
             if (lane == 0) {
@@ -571,10 +614,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 // such batches at hand, so that each is loaded long before its use
                 // and V's, which runs behind K's, is still there.
                 const int32_t *row = p.table + size_t(g.b) * p.width;
+                // (box numbers leave the gap out, as tiles do; box_of gives the sequence's)
                 const int box0 = (g.kt0 * kKeys) >> box_bits;
+                auto box_of = [&](int box) { return F == kSinks && box >= sink_tiles(p) * boxes ? box + g.gap * boxes : box; };
                 const int all_boxes = ((g.keys_end - 1) >> box_bits) + 1;
                 auto batch = [&](int n) -> int {
-                    const int at = box0 + 32 * n + lane;
+                    const int at = box_of(box0 + 32 * n + lane);
                     return at < all_boxes ? row[at >> (p.page_bits - box_bits)] : -1;
                 };
                 int ids0 = batch(0), ids1 = batch(1), ids2 = -1;
@@ -584,11 +629,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     const int e = j * boxes, n = (e >> 5) % 3;
                     const int id = __shfl_sync(0xFFFFFFFFu, n == 0 ? ids0 : n == 1 ? ids1 : ids2, (e + lane) & 31);
                     const int at = id >= 0 && id < p.n_pages ? id * p.kv_heads + g.kvh : p.n_pages * p.kv_heads;
-                    return (at << group_bits) + (((box0 + e + lane) << (box_bits - 3)) & ((1 << group_bits) - 1));
+                    return (at << group_bits) + ((box_of(box0 + e + lane) << (box_bits - 3)) & ((1 << group_bits) - 1));
                 };
                 auto load = [&](const CUtensorMap *map, int j, int first, int depth, Stage &st) {
                     const int grp = group_of(j);
-                    const int n = min(all_boxes - (box0 + j * boxes), boxes);
+                    const int n = min(all_boxes - box_of(box0 + j * boxes), boxes);
 #pragma unroll 1
                     for (int h = 0; h < P::kHalves && ok; ++h) {
                         const int s = first + st.s;
@@ -727,17 +772,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         };
         for (int i = 0; __any_sync(0xFFFFFFFFu, acquire(i)); ++i) {
             const int nt = warp_uniform(part_of(i).nt), pos0 = warp_uniform(part_of(i).pos0);
-            const int key0 = warp_uniform(part_of(i).kt0 * kKeys), keys_end = warp_uniform(part_of(i).keys_end);
+            const int kt0 = warp_uniform(part_of(i).kt0), keys_end = warp_uniform(part_of(i).keys_end);
+            const int gap = F == kSinks ? warp_uniform(part_of(i).gap) : 0;
             release(i);
             if (nt == 0) continue;
-            bool look = guarded(p, key0, keys_end, pos0);
+            bool look = guarded<F>(p, tile_of<F>(p, gap, kt0) * kKeys, keys_end, pos0);
             ask(look);
             for (int j = 0; j < nt && ok; ++j, ++t) {
-                const int key = key0 + j * kKeys;
+                const int key = tile_of<F>(p, gap, kt0 + j) * kKeys;
                 // The guard works one tile ahead where that tile's stages were
                 // last filled before this one's: waiting for their next fill
                 // it then cannot take the one before for it.
-                const bool next = j + 1 < nt && guarded(p, key + kKeys, keys_end, pos0);
+                const bool next = j + 1 < nt && guarded<F>(p, tile_of<F>(p, gap, kt0 + j + 1) * kKeys, keys_end, pos0);
                 if (P::kStagesV >= 2 * P::kHalves) ask(next);
                 if (j == 0 && nq++ > 0) ok = wait(o_empty, nq & 1);          // the part before is read
                 ok = ok && wait(p_full(t & 1), (t >> 1) & 1);
@@ -789,8 +835,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             ++np;
             bool found = false;
             for (int j = 0; j < g.nt && ok; ++j) {
-                const int key = (g.kt0 + j) * kKeys;
-                if (!guarded(p, key, g.keys_end, g.pos0)) {
+                const int key = tile_of<F>(p, g.gap, g.kt0 + j) * kKeys;
+                if (!guarded<F>(p, key, g.keys_end, g.pos0)) {
                     it += P::kHalves;
                     continue;
                 }
@@ -836,7 +882,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
 #pragma unroll 1
                     for (int k = first; some && k < seen; k += kStep) {
                         uint4 v = *piece(k);
-                        if ((k >= below && k < above) || not_finite(v) == 0u) continue;
+                        if (((k >= below || (F == kSinks && k < p.sinks - key)) && k < above) || not_finite(v) == 0u) continue;
                         found = true;
                         clear_not_finite(v);
                         *piece(k) = v;
@@ -861,6 +907,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         int use = 0, pairs = 0;                              // references handed on, parts ended by this pair of warps
         for (int i = 0; acquire(i); ++i) {
             const int nt = part_of(i).nt, rows = part_of(i).rows, kt0 = part_of(i).kt0;
+            const int gap = F == kSinks ? part_of(i).gap : 0;
             np += nt > 0;
             const bool mine = row < rows;
             const bool busy = 32 * quad < rows;              // some row of this warp is in use
@@ -888,7 +935,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 }
                 tc_fence_after();
                 uint32_t x[4][32];
-                const int key = (kt0 + j) * kKeys;
+                const int key = tile_of<F>(p, gap, kt0 + j) * kKeys;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(tmem + lanes + sb * kKeys + 32 * k, x[k]);
 #pragma unroll
@@ -896,12 +943,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_empty(sb));     // the scores are in registers
-                if (key + kKeys - 1 > sure_hi || key < sure_lo) {
+                if (key + kKeys - 1 > sure_hi || (key < sure_lo && (F != kSinks || key + kKeys > p.sinks))) {
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         const int hi = pos - key - 32 * b, lo = from - key - 32 * b;         // keys lo .. hi are seen
-                        const uint32_t seen = (hi < 0 ? 0u : 0xFFFFFFFFu >> (31 - min(hi, 31))) &
-                                              (lo > 31 ? 0u : 0xFFFFFFFFu << max(lo, 0));
+                        uint32_t from_lo = lo > 31 ? 0u : 0xFFFFFFFFu << max(lo, 0);
+                        if (F == kSinks) {
+                            const int first = p.sinks - key - 32 * b;                        // and keys before first
+                            from_lo |= first <= 0 ? 0u : 0xFFFFFFFFu >> (32 - min(first, 32));
+                        }
+                        const uint32_t seen = (hi < 0 ? 0u : 0xFFFFFFFFu >> (31 - min(hi, 31))) & from_lo;
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             if ((seen & (1u << k)) == 0u) x[b][k] = 0xFF800000u;             // -inf
@@ -1096,9 +1147,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 // the values that were cleared, for a row that sees them: the
                 // weight is above 0, so they make the sum what they are
                 const int below = max(g.keys_end - 1 - p.back, 0);
-                const int last = min((kt0 + nt) * kKeys - 1, pos);
+                const int last = min((tile_of<F>(p, gap, kt0 + nt - 1) + 1) * kKeys - 1, pos);
 #pragma unroll 1
-                for (int k = max(kt0 * kKeys, from); k <= last; ++k) {
+                for (int k = F == kSinks ? tile_of<F>(p, gap, kt0) * kKeys : max(kt0 * kKeys, from); k <= last; ++k) {
+                    if (F == kSinks) {
+                        if (k < p.sinks && k <= g.pos0) k = min(p.sinks, g.pos0 + 1);     // seen by every row
+                        if (k >= p.sinks && k < from) k = from;                          // not by this one
+                    }
                     if (k >= below && k <= g.pos0) k = g.pos0 + 1;       // seen by every row: not cleared
                     if (k > last) break;
                     const int id = p.table[size_t(g.b) * p.width + (k >> p.page_bits)];
@@ -1279,21 +1334,21 @@ Slots slots_of(int n_tokens, int B, int q_heads, int kv_heads, int max_context, 
     return s;
 }
 
-template <int D>
+template <int D, int F>
 w4v_status launch(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap, const Args &a, int grid,
                   cudaStream_t stream) {
     static int configured_for = -1;
     int dev = 0;
     cudaGetDevice(&dev);
     if (configured_for != dev) {
-        if (cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(paged_attn_kernel<D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Plan<D>::kBytes) != cudaSuccess) {
             cudaGetLastError();
             return W4V_ERR_CUDA;
         }
         configured_for = dev;
     }
-    if (launch_pdl(paged_attn_kernel<D>, dim3(grid), dim3(kThreads), Plan<D>::kBytes, stream, qmap, kmap, vmap, a) !=
+    if (launch_pdl(paged_attn_kernel<D, F>, dim3(grid), dim3(kThreads), Plan<D>::kBytes, stream, qmap, kmap, vmap, a) !=
             cudaSuccess ||
         launch_pdl(paged_attn_join_kernel<D>, dim3(grid, kJoinSplit), dim3(kJoinThreads), 0, stream, a) != cudaSuccess) {
         cudaGetLastError();
@@ -1311,7 +1366,7 @@ size_t paged_attn_ws_bytes(int n_tokens, int B, int q_heads, int kv_heads, int h
 }
 
 w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
-                             float scale, int window, uint16_t *out, float *lse, void *ws, bool invariant,
+                             float scale, int window, int sinks, uint16_t *out, float *lse, void *ws, bool invariant,
                              cudaStream_t stream) {
     const DeviceInfo *info = nullptr;
     w4v_status st = device_info(&info);
@@ -1345,6 +1400,8 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     a.page_bits = 0;
     while (1 << a.page_bits < kv.page) ++a.page_bits;
     a.back = window > 0 ? window - 1 : INT_MAX;
+    a.sinks = sinks;
+    a.gap_mask = invariant ? -2 : -1;
     a.slot_rows = slots.rows;
     a.invariant = invariant;
     a.unit_bits = invariant ? inv_tile_bits(kv.table_width * kv.page) : 0;
@@ -1369,9 +1426,13 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
         st = encode_tmap_sw128(&vmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, kv.v, kv_dims, kv_strides, kv_box);
     if (st != W4V_OK) return st;
     const int grid = std::min(info->sm_count, kMaxCtas);
-    return D == 64 ? launch<64>(qmap, kmap, vmap, a, grid, stream)
-                   : D == 128 ? launch<128>(qmap, kmap, vmap, a, grid, stream)
-                              : launch<256>(qmap, kmap, vmap, a, grid, stream);
+    if (sinks > 0 && window > 0)
+        return D == 64 ? launch<64, kSinks>(qmap, kmap, vmap, a, grid, stream)
+                       : D == 128 ? launch<128, kSinks>(qmap, kmap, vmap, a, grid, stream)
+                                  : launch<256, kSinks>(qmap, kmap, vmap, a, grid, stream);
+    return D == 64 ? launch<64, kPlain>(qmap, kmap, vmap, a, grid, stream)
+                   : D == 128 ? launch<128, kPlain>(qmap, kmap, vmap, a, grid, stream)
+                              : launch<256, kPlain>(qmap, kmap, vmap, a, grid, stream);
 }
 
 }  // namespace w4v

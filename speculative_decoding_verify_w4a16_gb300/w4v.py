@@ -129,6 +129,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.paged_attn_workspace_bytes.restype = S
             lib.paged_attn.argtypes = [P, P, L, I, I, F, I, P, P, P, S, U, P]
             lib.paged_attn.restype = I
+            lib.paged_attn_sinks.argtypes = [P, P, L, I, I, F, I, I, P, P, P, S, U, P]
+            lib.paged_attn_sinks.restype = I
             lib.kv_workspace_bytes.argtypes = [I, I]
             lib.kv_workspace_bytes.restype = S
             lib.kv_extend.argtypes = [P, P, P, P, S, P]
@@ -635,9 +637,10 @@ def paged_attn_workspace_bytes(n_tokens: int, B: int, q_heads: int, kv_heads: in
 
 
 def paged_attn(q, k_cache, v_cache, table, lengths, offsets, scale=None, window: int = 0, out=None, lse=None, ws=None,
-               stream=None, batch_invariant=False):
+               stream=None, batch_invariant=False, sinks: int = 0):
     """Causal attention of the new tokens' q [n][Hq][D] over the paged cache that holds them (scale
-    1/sqrt(D) unless given; window > 0: the last `window` tokens only).  Returns out [n][Hq][D].
+    1/sqrt(D) unless given; window > 0: the last `window` tokens only, and with `sinks` the sequence's first
+    ones).  Returns out [n][Hq][D].
     lse: float [n][Hq] to fill with the rows' log-sum-exp.
     Rows that no sequence's offsets cover are not written: in a new `out` they hold anything.
     batch_invariant: each row's result does not depend on what shares the call (W4V_BATCH_INVARIANT), as
@@ -654,9 +657,9 @@ def paged_attn(q, k_cache, v_cache, table, lengths, offsets, scale=None, window:
         raise W4VError(ERR_SHAPE if lse.shape != (n, Hq) else ERR_ARG, where)
     if ws is None:
         ws = workspace(paged_attn_workspace_bytes(n, B, Hq, heads, D, width * page, batch_invariant), q.device, stream)
-    code = load().paged_attn(kv, q.data_ptr(), stride, n, Hq, D ** -0.5 if scale is None else scale, int(window),
-                             out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
-                             BATCH_INVARIANT if batch_invariant else 0, _stream(stream))
+    code = load().paged_attn_sinks(kv, q.data_ptr(), stride, n, Hq, D ** -0.5 if scale is None else scale, int(window),
+                                   int(sinks), out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(),
+                                   ws.numel(), BATCH_INVARIANT if batch_invariant else 0, _stream(stream))
     if code != OK:
         raise W4VError(code, where)
     return out

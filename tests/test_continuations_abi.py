@@ -104,3 +104,25 @@ def test_binding_refuses_logprob_tensors(w4v_mod):
     assert code(x, t, top=4, out=out(3)) == w.ERR_SHAPE
     assert code(x, t, top=3, out=out(3)[:2] + (torch.zeros(3, 3), torch.zeros(3, 3))) == w.ERR_ARG
     assert code(x, t) == code(x, t, top=3, out=out(3)) == w.ERR_ARG      # tensors of the host
+
+
+def test_sinks_refusals(w4v_mod):
+    w = w4v_mod
+
+    def call(kv=None, q=FAKE, stride=2560, n=8, heads=20, scale=0.1, window=9, sinks=4, out=FAKE, lse=None, ws=FAKE,
+             nb=BIG, flags=0):
+        return w.load().paged_attn_sinks(_kv(w) if kv is None else kv, q, stride, n, heads, scale, window, sinks, out, lse,
+                                         ws, nb, flags, None)
+    for kw, code in KV_FAULTS:
+        assert call(kv=_kv(w, **kw)) == getattr(w, "ERR_" + code)
+    assert w.load().paged_attn_sinks(None, FAKE, 2560, 8, 20, 0.1, 9, 4, FAKE, None, FAKE, BIG, 0, None) == w.ERR_ARG
+    assert call(sinks=-1) == call(window=-1) == call(n=-1) == call(heads=18) == call(stride=2552) == w.ERR_SHAPE
+    assert call(flags=4) == call(scale=0.0) == call(q=None) == call(out=None) == w.ERR_ARG
+    assert call(q=FAKE + 8) == call(out=FAKE + 2) == call(lse=FAKE + 2) == call(ws=FAKE + 4) == w.ERR_ALIGN
+    assert call(ws=None) == call(nb=16) == call(nb=16, flags=2) == w.ERR_WORKSPACE
+    assert call(n=0, q=None, out=None, ws=None) == call(kv=_kv(w, B=0), q=None, ws=None) == w.OK
+    t = _tensors()
+    with pytest.raises(w.W4VError) as e:
+        w.paged_attn(t["q"], t["k"], t["k"], t["table"], t["lens"], t["offs"], window=4, sinks=-1,
+                     ws=torch.zeros(1 << 24, dtype=torch.uint8), stream=0)
+    assert e.value.code == w.ERR_SHAPE

@@ -91,3 +91,13 @@ def test_head_norm_by_hand():
     assert np.allclose(paged.head_norm(x, eps=0.0 + 1e-300)[0, 0], [1.2, 1.6, 0, 0])
     assert np.allclose(paged.head_norm(x, [1, 0.5, 1, 1], 1e-300, 1.0)[0, 0], [2.4, 2.4, 0, 0])
     assert np.allclose(paged.head_norm(x, None, 6.25 * 3)[0, 0], [0.6, 0.8, 0, 0]) and not paged.head_norm(x)[0, 1].any()
+
+
+def test_first_tokens_by_hand():
+    """Five tokens, a window of one, two first ones: the last row averages tokens 0, 1 and 4, the second 0 and 1, once."""
+    q = np.zeros((5, 1, 64), np.float16)
+    k = np.zeros((1, 1, 8, 64), np.float16)
+    v = np.zeros((1, 1, 8, 64), np.float16)
+    v[0, 0, :5, 0] = 1, 2, 4, 8, 16
+    o, lse, _, _ = paged.attention(q, k, v, np.array([[0]]), [5], [0, 5], 1.0, window=1, sinks=2)
+    assert np.allclose(o[:, 0, 0], [1, 1.5, 7 / 3, 11 / 3, 19 / 3]) and np.allclose(np.exp(lse[:, 0]), [1, 2, 3, 3, 3])
