@@ -124,5 +124,5 @@ def test_sinks_refusals(w4v_mod):
     t = _tensors()
     with pytest.raises(w.W4VError) as e:
         w.paged_attn(t["q"], t["k"], t["k"], t["table"], t["lens"], t["offs"], window=4, sinks=-1,
-                     ws=torch.zeros(1 << 24, dtype=torch.uint8), stream=0)
+                     out=torch.zeros_like(t["q"]), ws=torch.zeros(1 << 24, dtype=torch.uint8), stream=0)
     assert e.value.code == w.ERR_SHAPE
