@@ -580,6 +580,34 @@ w4v_status paged_attn_sinks(const w4v_kv_t *kv, const uint16_t *q, long long q_s
                             float scale, int window, int sinks, uint16_t *out, float *lse, void *workspace,
                             size_t workspace_bytes, unsigned flags, w4v_stream_t stream);
 
+/* paged_attn (without a window) for sequences that share a prefix, whose keys
+ * and values are then read once for all of them: continuations of one prompt,
+ * as kv_fork leaves them, requests behind one system prompt.  Group g is the
+ * batch's sequences groups[g] .. groups[g+1]-1, and the first prefix[g] tokens
+ * of each are the same; they are read from the pages of the group's first
+ * sequence, in whole pages and in the partly filled one behind them (which
+ * kv_fork copies).  The rows' results are those of paged_attn up to the order
+ * of the sums.
+ *   groups  device, int32 [n_groups + 1], not decreasing; sequences outside
+ *           [groups[0], groups[n_groups]) share nothing
+ *   prefix  device, int32 [n_groups]
+ * The device arrays are read as they are: a group whose first sequence holds
+ * fewer than prefix[g] tokens shares nothing (so when a group's first sequence
+ * ends, begin the group behind it), and neither does a sequence with fewer
+ * than prefix[g] tokens before its new ones; those attend over their own pages.
+ * Sequences without new tokens may lie anywhere in a group.
+ * flags must be 0 (how a row's sum is cut depends on the batch).  Sizes as
+ * paged_attn, n_groups from 0 to 2^24, and (2 (n_tokens / tok) + min(B,
+ * n_tokens) + min(n_groups, n_tokens)) * kv_heads * (table_width * page / 128
+ * + 5) < 2^31.
+ * Workspace: paged_attn_shared_workspace_bytes(...) with the call's own
+ * n_tokens or a larger one, zero-filled before first use; it holds two results
+ * of each row in 32 bits. */
+size_t paged_attn_shared_workspace_bytes(int n_tokens, int B, int n_groups, int q_heads, int kv_heads, int head_dim);
+w4v_status paged_attn_shared(const w4v_kv_t *kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
+                             float scale, const int32_t *groups, const int32_t *prefix, int n_groups, uint16_t *out,
+                             float *lse, void *workspace, size_t workspace_bytes, unsigned flags, w4v_stream_t stream);
+
 /* ------------------------------------------------------------ kv_* pages --
  * Bookkeeping of the pages, on the device (the accepted lengths that drive
  * it are there).  A page id stands for that page of every plane: pool is

@@ -523,24 +523,40 @@ w4v_status paged_attn(const w4v_kv_t *kv, const uint16_t *q, long long q_stride,
     return paged_attn_sinks(kv, q, q_stride, n_tokens, q_heads, scale, window, 0, out, lse, ws, ws_bytes, flags, stream);
 }
 
-w4v_status paged_attn_sinks(const w4v_kv_t *kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
-                            float scale, int window, int sinks, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
-                            unsigned flags, w4v_stream_t stream) {
-    if ((flags & ~unsigned(W4V_BATCH_INVARIANT)) != 0u) return W4V_ERR_ARG;
+namespace {
+// What paged_attn_sinks and paged_attn_shared check alike; `sizes`: whether what
+// they have apart is in range.  *done: nothing to compute.
+w4v_status attention_check(const w4v_kv_t *kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads, float scale,
+                           bool sizes, int groups, const uint16_t *out, const float *lse, bool *done) {
+    *done = false;
     const w4v_status st = kv_check(kv, n_tokens, q_heads);
     if (st != W4V_OK) return st;
-    if (q_heads % kv->kv_heads != 0 || q_heads / kv->kv_heads > w4v::kAttnMaxGroup || window < 0 || sinks < 0 ||
+    if (q_heads % kv->kv_heads != 0 || q_heads / kv->kv_heads > w4v::kAttnMaxGroup || !sizes ||
         !stride_ok(q_stride, q_heads, kv->head_dim))
         return W4V_ERR_SHAPE;
     // row tiles times key tiles of a whole table row (and the units that stand
     // for a row tile's other work): counted in 32 bits
     const int tok = w4v::kAttnMaxGroup / (q_heads / kv->kv_heads);
-    const double tiles = double(n_tokens / tok + std::min(kv->B, n_tokens)) * kv->kv_heads;
-    if (tiles * (double(kv->table_width) * kv->page / 128 + 5) >= 2147483648.0) return W4V_ERR_SHAPE;
+    double tiles = n_tokens / tok + std::min(kv->B, n_tokens);
+    if (groups > 0) tiles += n_tokens / tok + std::min(groups, n_tokens);
+    if (tiles * kv->kv_heads * (double(kv->table_width) * kv->page / 128 + 5) >= 2147483648.0) return W4V_ERR_SHAPE;
     if (!(scale > 0.f) || !std::isfinite(scale)) return W4V_ERR_ARG;
-    if (n_tokens == 0 || kv->B == 0) return W4V_OK;
+    *done = n_tokens == 0 || kv->B == 0;
+    if (*done) return W4V_OK;
     if (q == nullptr || out == nullptr) return W4V_ERR_ARG;
     if (!w4v::aligned16(q) || !w4v::aligned16(out) || !aligned4(lse)) return W4V_ERR_ALIGN;
+    return W4V_OK;
+}
+}  // namespace
+
+w4v_status paged_attn_sinks(const w4v_kv_t *kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
+                            float scale, int window, int sinks, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
+                            unsigned flags, w4v_stream_t stream) {
+    if ((flags & ~unsigned(W4V_BATCH_INVARIANT)) != 0u) return W4V_ERR_ARG;
+    bool done;
+    const w4v_status st =
+        attention_check(kv, q, q_stride, n_tokens, q_heads, scale, window >= 0 && sinks >= 0, 0, out, lse, &done);
+    if (st != W4V_OK || done) return st;
     const bool inv = (flags & W4V_BATCH_INVARIANT) != 0u;
     if (ws == nullptr || ws_bytes < w4v::paged_attn_ws_bytes(n_tokens, kv->B, q_heads, kv->kv_heads, kv->head_dim,
                                                              kv->table_width * kv->page, inv))
@@ -548,7 +564,30 @@ w4v_status paged_attn_sinks(const w4v_kv_t *kv, const uint16_t *q, long long q_s
     if (!w4v::aligned16(ws)) return W4V_ERR_ALIGN;
     // (first tokens past the table's are all that a row can see)
     return w4v::launch_paged_attn(*kv, q, q_stride, n_tokens, q_heads, scale, window,
-                                  std::min(sinks, kv->table_width * kv->page), out, lse, ws, inv,
+                                  std::min(sinks, kv->table_width * kv->page), nullptr, out, lse, ws, inv,
+                                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t paged_attn_shared_workspace_bytes(int n_tokens, int B, int n_groups, int q_heads, int kv_heads, int head_dim) {
+    if (n_groups < 0 || paged_attn_workspace_bytes(n_tokens, B, q_heads, kv_heads, head_dim, 0, 0u) == 0) return 0;
+    return w4v::paged_attn_shared_ws_bytes(n_tokens, q_heads, kv_heads, head_dim);
+}
+
+w4v_status paged_attn_shared(const w4v_kv_t *kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
+                             float scale, const int32_t *groups, const int32_t *prefix, int n_groups, uint16_t *out,
+                             float *lse, void *ws, size_t ws_bytes, unsigned flags, w4v_stream_t stream) {
+    if (flags != 0u) return W4V_ERR_ARG;
+    bool done;
+    const w4v_status st = attention_check(kv, q, q_stride, n_tokens, q_heads, scale, n_groups >= 0 && n_groups <= 1 << 24,
+                                          n_groups, out, lse, &done);
+    if (st != W4V_OK || done) return st;
+    if (n_groups > 0 && (groups == nullptr || prefix == nullptr)) return W4V_ERR_ARG;
+    if (!aligned4(groups) || !aligned4(prefix)) return W4V_ERR_ALIGN;
+    if (ws == nullptr || ws_bytes < w4v::paged_attn_shared_ws_bytes(n_tokens, q_heads, kv->kv_heads, kv->head_dim))
+        return W4V_ERR_WORKSPACE;
+    if (!w4v::aligned16(ws)) return W4V_ERR_ALIGN;
+    const w4v::PrefixGroups shared{groups, prefix, n_groups};
+    return w4v::launch_paged_attn(*kv, q, q_stride, n_tokens, q_heads, scale, 0, 0, &shared, out, lse, ws, false,
                                   reinterpret_cast<cudaStream_t>(stream));
 }
 

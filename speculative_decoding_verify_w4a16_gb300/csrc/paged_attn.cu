@@ -115,9 +115,10 @@ constexpr int kPartCost = 3;
 constexpr int kInvBits = 2;                     // least tiles of a batch-invariant part (2^this)
 constexpr int kInvParts = 32;                   // most parts of a row tile
 
-// What a row sees beside its own position and the window: nothing (kPlain), or
-// the sequence's first tokens (kSinks).
-enum Form { kPlain, kSinks };
+// The forms of a call, each a kernel of its own: kPlain, all tokens or a window;
+// kSinks, a window and the sequences' first tokens; kShared, groups of sequences
+// with a common prefix.
+enum Form { kPlain, kSinks, kShared };
 
 template <int D>
 struct Plan {
@@ -154,7 +155,8 @@ struct __align__(16) Share {
     int slot0, n;
     int n_mul;                  // 2^20 / n, rounded up: k * n_mul >> 20 is k / n for k < 1024
     int block;                  // rows that are fetched at a time
-    int count;                  // batch-invariant, entry 0: how many entries there are (default: one per range)
+    int count;                  // batch-invariant, entry 0: how many entries there are (default: one per range);
+                                // kShared: 0 of a prefix, 1 of what follows it
 };
 template <int D>
 constexpr int kHeld = D == 256 ? 40 : 12288 / (2 * D);      // rows of parts that it holds at a time
@@ -181,17 +183,60 @@ struct Args {
     uint32_t max_units;         // of one key/value head: what the workspace (batch-invariant) and 32 bits hold
     struct Share *shares;       // what the second kernel joins
     float scale_log2;
+    // kShared: group g is sequences [groups[g], groups[g + 1]) with prefix[g] tokens in common
+    const int32_t *groups, *prefix;
+    int n_groups;
+    float *res_o;               // [2][n_tokens q_heads][D]: over the prefixes, over what follows them
+    float2 *res_ml;             // [2][n_tokens q_heads]
+    int *planned;               // 1, or 0 where nothing was done
 };
 
 // ------------------------------------------------------------------ schedule
 struct Seq {
     int first, n, len;          // its rows, their count, cached tokens
+    int row, from;              // kShared: its row of the table; keys before this one are not its own (a prefix: -1)
 };
+__device__ __forceinline__ int offset_at(const Args &p, int b) { return min(max(p.offsets[b], 0), p.n_tokens); }
+__device__ __forceinline__ int length_at(const Args &p, int b) { return min(max(p.lengths[b], 0), p.width << p.page_bits); }
+
+// kShared counts the groups' prefixes as sequences of their own, before the
+// others: the rows of a prefix are those of all its sequences (they follow one
+// another), each of which sees every key of it.
+template <int F>
+__device__ __forceinline__ int sequences(const Args &p) { return F == kShared ? p.n_groups + p.B : p.B; }
+__device__ __forceinline__ Seq prefix_of(const Args &p, int g) {
+    const int b0 = min(max(p.groups[g], 0), p.B), b1 = min(max(p.groups[g + 1], 0), p.B);
+    Seq s{0, 0, 0, b0, -1};
+    if (b0 >= b1) return s;
+    s.first = offset_at(p, b0);
+    s.len = max(p.prefix[g], 0);
+    if (s.len > 0 && s.len <= length_at(p, b0)) s.n = max(offset_at(p, b1) - s.first, 0);
+    return s;
+}
+template <int F>
 __device__ __forceinline__ Seq seq_of(const Args &p, int b) {
+    if (F == kShared && b < p.n_groups) return prefix_of(p, b);
+    if (F == kShared) b -= p.n_groups;
     Seq s;
-    s.first = min(max(p.offsets[b], 0), p.n_tokens);
-    s.n = max(min(max(p.offsets[b + 1], 0), p.n_tokens) - s.first, 0);
-    s.len = min(max(p.lengths[b], 0), p.width << p.page_bits);
+    s.first = offset_at(p, b);
+    s.n = max(offset_at(p, b + 1) - s.first, 0);
+    s.len = length_at(p, b);
+    s.row = b;
+    s.from = 0;
+    if (F == kShared && p.n_groups > 0) {
+        int g = 0;                               // the last group that begins at or before b
+        for (int end = p.n_groups; end - g > 1;) {
+            const int mid = (g + end) >> 1;
+            if (p.groups[mid] <= b) g = mid;
+            else end = mid;
+        }
+        // It shares the prefix where the group's rows hold its own and all of
+        // them come after the prefix; else it reads its own pages from the first.
+        const Seq x = prefix_of(p, g);
+        if (p.groups[g] <= b && b < p.groups[g + 1] && s.first >= x.first && s.first + s.n <= x.first + x.n &&
+            x.len <= s.len - s.n)
+            s.from = x.len;
+    }
     return s;
 }
 
@@ -215,8 +260,8 @@ __device__ __forceinline__ Extent extent_of(const Args &p, const Seq &s, int qt)
     const int t0 = qt * p.tok, t1 = min(s.n, t0 + p.tok) - 1;
     const int p0 = max(s.len - s.n + t0, 0), p1 = max(s.len - s.n + t1, -1);
     Extent e;
-    e.lo = max(p0 - p.back, 0) >> kKeyBits;
-    e.hi = (p1 >> kKeyBits) + 1;
+    e.lo = (F == kShared ? max(s.from, 0) : max(p0 - p.back, 0)) >> kKeyBits;
+    e.hi = ((F == kShared && s.from < 0 ? s.len - 1 : p1) >> kKeyBits) + 1;
     e.gap = 0;
     int left_out = 0;           // units that lie in the gap
     if (F == kSinks) {
@@ -240,8 +285,8 @@ template <int F>
 __device__ __forceinline__ int lane_units(const Args &p, int b) {
     constexpr int kFew = 4;
     const int lane = threadIdx.x & 31;
-    Seq s{0, 0, 0};
-    if (b < p.B) s = seq_of(p, b);
+    Seq s{0, 0, 0, 0, 0};
+    if (b < sequences<F>(p)) s = seq_of<F>(p, b);
     const int tiles = row_tiles(p, s.n);
     uint32_t many = __ballot_sync(0xFFFFFFFFu, tiles > kFew);
     Seq o = s;
@@ -256,7 +301,8 @@ __device__ __forceinline__ int lane_units(const Args &p, int b) {
         if (many == 0) break;
         src = __ffs(many) - 1;
         many &= many - 1;
-        o = Seq{0, __shfl_sync(0xFFFFFFFFu, s.n, src), __shfl_sync(0xFFFFFFFFu, s.len, src)};
+        o = Seq{0, __shfl_sync(0xFFFFFFFFu, s.n, src), __shfl_sync(0xFFFFFFFFu, s.len, src), 0,
+                F == kShared ? __shfl_sync(0xFFFFFFFFu, s.from, src) : 0};
         qt = kFew + lane;
         end = __shfl_sync(0xFFFFFFFFu, tiles, src);
         step = 32;
@@ -309,8 +355,8 @@ __device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            if (pass == 0 || p.B > 32) u = lane_units<F>(p, b0 + lane);
+        for (int b0 = 0; b0 < sequences<F>(p); b0 += 32) {
+            if (pass == 0 || sequences<F>(p) > 32) u = lane_units<F>(p, b0 + lane);
             if (pass == 0) {
                 mine = min(mine + uint32_t(u), 0x7FFFFFFFu);
                 continue;
@@ -327,7 +373,7 @@ __device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place
             w.b = b0 + src;
             w.kvh = at / su;
             int rest = at - w.kvh * su;
-            const Seq s = seq_of(p, w.b);
+            const Seq s = seq_of<F>(p, w.b);
             const int tiles = row_tiles(p, s.n);
 #pragma unroll 1
             for (int q0 = 0;; q0 += 32) {
@@ -365,14 +411,15 @@ struct Part {
     int b, kvh;
     int slot;                   // where its partial result goes, -1: it is the whole
     int u, units;               // its first unit, the row tile's (without kPartCost)
-    int gap;                    // tiles left out (kSinks; else not set)
+    int gap;                    // kSinks: tiles left out; kShared: the sequence's `from`
 };
 static_assert(sizeof(Part) <= 48, "ring of parts");
 struct Cursor {
     Place w;
     int unit, left;             // index of the next unit, units left in the range
     Seq s;
-    __device__ __forceinline__ void load(const Args &p) { s = seq_of(p, w.b); }
+    template <int F>
+    __device__ __forceinline__ void load(const Args &p) { s = seq_of<F>(p, w.b); }
     // The next part, and the index of its first unit.
     template <int F>
     __device__ __forceinline__ bool next(const Args &p, int cta, Part &g, int &first) {
@@ -382,9 +429,10 @@ struct Cursor {
             const int t0 = w.qt * p.tok, toks = min(p.tok, s.n - t0);
             g.row0 = s.first + t0;
             g.rows = toks * p.group;
-            g.pos0 = s.len - s.n + t0;
-            g.keys_end = max(g.pos0 + toks, 0);
-            g.b = w.b;
+            const bool prefix = F == kShared && s.from < 0;
+            g.pos0 = prefix ? s.len - 1 : s.len - s.n + t0;
+            g.keys_end = prefix ? s.len : max(g.pos0 + toks, 0);
+            g.b = F == kShared ? s.row : w.b;
             g.kvh = w.kvh;
             g.u = w.u;
             g.units = e.units;
@@ -406,6 +454,7 @@ struct Cursor {
                 g.nt = take > 0 ? max(without_gap(end) - g.kt0, 0) : 0;
             } else {
                 const int c = ((e.lo >> p.unit_bits) + w.u) << p.unit_bits;
+                if (F == kShared) g.gap = s.from;
                 g.kt0 = max(e.lo, c);
                 g.nt = max(min(e.hi, c + (take << p.unit_bits)) - g.kt0, 0);
             }
@@ -426,8 +475,8 @@ struct Cursor {
 #pragma unroll 1
                         do {
                             ++w.b;
-                            load(p);
-                        } while (s.n == 0 && w.b < p.B - 1);
+                            load<F>(p);
+                        } while (s.n == 0 && w.b < sequences<F>(p) - 1);
                     }
                 }
             }
@@ -456,11 +505,11 @@ __device__ __forceinline__ void clear_not_finite(uint4 &v) {
 // not see some key of it (the first row sees those up to pos0, the last one
 // those from keys_end - window on), or its last step has spare keys.
 template <int F>
-__device__ __forceinline__ bool guarded(const Args &p, int key, int keys_end, int pos0) {
+__device__ __forceinline__ bool guarded(const Args &p, int key, int keys_end, int pos0, int gap) {
     const int seen = min(keys_end - key, kKeys);
     if (F == kSinks)                             // of the keys before the last row's window, the first ones are seen by all
         return seen % 16 != 0 || pos0 + 1 - key < seen || (keys_end - 1 - p.back > max(key, p.sinks) && p.sinks < key + seen);
-    return seen % 16 != 0 || pos0 + 1 - key < seen || (keys_end - 1 - p.back > key);
+    return seen % 16 != 0 || pos0 + 1 - key < seen || (F == kShared ? gap : keys_end - 1 - p.back) > key;
 }
 
 // A whole warp's wait for a phase, in as few instructions as it takes: they
@@ -581,12 +630,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         int all = 0;
         Split split;
         Cursor cur{};
-        if (!schedule<F>(p, blockIdx.x, gridDim.x, cur.w, all, split) && blockIdx.x == 0 && lane == 0)
-            atomicOr(p.status, 1u << kStatusShape);
+        const bool planned = schedule<F>(p, blockIdx.x, gridDim.x, cur.w, all, split);
+        if (!planned && blockIdx.x == 0 && lane == 0) atomicOr(p.status, 1u << kStatusShape);
+        if (F == kShared && blockIdx.x == 0 && lane == 0) *p.planned = planned;
         if (int(blockIdx.x) < split.ranges) {
             cur.unit = split.begin(blockIdx.x);
             cur.left = split.begin(blockIdx.x + 1) - cur.unit;
-            cur.load(p);
+            cur.load<F>(p);
         }
         const int box_bits = min(p.page_bits, 7);            // 2^box_bits tokens per TMA box
         const uint32_t box_bytes = P::kGroupBytes << (box_bits - 3);
@@ -674,7 +724,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             // the share of this range's first row tile, or of every unit's
             // (here, behind the loads, for the second kernel alone reads it)
             if (lane == 0 && (p.invariant ? g.nt >= 0 || all == 0 : i == 0)) {
-                Share e{g.row0, g.kvh, 0, unit - g.u, 0, 0, 1, p.invariant ? all : int(gridDim.x)};
+                Share e{g.row0, g.kvh, 0, unit - g.u, 0, 0, 1, F == kShared ? g.gap >= 0 : p.invariant ? all : int(gridDim.x)};
                 int share = g.u, shares = g.units;
                 if (p.invariant) {
                     e.n = g.units > 1 ? g.units : 0;
@@ -773,17 +823,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         for (int i = 0; __any_sync(0xFFFFFFFFu, acquire(i)); ++i) {
             const int nt = warp_uniform(part_of(i).nt), pos0 = warp_uniform(part_of(i).pos0);
             const int kt0 = warp_uniform(part_of(i).kt0), keys_end = warp_uniform(part_of(i).keys_end);
-            const int gap = F == kSinks ? warp_uniform(part_of(i).gap) : 0;
+            const int gap = F != kPlain ? warp_uniform(part_of(i).gap) : 0;
             release(i);
             if (nt == 0) continue;
-            bool look = guarded<F>(p, tile_of<F>(p, gap, kt0) * kKeys, keys_end, pos0);
+            bool look = guarded<F>(p, tile_of<F>(p, gap, kt0) * kKeys, keys_end, pos0, gap);
             ask(look);
             for (int j = 0; j < nt && ok; ++j, ++t) {
                 const int key = tile_of<F>(p, gap, kt0 + j) * kKeys;
                 // The guard works one tile ahead where that tile's stages were
                 // last filled before this one's: waiting for their next fill
                 // it then cannot take the one before for it.
-                const bool next = j + 1 < nt && guarded<F>(p, tile_of<F>(p, gap, kt0 + j + 1) * kKeys, keys_end, pos0);
+                const bool next = j + 1 < nt && guarded<F>(p, tile_of<F>(p, gap, kt0 + j + 1) * kKeys, keys_end, pos0, gap);
                 if (P::kStagesV >= 2 * P::kHalves) ask(next);
                 if (j == 0 && nq++ > 0) ok = wait(o_empty, nq & 1);          // the part before is read
                 ok = ok && wait(p_full(t & 1), (t >> 1) & 1);
@@ -836,7 +886,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             bool found = false;
             for (int j = 0; j < g.nt && ok; ++j) {
                 const int key = tile_of<F>(p, g.gap, g.kt0 + j) * kKeys;
-                if (!guarded<F>(p, key, g.keys_end, g.pos0)) {
+                if (!guarded<F>(p, key, g.keys_end, g.pos0, g.gap)) {
                     it += P::kHalves;
                     continue;
                 }
@@ -844,7 +894,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 ok = wait(v_ask(looked), (looked >> 1) & 1);
                 const int seen = min(g.keys_end - key, kKeys), cleared = (seen + 15) / 16 * 16;
                 const int above = min(max(g.pos0 + 1 - key, 0), seen);
-                const int below = min(max(g.keys_end - 1 - p.back, 0) - key, above);
+                const int below = min(max(F == kShared ? g.gap : g.keys_end - 1 - p.back, 0) - key, above);
 #pragma unroll 1
                 for (int h = 0; h < P::kHalves && ok; ++h, ++it) {
                     const int s = P::kStagesK + it % P::kStagesV;
@@ -907,12 +957,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         int use = 0, pairs = 0;                              // references handed on, parts ended by this pair of warps
         for (int i = 0; acquire(i); ++i) {
             const int nt = part_of(i).nt, rows = part_of(i).rows, kt0 = part_of(i).kt0;
-            const int gap = F == kSinks ? part_of(i).gap : 0;
+            const int gap = F != kPlain ? part_of(i).gap : 0;
             np += nt > 0;
             const bool mine = row < rows;
             const bool busy = 32 * quad < rows;              // some row of this warp is in use
-            const int pos = part_of(i).pos0 + row_tok;
-            const int from = max(max(pos, 0) - p.back, 0);
+            const int pos = part_of(i).pos0 + (F == kShared && gap < 0 ? 0 : row_tok);
+            const int from = F == kShared ? max(gap, 0) : max(max(pos, 0) - p.back, 0);
             // every key of [sure_lo, sure_hi] is seen by all of the warp's rows
             const int sure_hi = __reduce_min_sync(0xFFFFFFFFu, mine ? pos : 0x7FFFFFFF);
             const int sure_lo = __reduce_max_sync(0xFFFFFFFFu, mine ? from : 0);
@@ -1090,13 +1140,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             const float m2 = m * c - kShift;
             const size_t orow = size_t(g.row0 + row_tok) * p.q_heads + g.kvh * p.group + row_head;
             const size_t srow = size_t(whole ? 0 : g.slot) * p.slot_rows + row;
-            if (mine) {
+            // kShared: whole results are kept as they are too, for the last kernel
+            const size_t kept = (F == kShared && gap >= 0 ? size_t(p.n_tokens) * p.q_heads : 0) + orow;
+            if (F == kShared && mine) {
+                *(whole ? p.res_ml + kept : p.part_ml + srow) = make_float2(m2, l);
+            } else if (mine) {
                 if (!whole) p.part_ml[srow] = make_float2(m2, l);
                 else if (p.lse != nullptr) p.lse[orow] = nt > 0 ? (m2 + log2f(l)) * kLn2 : -INFINITY;
             }
             __syncwarp();
             __half *out = p.out + orow * D;
-            float *part = p.part_o + srow * D;
+            float *part = F == kShared && whole ? p.res_o + kept * D : p.part_o + srow * D;
 #pragma unroll 1
             for (int o = 0; o < D; o += 32) {
                 uint32_t r[32];
@@ -1111,7 +1165,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                         r[k] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(r[k]), weight),
                                                          __fmul_rn(__uint_as_float(q[k]), weight2)));
                 }
-                if (mine && whole) {
+                if (F == kShared && nt == 0)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) r[k] = 0u;      // no product was made
+                if (F != kShared && mine && whole) {
                     uint32_t w[16];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -1146,7 +1203,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             if (fix && mine) {
                 // the values that were cleared, for a row that sees them: the
                 // weight is above 0, so they make the sum what they are
-                const int below = max(g.keys_end - 1 - p.back, 0);
+                const int below = max(F == kShared ? gap : g.keys_end - 1 - p.back, 0);
                 const int last = min((tile_of<F>(p, gap, kt0 + nt - 1) + 1) * kKeys - 1, pos);
 #pragma unroll 1
                 for (int k = F == kSinks ? tile_of<F>(p, gap, kt0) * kKeys : max(kt0 * kKeys, from); k <= last; ++k) {
@@ -1164,7 +1221,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     for (int o = 0; o < D; ++o) {
                         const float y = __half2float(v[o]);
                         if (isfinite(y)) continue;
-                        if (whole) out[o] = __float2half_rn(__half2float(out[o]) + y);
+                        if (F != kShared && whole) out[o] = __float2half_rn(__half2float(out[o]) + y);
                         else part[o] += y;
                     }
                 }
@@ -1189,13 +1246,13 @@ constexpr int kJoinSplit = 4;
 constexpr int kJoinWeights = 3 * kRows + 2 * kMaxCtas;
 
 // o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over a row's parts, M the
-// largest m_i.  Latency bounds it: a warp fetches its rows' statistics and all
+// largest m_i (kKeep, for kShared: both sums and M as they are).  Latency bounds it: a warp fetches its rows' statistics and all
 // fetch o's parts, both to shared memory, before anything is waited for, and
 // the weights are worked out while the latter come in.  Sums run over the
 // parts in order, so that parts of which a row sees no key (o = 0) change
 // nothing.  A weight too small for fp32 still multiplies, so that it does not
 // hide what is not finite.
-template <int D>
+template <int D, bool kKeep>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_attn_join_kernel(const Args p) {
     __shared__ float2 ml[kJoinWeights];          // m, l; then the part's weight, its share of the sum
@@ -1270,7 +1327,8 @@ paged_attn_join_kernel(const Args p) {
                         for (int i = 0; i < n; ++i) l += x[i].y;
                         if ((lane & wide) == 0) {
                             scale[r] = l != 0.f ? 1.f / l : 0.f;
-                            if (p.lse != nullptr) p.lse[row_out(r)] = l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
+                            if (kKeep) p.res_ml[(g.count != 0 ? size_t(p.n_tokens) * p.q_heads : 0) + row_out(r)] = make_float2(top, l);
+                            else if (p.lse != nullptr) p.lse[row_out(r)] = l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
                         }
                     }
                 }
@@ -1288,6 +1346,11 @@ paged_attn_join_kernel(const Args p) {
                         o = make_float4(fmaf(w, y.x, o.x), fmaf(w, y.y, o.y), fmaf(w, y.z, o.z), fmaf(w, y.w, o.w));
                     }
                     if (i0 + m < n) continue;
+                    if (kKeep) {
+                        const size_t kept = (g.count != 0 ? size_t(p.n_tokens) * p.q_heads : 0) + row_out(b + r);
+                        *reinterpret_cast<float4 *>(p.res_o + kept * D + 4 * col) = o;
+                        continue;
+                    }
                     const float inv = scale[b + r];
                     uint2 h = make_uint2(0u, 0u);
                     if (inv != 0.f) {
@@ -1298,6 +1361,58 @@ paged_attn_join_kernel(const Args p) {
                 }
             }
         }
+    }
+}
+
+// kShared: a row's result over its group's prefix and the one over what follows
+// it, joined as above.  One CTA takes one token.
+constexpr int kMergeThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads)
+paged_attn_merge_kernel(const Args p) {
+    __shared__ int seq;
+    const int t = blockIdx.x, tid = threadIdx.x;
+    if (tid == 0) seq = -1;
+    grid_dep_wait();
+    grid_dep_launch();
+    __syncthreads();
+    if (*p.planned == 0) return;
+    for (int b = tid; b < p.B; b += kMergeThreads)
+        if (p.offsets[b] <= t && t < p.offsets[b + 1]) seq = b;
+    __syncthreads();
+    const int b = seq;
+    if (b < 0) return;                           // a row of no sequence is left alone
+    const bool shared = seq_of<kShared>(p, p.n_groups + b).from > 0;
+    const size_t rows = size_t(p.n_tokens) * p.q_heads, row0 = size_t(t) * p.q_heads;
+    constexpr int kCols = D / 8;                 // threads a row, eight columns each
+    for (int h = tid / kCols; h < p.q_heads; h += kMergeThreads / kCols) {
+        const size_t own = rows + row0 + h, pre = row0 + h;
+        const int col = 8 * (tid % kCols);
+        float4 o[2] = {*reinterpret_cast<const float4 *>(p.res_o + own * D + col),
+                       *reinterpret_cast<const float4 *>(p.res_o + own * D + col + 4)};
+        float2 x = p.res_ml[own];
+        if (shared) {
+            const float2 y = p.res_ml[pre];
+            const float top = fmaxf(x.x, y.x);
+            const float wx = top == -INFINITY ? 0.f : ex2(x.x - top), wy = top == -INFINITY ? 0.f : ex2(y.x - top);
+            x = make_float2(top, (x.y != 0.f ? wx * x.y : 0.f) + (y.y != 0.f ? wy * y.y : 0.f));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 a = *reinterpret_cast<const float4 *>(p.res_o + pre * D + col + 4 * i);
+                o[i] = make_float4(fmaf(wx, o[i].x, wy * a.x), fmaf(wx, o[i].y, wy * a.y), fmaf(wx, o[i].z, wy * a.z),
+                                   fmaf(wx, o[i].w, wy * a.w));
+            }
+        }
+        const float inv = x.y != 0.f ? 1.f / x.y : 0.f;
+        if (p.lse != nullptr && col == 0) p.lse[row0 + h] = x.y != 0.f ? (x.x + log2f(x.y)) * kLn2 : -INFINITY;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (inv != 0.f) {
+            w.x = h2_as_u32(__floats2half2_rn(o[0].x * inv, o[0].y * inv));
+            w.y = h2_as_u32(__floats2half2_rn(o[0].z * inv, o[0].w * inv));
+            w.z = h2_as_u32(__floats2half2_rn(o[1].x * inv, o[1].y * inv));
+            w.w = h2_as_u32(__floats2half2_rn(o[1].z * inv, o[1].w * inv));
+        }
+        *reinterpret_cast<uint4 *>(p.out + (row0 + h) * D + col) = w;
     }
 }
 
@@ -1350,7 +1465,10 @@ w4v_status launch(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtens
     }
     if (launch_pdl(paged_attn_kernel<D, F>, dim3(grid), dim3(kThreads), Plan<D>::kBytes, stream, qmap, kmap, vmap, a) !=
             cudaSuccess ||
-        launch_pdl(paged_attn_join_kernel<D>, dim3(grid, kJoinSplit), dim3(kJoinThreads), 0, stream, a) != cudaSuccess) {
+        launch_pdl(paged_attn_join_kernel<D, F == kShared>, dim3(grid, kJoinSplit), dim3(kJoinThreads), 0, stream, a) !=
+            cudaSuccess ||
+        (F == kShared &&
+         launch_pdl(paged_attn_merge_kernel<D>, dim3(a.n_tokens), dim3(kMergeThreads), 0, stream, a) != cudaSuccess)) {
         cudaGetLastError();
         return W4V_ERR_CUDA;
     }
@@ -1364,10 +1482,14 @@ size_t paged_attn_ws_bytes(int n_tokens, int B, int q_heads, int kv_heads, int h
     const Slots s = slots_of(n_tokens, B, q_heads, kv_heads, max_context, invariant);
     return s.count * (s.rows * (size_t(head_dim) * sizeof(float) + sizeof(float2)) + sizeof(Share)) + 256;
 }
+size_t paged_attn_shared_ws_bytes(int n_tokens, int q_heads, int kv_heads, int head_dim) {
+    return paged_attn_ws_bytes(n_tokens, 1, q_heads, kv_heads, head_dim, 0, false) +
+           2 * size_t(n_tokens) * q_heads * (size_t(head_dim) * sizeof(float) + sizeof(float2));
+}
 
 w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
-                             float scale, int window, int sinks, uint16_t *out, float *lse, void *ws, bool invariant,
-                             cudaStream_t stream) {
+                             float scale, int window, int sinks, const PrefixGroups *shared, uint16_t *out, float *lse,
+                             void *ws, bool invariant, cudaStream_t stream) {
     const DeviceInfo *info = nullptr;
     w4v_status st = device_info(&info);
     if (st != W4V_OK) return st;
@@ -1378,8 +1500,15 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     a.lse = lse;
     a.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0u;
     a.part_o = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + 31u) & ~uintptr_t(31));
-    a.part_ml = reinterpret_cast<float2 *>(a.part_o + slots.count * slots.rows * D);
-    a.shares = reinterpret_cast<Share *>((reinterpret_cast<uintptr_t>(a.part_ml + slots.count * slots.rows) + 15u) & ~uintptr_t(15));
+    const size_t kept = shared != nullptr ? 2 * size_t(n_tokens) * q_heads : 0;
+    a.res_o = a.part_o + slots.count * slots.rows * D;
+    a.part_ml = reinterpret_cast<float2 *>(a.res_o + kept * D);
+    a.res_ml = a.part_ml + slots.count * slots.rows;
+    a.shares = reinterpret_cast<Share *>((reinterpret_cast<uintptr_t>(a.res_ml + kept) + 15u) & ~uintptr_t(15));
+    a.planned = reinterpret_cast<int *>(a.shares + slots.count);
+    a.groups = shared != nullptr ? shared->groups : nullptr;
+    a.prefix = shared != nullptr ? shared->prefix : nullptr;
+    a.n_groups = shared != nullptr ? shared->count : 0;
     a.v = reinterpret_cast<const __half *>(kv.v);
     a.table = kv.table;
     a.lengths = kv.lengths;
@@ -1426,6 +1555,10 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
         st = encode_tmap_sw128(&vmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, kv.v, kv_dims, kv_strides, kv_box);
     if (st != W4V_OK) return st;
     const int grid = std::min(info->sm_count, kMaxCtas);
+    if (shared != nullptr)
+        return D == 64 ? launch<64, kShared>(qmap, kmap, vmap, a, grid, stream)
+                       : D == 128 ? launch<128, kShared>(qmap, kmap, vmap, a, grid, stream)
+                                  : launch<256, kShared>(qmap, kmap, vmap, a, grid, stream);
     if (sinks > 0 && window > 0)
         return D == 64 ? launch<64, kSinks>(qmap, kmap, vmap, a, grid, stream)
                        : D == 128 ? launch<128, kSinks>(qmap, kmap, vmap, a, grid, stream)

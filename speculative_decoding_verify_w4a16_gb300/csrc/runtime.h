@@ -167,11 +167,17 @@ w4v_status launch_rope_append(const w4v_kv_t &kv, const uint16_t *q, const uint1
                               const HeadNorm *norm, uint16_t *q_out, cudaStream_t stream);
 // Largest query heads per key/value head (a tile's 128 rows hold one token's).
 constexpr int kAttnMaxGroup = 128;
+// Groups of sequences with a common prefix (paged_attn_shared).
+struct PrefixGroups {
+    const int32_t *groups, *prefix;
+    int count;
+};
+size_t paged_attn_shared_ws_bytes(int n_tokens, int q_heads, int kv_heads, int head_dim);
 size_t paged_attn_ws_bytes(int n_tokens, int B, int q_heads, int kv_heads, int head_dim, int max_context,
                            bool invariant);
 w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
-                             float scale, int window, int sinks, uint16_t *out, float *lse, void *ws, bool invariant,
-                             cudaStream_t stream);
+                             float scale, int window, int sinks, const PrefixGroups *shared, uint16_t *out, float *lse,
+                             void *ws, bool invariant, cudaStream_t stream);
 size_t kv_pages_ws_bytes(int n_pages, int S);
 w4v_status launch_kv_extend(const w4v_pages_t &pages, const int32_t *want, int32_t *short_out, void *ws,
                             cudaStream_t stream);

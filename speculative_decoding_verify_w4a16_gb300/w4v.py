@@ -131,6 +131,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.paged_attn.restype = I
             lib.paged_attn_sinks.argtypes = [P, P, L, I, I, F, I, I, P, P, P, S, U, P]
             lib.paged_attn_sinks.restype = I
+            lib.paged_attn_shared_workspace_bytes.argtypes = [I, I, I, I, I, I]
+            lib.paged_attn_shared_workspace_bytes.restype = S
+            lib.paged_attn_shared.argtypes = [P, P, L, I, I, F, P, P, I, P, P, P, S, U, P]
+            lib.paged_attn_shared.restype = I
             lib.kv_workspace_bytes.argtypes = [I, I]
             lib.kv_workspace_bytes.restype = S
             lib.kv_extend.argtypes = [P, P, P, P, S, P]
@@ -660,6 +664,39 @@ def paged_attn(q, k_cache, v_cache, table, lengths, offsets, scale=None, window:
     code = load().paged_attn_sinks(kv, q.data_ptr(), stride, n, Hq, D ** -0.5 if scale is None else scale, int(window),
                                    int(sinks), out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(),
                                    ws.numel(), BATCH_INVARIANT if batch_invariant else 0, _stream(stream))
+    if code != OK:
+        raise W4VError(code, where)
+    return out
+
+
+def paged_attn_shared_workspace_bytes(n_tokens: int, B: int, n_groups: int, q_heads: int, kv_heads: int,
+                                      head_dim: int) -> int:
+    return load().paged_attn_shared_workspace_bytes(n_tokens, B, n_groups, q_heads, kv_heads, head_dim)
+
+
+def paged_attn_shared(q, k_cache, v_cache, table, lengths, offsets, groups, prefix, scale=None, out=None, lse=None,
+                      ws=None, stream=None):
+    """paged_attn for sequences that share a prefix, read once for all of them: sequences groups[g] ..
+    groups[g + 1] - 1 (int32 [G + 1]) have their first prefix[g] tokens (int32 [G]) in common, as after
+    kv_fork.  Returns out [n][Hq][D]; lse and rows of no sequence as in paged_attn."""
+    where = "paged_attn_shared"
+    kv, B, width, heads, page, D = _kv(where, k_cache, v_cache, table, lengths, offsets)
+    shape = q.shape
+    if len(shape) != 3 or prefix.dim() != 1:
+        raise W4VError(ERR_SHAPE, where)
+    n, Hq, _ = shape
+    G = prefix.shape[0]
+    stride = _rows(q, where, n, Hq, D)
+    g, p = _i32(groups, where, (G + 1,)), _i32(prefix, where, (G,))
+    if lse is not None and (lse.shape != (n, Hq) or lse.dtype is not _FLOAT or not lse.is_contiguous()):
+        raise W4VError(ERR_SHAPE if lse.shape != (n, Hq) else ERR_ARG, where)
+    _same_device(where, q, k_cache, v_cache, table, lengths, offsets, groups, prefix, out, lse, ws)
+    out = _dense_out(out, where, q, shape, stream)
+    if ws is None:
+        ws = workspace(paged_attn_shared_workspace_bytes(n, B, G, Hq, heads, D), q.device, stream)
+    code = load().paged_attn_shared(kv, q.data_ptr(), stride, n, Hq, D ** -0.5 if scale is None else scale, g, p, G,
+                                    out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), 0,
+                                    _stream(stream))
     if code != OK:
         raise W4VError(code, where)
     return out

@@ -126,3 +126,47 @@ def test_sinks_refusals(w4v_mod):
         w.paged_attn(t["q"], t["k"], t["k"], t["table"], t["lens"], t["offs"], window=4, sinks=-1,
                      out=torch.zeros_like(t["q"]), ws=torch.zeros(1 << 24, dtype=torch.uint8), stream=0)
     assert e.value.code == w.ERR_SHAPE
+
+
+def test_shared_refusals(w4v_mod):
+    w = w4v_mod
+
+    def call(kv=None, q=FAKE, stride=2560, n=8, heads=20, scale=0.1, g=FAKE, p=FAKE, G=2, out=FAKE, lse=None, ws=FAKE, nb=BIG,
+             flags=0):
+        return w.load().paged_attn_shared(_kv(w) if kv is None else kv, q, stride, n, heads, scale, g, p, G, out, lse, ws, nb,
+                                          flags, None)
+    for kw, code in KV_FAULTS:
+        assert call(kv=_kv(w, **kw)) == getattr(w, "ERR_" + code)
+    assert w.load().paged_attn_shared(None, FAKE, 2560, 8, 20, 0.1, FAKE, FAKE, 1, FAKE, None, FAKE, BIG, 0, None) == w.ERR_ARG
+    assert call(G=-1) == call(G=(1 << 24) + 1) == call(n=-1) == call(heads=18) == call(stride=2552) == w.ERR_SHAPE
+    assert call(flags=2) == call(flags=1) == call(scale=0.0) == call(scale=float("nan")) == w.ERR_ARG
+    assert call(q=None) == call(out=None) == call(g=None) == call(p=None) == w.ERR_ARG
+    assert call(q=FAKE + 8) == call(out=FAKE + 2) == call(lse=FAKE + 2) == call(ws=FAKE + 4) == w.ERR_ALIGN
+    assert call(g=FAKE + 2) == call(p=FAKE + 1) == w.ERR_ALIGN
+    size = w.paged_attn_shared_workspace_bytes
+    assert call(ws=None) == call(nb=size(8, 2, 2, 20, 4, 128) - 1) == w.ERR_WORKSPACE
+    assert call(n=0, q=None, out=None, ws=None) == call(kv=_kv(w, B=0), q=None, ws=None) == w.OK
+    assert size(8, 2, 2, 20, 4, 128) >= 2 * 8 * 20 * (128 * 4 + 8) and size(9, 2, 2, 20, 4, 128) > size(8, 2, 2, 20, 4, 128)
+    assert size(-1, 2, 2, 20, 4, 128) == size(8, 2, -1, 20, 4, 128) == size(8, 2, 2, 18, 4, 128) == size(8, 2, 2, 20, 4, 96) == 0
+
+
+@pytest.mark.parametrize("row_tiles,code", [((1 << 31) // (133 * 64), "SHAPE"), ((1 << 31) // (133 * 64) - 2, "WORKSPACE")])
+def test_shared_work_fits_32_bits(w4v_mod, row_tiles, code):
+    # both passes' row tiles of 128 tokens (and one more each for the sequence and the group), 64 heads, 133 units a row tile
+    w, half = w4v_mod, row_tiles // 2
+    kv = _kv(w, B=1, table_width=128, page=128, kv_heads=64)
+    n = 128 * half - (128 if code == "WORKSPACE" else 0)
+    assert (2 * (n // 128 + 1) * 64 * 133 >= 1 << 31) == (code == "SHAPE")
+    assert w.load().paged_attn_shared(kv, FAKE, 64 * 128, n, 64, 0.1, FAKE, FAKE, 1, FAKE, None, FAKE, 16, 0,
+                                      None) == getattr(w, "ERR_" + code)
+
+
+def test_binding_refuses_shared_tensors(w4v_mod):
+    w, t, i = w4v_mod, _tensors(), torch.int32
+    cache = (t["k"], t["k"], t["table"], t["lens"], t["offs"])
+    code = lambda *a, **kw: _code(w, w.paged_attn_shared, *a, **kw)  # noqa: E731
+    g, p = torch.zeros(2, dtype=i), torch.zeros(1, dtype=i)
+    assert code(t["q"], *cache, g[:1], p) == code(t["q"], *cache, g, p[None]) == code(t["q"][0], *cache, g, p) == w.ERR_SHAPE
+    assert code(t["q"], *cache, g.long(), p) == code(t["q"], *cache, g, p.float()) == code(t["q"].float(), *cache, g, p) == w.ERR_ARG
+    assert code(t["q"], *cache, g, p, lse=torch.zeros(5, 3)) == w.ERR_SHAPE
+    assert code(t["q"], *cache, g, p) == w.ERR_ARG                       # tensors of the host
