@@ -155,8 +155,7 @@ struct __align__(16) Share {
     int slot0, n;
     int n_mul;                  // 2^20 / n, rounded up: k * n_mul >> 20 is k / n for k < 1024
     int block;                  // rows that are fetched at a time
-    int count;                  // batch-invariant, entry 0: how many entries there are (default: one per range);
-                                // kShared: 0 of a prefix, 1 of what follows it
+    int count;                  // batch-invariant, entry 0: how many entries there are (default: one per range)
 };
 template <int D>
 constexpr int kHeld = D == 256 ? 40 : 12288 / (2 * D);      // rows of parts that it holds at a time
@@ -188,6 +187,7 @@ struct Args {
     int n_groups;
     float *res_o;               // [2][n_tokens q_heads][D]: over the prefixes, over what follows them
     float2 *res_ml;             // [2][n_tokens q_heads]
+    uint32_t *places;           // [2][n_tokens kv_heads]: see place_of()
     int *planned;               // 1, or 0 where nothing was done
 };
 
@@ -198,6 +198,14 @@ struct Seq {
 };
 __device__ __forceinline__ int offset_at(const Args &p, int b) { return min(max(p.offsets[b], 0), p.n_tokens); }
 __device__ __forceinline__ int length_at(const Args &p, int b) { return min(max(p.lengths[b], 0), p.width << p.page_bits); }
+
+// Where the last kernel finds a token's results (kShared): the first range of
+// its row tile, how many ranges hold parts of it (1: the whole result), its
+// number in the tile, and whether it shares a prefix.
+__device__ __forceinline__ uint32_t place_of(int range, int parts, int tok, bool shares) {
+    static_assert(kMaxCtas <= 256 && kRows <= 128, "fields of a place");
+    return uint32_t(range) | uint32_t(parts) << 8 | uint32_t(tok) << 17 | uint32_t(shares) << 24;
+}
 
 // kShared counts the groups' prefixes as sequences of their own, before the
 // others: the rows of a prefix are those of all its sequences (they follow one
@@ -282,11 +290,9 @@ __device__ __forceinline__ int row_tiles(const Args &p, int n) {
 // A lane counts a few row tiles by itself; the warp together those of a
 // sequence with more.
 template <int F>
-__device__ __forceinline__ int lane_units(const Args &p, int b) {
+__device__ __forceinline__ int lane_units(const Args &p, const Seq &s) {
     constexpr int kFew = 4;
     const int lane = threadIdx.x & 31;
-    Seq s{0, 0, 0, 0, 0};
-    if (b < sequences<F>(p)) s = seq_of<F>(p, b);
     const int tiles = row_tiles(p, s.n);
     uint32_t many = __ballot_sync(0xFFFFFFFFu, tiles > kFew);
     Seq o = s;
@@ -308,6 +314,13 @@ __device__ __forceinline__ int lane_units(const Args &p, int b) {
         step = 32;
     }
     return u;
+}
+
+template <int F>
+__device__ __forceinline__ int lane_units(const Args &p, int b) {
+    Seq s{0, 0, 0, 0, 0};
+    if (b < sequences<F>(p)) s = seq_of<F>(p, b);
+    return lane_units<F>(p, s);
 }
 
 // The same value in every lane, as one that the compiler knows to be so.
@@ -346,8 +359,10 @@ struct Place {
 // the second one has the first one's counts.  The host has seen that rows
 // counted once fit; offsets that go up and down count rows again and again, so
 // the sum is looked at here, and too large a one leaves nothing to do (false).
+// kShared: seqs and counts, if not null, hold every sequence and its units.
 template <int F>
-__device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place &w, int &all, Split &split) {
+__device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place &w, int &all, Split &split,
+                                         const Seq *seqs, const int *counts) {
     const int lane = threadIdx.x & 31;
     int u = 0, at = 0;
     uint32_t mine = 0;                           // this lane's sequences, no further than 2^31 - 1
@@ -356,7 +371,8 @@ __device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
         for (int b0 = 0; b0 < sequences<F>(p); b0 += 32) {
-            if (pass == 0 || sequences<F>(p) > 32) u = lane_units<F>(p, b0 + lane);
+            if (F == kShared && counts != nullptr) u = b0 + lane < sequences<F>(p) ? counts[b0 + lane] : 0;
+            else if (pass == 0 || sequences<F>(p) > 32) u = lane_units<F>(p, b0 + lane);
             if (pass == 0) {
                 mine = min(mine + uint32_t(u), 0x7FFFFFFFu);
                 continue;
@@ -373,7 +389,7 @@ __device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place
             w.b = b0 + src;
             w.kvh = at / su;
             int rest = at - w.kvh * su;
-            const Seq s = seq_of<F>(p, w.b);
+            const Seq s = F == kShared && seqs != nullptr ? seqs[w.b] : seq_of<F>(p, w.b);
             const int tiles = row_tiles(p, s.n);
 #pragma unroll 1
             for (int q0 = 0;; q0 += 32) {
@@ -418,8 +434,26 @@ struct Cursor {
     Place w;
     int unit, left;             // index of the next unit, units left in the range
     Seq s;
+    // kShared: a lane holds sequence held + lane, for finding one takes a chain
+    // of loads
+    Seq mine;
+    int held;
+    __device__ __forceinline__ void hold(const Args &p, const Seq *cached) {
+        const int b = w.b + int(threadIdx.x & 31);
+        held = w.b;
+        mine = Seq{0, 0, 0, 0, 0};
+        if (b < sequences<kShared>(p)) mine = cached != nullptr ? cached[b] : seq_of<kShared>(p, b);
+    }
     template <int F>
-    __device__ __forceinline__ void load(const Args &p) { s = seq_of<F>(p, w.b); }
+    __device__ __forceinline__ void load(const Args &p) {
+        if (F != kShared) {
+            s = seq_of<F>(p, w.b);
+            return;
+        }
+        if (w.b - held >= 32) hold(p, nullptr);
+        auto from = [&](int x) { return __shfl_sync(0xFFFFFFFFu, x, w.b - held); };
+        s = Seq{from(mine.first), from(mine.n), from(mine.len), from(mine.row), from(mine.from)};
+    }
     // The next part, and the index of its first unit.
     template <int F>
     __device__ __forceinline__ bool next(const Args &p, int cta, Part &g, int &first) {
@@ -610,6 +644,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     grid_dep_wait();
     grid_dep_launch();
     bool ok = (base & 1023u) == 0u;              // the operands' swizzle needs it
+    // kShared: every sequence and its units, found by all warps side by side, in
+    // the room of the first queries until those are loaded
+    constexpr int kCached = P::kQBytes / int(sizeof(Seq) + sizeof(int));
+    Seq *seqs = F == kShared && sequences<F>(p) <= kCached ? reinterpret_cast<Seq *>(smem) : nullptr;
+    int *counts = F == kShared && seqs != nullptr ? reinterpret_cast<int *>(smem + kCached * sizeof(Seq)) : nullptr;
+    if (F == kShared && seqs != nullptr) {
+#pragma unroll 1
+        for (int b0 = 32 * warp; b0 < sequences<F>(p); b0 += kThreads) {
+            const int b = b0 + lane;
+            Seq s{0, 0, 0, 0, 0};
+            if (b < sequences<F>(p)) s = seq_of<F>(p, b);
+            const int u = lane_units<F>(p, s);
+            if (b >= sequences<F>(p)) continue;
+            seqs[b] = s;
+            counts[b] = u;
+        }
+        __syncthreads();
+    }
 
     // The next part (its number in the ring is `i`); the warp gives it back
     // with release() once it has read what it needs.
@@ -630,13 +682,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         int all = 0;
         Split split;
         Cursor cur{};
-        const bool planned = schedule<F>(p, blockIdx.x, gridDim.x, cur.w, all, split);
+        const bool planned = schedule<F>(p, blockIdx.x, gridDim.x, cur.w, all, split, seqs, counts);
         if (!planned && blockIdx.x == 0 && lane == 0) atomicOr(p.status, 1u << kStatusShape);
         if (F == kShared && blockIdx.x == 0 && lane == 0) *p.planned = planned;
         if (int(blockIdx.x) < split.ranges) {
             cur.unit = split.begin(blockIdx.x);
             cur.left = split.begin(blockIdx.x + 1) - cur.unit;
+            if (F == kShared) cur.hold(p, seqs);
             cur.load<F>(p);
+        }
+        if (F == kShared) {                                  // the queries may come where the sequences were
+            __syncwarp();
+            fence_proxy_async_shared();
         }
         const int box_bits = min(p.page_bits, 7);            // 2^box_bits tokens per TMA box
         const uint32_t box_bytes = P::kGroupBytes << (box_bits - 3);
@@ -723,8 +780,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             }
             // the share of this range's first row tile, or of every unit's
             // (here, behind the loads, for the second kernel alone reads it)
-            if (lane == 0 && (p.invariant ? g.nt >= 0 || all == 0 : i == 0)) {
-                Share e{g.row0, g.kvh, 0, unit - g.u, 0, 0, 1, F == kShared ? g.gap >= 0 : p.invariant ? all : int(gridDim.x)};
+            if (F == kShared && g.nt >= 0 && g.u == 0) {
+                // the tile's tokens are found from where it begins
+                const int first = unit - g.u, toks = g.rows / p.group, which = g.gap >= 0;
+                const int parts = split.owner(first + g.units - 1) - int(blockIdx.x) + 1;
+                uint32_t *at = p.places + size_t(which) * p.n_tokens * p.kv_heads + g.kvh;
+#pragma unroll 1
+                for (int k = lane; k < toks; k += 32)
+                    at[size_t(g.row0 + k) * p.kv_heads] = place_of(blockIdx.x, parts, k, g.gap > 0);
+            }
+            if (F != kShared && lane == 0 && (p.invariant ? g.nt >= 0 || all == 0 : i == 0)) {
+                Share e{g.row0, g.kvh, 0, unit - g.u, 0, 0, 1, p.invariant ? all : int(gridDim.x)};
                 int share = g.u, shares = g.units;
                 if (p.invariant) {
                     e.n = g.units > 1 ? g.units : 0;
@@ -745,7 +811,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             if (g.nt < 0) break;
         }
         // A range that was given up leaves nothing to join.
-        if (!ok)
+        if (F != kShared && !ok)
             for (int e = (p.invariant ? split.begin(blockIdx.x) : int(blockIdx.x)) + lane;
                  e < (p.invariant ? min(split.begin(blockIdx.x + 1), max(all, 1)) : int(blockIdx.x) + 1); e += 32) {
                 p.shares[e].n = 0;
@@ -1246,13 +1312,13 @@ constexpr int kJoinSplit = 4;
 constexpr int kJoinWeights = 3 * kRows + 2 * kMaxCtas;
 
 // o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over a row's parts, M the
-// largest m_i (kKeep, for kShared: both sums and M as they are).  Latency bounds it: a warp fetches its rows' statistics and all
+// largest m_i.  Latency bounds it: a warp fetches its rows' statistics and all
 // fetch o's parts, both to shared memory, before anything is waited for, and
 // the weights are worked out while the latter come in.  Sums run over the
 // parts in order, so that parts of which a row sees no key (o = 0) change
 // nothing.  A weight too small for fp32 still multiplies, so that it does not
 // hide what is not finite.
-template <int D, bool kKeep>
+template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_attn_join_kernel(const Args p) {
     __shared__ float2 ml[kJoinWeights];          // m, l; then the part's weight, its share of the sum
@@ -1327,8 +1393,7 @@ paged_attn_join_kernel(const Args p) {
                         for (int i = 0; i < n; ++i) l += x[i].y;
                         if ((lane & wide) == 0) {
                             scale[r] = l != 0.f ? 1.f / l : 0.f;
-                            if (kKeep) p.res_ml[(g.count != 0 ? size_t(p.n_tokens) * p.q_heads : 0) + row_out(r)] = make_float2(top, l);
-                            else if (p.lse != nullptr) p.lse[row_out(r)] = l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
+                            if (p.lse != nullptr) p.lse[row_out(r)] = l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
                         }
                     }
                 }
@@ -1346,11 +1411,6 @@ paged_attn_join_kernel(const Args p) {
                         o = make_float4(fmaf(w, y.x, o.x), fmaf(w, y.y, o.y), fmaf(w, y.z, o.z), fmaf(w, y.w, o.w));
                     }
                     if (i0 + m < n) continue;
-                    if (kKeep) {
-                        const size_t kept = (g.count != 0 ? size_t(p.n_tokens) * p.q_heads : 0) + row_out(b + r);
-                        *reinterpret_cast<float4 *>(p.res_o + kept * D + 4 * col) = o;
-                        continue;
-                    }
                     const float inv = scale[b + r];
                     uint2 h = make_uint2(0u, 0u);
                     if (inv != 0.f) {
@@ -1364,55 +1424,111 @@ paged_attn_join_kernel(const Args p) {
     }
 }
 
-// kShared: a row's result over its group's prefix and the one over what follows
-// it, joined as above.  One CTA takes one token.
-constexpr int kMergeThreads = 256;
+// kShared: a row's parts over its group's prefix and those over what follows
+// it, joined as above in one go.  A warp takes a row, a CTA the rows of a token
+// that read one key/value head.  Latency bounds it here too: the parts' first
+// eight are fetched before their statistics have come.
+constexpr int kMergeThreads = 128;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
 paged_attn_merge_kernel(const Args p) {
-    __shared__ int seq;
-    const int t = blockIdx.x, tid = threadIdx.x;
-    if (tid == 0) seq = -1;
+    __shared__ int covered;
+    constexpr int kCols = D / 32;                // of a lane: 2, 4 or twice 4
+    constexpr int kAhead = 8;
+    const int t = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) covered = 0;
     grid_dep_wait();
     grid_dep_launch();
+    const int planned = *p.planned;
     __syncthreads();
-    if (*p.planned == 0) return;
     for (int b = tid; b < p.B; b += kMergeThreads)
-        if (p.offsets[b] <= t && t < p.offsets[b + 1]) seq = b;
-    __syncthreads();
-    const int b = seq;
-    if (b < 0) return;                           // a row of no sequence is left alone
-    const bool shared = seq_of<kShared>(p, p.n_groups + b).from > 0;
-    const size_t rows = size_t(p.n_tokens) * p.q_heads, row0 = size_t(t) * p.q_heads;
-    constexpr int kCols = D / 8;                 // threads a row, eight columns each
-    for (int h = tid / kCols; h < p.q_heads; h += kMergeThreads / kCols) {
-        const size_t own = rows + row0 + h, pre = row0 + h;
-        const int col = 8 * (tid % kCols);
-        float4 o[2] = {*reinterpret_cast<const float4 *>(p.res_o + own * D + col),
-                       *reinterpret_cast<const float4 *>(p.res_o + own * D + col + 4)};
-        float2 x = p.res_ml[own];
-        if (shared) {
-            const float2 y = p.res_ml[pre];
-            const float top = fmaxf(x.x, y.x);
-            const float wx = top == -INFINITY ? 0.f : ex2(x.x - top), wy = top == -INFINITY ? 0.f : ex2(y.x - top);
-            x = make_float2(top, (x.y != 0.f ? wx * x.y : 0.f) + (y.y != 0.f ? wy * y.y : 0.f));
+        if (p.offsets[b] <= t && t < p.offsets[b + 1]) covered = 1;
+    const size_t rows = size_t(p.n_tokens) * p.q_heads, tokens = size_t(p.n_tokens) * p.kv_heads;
+#pragma unroll 1
+    for (int kvh = blockIdx.y; kvh < p.kv_heads; kvh += gridDim.y) {
+        const size_t at = size_t(t) * p.kv_heads + kvh;
+        const uint32_t own = p.places[tokens + at], pre = p.places[at];
+        __syncthreads();
+        if (planned == 0 || covered == 0) return;            // a row of no sequence is left alone
+        const int n_own = own >> 8 & 0x1FF, n = n_own + ((own >> 24 & 1u) != 0u ? int(pre >> 8 & 0x1FF) : 0);
+#pragma unroll 1
+        for (int g = warp; g < p.group; g += kMergeThreads / 32) {
+            const size_t row = size_t(t) * p.q_heads + kvh * p.group + g;
+            // part i: of what follows the prefix, then of the prefix
+            struct {
+                const float *o;
+                const float2 *ml;
+            } src;
+            auto part = [&](int i) {
+                const bool follows = i < n_own;
+                const uint32_t w = follows ? own : pre;
+                const int k = follows ? i : i - n_own;
+                if ((w >> 8 & 0x1FF) == 1) {
+                    const size_t r = (follows ? rows : 0) + row;
+                    src.o = p.res_o + r * D;
+                    src.ml = p.res_ml + r;
+                } else {
+                    const int slot = 2 * (int(w & 0xFF) + k) + (k == 0);
+                    const size_t r = size_t(slot) * p.slot_rows + (w >> 17 & 0x7F) * p.group + g;
+                    src.o = p.part_o + r * D;
+                    src.ml = p.part_ml + r;
+                }
+                return src;
+            };
+            float v[kAhead][kCols];
+            auto fetch = [&](int i0) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 a = *reinterpret_cast<const float4 *>(p.res_o + pre * D + col + 4 * i);
-                o[i] = make_float4(fmaf(wx, o[i].x, wy * a.x), fmaf(wx, o[i].y, wy * a.y), fmaf(wx, o[i].z, wy * a.z),
-                                   fmaf(wx, o[i].w, wy * a.w));
+                for (int u = 0; u < kAhead; ++u) {
+                    if (i0 + u >= n) break;
+                    const float *o = part(i0 + u).o + lane * kCols;
+                    if (kCols == 2) {
+                        *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(o);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kCols; c += 4)
+                            *reinterpret_cast<float4 *>(v[u] + c) = *reinterpret_cast<const float4 *>(o + c);
+                    }
+                }
+            };
+            fetch(0);
+            float top = -INFINITY, l = 0.f, w = 0.f, o[kCols];
+            for (int i = lane; i < n; i += 32) top = fmaxf(top, part(i).ml->x);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) o[c] = 0.f;
+#pragma unroll 1
+            for (int i0 = 0; i0 < n; i0 += kAhead) {
+                if (i0 > 0) fetch(i0);
+                if (i0 % 32 == 0) {              // the weights of 32 parts, one a lane
+                    w = 0.f;
+                    if (i0 + lane < n) {
+                        const float2 ml = *part(i0 + lane).ml;
+                        w = top == -INFINITY ? 0.f : ex2(ml.x - top);
+                        l += ml.y != 0.f ? w * ml.y : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    if (i0 + u >= n) break;
+                    const float x = __shfl_sync(0xFFFFFFFFu, w, (i0 + u) % 32);
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) o[c] = fmaf(x, v[u][c], o[c]);
+                }
             }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            if (p.lse != nullptr && lane == 0) p.lse[row] = l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
+            uint32_t h[kCols / 2];
+#pragma unroll
+            for (int c = 0; c < kCols; c += 2)
+                h[c / 2] = inv != 0.f ? h2_as_u32(__floats2half2_rn(o[c] * inv, o[c + 1] * inv)) : 0u;
+            __half *out = p.out + row * D + lane * kCols;
+            if (kCols == 2) *reinterpret_cast<uint32_t *>(out) = h[0];
+            else if (kCols == 4) *reinterpret_cast<uint2 *>(out) = make_uint2(h[0], h[1]);
+            else *reinterpret_cast<uint4 *>(out) = make_uint4(h[0], h[1], h[kCols / 2 - 2], h[kCols / 2 - 1]);
         }
-        const float inv = x.y != 0.f ? 1.f / x.y : 0.f;
-        if (p.lse != nullptr && col == 0) p.lse[row0 + h] = x.y != 0.f ? (x.x + log2f(x.y)) * kLn2 : -INFINITY;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (inv != 0.f) {
-            w.x = h2_as_u32(__floats2half2_rn(o[0].x * inv, o[0].y * inv));
-            w.y = h2_as_u32(__floats2half2_rn(o[0].z * inv, o[0].w * inv));
-            w.z = h2_as_u32(__floats2half2_rn(o[1].x * inv, o[1].y * inv));
-            w.w = h2_as_u32(__floats2half2_rn(o[1].z * inv, o[1].w * inv));
-        }
-        *reinterpret_cast<uint4 *>(p.out + (row0 + h) * D + col) = w;
     }
 }
 
@@ -1465,10 +1581,10 @@ w4v_status launch(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtens
     }
     if (launch_pdl(paged_attn_kernel<D, F>, dim3(grid), dim3(kThreads), Plan<D>::kBytes, stream, qmap, kmap, vmap, a) !=
             cudaSuccess ||
-        launch_pdl(paged_attn_join_kernel<D, F == kShared>, dim3(grid, kJoinSplit), dim3(kJoinThreads), 0, stream, a) !=
-            cudaSuccess ||
-        (F == kShared &&
-         launch_pdl(paged_attn_merge_kernel<D>, dim3(a.n_tokens), dim3(kMergeThreads), 0, stream, a) != cudaSuccess)) {
+        (F == kShared ? launch_pdl(paged_attn_merge_kernel<D>, dim3(a.n_tokens, std::min(a.kv_heads, 65535)),
+                                   dim3(kMergeThreads), 0, stream, a)
+                      : launch_pdl(paged_attn_join_kernel<D>, dim3(grid, kJoinSplit), dim3(kJoinThreads), 0, stream, a)) !=
+            cudaSuccess) {
         cudaGetLastError();
         return W4V_ERR_CUDA;
     }
@@ -1484,7 +1600,7 @@ size_t paged_attn_ws_bytes(int n_tokens, int B, int q_heads, int kv_heads, int h
 }
 size_t paged_attn_shared_ws_bytes(int n_tokens, int q_heads, int kv_heads, int head_dim) {
     return paged_attn_ws_bytes(n_tokens, 1, q_heads, kv_heads, head_dim, 0, false) +
-           2 * size_t(n_tokens) * q_heads * (size_t(head_dim) * sizeof(float) + sizeof(float2));
+           2 * size_t(n_tokens) * (q_heads * (size_t(head_dim) * sizeof(float) + sizeof(float2)) + kv_heads * sizeof(uint32_t));
 }
 
 w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_stride, int n_tokens, int q_heads,
@@ -1505,7 +1621,8 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     a.part_ml = reinterpret_cast<float2 *>(a.res_o + kept * D);
     a.res_ml = a.part_ml + slots.count * slots.rows;
     a.shares = reinterpret_cast<Share *>((reinterpret_cast<uintptr_t>(a.res_ml + kept) + 15u) & ~uintptr_t(15));
-    a.planned = reinterpret_cast<int *>(a.shares + slots.count);
+    a.places = reinterpret_cast<uint32_t *>(a.shares + slots.count);
+    a.planned = reinterpret_cast<int *>(a.places + (shared != nullptr ? 2 * size_t(n_tokens) * kv.kv_heads : 0));
     a.groups = shared != nullptr ? shared->groups : nullptr;
     a.prefix = shared != nullptr ? shared->prefix : nullptr;
     a.n_groups = shared != nullptr ? shared->count : 0;
