@@ -112,6 +112,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // the CTAs that hold the short rows of prompts end last: 272 -> 314 us for
 // 8192 tokens, 245 -> 338 for prompts in chunks; 6 costs up to 2% more.
 constexpr int kPartCost = 3;
+constexpr int kPartCostFew = 3;
+// Bytes of prefixes that row tiles share from which on their ranges are aligned.
+constexpr size_t kAlignBytes = size_t(64) << 20;
 constexpr int kInvBits = 2;                     // least tiles of a batch-invariant part (2^this)
 constexpr int kInvParts = 32;                   // most parts of a row tile
 
@@ -195,9 +198,17 @@ struct Args {
 struct Seq {
     int first, n, len;          // its rows, their count, cached tokens
     int row, from;              // kShared: its row of the table; keys before this one are not its own (a prefix: -1)
+    int cost;                   // kShared: units that stand for a row tile's other work
 };
-__device__ __forceinline__ int offset_at(const Args &p, int b) { return min(max(p.offsets[b], 0), p.n_tokens); }
-__device__ __forceinline__ int length_at(const Args &p, int b) { return min(max(p.lengths[b], 0), p.width << p.page_bits); }
+// The call's arrays on the device, or copies of them in shared memory.
+struct Arrays {
+    const int32_t *offsets, *lengths, *groups, *prefix;
+};
+__device__ __forceinline__ Arrays arrays_of(const Args &p) { return Arrays{p.offsets, p.lengths, p.groups, p.prefix}; }
+__device__ __forceinline__ int offset_at(const Args &p, const Arrays &a, int b) { return min(max(a.offsets[b], 0), p.n_tokens); }
+__device__ __forceinline__ int length_at(const Args &p, const Arrays &a, int b) {
+    return min(max(a.lengths[b], 0), p.width << p.page_bits);
+}
 
 // Where the last kernel finds a token's results (kShared): the first range of
 // its row tile, how many ranges hold parts of it (1: the whole result), its
@@ -212,41 +223,44 @@ __device__ __forceinline__ uint32_t place_of(int range, int parts, int tok, bool
 // another), each of which sees every key of it.
 template <int F>
 __device__ __forceinline__ int sequences(const Args &p) { return F == kShared ? p.n_groups + p.B : p.B; }
-__device__ __forceinline__ Seq prefix_of(const Args &p, int g) {
-    const int b0 = min(max(p.groups[g], 0), p.B), b1 = min(max(p.groups[g + 1], 0), p.B);
-    Seq s{0, 0, 0, b0, -1};
+__device__ __forceinline__ Seq prefix_of(const Args &p, const Arrays &a, int g) {
+    const int b0 = min(max(a.groups[g], 0), p.B), b1 = min(max(a.groups[g + 1], 0), p.B);
+    Seq s{0, 0, 0, b0, -1, p.part_cost};
     if (b0 >= b1) return s;
-    s.first = offset_at(p, b0);
-    s.len = max(p.prefix[g], 0);
-    if (s.len > 0 && s.len <= length_at(p, b0)) s.n = max(offset_at(p, b1) - s.first, 0);
+    s.first = offset_at(p, a, b0);
+    s.len = max(a.prefix[g], 0);
+    if (s.len > 0 && s.len <= length_at(p, a, b0)) s.n = max(offset_at(p, a, b1) - s.first, 0);
     return s;
 }
 template <int F>
-__device__ __forceinline__ Seq seq_of(const Args &p, int b) {
-    if (F == kShared && b < p.n_groups) return prefix_of(p, b);
+__device__ __forceinline__ Seq seq_of(const Args &p, const Arrays &a, int b) {
+    if (F == kShared && b < p.n_groups) return prefix_of(p, a, b);
     if (F == kShared) b -= p.n_groups;
     Seq s;
-    s.first = offset_at(p, b);
-    s.n = max(offset_at(p, b + 1) - s.first, 0);
-    s.len = length_at(p, b);
+    s.first = offset_at(p, a, b);
+    s.n = max(offset_at(p, a, b + 1) - s.first, 0);
+    s.len = length_at(p, a, b);
     s.row = b;
     s.from = 0;
+    s.cost = p.part_cost;
     if (F == kShared && p.n_groups > 0) {
         int g = 0;                               // the last group that begins at or before b
         for (int end = p.n_groups; end - g > 1;) {
             const int mid = (g + end) >> 1;
-            if (p.groups[mid] <= b) g = mid;
+            if (a.groups[mid] <= b) g = mid;
             else end = mid;
         }
         // It shares the prefix where the group's rows hold its own and all of
         // them come after the prefix; else it reads its own pages from the first.
-        const Seq x = prefix_of(p, g);
-        if (p.groups[g] <= b && b < p.groups[g + 1] && s.first >= x.first && s.first + s.n <= x.first + x.n &&
+        const Seq x = prefix_of(p, a, g);
+        if (a.groups[g] <= b && b < a.groups[g + 1] && s.first >= x.first && s.first + s.n <= x.first + x.n &&
             x.len <= s.len - s.n)
             s.from = x.len;
     }
     return s;
 }
+template <int F>
+__device__ __forceinline__ Seq seq_of(const Args &p, int b) { return seq_of<F>(p, arrays_of(p), b); }
 
 // Key tiles that row tile qt reads, and its units: one per key tile (one where
 // there are none), and in the default schedule kPartCost more, last, that
@@ -255,6 +269,7 @@ __device__ __forceinline__ Seq seq_of(const Args &p, int b) {
 struct Extent {
     int lo, hi, units;          // tiles [lo, hi)
     int gap;                    // tiles left out between those of the first tokens and lo (kSinks)
+    int cost;                   // of the units, those that stand for other work
 };
 // Tiles are numbered without the gap where one is left out: tile v is the
 // sequence's tile_of(v).
@@ -277,7 +292,8 @@ __device__ __forceinline__ Extent extent_of(const Args &p, const Seq &s, int qt)
         if (e.gap > 0) left_out = max(((sink_tiles(p) + e.gap) >> p.unit_bits) - ((sink_tiles(p) - 1) >> p.unit_bits) - 1, 0);
         e.lo = 0;
     }
-    e.units = max(((e.hi - 1) >> p.unit_bits) - (e.lo >> p.unit_bits) + 1 - left_out, 1) + p.part_cost;
+    e.cost = F == kShared ? s.cost : p.part_cost;
+    e.units = max(((e.hi - 1) >> p.unit_bits) - (e.lo >> p.unit_bits) + 1 - left_out, 1) + e.cost;
     return e;
 }
 
@@ -308,7 +324,7 @@ __device__ __forceinline__ int lane_units(const Args &p, const Seq &s) {
         src = __ffs(many) - 1;
         many &= many - 1;
         o = Seq{0, __shfl_sync(0xFFFFFFFFu, s.n, src), __shfl_sync(0xFFFFFFFFu, s.len, src), 0,
-                F == kShared ? __shfl_sync(0xFFFFFFFFu, s.from, src) : 0};
+                F == kShared ? __shfl_sync(0xFFFFFFFFu, s.from, src) : 0, F == kShared ? __shfl_sync(0xFFFFFFFFu, s.cost, src) : 0};
         qt = kFew + lane;
         end = __shfl_sync(0xFFFFFFFFu, tiles, src);
         step = 32;
@@ -318,7 +334,7 @@ __device__ __forceinline__ int lane_units(const Args &p, const Seq &s) {
 
 template <int F>
 __device__ __forceinline__ int lane_units(const Args &p, int b) {
-    Seq s{0, 0, 0, 0, 0};
+    Seq s{0, 0, 0, 0, 0, 0};
     if (b < sequences<F>(p)) s = seq_of<F>(p, b);
     return lane_units<F>(p, s);
 }
@@ -338,13 +354,21 @@ __device__ __forceinline__ int warp_scan(int x) {
 // An even split of `units` over at most `ctas` ranges, none of them empty.
 struct Split {
     int ranges = 0, each = 0, more = 0;          // the first `more` ranges hold one unit more than `each`
+    int units = INT_MAX;                         // where ranges of a given size end
     __device__ __forceinline__ Split() {}
+    static __device__ __forceinline__ Split by(int units, int each) {
+        Split s;
+        s.ranges = (units + each - 1) / each;
+        s.each = each;
+        s.units = units;
+        return s;
+    }
     __device__ __forceinline__ Split(int units, int ctas) {
         ranges = min(units, ctas);
         each = ranges > 0 ? units / ranges : 0;
         more = units - each * ranges;
     }
-    __device__ __forceinline__ int begin(int c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int begin(int c) const { return min(c * each + min(c, more), units); }
     __device__ __forceinline__ int owner(int u) const {
         const int past = u - more * (each + 1);
         return past < 0 ? u / (each + 1) : more + past / each;
@@ -362,7 +386,7 @@ struct Place {
 // kShared: seqs and counts, if not null, hold every sequence and its units.
 template <int F>
 __device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place &w, int &all, Split &split,
-                                         const Seq *seqs, const int *counts) {
+                                         const Seq *seqs, const int *counts, int each) {
     const int lane = threadIdx.x & 31;
     int u = 0, at = 0;
     uint32_t mine = 0;                           // this lane's sequences, no further than 2^31 - 1
@@ -411,12 +435,46 @@ __device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place
                                  __reduce_add_sync(0xFFFFFFFFu, mine & 0xFFFFu);
             if (sum > p.max_units) return false;
             all = int(sum) * p.kv_heads;
-            split = Split(all, ctas);
+            split = F == kShared && each > 0 ? Split::by(all, each) : Split(all, ctas);
             if (cta >= split.ranges) break;
             at = split.begin(cta);
         }
     }
     return true;
+}
+
+// kShared: row tiles over the same prefix read the same keys, from L2 if they do
+// so at about the same time.  Where the prefixes are too large for L2 to keep,
+// every one of their row tiles is given whole ranges, by units without work at
+// its end, so that its ranges begin at the same keys as the others'.  Returns
+// the size of a range, or 0 for the even split (one warp; 64 continuations of
+// 32,781 tokens, 16 heads on 4 of 256: N us against M).
+__device__ __forceinline__ int align_prefixes(const Args &p, Seq *seqs, int *counts, int ctas, int bytes_per_token) {
+    const int lane = threadIdx.x & 31;
+    if (p.n_groups > 32 || p.kv_heads > ctas) return 0;
+    int all = 0, tiles = 0, each_tile = 0;
+#pragma unroll 1
+    for (int b = p.n_groups + lane; b < sequences<kShared>(p); b += 32) all = min(all + counts[b], INT_MAX / 64);
+    if (lane < p.n_groups) tiles = row_tiles(p, seqs[lane].n);
+    if (tiles > 0) each_tile = counts[lane] / tiles;
+    const long long own_all = (long long)__reduce_add_sync(0xFFFFFFFFu, all) * p.kv_heads;
+    const int ranges = __reduce_add_sync(0xFFFFFFFFu, min(tiles, ctas)) * p.kv_heads;
+    const int kept = __reduce_add_sync(0xFFFFFFFFu, tiles > 1 ? min(seqs[lane].len, INT_MAX / 64) >> 10 : 0);
+    if (own_all > INT_MAX / 4 || 4 * ranges > ctas || size_t(kept) * 1024 * bytes_per_token * p.kv_heads < kAlignBytes) return 0;
+    const int own = int(own_all);                // (and no more than 64 prefix row tiles of 2^24 units)
+    int each = (own + __reduce_add_sync(0xFFFFFFFFu, each_tile * tiles) * p.kv_heads + ctas - 1) / ctas;
+#pragma unroll 1
+    for (;; each += max(each >> 4, 1)) {
+        const int mine = (each_tile + each - 1) / each * tiles;
+        if (__reduce_add_sync(0xFFFFFFFFu, mine) * p.kv_heads + (own + each - 1) / each <= ctas) break;
+    }
+    if (tiles > 0) {
+        const int units = (each_tile + each - 1) / each * each;
+        seqs[lane].cost += units - each_tile;
+        counts[lane] = tiles * units;
+    }
+    __syncwarp();
+    return each;
 }
 
 // A run of units of one row tile.
@@ -441,7 +499,7 @@ struct Cursor {
     __device__ __forceinline__ void hold(const Args &p, const Seq *cached) {
         const int b = w.b + int(threadIdx.x & 31);
         held = w.b;
-        mine = Seq{0, 0, 0, 0, 0};
+        mine = Seq{0, 0, 0, 0, 0, 0};
         if (b < sequences<kShared>(p)) mine = cached != nullptr ? cached[b] : seq_of<kShared>(p, b);
     }
     template <int F>
@@ -452,7 +510,7 @@ struct Cursor {
         }
         if (w.b - held >= 32) hold(p, nullptr);
         auto from = [&](int x) { return __shfl_sync(0xFFFFFFFFu, x, w.b - held); };
-        s = Seq{from(mine.first), from(mine.n), from(mine.len), from(mine.row), from(mine.from)};
+        s = Seq{from(mine.first), from(mine.n), from(mine.len), from(mine.row), from(mine.from), from(mine.cost)};
     }
     // The next part, and the index of its first unit.
     template <int F>
@@ -472,7 +530,7 @@ struct Cursor {
             g.units = e.units;
             first = unit;
             const int step = min(e.units - w.u, p.invariant ? 1 : left);
-            g.units -= p.part_cost;
+            g.units -= e.cost;
             take = max(min(g.units - w.u, step), 0);         // none: a range may begin past the keys
             if (F == kSinks) {
                 // Unit u lies past the gap's units from the first one on that
@@ -644,17 +702,30 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
     grid_dep_wait();
     grid_dep_launch();
     bool ok = (base & 1023u) == 0u;              // the operands' swizzle needs it
-    // kShared: every sequence and its units, found by all warps side by side, in
-    // the room of the first queries until those are loaded
+    // kShared: every sequence and its units, found by all warps side by side out
+    // of copies of the arrays (what is looked up there is a chain of up to four
+    // loads), in the room of the first queries and keys until those are loaded.
     constexpr int kCached = P::kQBytes / int(sizeof(Seq) + sizeof(int));
+    static_assert((4 * kCached + 2) * sizeof(int) <= P::kStagesK * P::kStageBytes, "copies of the arrays");
     Seq *seqs = F == kShared && sequences<F>(p) <= kCached ? reinterpret_cast<Seq *>(smem) : nullptr;
     int *counts = F == kShared && seqs != nullptr ? reinterpret_cast<int *>(smem + kCached * sizeof(Seq)) : nullptr;
     if (F == kShared && seqs != nullptr) {
+        int32_t *copy = reinterpret_cast<int32_t *>(smem + P::kQBytes);
+        const Arrays a{copy, copy + p.B + 1, copy + 2 * p.B + 1, copy + 2 * p.B + p.n_groups + 2};
+        for (int i = threadIdx.x; i <= p.B; i += kThreads) {
+            copy[i] = p.offsets[i];
+            if (i < p.B) copy[p.B + 1 + i] = p.lengths[i];
+        }
+        for (int i = threadIdx.x; i <= p.n_groups && p.n_groups > 0; i += kThreads) {
+            copy[2 * p.B + 1 + i] = p.groups[i];
+            if (i < p.n_groups) copy[2 * p.B + p.n_groups + 2 + i] = p.prefix[i];
+        }
+        __syncthreads();
 #pragma unroll 1
         for (int b0 = 32 * warp; b0 < sequences<F>(p); b0 += kThreads) {
             const int b = b0 + lane;
-            Seq s{0, 0, 0, 0, 0};
-            if (b < sequences<F>(p)) s = seq_of<F>(p, b);
+            Seq s{0, 0, 0, 0, 0, 0};
+            if (b < sequences<F>(p)) s = seq_of<F>(p, a, b);
             const int u = lane_units<F>(p, s);
             if (b >= sequences<F>(p)) continue;
             seqs[b] = s;
@@ -682,7 +753,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
         int all = 0;
         Split split;
         Cursor cur{};
-        const bool planned = schedule<F>(p, blockIdx.x, gridDim.x, cur.w, all, split, seqs, counts);
+        const int each = F == kShared && seqs != nullptr ? align_prefixes(p, seqs, counts, gridDim.x, 4 * D) : 0;
+        const bool planned = schedule<F>(p, blockIdx.x, gridDim.x, cur.w, all, split, seqs, counts, each);
         if (!planned && blockIdx.x == 0 && lane == 0) atomicOr(p.status, 1u << kStatusShape);
         if (F == kShared && blockIdx.x == 0 && lane == 0) *p.planned = planned;
         if (int(blockIdx.x) < split.ranges) {
@@ -1426,14 +1498,15 @@ paged_attn_join_kernel(const Args p) {
 
 // kShared: a row's parts over its group's prefix and those over what follows
 // it, joined as above in one go.  A warp takes a row, a CTA the rows of a token
-// that read one key/value head.  Latency bounds it here too: the parts' first
-// eight are fetched before their statistics have come.
-constexpr int kMergeThreads = 128;
+// that read one key/value head.  Latency bounds it here too: the first parts
+// are fetched before their statistics have come.
+constexpr int kMergeWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads)
+__global__ void __launch_bounds__(32 * kMergeWarps)
 paged_attn_merge_kernel(const Args p) {
     __shared__ int covered;
-    constexpr int kCols = D / 32;                // of a lane: 2, 4 or twice 4
+    constexpr int kCols = D == 64 ? 2 : 4;       // of a lane
+    constexpr int kSlices = D / (32 * kCols);    // warps a row
     constexpr int kAhead = 8;
     const int t = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) covered = 0;
@@ -1441,9 +1514,10 @@ paged_attn_merge_kernel(const Args p) {
     grid_dep_launch();
     const int planned = *p.planned;
     __syncthreads();
-    for (int b = tid; b < p.B; b += kMergeThreads)
+    for (int b = tid; b < p.B; b += int(blockDim.x))
         if (p.offsets[b] <= t && t < p.offsets[b + 1]) covered = 1;
     const size_t rows = size_t(p.n_tokens) * p.q_heads, tokens = size_t(p.n_tokens) * p.kv_heads;
+    const size_t kept = size_t(p.res_ml - p.part_ml);        // the kept results' rows follow the slots'
 #pragma unroll 1
     for (int kvh = blockIdx.y; kvh < p.kv_heads; kvh += gridDim.y) {
         const size_t at = size_t(t) * p.kv_heads + kvh;
@@ -1452,82 +1526,74 @@ paged_attn_merge_kernel(const Args p) {
         if (planned == 0 || covered == 0) return;            // a row of no sequence is left alone
         const int n_own = own >> 8 & 0x1FF, n = n_own + ((own >> 24 & 1u) != 0u ? int(pre >> 8 & 0x1FF) : 0);
 #pragma unroll 1
-        for (int g = warp; g < p.group; g += kMergeThreads / 32) {
-            const size_t row = size_t(t) * p.q_heads + kvh * p.group + g;
-            // part i: of what follows the prefix, then of the prefix
-            struct {
-                const float *o;
-                const float2 *ml;
-            } src;
-            auto part = [&](int i) {
+        for (int g = warp; g < p.group * kSlices; g += int(blockDim.x) / 32) {
+            const int head = g / kSlices, col = g % kSlices * (32 * kCols) + lane * kCols;
+            const size_t row = size_t(t) * p.q_heads + kvh * p.group + head;
+            float top = -INFINITY, l = 0.f, o[kCols];
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) o[c] = 0.f;
+            // Parts 32 at a time, one a lane: first those of what follows the
+            // prefix.  A running maximum over more than 32.
+#pragma unroll 1
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                const int i = i0 + lane;
                 const bool follows = i < n_own;
                 const uint32_t w = follows ? own : pre;
                 const int k = follows ? i : i - n_own;
-                if ((w >> 8 & 0x1FF) == 1) {
-                    const size_t r = (follows ? rows : 0) + row;
-                    src.o = p.res_o + r * D;
-                    src.ml = p.res_ml + r;
-                } else {
-                    const int slot = 2 * (int(w & 0xFF) + k) + (k == 0);
-                    const size_t r = size_t(slot) * p.slot_rows + (w >> 17 & 0x7F) * p.group + g;
-                    src.o = p.part_o + r * D;
-                    src.ml = p.part_ml + r;
-                }
-                return src;
-            };
-            float v[kAhead][kCols];
-            auto fetch = [&](int i0) {
+                size_t r = kept + (follows ? rows : 0) + row;
+                if ((w >> 8 & 0x1FF) != 1)
+                    r = size_t(2 * (int(w & 0xFF) + k) + (k == 0)) * p.slot_rows + (w >> 17 & 0x7F) * p.group + head;
+                float2 ml = make_float2(-INFINITY, 0.f);
+                if (i < n) ml = p.part_ml[r];
+                float v[kAhead][kCols];
+                auto fetch = [&](int j0) {
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    if (i0 + u >= n) break;
-                    const float *o = part(i0 + u).o + lane * kCols;
-                    if (kCols == 2) {
-                        *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(o);
-                    } else {
+                    for (int u = 0; u < kAhead; ++u) {
+                        const size_t from = __shfl_sync(0xFFFFFFFFu, r, j0 + u);
 #pragma unroll
-                        for (int c = 0; c < kCols; c += 4)
-                            *reinterpret_cast<float4 *>(v[u] + c) = *reinterpret_cast<const float4 *>(o + c);
+                        for (int c = 0; c < kCols; ++c) v[u][c] = 0.f;
+                        if (i0 + j0 + u >= n) continue;
+                        const float *src = p.part_o + from * D + col;
+                        if (kCols == 2) *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(src);
+                        else *reinterpret_cast<float4 *>(v[u]) = *reinterpret_cast<const float4 *>(src);
                     }
+                };
+                fetch(0);
+                float most = ml.x;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+                if (most > top) {
+                    const float a = top == -INFINITY ? 0.f : ex2(top - most);
+                    l *= a;
+                    if (i0 > 0)
+#pragma unroll
+                        for (int c = 0; c < kCols; ++c) o[c] *= a;
+                    top = most;
                 }
-            };
-            fetch(0);
-            float top = -INFINITY, l = 0.f, w = 0.f, o[kCols];
-            for (int i = lane; i < n; i += 32) top = fmaxf(top, part(i).ml->x);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) o[c] = 0.f;
+                const float weight = i < n && top > -INFINITY ? ex2(ml.x - top) : 0.f;
+                l += ml.y != 0.f ? weight * ml.y : 0.f;
 #pragma unroll 1
-            for (int i0 = 0; i0 < n; i0 += kAhead) {
-                if (i0 > 0) fetch(i0);
-                if (i0 % 32 == 0) {              // the weights of 32 parts, one a lane
-                    w = 0.f;
-                    if (i0 + lane < n) {
-                        const float2 ml = *part(i0 + lane).ml;
-                        w = top == -INFINITY ? 0.f : ex2(ml.x - top);
-                        l += ml.y != 0.f ? w * ml.y : 0.f;
+                for (int j = 0; j < 32 && i0 + j < n; j += kAhead) {
+                    if (j > 0) fetch(j);
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) {
+                        const float x = __shfl_sync(0xFFFFFFFFu, weight, j + u);
+#pragma unroll
+                        for (int c = 0; c < kCols; ++c) o[c] = fmaf(x, v[u][c], o[c]);
                     }
-                }
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    if (i0 + u >= n) break;
-                    const float x = __shfl_sync(0xFFFFFFFFu, w, (i0 + u) % 32);
-#pragma unroll
-                    for (int c = 0; c < kCols; ++c) o[c] = fmaf(x, v[u][c], o[c]);
                 }
             }
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
             const float inv = l != 0.f ? 1.f / l : 0.f;
-            if (p.lse != nullptr && lane == 0) p.lse[row] = l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
+            if (p.lse != nullptr && lane == 0 && g % kSlices == 0) p.lse[row] = l != 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
             uint32_t h[kCols / 2];
 #pragma unroll
             for (int c = 0; c < kCols; c += 2)
                 h[c / 2] = inv != 0.f ? h2_as_u32(__floats2half2_rn(o[c] * inv, o[c + 1] * inv)) : 0u;
-            __half *out = p.out + row * D + lane * kCols;
+            __half *out = p.out + row * D + col;
             if (kCols == 2) *reinterpret_cast<uint32_t *>(out) = h[0];
-            else if (kCols == 4) *reinterpret_cast<uint2 *>(out) = make_uint2(h[0], h[1]);
-            else *reinterpret_cast<uint4 *>(out) = make_uint4(h[0], h[1], h[kCols / 2 - 2], h[kCols / 2 - 1]);
+            else *reinterpret_cast<uint2 *>(out) = make_uint2(h[0], h[kCols / 2 - 1]);
         }
     }
 }
@@ -1565,6 +1631,12 @@ Slots slots_of(int n_tokens, int B, int q_heads, int kv_heads, int max_context, 
     return s;
 }
 
+// Warps of a CTA that shares out `rows` evenly.
+int merge_warps(int rows) {
+    const int rounds = (rows + kMergeWarps - 1) / kMergeWarps;
+    return (rows + rounds - 1) / rounds;
+}
+
 template <int D, int F>
 w4v_status launch(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap, const Args &a, int grid,
                   cudaStream_t stream) {
@@ -1582,7 +1654,7 @@ w4v_status launch(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtens
     if (launch_pdl(paged_attn_kernel<D, F>, dim3(grid), dim3(kThreads), Plan<D>::kBytes, stream, qmap, kmap, vmap, a) !=
             cudaSuccess ||
         (F == kShared ? launch_pdl(paged_attn_merge_kernel<D>, dim3(a.n_tokens, std::min(a.kv_heads, 65535)),
-                                   dim3(kMergeThreads), 0, stream, a)
+                                   dim3(32 * merge_warps(a.group * (D == 256 ? 2 : 1))), 0, stream, a)
                       : launch_pdl(paged_attn_join_kernel<D>, dim3(grid, kJoinSplit), dim3(kJoinThreads), 0, stream, a)) !=
             cudaSuccess) {
         cudaGetLastError();
@@ -1652,6 +1724,7 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     a.invariant = invariant;
     a.unit_bits = invariant ? inv_tile_bits(kv.table_width * kv.page) : 0;
     a.part_cost = invariant ? 0 : kPartCost;
+    if (!invariant && (shared != nullptr || sinks > 0) && n_tokens <= (long long)kv.B * a.tok) a.part_cost = kPartCostFew;
     a.max_units = uint32_t(std::min(invariant ? slots.count : size_t(INT_MAX), size_t(INT_MAX)) / kv.kv_heads);
     a.scale_log2 = scale * 1.4426950408889634f;
     // K and V as (64 elements, 8 tokens, blocks of a head, 8-token groups):
