@@ -112,7 +112,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 // the CTAs that hold the short rows of prompts end last: 272 -> 314 us for
 // 8192 tokens, 245 -> 338 for prompts in chunks; 6 costs up to 2% more.
 constexpr int kPartCost = 3;
-constexpr int kPartCostFew = 3;
 // Bytes of prefixes that row tiles share from which on their ranges are aligned.
 constexpr size_t kAlignBytes = size_t(64) << 20;
 constexpr int kInvBits = 2;                     // least tiles of a batch-invariant part (2^this)
@@ -1724,7 +1723,6 @@ w4v_status launch_paged_attn(const w4v_kv_t &kv, const uint16_t *q, long long q_
     a.invariant = invariant;
     a.unit_bits = invariant ? inv_tile_bits(kv.table_width * kv.page) : 0;
     a.part_cost = invariant ? 0 : kPartCost;
-    if (!invariant && (shared != nullptr || sinks > 0) && n_tokens <= (long long)kv.B * a.tok) a.part_cost = kPartCostFew;
     a.max_units = uint32_t(std::min(invariant ? slots.count : size_t(INT_MAX), size_t(INT_MAX)) / kv.kv_heads);
     a.scale_log2 = scale * 1.4426950408889634f;
     // K and V as (64 elements, 8 tokens, blocks of a head, 8-token groups):

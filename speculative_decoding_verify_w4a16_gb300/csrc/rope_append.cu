@@ -357,6 +357,145 @@ norm_rope_append_kernel(const Args p) {
     }
 }
 
+// The same for many tokens in whole pieces.  There the instructions count (45 us
+// for 8192 rows of 24 x 256 with 78% of the issue slots in use), so a warp takes
+// a token: the factors of its pieces lie in registers for all heads, and there
+// is no barrier; 5039 -> 2810 instructions a token.  kAheadMany passes over 256
+// / D heads are loaded ahead; more of them cost more in warps at a time than
+// they bring (8192 rows, by passes ahead and CTAs an SM: 2 and 7 38.2 us, 5.3
+// TB/s, 2 and 8 38.4, 3 and 7 40.8, 1 and 8 43.9, 4 and 5 48.5; 24 x 128 27.3 of
+// 31.7, 36 x 64 19.0 of 26.7 with a CTA a token).  From 24 rows an SM on: 2560
+// rows take 13.3 us like this and 12.1 with a CTA each, some 4100 21.2 and 22.1.
+constexpr int kWarpThreads = 128, kAheadMany = 2, kWarpRows = 24;
+template <bool kInter, int D>
+__global__ void __launch_bounds__(kWarpThreads, 7)
+norm_rope_append_warp_kernel(const Args p) {
+    constexpr int kLanes = D / 8, kHeads = 32 / kLanes;          // lanes a head, heads a pass
+    __shared__ float2 cs[kWarpThreads / 32][D / 2];
+    const int lane = threadIdx.x & 31, warp = int(threadIdx.x) >> 5, t = blockIdx.x * (kWarpThreads / 32) + warp;
+    grid_dep_wait();
+    grid_dep_launch();
+    if (t >= p.n_tokens) return;
+    const __half *qs = p.q + t * p.q_stride, *ks = p.k + t * p.k_stride, *vs = p.v + t * p.v_stride;
+    const int e = 8 * (lane % kLanes), sub = lane / kLanes;
+    const int turned = p.q_heads + p.kv_heads, heads = turned + p.kv_heads, passes = (heads + kHeads - 1) / kHeads;
+    const bool turn = e < p.rot, upper = !kInter && e >= p.rot / 2;
+    // The lane that holds the partner piece (half layout), or this one.
+    const int partner = kInter || !turn ? lane : lane + (upper ? -p.rot / 16 : p.rot / 16);
+    Piece a[kAheadMany];
+    auto load = [&](int pass) {
+        const int h = pass * kHeads + sub;
+        const __half *src = h < p.q_heads ? qs + h * D : h < turned ? ks + (h - p.q_heads) * D : vs + (h - turned) * D;
+        return h < heads ? *reinterpret_cast<const uint4 *>(src + e) : make_uint4(0u, 0u, 0u, 0u);
+    };
+#pragma unroll
+    for (int u = 0; u < kAheadMany; ++u) a[u].u = load(u);
+
+    int b = -1;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const bool here = b0 + lane < p.B && p.offsets[b0 + lane] <= t && t < p.offsets[b0 + lane + 1];
+        const uint32_t some = __ballot_sync(0xFFFFFFFFu, here);
+        if (some != 0) b = b0 + __ffs(some) - 1;
+    }
+    if (b < 0) return;
+    const int end = min(p.offsets[b + 1], p.n_tokens);
+    const int cap = p.table_width << p.page_bits, last = (1 << p.page_bits) - 1;
+    const int at = min(max(p.lengths[b], 0), cap) - end + t;      // may be negative: the row has no slot
+    const int pos = p.positions != nullptr ? p.positions[t] : at;
+    for (int i = lane; i < p.rot / 2; i += 32) {
+        const uint32_t part = uint32_t((uint64_t(int64_t(pos)) * p.phases[i]) >> 32);
+        float s, c;
+        sincospif(float(int32_t(part)) * (1.f / 2147483648.f), &s, &c);   // 2 pi part / 2^32
+        cs[warp][i] = make_float2(c * p.mul, s * p.mul);
+    }
+    long long slot = -1;                                         // head 0's elements of this token
+    if (at >= 0) {
+        const int id = p.table[size_t(b) * p.table_width + (at >> p.page_bits)];
+        if (id >= 0 && id < p.n_pages) slot = (((long long)id * p.kv_heads << p.page_bits) + (at & last)) * D;
+    }
+    __syncwarp();
+    // Elements 2i and 2i + 1 of the piece are r (x own + x_partner other).
+    float2 own[4], other[4];
+    auto factors = [&](const __half *weight) {
+        Piece w, z;
+        if (weight != nullptr) w.u = *reinterpret_cast<const uint4 *>(weight + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 x = make_float2(1.f, 1.f);
+            if (weight != nullptr) {
+                x = __half22float2(w.h[i]);
+                x = make_float2(x.x + p.centre, x.y + p.centre);
+            }
+            own[i] = x;
+            other[i] = make_float2(0.f, 0.f);
+        }
+        if (!turn) return;
+        if (weight != nullptr && !kInter) z.u = *reinterpret_cast<const uint4 *>(weight + (upper ? e - p.rot / 2 : e + p.rot / 2));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 y = make_float2(own[i].y, own[i].x);          // the partners' weights
+            if (!kInter) {
+                y = make_float2(1.f, 1.f);
+                if (weight != nullptr) {
+                    y = __half22float2(z.h[i]);
+                    y = make_float2(y.x + p.centre, y.y + p.centre);
+                }
+            }
+            const float2 v0 = cs[warp][kInter ? e / 2 + i : (upper ? e - p.rot / 2 : e) + 2 * i];
+            const float2 v1 = kInter ? v0 : cs[warp][(upper ? e - p.rot / 2 : e) + 2 * i + 1];
+            own[i] = make_float2(own[i].x * v0.x, own[i].y * v1.x);
+            other[i] = make_float2(y.x * (upper ? v0.y : -v0.y), y.y * (kInter || upper ? v1.y : -v1.y));
+        }
+    };
+    factors(p.q_weight);
+    const long long hop = (long long)D << p.page_bits;           // from head to head within a page
+    __half *qd = p.q_out + size_t(t) * p.q_heads * D + e, *kd = p.k_cache + slot + e, *vd = p.v_cache + slot + e;
+    const int k_pass = p.q_heads / kHeads;                       // the first pass with a key head
+    auto finish = [&](const Piece &x) {
+        float2 q = make_float2(0.f, 0.f), f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = __half22float2(x.h[i]);
+            q = __ffma2_rn(f[i], f[i], q);
+        }
+        float sum = q.x + q.y;
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        const float r = rsqrtf(sum * (1.f / D) + p.eps);
+        Piece o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 y = make_float2(f[i].y, f[i].x);
+            if (!kInter) y = __half22float2(u32_as_h2(__shfl_sync(0xFFFFFFFFu, h2_as_u32(x.h[i]), partner)));
+            const float2 z = __ffma2_rn(y, other[i], __fmul2_rn(f[i], own[i]));
+            o.h[i] = __float22half2_rn(__fmul2_rn(z, make_float2(r, r)));
+        }
+        return o.u;
+    };
+    // The query heads, and what shares a pass with them; then key heads by
+    // their own factors; then values as they are.
+#pragma unroll 1
+    for (int pass0 = 0; pass0 < passes; pass0 += kAheadMany) {
+#pragma unroll
+        for (int u = 0; u < kAheadMany; ++u) {
+            const int pass = pass0 + u, h = pass * kHeads + sub;
+            if (pass >= passes) break;                           // the same for all lanes
+            Piece x;
+            x.u = a[u].u;
+            a[u].u = load(pass + kAheadMany);
+            uint4 out = x.u;
+            if (pass * kHeads < p.q_heads) out = finish(x);
+            if (h < p.q_heads) *reinterpret_cast<uint4 *>(qd + h * D) = out;
+            if (pass < k_pass) continue;
+            if (pass == k_pass) factors(p.k_weight);             // (its key heads are done again with them)
+            if (pass * kHeads < turned) out = finish(x);
+            if (slot < 0) continue;
+            if (h >= p.q_heads && h < turned) *reinterpret_cast<uint4 *>(kd + (h - p.q_heads) * hop) = out;
+            if (h >= turned && h < heads) *reinterpret_cast<uint4 *>(vd + (h - turned) * hop) = x.u;
+        }
+    }
+}
+
 // CTAs of 256 threads for a few tokens, of 128 for many, where twice as many
 // tokens side by side count for more than each one's own time (one GB300: 16
 // rows of 28 x 128 2.8 against 3.1 us, 8192 rows of 24 x 256 39.7 against
@@ -364,6 +503,17 @@ norm_rope_append_kernel(const Args p) {
 template <bool kInter, bool kVec>
 w4v_status launch(const Args &a, bool norm, int sms, cudaStream_t stream) {
     const bool many = a.n_tokens >= 16 * sms;
+    if (norm && kVec && a.n_tokens >= kWarpRows * sms) {
+        const auto kernel = a.head_dim == 64 ? norm_rope_append_warp_kernel<kInter, 64>
+                            : a.head_dim == 128 ? norm_rope_append_warp_kernel<kInter, 128>
+                                                : norm_rope_append_warp_kernel<kInter, 256>;
+        constexpr int kTokens = kWarpThreads / 32;
+        if (launch_pdl(kernel, dim3((a.n_tokens + kTokens - 1) / kTokens), dim3(kWarpThreads), 0, stream, a) != cudaSuccess) {
+            cudaGetLastError();
+            return W4V_ERR_CUDA;
+        }
+        return W4V_OK;
+    }
     const auto kernel = norm ? many ? norm_rope_append_kernel<kInter, kVec, 128> : norm_rope_append_kernel<kInter, kVec, 256>
                              : many ? rope_append_kernel<kInter, kVec, 128> : rope_append_kernel<kInter, kVec, 256>;
     if (launch_pdl(kernel, dim3(a.n_tokens), dim3(many ? 128 : 256), 0, stream, a) != cudaSuccess) {

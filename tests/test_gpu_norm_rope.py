@@ -146,6 +146,33 @@ def test_many_rows(w4v_mod, gpu, D, rot, inter):
     check(w4v_mod, gpu, c, rot, inter, *x, in_place=True)
 
 
+@pytest.mark.parametrize("D,rot,inter", [(64, 64, False), (64, 32, True), (128, 128, False), (256, 64, False), (256, 256, True)])
+@pytest.mark.parametrize("Hq,Hkv", [(5, 3), (8, 2)])
+def test_a_long_prompt(w4v_mod, gpu, D, rot, inter, Hq, Hkv):
+    """Enough rows for a warp each; passes that hold query and key heads, and rows without a place or a sequence."""
+    rng, w = np.random.default_rng([D, rot, Hq]), w4v_mod
+    n = 4100
+    c = cache(rng, [3000, 0, n - 3000], [3100, 5, n - 3000], 1, Hkv, D, 64)
+    x = rows(rng, n, Hq, Hkv, D) + weights(rng, D, True)
+    check(w, gpu, c, rot, inter, *x, centred=True)
+    check(w, gpu, c, rot, inter, *x[:3], in_place=True)
+    c["lengths"][0] = 2990                                # its first ten rows sit before position 0
+    c["table"][2, 3] = -1
+    d = {a: to_dev(b, gpu) for a, b in c.items()}
+    q, k, v = (to_dev(torch.cat([torch.from_numpy(b), torch.from_numpy(b[:7])]).numpy(), gpu) for b in x[:3])
+    out = torch.full_like(q, 5.0)
+    w.norm_rope_append(q, k, v, d["k"], d["v"], d["table"], d["lengths"], d["offsets"], w.Rope(rot, interleaved=inter),
+                       w.HeadNorm(), q_out=out)
+    torch.cuda.synchronize()
+    assert torch.all(out[n:] == 5.0) and not torch.any(torch.all((out[:n] == 5.0).flatten(1), 1))
+    want = c["v"].copy()
+    for t in range(n):
+        b, p = (0, t - 10) if t < 3000 else (2, t - 3000)
+        if p >= 0 and c["table"][b, p // 64] >= 0:
+            want[c["table"][b, p // 64], :, p % 64] = x[2][t]
+    assert np.array_equal(d["v"].cpu().numpy(), want)
+
+
 def test_rows_without_a_place(w4v_mod, gpu):
     """Rows before position 0 and pages that are not there are not written; rows of no sequence are left alone."""
     rng = np.random.default_rng(8)
