@@ -18,7 +18,7 @@
 // The `top` largest, ties to the lower index, without sorting.  The threads in
 // 64 groups: the top-th largest of the groups' largest logits is a bound that
 // at least `top` logits reach, and few exceed where they lie without order.
-// The first 16,384 logits give such a bound.  From then on a thread looks
+// The first 8192 logits (16,384 of fp16) give such a bound.  From then on a thread looks
 // whether its 16 next logits' largest, which it has anyway, is above it (a logit
 // equal to it comes too late, by its index), and if so notes the batch.  At the
 // end the groups' largest of all logits give a second, closer bound; the noted
@@ -39,7 +39,6 @@ namespace w4v {
 namespace {
 
 constexpr int kBatch = 16;                      // logits of a thread that are looked at together
-constexpr int kLoads = 8;                       // 16-byte loads of a thread in flight
 constexpr float kSlack = 2.f;
 constexpr int kGroups = 64;
 constexpr int kMost = kLogprobsMaxTop;
@@ -111,13 +110,6 @@ struct Vec<float> {
         x[3] = __uint_as_float(w.w);
     }
     static __device__ __forceinline__ float one(const float *p) { return *p; }
-    // The logits [first, first + 4) of a row of V as far as there are, else -inf.
-    static __device__ __forceinline__ uint4 some(const float *row, int first, int V) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = first + j >= 0 && first + j < V ? __float_as_uint(row[first + j]) : kLowest;
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
 };
 template <>
 struct Vec<__half> {
@@ -133,17 +125,6 @@ struct Vec<__half> {
         }
     }
     static __device__ __forceinline__ float one(const __half *p) { return __half2float(*p); }
-    static __device__ __forceinline__ uint4 some(const __half *row, int first, int V) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = first + 2 * j;
-            const uint32_t lo = k >= 0 && k < V ? __half_as_ushort(row[k]) : 0xFC00u;
-            const uint32_t hi = k + 1 >= 0 && k + 1 < V ? __half_as_ushort(row[k + 1]) : 0xFC00u;
-            w[j] = lo | hi << 16;
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
 };
 
 // A batch whose largest logit may be among the row's `top`.
@@ -169,7 +150,7 @@ struct __align__(8) Shared {
     uint64_t ties[kTies];
     uint64_t best[kMost];                       // the CTA's largest, in order (0: none)
     uint64_t group_key[kGroups], bound_key;
-    float group[kGroups], bound;
+    float group[2][kGroups], bound[2];          // by turns
     Sums warp[kWarps], all;
     int n, n_ties, n_notes;
     int scan[kWarps];
@@ -196,19 +177,18 @@ __device__ __forceinline__ int2 groups_above(const K *group, K mine) {
 }
 
 // The top-th largest of the groups' largest logits, `most` this thread's.
-// Every thread calls it; begins and ends with a barrier.
+// Every thread calls it, with another `turn` than the last time; two barriers.
 template <int kThreads>
-__device__ __forceinline__ float bound_of_groups(Shared<kThreads> &sh, float most, int top) {
+__device__ __forceinline__ float bound_of_groups(Shared<kThreads> &sh, float most, int top, int turn) {
     constexpr int kLanes = Shared<kThreads>::kLanes;
 #pragma unroll
     for (int d = 1; d < kLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+    if (threadIdx.x % kLanes == 0) sh.group[turn][threadIdx.x / kLanes] = most;
     __syncthreads();
-    if (threadIdx.x % kLanes == 0) sh.group[threadIdx.x / kLanes] = most;
+    const int2 n = groups_above<kLanes>(sh.group[turn], most);
+    if (n.x < top && top <= n.y) sh.bound[turn] = most;          // (several groups: the same value)
     __syncthreads();
-    const int2 n = groups_above<kLanes>(sh.group, most);
-    if (n.x < top && top <= n.y) sh.bound = most;                // (several groups: the same value)
-    __syncthreads();
-    return sh.bound;
+    return sh.bound[turn];
 }
 
 // sh.best: the `top` largest of sh.list[0 .. n), in order; n < top: all, then 0.
@@ -245,8 +225,10 @@ __device__ __noinline__ void best_of_list(Shared<kThreads> &sh, int top, int n) 
             n = sh.n_ties;
         }
     }
-    if (tid < kMost) sh.best[tid] = 0;
-    __syncthreads();
+    if (n < top) {                               // else every place is written
+        if (tid < kMost) sh.best[tid] = 0;
+        __syncthreads();
+    }
     // each counts those above it, two threads a key
     for (int i = tid / 2; i < (n + 15) / 16 * 16; i += kThreads / 2) {       // (whole warps)
         const uint64_t key = i < n ? list[i] : 0;
@@ -312,7 +294,8 @@ template <int W, int kThreads>
 __device__ __noinline__ void collect(Shared<kThreads> &sh, const float (&x)[kBatch], float most, int first, int limit, int top) {
     const int tid = threadIdx.x;
     if (tid == 0) sh.n_ties = 0;
-    const float bound = bound_of_groups(sh, most, top);
+    __syncthreads();
+    const float bound = bound_of_groups(sh, most, top, 0);
     const int before = sh.n;
     __syncthreads();
     if (most >= bound && most > -INFINITY)
@@ -346,45 +329,46 @@ token_logprobs_kernel(const Args p) {
     using Sh = Shared<kThreads>;
     __shared__ Sh sh;
     constexpr int W = Vec<T>::kCount, kRows = kBatch / W;        // vectors of a batch
+    // 16-byte loads of a thread in flight.  More of them spill with alternatives
+    // (2048 rows: 208 us with 4, 220 with 8; without 186 and 176).
+    constexpr int kLoads = kTop ? 4 : 8;
     constexpr int kWarps = Sh::kWarps;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cluster = 1 << p.cluster_bits, rank = int(blockIdx.x) & (cluster - 1), row = int(blockIdx.x) >> p.cluster_bits;
     grid_dep_wait();
     grid_dep_launch();
-    // Vectors of 16 bytes from the boundary at or before the row's first
-    // logit: vector v holds logits v W - shift ...
+    // Vectors of 16 bytes from the boundary at or before the row's first logit:
+    // vector v holds logits v W - shift ...  Whole ones are dealt out; the few
+    // logits at the row's ends are a thread's each, of the first CTA.
     const T *x0 = static_cast<const T *>(p.logits) + row * p.stride;
     const int shift = int(reinterpret_cast<uintptr_t>(x0) & 15u) / int(sizeof(T));
     const uint4 *base = reinterpret_cast<const uint4 *>(x0 - shift);
-    const int vecs = int((unsigned(p.V) + shift + W - 1) / W);
-    const int each = (vecs + cluster - 1) >> p.cluster_bits;
-    const int begin = min(rank * each, vecs), end = min(begin + each, vecs);
-    const int whole0 = shift > 0, whole1 = min(int((unsigned(p.V) + shift) / W), end);       // whole vectors: [whole0, whole1)
-    const int limit = min(end * W - shift, p.V);                 // this CTA's logits end here
+    const int whole0 = shift > 0, whole1 = max(int((unsigned(p.V) + shift) / W), whole0);    // whole vectors: [whole0, whole1)
+    const int each = (whole1 - whole0 + cluster - 1) >> p.cluster_bits;
+    const int begin = min(whole0 + rank * each, whole1), end = min(begin + each, whole1);
+    const int limit = end * W - shift;                           // the dealt logits of this CTA end here
+    const int head = min(whole0 * W - whole0 * shift, p.V), tail = max(whole1 * W - shift, head);
+    const int at_end = rank == 0 ? (tid < head ? tid : tail + tid - head < p.V ? tail + tid - head : -1) : -1;
 
     Sums mine{-INFINITY, 0.f, 0.f};
     float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
     float bound = -INFINITY, most = -INFINITY;
     bool again = false;                          // the row once more, every batch collected by all
+    const float edge = at_end >= 0 ? Vec<T>::one(x0 + at_end) : -INFINITY;
     if (kTop) {
         if (tid == 0) sh.n = sh.n_notes = 0;
         __syncthreads();
     }
     for (;;) {
+        if (kTop && at_end >= 0) sh.list[atomicAdd(&sh.n, 1)] = key_of(edge, at_end);          // (14 at most)
+        // (a vector's room is filled again as soon as it is done with)
+        uint4 w[kLoads];
+        auto fetch = [&](int v) {
+            return v < end ? base[v] : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
+        };
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) w[i] = fetch(begin + i * kThreads + tid);
         for (int v0 = begin; v0 == begin || v0 < end; v0 += kThreads * kLoads) {
-            uint4 w[kLoads];
-            if (v0 >= whole0 && v0 + kThreads * kLoads <= whole1) {
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) w[i] = base[v0 + i * kThreads + tid];
-            } else {
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int v = v0 + i * kThreads + tid;
-                    if (v >= whole0 && v < whole1) w[i] = base[v];
-                    else if (v < end) w[i] = Vec<T>::some(x0, v * W - shift, p.V);
-                    else w[i] = make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
-                }
-            }
             const bool opening = kTop && !again && v0 == begin;
             if (opening) {
                 float x[W];
@@ -394,7 +378,7 @@ token_logprobs_kernel(const Args p) {
 #pragma unroll
                     for (int k = 0; k < W; k += 2) most = max3(most, x[k], x[k + 1]);
                 }
-                bound = bound_of_groups(sh, most, p.top);
+                bound = bound_of_groups(sh, most, p.top, 0);
             }
 #pragma unroll
             for (int b = 0; b < kLoads; b += kRows) {
@@ -402,6 +386,10 @@ token_logprobs_kernel(const Args p) {
                 float x[kBatch];
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) Vec<T>::get(w[b + i], x + i * W);
+                auto refill = [&] {
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i) w[b + i] = fetch(v0 + (kLoads + b + i) * kThreads + tid);
+                };
                 float top = x[0];
 #pragma unroll
                 for (int k = 1; k < kBatch - 1; k += 2) top = max3(top, x[k], x[k + 1]);
@@ -416,12 +404,15 @@ token_logprobs_kernel(const Args p) {
                         best_of_list(sh, p.top, sh.n);
                         if (tid < p.top) sh.list[tid] = sh.best[tid];
                         if (tid == 0) sh.n = p.top;
+                        refill();
                         continue;
                     }
                     // Few groups hold a token above -inf, so the first batch has
                     // all those of -inf that may be wanted (or it is all there is).
-                    const int n = in_order<W>(sh, y, -INFINITY, first, limit, 0, p.top);
-                    if (tid == 0) sh.n = n;
+                    const int before = sh.n;
+                    __syncthreads();
+                    const int n = in_order<W>(sh, y, -INFINITY, first, limit, before, p.top);
+                    if (tid == 0) sh.n = before + n;
                 }
                 if (kTop) {
                     most = fmaxf(most, top);
@@ -450,10 +441,11 @@ token_logprobs_kernel(const Args p) {
                     d.y = fmaxf(d.y, -3e38f);
                     t = __ffma2_rn(e, d, t);
                 }
+                refill();
             }
         }
         if (!kTop || again) break;
-        const float second = bound_of_groups(sh, most, p.top);
+        const float second = bound_of_groups(sh, most, p.top, 1);        // (and every note is there)
         const int notes = sh.n_notes;
         if (notes <= Sh::kNotes) {
             for (int i = tid; i < notes * kRows; i += kThreads) {
@@ -461,7 +453,7 @@ token_logprobs_kernel(const Args p) {
                 const int first = note.first + i % kRows * (kThreads * W), v = (first + shift) / W;
                 if (note.most < second || v >= end) continue;
                 float x[W];
-                Vec<T>::get(v >= whole0 && v < whole1 ? base[v] : Vec<T>::some(x0, first, p.V), x);
+                Vec<T>::get(base[v], x);
 #pragma unroll
                 for (int j = 0; j < W; ++j)
                     if (x[j] >= second && x[j] > -INFINITY) {
@@ -474,9 +466,22 @@ token_logprobs_kernel(const Args p) {
         }
         __syncthreads();
         if (tid == 0) sh.n = 0;
+        __syncthreads();
         again = true;
     }
     if (kTop) best_of_list(sh, p.top, sh.n);
+    if (at_end >= 0 && (edge > -INFINITY || edge != edge)) {
+        if (edge > mine.m) {
+            const float d = mine.m - edge, a = mine.m == -INFINITY ? 1.f : ex2(d * p.heat_log2);
+            if (mine.m > -INFINITY)
+                t = a == 0.f ? make_float2(0.f, 0.f) : make_float2(a * (t.x + d * s.x), a * (t.y + d * s.y));
+            s = make_float2(a * s.x, a * s.y);
+            mine.m = edge;
+        }
+        const float d = edge - (mine.m == -INFINITY ? 0.f : mine.m), e2 = ex2(d * p.heat_log2);
+        s.x += e2;
+        t.x += e2 * fmaxf(d, -3e38f);
+    }
     mine.s = s.x + s.y;
     mine.t = t.x + t.y;
 
