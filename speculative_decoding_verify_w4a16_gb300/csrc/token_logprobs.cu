@@ -18,16 +18,21 @@
 // The `top` largest, ties to the lower index, without sorting.  The threads in
 // 64 groups: the top-th largest of the groups' largest logits is a bound that
 // at least `top` logits reach, and few exceed where they lie without order.
-// The first 8192 logits (16,384 of fp16) give such a bound.  From then on a thread looks
-// whether its 16 next logits' largest, which it has anyway, is above it (a logit
-// equal to it comes too late, by its index), and if so notes the batch.  At the
-// end the groups' largest of all logits give a second, closer bound; the noted
-// batches that reach it, some 25, are read once more, and the logits that reach
-// it count how many are above them.  (Collecting logits on the way instead of
-// notes cost 100 instructions a batch.)  Where more come than there is room for
-// (a row in ascending order, one of few different values), the row is gone
-// through once more, a batch of every thread at a time.
+// A CTA's first loads give such a bound.  From then on a thread looks whether
+// its 16 next logits' largest, which it has anyway, is above it (a logit equal
+// to it comes too late, by its index), and if so notes the batch; CTAs of 128
+// threads, whose first loads are few, take a closer bound whenever the logits
+// seen have doubled.  At the end the groups' largest of all logits give the last
+// bound; the noted batches that reach it, some 25, are read once more, and the
+// logits that reach it count how many are above them.  (Collecting logits on the
+// way instead of notes cost 100 instructions a batch.)  Where more come than
+// there is room for (a row in ascending order, one of few different values), the
+// row is gone through once more, a batch of every thread at a time.
 //
+// Measured (one GB300, device time; bound: the logits' bytes at 6.78 TB/s):
+//   1 row of 151,936                          4.7 us (0.1: latency); with 20 alternatives 9.2
+//   300 rows of 50,001 fp16, masked, 20       14.7 us (4.4: latency of a row's ends)
+//   2048 rows of 151,936, 5                   194 us (184: bytes, 6.4 TB/s); none 174, 20 201
 // What bounds it: the bytes.  The powers, at 16 a clock and SM, take a third of
 // the time that 4-byte logits take from HBM.
 #include <climits>
@@ -44,8 +49,12 @@ constexpr int kGroups = 64;
 constexpr int kMost = kLogprobsMaxTop;
 static_assert(kMost <= kGroups, "the bound is a group's largest");
 constexpr int kMaxCluster = 8;
-// Vocabularies up to this size: CTAs of 128 threads.
-constexpr int kSmall = 8192;
+// CTAs of 128 threads, eight an SM, for vocabularies up to kSmall (2048 rows of
+// 1024: 14 us against 51) and from kManyRows rows an SM on, where the others'
+// loads cover what a CTA does at a row's ends (2048 rows of 151,936 with five
+// alternatives 194 against 208 us; 700 rows with twenty 91 against 84).  With
+// fewer rows CTAs of 512, two an SM.
+constexpr int kSmall = 8192, kManyRows = 8;
 
 struct Args {
     const void *logits;
@@ -354,6 +363,7 @@ token_logprobs_kernel(const Args p) {
     float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
     float bound = -INFINITY, most = -INFINITY;
     bool again = false;                          // the row once more, every batch collected by all
+    int renew = begin + 2 * kThreads * kLoads, turn = 1;     // where the next closer bound is taken
     const float edge = at_end >= 0 ? Vec<T>::one(x0 + at_end) : -INFINITY;
     if (kTop) {
         if (tid == 0) sh.n = sh.n_notes = 0;
@@ -379,6 +389,11 @@ token_logprobs_kernel(const Args p) {
                     for (int k = 0; k < W; k += 2) most = max3(most, x[k], x[k + 1]);
                 }
                 bound = bound_of_groups(sh, most, p.top, 0);
+            }
+            if (kTop && kThreads < 512 && !again && v0 == renew) {
+                bound = bound_of_groups(sh, most, p.top, turn);
+                turn ^= 1;
+                renew += renew - begin;
             }
 #pragma unroll
             for (int b = 0; b < kLoads; b += kRows) {
@@ -445,7 +460,7 @@ token_logprobs_kernel(const Args p) {
             }
         }
         if (!kTop || again) break;
-        const float second = bound_of_groups(sh, most, p.top, 1);        // (and every note is there)
+        const float second = bound_of_groups(sh, most, p.top, turn);     // (and every note is there)
         const int notes = sh.n_notes;
         if (notes <= Sh::kNotes) {
             for (int i = tid; i < notes * kRows; i += kThreads) {
@@ -580,7 +595,7 @@ w4v_status launch_token_logprobs(const void *logits, bool half, long long stride
     a.heat = 1.f / temperature;
     a.heat_log2 = 1.4426950408889634f / temperature;
     a.slack = kSlack / a.heat_log2;
-    const bool small = V <= kSmall;
+    const bool small = V <= kSmall || M >= kManyRows * info->sm_count;
     // Rows are cut while there are fewer CTAs than the GPU holds at a time and a
     // piece has more logits than its threads take at once.
     a.cluster_bits = 0;

@@ -74,6 +74,25 @@ def test_many_rows(w4v_mod, gpu, M, V):
     check(w4v_mod, gpu, logits(rng, M, V), given(rng, M, V, 1), top=7)
 
 
+@pytest.mark.parametrize("half,V,top", [(False, 20011, 32), (True, 20011, 5), (False, 151936, 20), (True, 151936, 32)])
+def test_a_long_prompt(w4v_mod, gpu, half, V, top):
+    """Enough rows for small CTAs at any vocabulary; rows of every shape among them, and all of a few values."""
+    w, M = w4v_mod, 1300
+    g = torch.Generator(device=gpu).manual_seed(V)
+    x = torch.randn((M, V), generator=g, device=gpu).mul_(2).to(torch.float16 if half else torch.float32)
+    shaped = shaped_rows(V, half)
+    at = [7 + 90 * i for i in range(len(shaped))]
+    x[at] = to_dev(shaped, gpu)
+    x[3, V // 2], x[5, ::2], x[1299, :] = float("nan"), -float("inf"), 0.25
+    t = torch.randint(0, V, (M, 2), generator=g, device=gpu).int()
+    got = w.token_logprobs(x, t, top=top)
+    rows = sorted([0, 3, 5, 640, 1299] + at)
+    compare(x[rows].cpu().numpy(), t[rows].cpu().numpy(), top, 1.0, [y[rows] for y in got])
+    few = w.token_logprobs(x[640:700], t[640:700], top=top)
+    assert torch.equal(few[2], got[2][640:700])
+    assert torch.allclose(few[0], got[0][640:700], rtol=1e-5, atol=2e-5) and torch.allclose(few[1], got[1][640:700], rtol=1e-5)
+
+
 @pytest.mark.parametrize("top", [0, 1, 2, 19, 31, 32])
 @pytest.mark.parametrize("temperature", [0.05, 0.5, 1.0, 3.0])
 def test_alternatives_and_temperatures(w4v_mod, gpu, top, temperature):
