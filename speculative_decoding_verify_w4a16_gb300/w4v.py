@@ -526,19 +526,20 @@ def _i32(t, where, shape):
     return t.data_ptr()
 
 
-def _same_device(where, first, *others):
-    """Everything on the GPU that is current (the library launches there)."""
-    at = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != at:
-            raise W4VError(ERR_ARG, where)
-    if at < 0 or at != _torch_device():
-        raise W4VError(ERR_ARG, where)
-
-
-def _torch_device():
+def _here(at):
+    """Whether device `at` is the GPU that is current (the library launches there)."""
+    if at < 0:
+        return False
     cuda = _torch.cuda
-    return _torch._C._cuda_getDevice() if cuda.is_initialized() else cuda.current_device()
+    return at == (_torch._C._cuda_getDevice() if cuda.is_initialized() else cuda.current_device())
+
+
+def _other(at, *tensors):
+    """Whether one of the tensors (None: not given) lies elsewhere than on device `at`."""
+    for t in tensors:
+        if t is not None and t.get_device() != at:
+            return True
+    return False
 
 
 def _rows(t, where, n, heads, head_dim):
@@ -622,7 +623,11 @@ def norm_rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: R
         raise W4VError(ERR_SHAPE, where)
     strides = _rows(q, where, n, Hq, D), _rows(k, where, n, heads, D), _rows(v, where, n, heads, D)
     pos = _i32(positions, where, (n,))
-    _same_device(where, q, k, v, k_cache, v_cache, table, lengths, offsets, rope.phases, wq, wk, q_out, positions)
+    at = q.get_device()
+    if not (at == k.get_device() == v.get_device() == k_cache.get_device() == v_cache.get_device() == table.get_device() ==
+            lengths.get_device() == offsets.get_device() == rope.phases.get_device()) or not _here(at) or \
+            _other(at, wq, wk, q_out, positions):
+        raise W4VError(ERR_ARG, where)
     q_out = _dense_out(q_out, where, q, shape, stream)
     code = load().norm_rope_append(kv, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, n, Hq,
                                    None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(),
@@ -690,7 +695,11 @@ def paged_attn_shared(q, k_cache, v_cache, table, lengths, offsets, groups, pref
     g, p = _i32(groups, where, (G + 1,)), _i32(prefix, where, (G,))
     if lse is not None and (lse.shape != (n, Hq) or lse.dtype is not _FLOAT or not lse.is_contiguous()):
         raise W4VError(ERR_SHAPE if lse.shape != (n, Hq) else ERR_ARG, where)
-    _same_device(where, q, k_cache, v_cache, table, lengths, offsets, groups, prefix, out, lse, ws)
+    at = q.get_device()
+    if not (at == k_cache.get_device() == v_cache.get_device() == table.get_device() == lengths.get_device() ==
+            offsets.get_device() == groups.get_device() == prefix.get_device()) or not _here(at) or \
+            _other(at, out, lse, ws):
+        raise W4VError(ERR_ARG, where)
     out = _dense_out(out, where, q, shape, stream)
     if ws is None:
         ws = workspace(paged_attn_shared_workspace_bytes(n, B, G, Hq, heads, D), q.device, stream)
@@ -719,21 +728,23 @@ def token_logprobs(logits, tokens=None, top: int = 0, temperature: float = 1.0, 
     half = logits.dtype is _HALF
     if not (half or logits.dtype is _FLOAT) or (M and V > 1 and logits.stride(1) != 1):
         raise W4VError(ERR_ARG, where)
-    shape = (M, 0) if tokens is None else tuple(tokens.shape)
+    shape = (M, 0) if tokens is None else tokens.shape
     if len(shape) not in (1, 2) or shape[0] != M:
         raise W4VError(ERR_SHAPE, where)
     at, n = _i32(tokens, where, shape), shape[1] if len(shape) == 2 else 1
+    dev = logits.get_device()
+    if not _here(dev) or _other(dev, tokens):
+        raise W4VError(ERR_ARG, where)
     if out is None:
-        _same_device(where, logits, tokens)
         new = lambda shape, dtype: _new(shape, dtype, logits.device, stream)  # noqa: E731
-        out = new(shape, _FLOAT), new(M, _FLOAT), new((M, top), _INT32), new((M, top), _FLOAT)
-    lp, entropy, ids, tops = out
-    for t, s, dtype in ((lp, shape, _FLOAT), (entropy, (M,), _FLOAT), (ids, (M, top), _INT32), (tops, (M, top), _FLOAT)):
-        if t.shape != s:
+        lp, entropy, ids, tops = out = new(shape, _FLOAT), new(M, _FLOAT), new((M, top), _INT32), new((M, top), _FLOAT)
+    else:
+        lp, entropy, ids, tops = out
+        if lp.shape != shape or entropy.shape != (M,) or ids.shape != (M, top) or tops.shape != (M, top):
             raise W4VError(ERR_SHAPE, where)
-        if t.dtype is not dtype or not t.is_contiguous():
+        if not (lp.dtype is entropy.dtype is tops.dtype is _FLOAT and ids.dtype is _INT32 and lp.is_contiguous() and
+                entropy.is_contiguous() and ids.is_contiguous() and tops.is_contiguous()) or _other(dev, *out):
             raise W4VError(ERR_ARG, where)
-    _same_device(where, logits, tokens, *out)
     code = load().token_logprobs(logits.data_ptr(), logits.stride(0) if M > 1 else V, M, V, at, n, temperature,
                                  lp.data_ptr(), entropy.data_ptr(), top, ids.data_ptr(), tops.data_ptr(),
                                  LOGITS_FP16 if half else 0, _stream(stream))

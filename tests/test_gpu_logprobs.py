@@ -186,6 +186,26 @@ def test_forms_of_a_call(w4v_mod, gpu):
     assert [tuple(y.shape) for y in empty] == [(0, 1), (0,), (0, 8), (0, 8)]
 
 
+def test_results_that_do_not_fit_are_refused(w4v_mod, gpu):
+    w, i = w4v_mod, torch.int32
+    x, t = torch.zeros(3, 50, device=gpu), torch.zeros(3, 2, dtype=i, device=gpu)
+    out = lambda top: [torch.zeros(3, 2, device=gpu), torch.zeros(3, device=gpu), torch.zeros(3, top, dtype=i, device=gpu),  # noqa: E731
+                       torch.zeros(3, top, device=gpu)]
+    w.token_logprobs(x, t, top=3, out=out(3))
+    for at, bad, code in ((0, torch.zeros(3, 3, device=gpu), "SHAPE"), (1, torch.zeros(2, device=gpu), "SHAPE"),
+                          (2, torch.zeros(3, 4, dtype=i, device=gpu), "SHAPE"), (3, torch.zeros(2, 3, device=gpu), "SHAPE"),
+                          (0, torch.zeros(3, 2, device=gpu).half(), "ARG"), (1, torch.zeros(6, device=gpu)[::2], "ARG"),
+                          (2, torch.zeros(3, 3, device=gpu), "ARG"), (3, torch.zeros(3, 3), "ARG")):
+        given_out = out(3)
+        given_out[at] = bad
+        with pytest.raises(w.W4VError) as e:
+            w.token_logprobs(x, t, top=3, out=given_out)
+        assert e.value.code == getattr(w, "ERR_" + code)
+    with pytest.raises(w.W4VError) as e:
+        w.token_logprobs(x, t.cpu(), top=3)
+    assert e.value.code == w.ERR_ARG
+
+
 def test_another_stream_and_graph_replay(w4v_mod, gpu):
     rng, w = np.random.default_rng(6), w4v_mod
     x, t = logits(rng, 4, 12345), given(rng, 4, 12345, 2)
