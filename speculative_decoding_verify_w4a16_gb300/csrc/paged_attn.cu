@@ -446,21 +446,23 @@ __device__ __forceinline__ bool schedule(const Args &p, int cta, int ctas, Place
 // so at about the same time.  Where the prefixes are too large for L2 to keep,
 // every one of their row tiles is given whole ranges, by units without work at
 // its end, so that its ranges begin at the same keys as the others'.  Returns
-// the size of a range, or 0 for the even split (one warp; 64 continuations of
-// 32,781 tokens, 16 heads on 4 of 256: N us against M).
+// the size of a range, or 0 for the even split (one warp).  2 x 16 blocks of 4
+// over 20,000 tokens, 20 heads on 4 of 256: 56 us, and 66 as the split falls.
 __device__ __forceinline__ int align_prefixes(const Args &p, Seq *seqs, int *counts, int ctas, int bytes_per_token) {
     const int lane = threadIdx.x & 31;
     if (p.n_groups > 32 || p.kv_heads > ctas) return 0;
     int all = 0, tiles = 0, each_tile = 0;
+    if (lane < p.n_groups) tiles = row_tiles(p, seqs[lane].n);
+    const int kept = __reduce_add_sync(0xFFFFFFFFu, tiles > 1 ? min(seqs[lane].len, INT_MAX / 64) >> 10 : 0);
+    if (size_t(kept) * 1024 * bytes_per_token * p.kv_heads < kAlignBytes) return 0;
+    const int ranges = __reduce_add_sync(0xFFFFFFFFu, min(tiles, ctas)) * p.kv_heads;
+    if (4 * ranges > ctas) return 0;             // (so no more than 64 row tiles of 2^24 units)
 #pragma unroll 1
     for (int b = p.n_groups + lane; b < sequences<kShared>(p); b += 32) all = min(all + counts[b], INT_MAX / 64);
-    if (lane < p.n_groups) tiles = row_tiles(p, seqs[lane].n);
     if (tiles > 0) each_tile = counts[lane] / tiles;
     const long long own_all = (long long)__reduce_add_sync(0xFFFFFFFFu, all) * p.kv_heads;
-    const int ranges = __reduce_add_sync(0xFFFFFFFFu, min(tiles, ctas)) * p.kv_heads;
-    const int kept = __reduce_add_sync(0xFFFFFFFFu, tiles > 1 ? min(seqs[lane].len, INT_MAX / 64) >> 10 : 0);
-    if (own_all > INT_MAX / 4 || 4 * ranges > ctas || size_t(kept) * 1024 * bytes_per_token * p.kv_heads < kAlignBytes) return 0;
-    const int own = int(own_all);                // (and no more than 64 prefix row tiles of 2^24 units)
+    if (own_all > INT_MAX / 4) return 0;
+    const int own = int(own_all);
     int each = (own + __reduce_add_sync(0xFFFFFFFFu, each_tile * tiles) * p.kv_heads + ctas - 1) / ctas;
 #pragma unroll 1
     for (;; each += max(each >> 4, 1)) {

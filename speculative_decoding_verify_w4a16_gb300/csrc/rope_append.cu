@@ -192,8 +192,8 @@ constexpr int kNormAhead = 2;
 template <bool kInter, bool kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1280 / kThreads)
 norm_rope_append_kernel(const Args p) {
-    // Element i of q (0) or k (1) is r (x_i coef.x + x_partner coef.y); elements
-    // 2j and 2j + 1 of piece c lie in coef[.][j][c].
+    // Elements 2j and 2j + 1 of piece c of q (0) or k (1) are r (x coef.xy +
+    // x_partner coef.zw), coef[.][j][c].
     __shared__ float4 coef[2][4][32];
     __shared__ int seq;
     const int t = blockIdx.x, D = p.head_dim, tid = threadIdx.x;
@@ -247,8 +247,13 @@ norm_rope_append_kernel(const Args p) {
     const int cap = p.table_width << p.page_bits, last = (1 << p.page_bits) - 1;
     const int at = min(max(p.lengths[b], 0), cap) - end + t;      // may be negative: the row has no slot
     const int pos = p.positions != nullptr ? p.positions[t] : at;
-    auto at_element = [&](int x, int i) -> float2 & {
-        return reinterpret_cast<float2 *>(&coef[x][i / 2 & 3][i / 8])[i & 1];
+    auto at_element = [&](int x, int i) {        // its own factor; two on its partner's
+        return reinterpret_cast<float *>(&coef[x][i / 2 & 3][i / 8]) + (i & 1);
+    };
+    auto put = [&](int x, int i, float own, float other) {
+        float *m = at_element(x, i);
+        m[0] = own;
+        m[2] = other;
     };
 #pragma unroll
     for (int n = 0; n < kItems; ++n) {
@@ -265,8 +270,8 @@ norm_rope_append_kernel(const Args p) {
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            if (i < pairs) at_element(x, g) = make_float2(w[n][x][1] * c, w[n][x][0] * s);
-            at_element(x, f) = make_float2(w[n][x][0] * c, -w[n][x][1] * s);
+            if (i < pairs) put(x, g, w[n][x][1] * c, w[n][x][0] * s);
+            put(x, f, w[n][x][0] * c, -w[n][x][1] * s);
         }
     }
     long long slot = -1;                                         // head 0's elements of this token
@@ -285,39 +290,38 @@ norm_rope_append_kernel(const Args p) {
             float sum[kNormAhead];
 #pragma unroll
             for (int u = 0; u < kNormAhead; ++u) {
-                sum[u] = 0.f;
+                float2 q = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 x = __half22float2(a[u].h[i]);
-                    sum[u] = fmaf(x.x, x.x, fmaf(x.y, x.y, sum[u]));
+                    q = __ffma2_rn(x, x, q);
                 }
+                sum[u] = q.x + q.y;
             }
             head_sums(sum, D / 8);
 #pragma unroll
             for (int u = 0; u < kNormAhead; ++u) {
                 const int h = h0 + u * step;
-                Piece z;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t w = h2_as_u32(a[u].h[i]);
-                    z.h[i] = kInter ? __lowhigh2highlow(a[u].h[i]) : u32_as_h2(__shfl_sync(0xFFFFFFFFu, w, partner));
-                }
-                if (h >= heads || (h >= p.q_heads && slot < 0)) continue;
-                __half *dst = (h < p.q_heads ? qd + h * D
-                                             : h < turned ? p.k_cache + slot + (h - p.q_heads) * hop
-                                                          : p.v_cache + slot + (h - turned) * hop) + e;
-                if (h < turned) {
+                const bool normed = h < turned;
+                if (__any_sync(0xFFFFFFFFu, normed)) {
                     const float r = rsqrtf(sum[u] * mean + p.eps);
                     Piece o;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float4 m = coef[h < p.q_heads ? 0 : 1][i][e / 8];
+                        const uint32_t w = h2_as_u32(a[u].h[i]);
                         const float2 x = __half22float2(a[u].h[i]);
-                        const float2 y = __half22float2(z.h[i]);
-                        o.h[i] = __floats2half2_rn((x.x * m.x + y.x * m.y) * r, (x.y * m.z + y.y * m.w) * r);
+                        const float2 y = kInter ? make_float2(x.y, x.x)
+                                                : __half22float2(u32_as_h2(__shfl_sync(0xFFFFFFFFu, w, partner)));
+                        const float2 v = __ffma2_rn(y, make_float2(m.z, m.w), __fmul2_rn(x, make_float2(m.x, m.y)));
+                        o.h[i] = __float22half2_rn(__fmul2_rn(v, make_float2(r, r)));
                     }
-                    a[u].u = o.u;
+                    if (normed) a[u].u = o.u;
                 }
+                if (h >= heads || (h >= p.q_heads && slot < 0)) continue;
+                __half *dst = (h < p.q_heads ? qd + h * D
+                                             : h < turned ? p.k_cache + slot + (h - p.q_heads) * hop
+                                                          : p.v_cache + slot + (h - turned) * hop) + e;
                 *reinterpret_cast<uint4 *>(dst) = a[u].u;
             }
         }
@@ -342,13 +346,10 @@ norm_rope_append_kernel(const Args p) {
             for (int i = lane; i < items; i += 32) {
                 int f, g;
                 places(i, f, g);
-                const float2 m = at_element(isq ? 0 : 1, f);
+                const float *m = at_element(isq ? 0 : 1, f), *l = at_element(isq ? 0 : 1, g);
                 const float x = __half2float(src[f]), y = __half2float(src[g]);
-                if (i < pairs) {
-                    const float2 l = at_element(isq ? 0 : 1, g);
-                    dst[g] = __float2half_rn((y * l.x + x * l.y) * r);
-                }
-                dst[f] = __float2half_rn(i < pairs ? (x * m.x + y * m.y) * r : x * m.x * r);
+                if (i < pairs) dst[g] = __float2half_rn((y * l[0] + x * l[2]) * r);
+                dst[f] = __float2half_rn(i < pairs ? (x * m[0] + y * m[2]) * r : x * m[0] * r);
             }
         }
         if (slot >= 0)
