@@ -779,20 +779,52 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             uint32_t phase;
         } sk{0, 0}, sv{0, 0};
         int nq = 0;
+        // V runs kScores key tiles behind K, in the issuers' order and from part to
+        // part: the last tiles of V are loaded behind the next part's queries and
+        // first keys, which would wait behind them for the products otherwise.
+        // The tiles that are held back: this lane's box, the boxes, and the part.
+        struct Held {
+            int grp, n, part;
+        } held[2] = {};
+        int behind = 0;
+        auto load = [&](const CUtensorMap *map, int grp, int n, int first, int depth, Stage &st) {
+#pragma unroll 1
+            for (int h = 0; h < P::kHalves && ok; ++h) {
+                const int s = first + st.s;
+                ok = wait(kv_empty(s), st.phase ^ 1);    // the first time round: passes
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(kv_full(s), n * box_bytes);
+                __syncwarp();
+                if (lane < n)
+                    tma_load_4d(box_at + s * P::kStageBytes, map, 0, 0, h * P::kStageBlocks, grp, kv_full(s));
+                if (++st.s == depth) {
+                    st.s = 0;
+                    st.phase ^= 1;
+                }
+            }
+        };
+        auto load_held = [&] {
+            load(&vmap, held[0].grp, held[0].n, P::kStagesK, P::kStagesV, sv);
+            held[0] = held[1];
+            --behind;
+        };
         for (int i = 0; ok; ++i) {
             Part g{};
             int unit = 0;
             if (!cur.next<F>(p, blockIdx.x, g, unit)) g.nt = -1;
-            if (i >= kParts) ok = wait(part_empty(i % kParts), (i / kParts - 1) & 1);
+            // The part before the last needs all its values to give its place in the
+            // ring back; behind the last part nothing comes.
+#pragma unroll 1
+            while (ok && behind > 0 && (g.nt < 0 || held[0].part + kParts <= i)) load_held();
+            if (ok && i >= kParts) ok = wait(part_empty(i % kParts), (i / kParts - 1) & 1);
             if (!ok) break;
             if (lane == 0) {
                 ring[i % kParts] = g;
                 mbar_arrive(part_full(i % kParts));
             }
             if (g.nt > 0) {
-                // Page ids of the part's boxes, 32 at a time, one per lane: three
-                // such batches at hand, so that each is loaded long before its use
-                // and V's, which runs behind K's, is still there.
+                // Page ids of the part's boxes, 32 at a time, one per lane: two such
+                // batches at hand, so that each is loaded long before its use.
                 const int32_t *row = p.table + size_t(g.b) * p.width;
                 // (box numbers leave the gap out, as tiles do; box_of gives the sequence's)
                 const int box0 = (g.kt0 * kKeys) >> box_bits;
@@ -802,33 +834,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     const int at = box_of(box0 + 32 * n + lane);
                     return at < all_boxes ? row[at >> (p.page_bits - box_bits)] : -1;
                 };
-                int ids0 = batch(0), ids1 = batch(1), ids2 = -1;
-                // this lane's box of key tile j: its first 8-token group (that of
-                // no page is one past the cache, which TMA fills with zeros)
-                auto group_of = [&](int j) -> int {
-                    const int e = j * boxes, n = (e >> 5) % 3;
-                    const int id = __shfl_sync(0xFFFFFFFFu, n == 0 ? ids0 : n == 1 ? ids1 : ids2, (e + lane) & 31);
-                    const int at = id >= 0 && id < p.n_pages ? id * p.kv_heads + g.kvh : p.n_pages * p.kv_heads;
-                    return (at << group_bits) + ((box_of(box0 + e + lane) << (box_bits - 3)) & ((1 << group_bits) - 1));
-                };
-                auto load = [&](const CUtensorMap *map, int j, int first, int depth, Stage &st) {
-                    const int grp = group_of(j);
-                    const int n = min(all_boxes - box_of(box0 + j * boxes), boxes);
-#pragma unroll 1
-                    for (int h = 0; h < P::kHalves && ok; ++h) {
-                        const int s = first + st.s;
-                        ok = wait(kv_empty(s), st.phase ^ 1);    // the first time round: passes
-                        if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(kv_full(s), n * box_bytes);
-                        __syncwarp();
-                        if (lane < n)
-                            tma_load_4d(box_at + s * P::kStageBytes, map, 0, 0, h * P::kStageBlocks, grp, kv_full(s));
-                        if (++st.s == depth) {
-                            st.s = 0;
-                            st.phase ^= 1;
-                        }
-                    }
-                };
+                int ids = batch(0), ids_next = batch(1);
                 if (nq > 0) ok = wait(q_empty, (nq - 1) & 1);
                 if (ok) {
                     if (lane == 0) mbar_arrive_expect_tx(q_full, P::kBlocks * p.tok * p.group * 128u);
@@ -837,18 +843,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                         tma_load_4d(base + lane * kRows * 128, &qmap, 0, g.kvh * p.group, g.row0, lane, q_full);
                     ++nq;
                 }
-                // K runs kScores tiles ahead of V, in the issuers' order
-                for (int j = 0; j < g.nt + P::kScores && ok; ++j) {
+                for (int j = 0; j < g.nt && ok; ++j) {
                     const int e = j * boxes;
-                    if ((e & 31) == 0 && e > 0) {                // K enters a batch: on its way, the next one
-                        const int n = (e >> 5) + 1;
-                        const int next = n % 3;
-                        if (next == 0) ids0 = batch(n);
-                        else if (next == 1) ids1 = batch(n);
-                        else ids2 = batch(n);
+                    if ((e & 31) == 0 && e > 0) {                // a batch is done with: on its way, the next but one
+                        ids = ids_next;
+                        ids_next = batch((e >> 5) + 1);
                     }
-                    if (j < g.nt) load(&kmap, j, 0, P::kStagesK, sk);
-                    if (j >= P::kScores) load(&vmap, j - P::kScores, P::kStagesK, P::kStagesV, sv);
+                    // this lane's box of key tile j: its first 8-token group (that of
+                    // no page is one past the cache, which TMA fills with zeros)
+                    const int id = __shfl_sync(0xFFFFFFFFu, ids, (e + lane) & 31);
+                    const int at = id >= 0 && id < p.n_pages ? id * p.kv_heads + g.kvh : p.n_pages * p.kv_heads;
+                    const int grp = (at << group_bits) + ((box_of(box0 + e + lane) << (box_bits - 3)) & ((1 << group_bits) - 1));
+                    const int n = min(all_boxes - box_of(box0 + e), boxes);
+                    load(&kmap, grp, n, 0, P::kStagesK, sk);
+                    if (ok && behind == P::kScores) load_held();
+                    held[1] = Held{grp, n, i};
+                    if (behind == 0) held[0] = held[1];
+                    ++behind;
                 }
             }
             // the share of this range's first row tile, or of every unit's
