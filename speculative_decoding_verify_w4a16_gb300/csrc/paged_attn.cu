@@ -37,7 +37,21 @@
 // a part leaves o, m and l in the workspace (at most two parts a CTA), and a
 // second kernel joins them, each boundary's CTAs a share of the tile's rows.
 // The lengths are on the device, so each CTA finds its own range by a scan
-// over the sequences.  With batch invariance the unit is a fixed range of
+// over the sequences.
+//
+// First tokens beside a window (kSinks): a row tile's key tiles are those of the
+// first tokens and those of the window, numbered without the gap between them;
+// only where a tile's keys are named (pages, masks, the looking over) is the gap
+// put back.  With batch invariance the gap is an even number of tiles, so that
+// the same tiles fall to the same softmax group whatever the window's first one.
+//
+// Shared prefixes (kShared): the rows of a group's sequences follow one another,
+// so the group's prefix counts as one more sequence whose rows they all are, with
+// every key visible to every row: its keys are read once per 128 rows instead of
+// once per sequence, and 128 rows are in use.  What follows the prefix is each
+// sequence's own.  Every part keeps its unnormalised output in 32 bits, and one
+// last kernel joins a row's parts of both kinds, told by a word per token and
+// key/value head where they are.  With batch invariance the unit is a fixed range of
 // keys, every one a part of its own: which keys meet in one running sum then
 // depends on the row alone.
 //
@@ -48,7 +62,8 @@
 // A drafted token that overflowed thus spoils no position before it.
 //
 // Roles (12 warps): 0 producer (the CTA's parts, which it hands on through a
-// ring in shared memory, page ids, TMA), 1 issuer of Q K^T, 2 issuer of P V,
+// ring in shared memory, page ids, TMA; the last values of a part go behind the
+// next one's queries and first keys, 23.9 -> 23.3 us with a window), 1 issuer of Q K^T, 2 issuer of P V,
 // 3 guard (the looking over, a tile ahead of the issuer) and tensor-memory
 // owner, 4-7 and 8-11 softmax.  S and P have buffers of their own, so Q K^T
 // runs ahead (two tiles; one for heads of 256, whose O leaves room for one S)
@@ -74,7 +89,7 @@
 //   1 token over 1000, 20 heads on 4 of 128              9.9 us (11.6; bound 0.3: latency)
 //   16 tokens over 32,781, 16 heads on 4 of 256         34.4 us (41.6; bound 20.2: bytes)
 //   8 x 21 tokens over up to 9000, 20 heads of 128      70.4 us (97; bound 60.8: bytes; 5.8 TB/s)
-//   32 x up to 40 tokens, window 1000, 20 on 4 of 64    23.6 us (31; bound 3.9: bytes)
+//   32 x up to 40 tokens, window 1000, 20 on 4 of 64    23.3 us (31; bound 3.9: bytes)
 //   4 x up to 1500 tokens over 12,000, 16 on 4 of 256    225 us (534; bound 173: 1465 TFLOP/s)
 //   8192 tokens, 20 heads of 128                         253 us (672; bound 180: 1357 TFLOP/s)
 // The short ones are a chain of latencies.  By the clock, us from the end of
@@ -86,6 +101,18 @@
 // Prompts are bound by a row's softmax between its two products (maximum 340
 // cycles, powers 910, loads and stores 350 of 1500 a tile and group, the
 // tensor pipe 61-71% active).
+// First tokens and shared prefixes (bounds as above):
+//   1 token over 20,000, window 1000, 4 first, 20 on 4 of 128        10.2 us (0.3: latency)
+//   24 x up to 21 over 12,000, window 2000, 300 first, 16 on 4 of 256 45.4 us (27.3: bytes)
+//   8192 tokens, window 1024, 64 first, 20 heads of 128               111 us (45: products)
+//   8 x 1 token over 2000 shared and 100, 20 on 4 of 128             13.6 us (0.7: latency; apart 13.6)
+//   2 x 16 x up to 16 over 8200 shared and 700, 20 on 4 of 128       36.0 us (8.2: products; apart 59)
+//   64 x 1 over 32,781 shared and 900, 16 on 4 of 256                64.2 us (37.6: bytes; apart 784)
+// ("apart": kPlain, every sequence over all its pages.)  A window's row tiles are
+// ten key tiles, and between two of them the product waits for O to be read and
+// stored (some 4000 cycles of 24,000; 106 us without the stores).  64 tokens are
+// two row tiles over the prefix: their 128 x 128 tiles of 256-wide heads run at
+// 0.70 of the products' rate, and all that the CTAs load comes out of L2 at 10 TB/s.
 #include <algorithm>
 #include <climits>
 

@@ -24,7 +24,9 @@
 // log2(D / 8) shuffles.  Weight and rotation are both linear in x, so element i
 // becomes r (x_i (w_i c_i) + x_j (w_j s_i)), j its partner: the products in
 // brackets are worked out once per CTA and lie in shared memory by piece, and
-// r, the head's factor, multiplies last.
+// r, the head's factor, multiplies last.  Measured (device time): 16 rows of 28 x
+// 128 2.9 us, 660 rows of 60 x 128 6.7 (bound 3.4: bytes), 8192 rows of 24 x 256
+// 38.1 (29.7; 5.3 TB/s).
 #include <algorithm>
 
 #include "runtime.h"
@@ -185,9 +187,8 @@ __device__ __forceinline__ void head_sums(float (&x)[n], int lanes) {
 // The same with norms.  kVec as above; without it a warp takes a head, pair by
 // pair.  Partner pieces come from their lanes by shuffles: read again from L1
 // they held 12 registers more across the waits, 49.7 us against 44.8 for 8192
-// rows of 24 x 256.  Two heads a thread ahead: 630 rows of 60 x 128 6.9 us
-// (three 7.7, with registers spilled), 16 rows of 28 x 128 2.9 (3.2), 8192 rows
-// 45.2 (44.8).
+// rows of 24 x 256.  Two heads a thread ahead: 660 rows of 60 x 128 6.7 us
+// (three 7.2), 16 rows of 28 x 128 2.9 (3.2).
 constexpr int kNormAhead = 2;
 template <bool kInter, bool kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1280 / kThreads)

@@ -32,7 +32,7 @@
 // Measured (one GB300, device time; bound: the logits' bytes at 6.78 TB/s):
 //   1 row of 151,936                          4.7 us (0.1: latency); with 20 alternatives 9.2
 //   300 rows of 50,001 fp16, masked, 20       14.7 us (4.4: latency of a row's ends)
-//   2048 rows of 151,936, 5                   194 us (184: bytes, 6.4 TB/s); none 174, 20 201
+//   2048 rows of 151,936, 5                   191 us (184: bytes, 6.5 TB/s); none 172, 20 197
 // What bounds it: the bytes.  The powers, at 16 a clock and SM, take a third of
 // the time that 4-byte logits take from HBM.
 #include <climits>
