@@ -78,7 +78,8 @@ w4v_status w4v_init(void);
 /* Synchronizes `stream`, then returns and clears the device status word of
  * the current device: W4V_OK, or what happened since the last call:
  * W4V_ERR_TIMEOUT if a kernel gave up a wait, else W4V_ERR_SHAPE if the arrays
- * that paged_attn found on the device ask for more than its arguments allow. */
+ * that paged_attn (or _sinks, _shared) found on the device ask for more than its
+ * arguments allow. */
 w4v_status w4v_get_status(w4v_stream_t stream);
 
 /* ------------------------------------------------------- int4 weight packing
@@ -503,7 +504,8 @@ w4v_status rope_append(const w4v_kv_t *kv, const uint16_t *q, const uint16_t *k,
  * c = 0, or 1 with W4V_NORM_ZERO_CENTRED (weights kept around zero; no
  * meaning where the weights are NULL), and is then rotated and written as
  * above; nothing is rounded in between.  eps >= 0 and finite; with eps = 0 a
- * head of zeros gives NaN.  Values are not normed.  Everything else as
+ * head of zeros gives NaN.  Values are not normed.  A row's results do not
+ * depend on the call's other rows, bit for bit.  Everything else as
  * rope_append. */
 #define W4V_NORM_ZERO_CENTRED 8u
 w4v_status norm_rope_append(const w4v_kv_t *kv, const uint16_t *q, const uint16_t *k, const uint16_t *v,
@@ -596,8 +598,9 @@ w4v_status paged_attn_sinks(const w4v_kv_t *kv, const uint16_t *q, long long q_s
  * ends, begin the group behind it), and neither does a sequence with fewer
  * than prefix[g] tokens before its new ones; those attend over their own pages.
  * Sequences without new tokens may lie anywhere in a group.
+ * A row that several sequences name gets no meaningful result.
  * flags must be 0 (how a row's sum is cut depends on the batch).  Sizes as
- * paged_attn, n_groups from 0 to 2^24, and (2 (n_tokens / tok) + min(B,
+ * paged_attn, 0 <= n_groups <= B (a group may be empty), and (2 (n_tokens / tok) + min(B,
  * n_tokens) + min(n_groups, n_tokens)) * kv_heads * (table_width * page / 128
  * + 5) < 2^31.
  * Workspace: paged_attn_shared_workspace_bytes(...) with the call's own

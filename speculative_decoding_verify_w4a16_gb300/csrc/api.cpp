@@ -578,8 +578,8 @@ w4v_status paged_attn_shared(const w4v_kv_t *kv, const uint16_t *q, long long q_
                              float *lse, void *ws, size_t ws_bytes, unsigned flags, w4v_stream_t stream) {
     if (flags != 0u) return W4V_ERR_ARG;
     bool done;
-    const w4v_status st = attention_check(kv, q, q_stride, n_tokens, q_heads, scale, n_groups >= 0 && n_groups <= 1 << 24,
-                                          n_groups, out, lse, &done);
+    const bool sizes = n_groups >= 0 && (kv == nullptr || kv->B == 0 || n_groups <= kv->B);
+    const w4v_status st = attention_check(kv, q, q_stride, n_tokens, q_heads, scale, sizes, n_groups, out, lse, &done);
     if (st != W4V_OK || done) return st;
     if (n_groups > 0 && (groups == nullptr || prefix == nullptr)) return W4V_ERR_ARG;
     if (!aligned4(groups) || !aligned4(prefix)) return W4V_ERR_ALIGN;

@@ -299,7 +299,7 @@ struct Extent {
 };
 // Tiles are numbered without the gap where one is left out: tile v is the
 // sequence's tile_of(v).
-__device__ __forceinline__ int sink_tiles(const Args &p) { return (p.sinks + kKeys - 1) >> kKeyBits; }
+__device__ __forceinline__ int sink_tiles(const Args &p) { return ((p.sinks - 1) >> kKeyBits) + 1; }
 template <int F>
 __device__ __forceinline__ int tile_of(const Args &p, int gap, int v) {
     return F == kSinks && v >= sink_tiles(p) ? v + gap : v;
@@ -1170,7 +1170,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_empty(sb));     // the scores are in registers
-                if (key + kKeys - 1 > sure_hi || (key < sure_lo && (F != kSinks || key + kKeys > p.sinks))) {
+                if (key + kKeys - 1 > sure_hi || (key < sure_lo && (F != kSinks || key > p.sinks - kKeys))) {
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         const int hi = pos - key - 32 * b, lo = from - key - 32 * b;         // keys lo .. hi are seen

@@ -542,10 +542,8 @@ token_logprobs_kernel(const Args p) {
         if (kTop) {
             if (cluster > 1) {
                 const int n = p.top << p.cluster_bits;
-                uint64_t key = 0;
-                if (tid < n) key = ld_cluster_u64(mapa_shared(smem_u32(&sh.best[tid >> p.cluster_bits]), tid & (cluster - 1)));
-                __syncthreads();
-                if (tid < n) sh.list[tid] = key;
+                for (int i = tid; i < n; i += kThreads)
+                    sh.list[i] = ld_cluster_u64(mapa_shared(smem_u32(&sh.best[i >> p.cluster_bits]), i & (cluster - 1)));
                 best_of_list(sh, p.top, n);
             }
             if (tid < p.top) {

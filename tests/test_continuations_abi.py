@@ -136,7 +136,7 @@ def test_shared_refusals(w4v_mod):
     for kw, code in KV_FAULTS:
         assert call(kv=_kv(w, **kw)) == getattr(w, "ERR_" + code)
     assert w.load().paged_attn_shared(None, FAKE, 2560, 8, 20, 0.1, FAKE, FAKE, 1, FAKE, None, FAKE, BIG, 0, None) == w.ERR_ARG
-    assert call(G=-1) == call(G=(1 << 24) + 1) == call(n=-1) == call(heads=18) == call(stride=2552) == w.ERR_SHAPE
+    assert call(G=-1) == call(G=3) == call(n=-1) == call(heads=18) == call(stride=2552) == w.ERR_SHAPE
     assert call(flags=2) == call(flags=1) == call(scale=0.0) == call(scale=float("nan")) == w.ERR_ARG
     assert call(q=None) == call(out=None) == call(g=None) == call(p=None) == w.ERR_ARG
     assert call(q=FAKE + 8) == call(out=FAKE + 2) == call(lse=FAKE + 2) == call(ws=FAKE + 4) == w.ERR_ALIGN

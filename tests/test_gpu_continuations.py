@@ -10,7 +10,8 @@ import torch
 
 from helpers import to_dev
 from oracle import paged, scores
-from paged_helpers import attention_bounds
+from paged_helpers import attention_bounds, cache
+from test_gpu_streams import MODES, on_side_stream
 
 pytestmark = pytest.mark.gpu
 
@@ -149,6 +150,57 @@ def test_continuations_of_one_prompt(w4v_mod, gpu, captured):
         if step == 3:                                                    # it ends too: the group begins behind it
             w.kv_truncate(s.refs, s.table, s.lengths, i32([0] + [9999] * (C - 1)), PAGE)
             s.groups.copy_(i32([2, C]))
+
+
+@MODES
+def test_workspaces_and_results_on_a_stream_of_their_own(w4v_mod, gpu, raw, late):
+    """What the binding allocates for these calls belongs to their stream, as for the others."""
+    w, rng = w4v_mod, np.random.default_rng(3)
+    c = cache(rng, [16, 1], [3000, 500], 4, 2, 64, 16)
+    d = {x: to_dev(a, gpu) for x, a in c.items()}
+    at = [d[x] for x in ("k", "v", "table", "lengths", "offsets")]
+    groups, prefix = torch.tensor([0, 1, 2], dtype=torch.int32, device=gpu), torch.tensor([2000, 400], dtype=torch.int32, device=gpu)
+    kn, vn = (d[x][:17, :, 0].contiguous() for x in "kv")
+    rope, norm = w.Rope(64), w.HeadNorm()
+    x, t = torch.randn((17, 30000), device=gpu), torch.zeros(17, dtype=torch.int32, device=gpu)
+    nq = c["q"].nbytes
+    for call, sizes in ((lambda s: [w.norm_rope_append(d["q"], kn, vn, *at, rope, norm, stream=s)], (nq,)),
+                        (lambda s: [w.paged_attn(d["q"], *at, window=700, sinks=9, stream=s)],
+                         (w.paged_attn_workspace_bytes(17, 2, 4, 2, 64, d["table"].shape[1] * 16), nq)),
+                        (lambda s: [w.paged_attn_shared(d["q"], *at, groups, prefix, stream=s)],
+                         (w.paged_attn_shared_workspace_bytes(17, 2, 2, 4, 2, 64), nq)),
+                        (lambda s: list(w.token_logprobs(x, t, top=5, stream=s)), (4 * 17, 4 * 17 * 5))):
+        want = [y.clone() for y in call(None)]
+        torch.cuda.synchronize()
+        got = on_side_stream(call, raw, late, sizes)
+        assert w.get_status() == w.OK
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+
+
+def test_two_calls_at_once(w4v_mod, gpu):
+    """The same operators on two streams, each with a workspace of its own, while the other runs."""
+    w, rng = w4v_mod, np.random.default_rng(4)
+    c = cache(rng, [16] * 6, [9000, 700, 5000, 40, 3000, 16], 8, 2, 128, 16)
+    d = {x: to_dev(a, gpu) for x, a in c.items()}
+    at = [d[x] for x in ("k", "v", "table", "lengths", "offsets")]
+    groups, prefix = (torch.tensor(v, dtype=torch.int32, device=gpu) for v in ([0, 1, 2, 3, 4, 5, 6], [8000, 600, 4000, 0, 2000, 0]))
+    x, t = torch.randn((96, 50001), device=gpu), torch.zeros(96, dtype=torch.int32, device=gpu)
+
+    def both():
+        return [w.paged_attn_shared(d["q"], *at, groups, prefix), w.paged_attn(d["q"], *at, window=500, sinks=130),
+                *w.token_logprobs(x, t, top=20)]
+    want = [y.clone() for y in both()]
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, g in zip(streams, got):
+            with torch.cuda.stream(s):
+                g.append(both())
+    torch.cuda.synchronize()
+    assert w.get_status() == w.OK
+    for results in got[0] + got[1]:
+        assert all(torch.equal(a, b) for a, b in zip(want, results))
 
 
 def test_the_example_ranks_its_continuations(w4v_mod, gpu):

@@ -220,6 +220,22 @@ def test_graph_replay_follows_what_changes(w4v_mod, gpu):
     assert np.all(np.abs(out.cpu().numpy() - y) <= bound(y, nq, mul))
 
 
+@pytest.mark.parametrize("D,rot,inter", [(64, 64, False), (128, 96, True), (256, 64, False), (128, 50, False), (64, 22, True)])
+def test_rows_do_not_depend_on_the_others(w4v_mod, gpu, D, rot, inter):
+    """The same bits in a long prompt, in a chunk of it and alone: verified positions equal the steps they stand for."""
+    rng, w = np.random.default_rng([D, 11]), w4v_mod
+    c = cache(rng, [4000], [4096], 1, 2, D, 64)
+    q, k, v = (to_dev(x, gpu) for x in rows(rng, 4000, 6, 2, D))
+    norm = w.HeadNorm(*(to_dev(x, gpu) for x in weights(rng, D)))
+    d, rope = {x: to_dev(a, gpu) for x, a in c.items()}, w.Rope(rot, interleaved=inter)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=gpu)  # noqa: E731
+    whole = w.norm_rope_append(q, k, v, d["k"], d["v"], d["table"], d["lengths"], d["offsets"], rope, norm)
+    kept = d["k"].clone()
+    for a, b in ((0, 2500), (17, 18), (1000, 1016), (3999, 4000)):
+        got = w.norm_rope_append(q[a:b], k[a:b], v[a:b], d["k"], d["v"], d["table"], i32(96 + b), i32(0, b - a), rope, norm)
+        assert torch.equal(got, whole[a:b]) and torch.equal(d["k"], kept)
+
+
 def test_agrees_with_the_separate_steps(w4v_mod, gpu):
     """rope_append of heads normed beforehand: one more rounding to fp16, of the normed head."""
     rng, w = np.random.default_rng(10), w4v_mod

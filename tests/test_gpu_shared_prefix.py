@@ -95,6 +95,58 @@ def test_many_groups(w4v_mod, gpu):
     check(w4v_mod, gpu, c)
 
 
+@pytest.mark.parametrize("D,C", [(64, 400), (128, 900)])
+def test_more_sequences_than_shared_memory_lists(w4v_mod, gpu, D, C):
+    rng = np.random.default_rng(C)
+    groups = [range(C // 2), range(C // 2, C)] + [range(b, b + 1) for b in range(C, C + C // 2)]
+    B = C + C // 2
+    c = forked(rng, groups, [130, 60] + [9] * (C // 2), rng.integers(0, 2, B), rng.integers(0, 30, B), 2, 1, D, 16)
+    check(w4v_mod, gpu, c)
+
+
+def test_long_runs_of_sequences_without_new_tokens(w4v_mod, gpu):
+    """Requests that wait: a range's next sequence with something to do is more than a warp's lanes away."""
+    rng = np.random.default_rng(13)
+    n = np.zeros(300, np.int64)
+    n[[0, 70, 71, 190, 299]] = 3, 1, 40, 2, 5
+    c = forked(rng, [range(150), range(150, 300)], [300, 40], n, np.where(n > 0, 200, rng.integers(0, 20, 300)), 4, 1, 64, 16)
+    check(w4v_mod, gpu, c)
+    n[[0, 70, 71, 190]] = 0
+    check(w4v_mod, gpu, forked(rng, [range(150), range(150, 300)], [30, 40], n, rng.integers(0, 9, 300), 4, 2, 128, 16))
+
+
+def test_large_prefixes_side_by_side(w4v_mod, gpu):
+    """Prefixes beyond what L2 keeps, with two row tiles each: their ranges are aligned.  What the pages hold repeats,
+    so that a short oracle stands for the long prefix: m copies of every key add ln m to the log-sum-exp and change
+    no average (the lse's bound takes the longer sums)."""
+    rng = np.random.default_rng(14)
+    m, page, D, Hkv = 513, 64, 256, 2
+    c = forked(rng, [range(34), range(34, 68)], [page, page], [1] * 68, [0] * 68, 8, Hkv, D, page)
+    wide = np.full((68, m + 2), -1, np.int32)
+    wide[:, :m] = c["table"][:, :1]
+    wide[:, m] = c["table"][:, 1]
+    long = dict(c, table=wide, lengths=np.full(68, m * page + 1, np.int32), prefix=np.full(2, m * page, np.int32))
+    assert 2 * m * page * Hkv * D * 4 > 64 << 20
+    got, lse = run(w4v_mod, gpu, long)
+    # the new token's own weight is 1 / m of what the short sequence gives it
+    s = D ** -0.5
+    for t in range(0, 68, 5):
+        K = np.concatenate([c["k"][c["table"][t, 0]], c["k"][c["table"][t, 1]][:, :1]], 1).astype(np.float64)      # [Hkv][page + 1][D]
+        Vv = np.concatenate([c["v"][c["table"][t, 0]], c["v"][c["table"][t, 1]][:, :1]], 1).astype(np.float64)
+        for h in range(8):
+            x = K[h // 4] @ c["q"][t, h].astype(np.float64) * s
+            p = np.exp(x - x.max())
+            p[:page] *= m
+            o, want = p @ Vv[h // 4] / p.sum(), x.max() + np.log(p.sum())
+            mag = p @ np.abs(Vv[h // 4]) / p.sum()
+            absdot = (np.abs(K[h // 4]) @ np.abs(c["q"][t, h].astype(np.float64))).max() * s
+            eps = (D + 8) * 2.0 ** -23 * absdot + 2.0 ** -20            # as attention_bounds, over the long table
+            keys = wide.shape[1] * page + 64
+            rel = 2.0 ** -11 + 2 * eps + 2 * keys * 2.0 ** -23
+            assert np.all(np.abs(got[t, h] - o) <= 2.0 ** -11 * np.abs(o) + rel * (1 + 2.0 ** -10) * mag + 2.0 ** -24)
+            assert abs(lse[t, h] - want) <= eps + keys * 2.0 ** -23 + 2.0 ** -22 * abs(want)
+
+
 def test_a_prompt_chunk_behind_a_shared_prefix(w4v_mod, gpu):
     """Row tiles of many tokens, over the group's sequences and their own."""
     rng = np.random.default_rng(4)
