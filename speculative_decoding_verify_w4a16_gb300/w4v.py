@@ -528,10 +528,12 @@ def _i32(t, where, shape):
 
 def _here(at):
     """Whether device `at` is the GPU that is current (the library launches there)."""
-    if at < 0:
-        return False
-    cuda = _torch.cuda
-    return at == (_torch._C._cuda_getDevice() if cuda.is_initialized() else cuda.current_device())
+    return at >= 0 and at == _torch._C._cuda_getDevice()
+
+
+def _raw_stream(at):
+    """The current stream of the current device `at`, where a tensor lies."""
+    return _torch._C._cuda_getCurrentRawStream(at)
 
 
 def _other(at, *tensors):
@@ -633,7 +635,8 @@ def norm_rope_append(q, k, v, k_cache, v_cache, table, lengths, offsets, rope: R
                                    None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(),
                                    norm.eps, pos, rope.phases.data_ptr(), rope.rot, rope.mul,
                                    (ROPE_INTERLEAVED if rope.interleaved else 0) |
-                                   (NORM_ZERO_CENTRED if norm.zero_centred else 0), q_out.data_ptr(), _stream(stream))
+                                   (NORM_ZERO_CENTRED if norm.zero_centred else 0), q_out.data_ptr(),
+                                   _raw_stream(at) if stream is None else _stream(stream))
     if code != OK:
         raise W4VError(code, where)
     return q_out
@@ -705,7 +708,7 @@ def paged_attn_shared(q, k_cache, v_cache, table, lengths, offsets, groups, pref
         ws = workspace(paged_attn_shared_workspace_bytes(n, B, G, Hq, heads, D), q.device, stream)
     code = load().paged_attn_shared(kv, q.data_ptr(), stride, n, Hq, D ** -0.5 if scale is None else scale, g, p, G,
                                     out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), 0,
-                                    _stream(stream))
+                                    _raw_stream(at) if stream is None else _stream(stream))
     if code != OK:
         raise W4VError(code, where)
     return out
@@ -747,7 +750,7 @@ def token_logprobs(logits, tokens=None, top: int = 0, temperature: float = 1.0, 
             raise W4VError(ERR_ARG, where)
     code = load().token_logprobs(logits.data_ptr(), logits.stride(0) if M > 1 else V, M, V, at, n, temperature,
                                  lp.data_ptr(), entropy.data_ptr(), top, ids.data_ptr(), tops.data_ptr(),
-                                 LOGITS_FP16 if half else 0, _stream(stream))
+                                 LOGITS_FP16 if half else 0, _raw_stream(dev) if stream is None else _stream(stream))
     if code != OK:
         raise W4VError(code, where)
     return out
