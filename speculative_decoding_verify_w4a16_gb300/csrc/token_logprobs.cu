@@ -161,6 +161,10 @@ struct __align__(8) Shared {
     uint64_t group_key[kGroups], bound_key;
     float group[2][kGroups], bound[2];          // by turns
     Sums warp[kWarps], all;
+    // Keys in the list, those equal to a bound, noted batches.  Counted up by
+    // whoever adds one, cleared by thread 0; they are read only behind a barrier
+    // that follows the last write, and written again only behind one that follows
+    // the reads.  How long the list is goes on as a value from there.
     int n, n_ties, n_notes;
     int scan[kWarps];
 };
@@ -215,7 +219,7 @@ __device__ __noinline__ void best_of_list(Shared<kThreads> &sh, int top, int n) 
 #pragma unroll
         for (int d = 1; d < kLanes; d <<= 1) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
         if (tid % kLanes == 0) sh.group_key[tid / kLanes] = g;
-        if (tid == 0) sh.n_ties = 0;
+        if (tid == 0) sh.n_ties = 0;             // (collect()'s was read before this function's first barrier)
         __syncthreads();
         const int2 above = groups_above<kLanes>(sh.group_key, g);
         if (above.x < top && top <= above.y) sh.bound_key = g;
@@ -228,7 +232,7 @@ __device__ __noinline__ void best_of_list(Shared<kThreads> &sh, int top, int n) 
                 const int at = atomicAdd(&sh.n_ties, 1);
                 if (at < Shared<kThreads>::kTies) sh.ties[at] = key;
             }
-        __syncthreads();
+        __syncthreads();                         // every tie is counted; the last barrier parts this read from collect()
         if (sh.n_ties <= Shared<kThreads>::kTies) {
             list = sh.ties;
             n = sh.n_ties;
@@ -297,16 +301,17 @@ __device__ __forceinline__ int in_order(Shared<kThreads> &sh, const float (&x)[k
 
 // A batch of every thread: logit k of a thread has index first + k / W * kThreads
 // * W + k % W, and is there at all where that is in [0, limit) (else it reads
-// -inf).  Those that may be among the `top` largest go to the end of sh.list.
+// -inf).  Those that may be among the `top` largest go behind the sh.n keys in
+// sh.list; returns how many are there then, to every thread (sh.n is not kept up).
 // Every thread calls it; begins and ends with a barrier.
 template <int W, int kThreads>
-__device__ __noinline__ void collect(Shared<kThreads> &sh, const float (&x)[kBatch], float most, int first, int limit, int top) {
+__device__ __noinline__ int collect(Shared<kThreads> &sh, const float (&x)[kBatch], float most, int first, int limit, int top) {
     const int tid = threadIdx.x;
-    if (tid == 0) sh.n_ties = 0;
+    if (tid == 0) sh.n_ties = 0;                 // (last read before best_of_list()'s last barrier)
     __syncthreads();
     const float bound = bound_of_groups(sh, most, top, 0);
-    const int before = sh.n;
-    __syncthreads();
+    const int before = sh.n;                     // written before the barriers above
+    __syncthreads();                             // read by all: from here on it grows
     if (most >= bound && most > -INFINITY)
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
@@ -319,7 +324,7 @@ __device__ __noinline__ void collect(Shared<kThreads> &sh, const float (&x)[kBat
                 if (at < Shared<kThreads>::kTies) sh.ties[at] = key;
             }
         }
-    __syncthreads();
+    __syncthreads();                             // all are counted
     const int n = sh.n;
     int add = sh.n_ties;
     if (add <= Shared<kThreads>::kTies && bound > -INFINITY) {
@@ -328,8 +333,7 @@ __device__ __noinline__ void collect(Shared<kThreads> &sh, const float (&x)[kBat
         add = in_order<W>(sh, x, bound, first, limit, n, max(top - (n - before), 0));
     }
     __syncthreads();
-    if (tid == 0) sh.n = n + add;
-    __syncthreads();
+    return n + add;
 }
 
 template <typename T, bool kTop, int kThreads>
@@ -363,11 +367,12 @@ token_logprobs_kernel(const Args p) {
     float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
     float bound = -INFINITY, most = -INFINITY;
     bool again = false;                          // the row once more, every batch collected by all
+    int listed = p.top;                          // keys in sh.list at the end (gone through again: each batch leaves top)
     int renew = begin + 2 * kThreads * kLoads, turn = 1;     // where the next closer bound is taken
     const float edge = at_end >= 0 ? Vec<T>::one(x0 + at_end) : -INFINITY;
     if (kTop) {
         if (tid == 0) sh.n = sh.n_notes = 0;
-        __syncthreads();
+        __syncthreads();                         // the counts are 0 before anyone adds
     }
     for (;;) {
         if (kTop && at_end >= 0) sh.list[atomicAdd(&sh.n, 1)] = key_of(edge, at_end);          // (14 at most)
@@ -415,19 +420,18 @@ token_logprobs_kernel(const Args p) {
 #pragma unroll
                     for (int k = 0; k < kBatch; ++k) y[k] = x[k];
                     if (again) {
-                        collect<W>(sh, y, top, first, limit, p.top);
-                        best_of_list(sh, p.top, sh.n);
+                        best_of_list(sh, p.top, collect<W>(sh, y, top, first, limit, p.top));
                         if (tid < p.top) sh.list[tid] = sh.best[tid];
-                        if (tid == 0) sh.n = p.top;
+                        if (tid == 0) sh.n = p.top;          // for the next collect(), whose barriers come before its read
                         refill();
                         continue;
                     }
                     // Few groups hold a token above -inf, so the first batch has
                     // all those of -inf that may be wanted (or it is all there is).
-                    const int before = sh.n;
+                    const int before = sh.n;                 // the row's ends, counted before the bound's barriers
                     __syncthreads();
                     const int n = in_order<W>(sh, y, -INFINITY, first, limit, before, p.top);
-                    if (tid == 0) sh.n = before + n;
+                    if (tid == 0) sh.n = before + n;         // (next used behind the last bound's barriers)
                 }
                 if (kTop) {
                     most = fmaxf(most, top);
@@ -476,15 +480,19 @@ token_logprobs_kernel(const Args p) {
                         if (at < Sh::kKeys) sh.keys[at] = key_of(x[j], first + j);
                     }
             }
-            __syncthreads();
-            if (sh.n <= Sh::kKeys) break;
+            __syncthreads();                     // every key is counted
+            listed = sh.n;
+            if (listed <= Sh::kKeys) break;
         }
-        __syncthreads();
+        __syncthreads();                         // both counts are read by all
         if (tid == 0) sh.n = 0;
+        listed = p.top;
         __syncthreads();
         again = true;
     }
-    if (kTop) best_of_list(sh, p.top, sh.n);
+    // The count as a value: after a row gone through again sh.n is thread 0's
+    // last write, which no barrier has parted from this.
+    if (kTop) best_of_list(sh, p.top, listed);
     if (at_end >= 0 && (edge > -INFINITY || edge != edge)) {
         if (edge > mine.m) {
             const float d = mine.m - edge, a = mine.m == -INFINITY ? 1.f : ex2(d * p.heat_log2);

@@ -121,6 +121,25 @@ def test_ties_orders_and_masks(w4v_mod, gpu, half, V, top):
 
 
 @pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("M,V", [(60, 5000), (5, 170001), (1300, 20011)])
+@pytest.mark.parametrize("top", [1, 20, 32])
+def test_rows_gone_through_again_every_time(w4v_mod, gpu, half, M, V, top):
+    """Rows in ascending order, and of values that very many tokens share, many times over: the last batch leaves
+    hundreds of candidates, which must not be taken for the list's length behind it."""
+    i = torch.arange(V, device=gpu, dtype=torch.float64)
+    shapes = [i / V * 30, torch.floor(i / V * 10), torch.where(i % 2 == 0, 1.0, 2.0), (i % 4096) / 200,
+              torch.where(i % 16 < 4, 20.0 + i / V, 0.0), i / V * 30 - 60 * (i % 3 == 1)]
+    x = torch.stack(shapes).to(torch.float16 if half else torch.float32)
+    want = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :top].int()
+    at = torch.arange(M, device=gpu) % len(x)
+    x, want = x[at], want[at]
+    for _ in range(100):
+        ids, lps = w4v_mod.token_logprobs(x, top=top)[2:]
+        assert torch.equal(ids, want)
+        assert torch.all(lps[:, 1:] <= lps[:, :-1])
+
+
+@pytest.mark.parametrize("half", [False, True])
 @pytest.mark.parametrize("V", [64, 3001, 25000])
 def test_what_is_not_finite(w4v_mod, gpu, half, V):
     rng = np.random.default_rng(2)
