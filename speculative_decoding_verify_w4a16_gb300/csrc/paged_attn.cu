@@ -116,6 +116,7 @@
 #include <algorithm>
 #include <climits>
 
+#include "attn_place.h"
 #include "runtime.h"
 #include "sm103_ptx.cuh"
 
@@ -216,7 +217,7 @@ struct Args {
     int n_groups;
     float *res_o;               // [2][n_tokens q_heads][D]: over the prefixes, over what follows them
     float2 *res_ml;             // [2][n_tokens q_heads]
-    uint32_t *places;           // [2][n_tokens kv_heads]: see place_of()
+    uint32_t *places;           // [2][n_tokens kv_heads]: see attn_place.h
     int *planned;               // 1, or 0 where nothing was done
 };
 
@@ -236,13 +237,7 @@ __device__ __forceinline__ int length_at(const Args &p, const Arrays &a, int b) 
     return min(max(a.lengths[b], 0), p.width << p.page_bits);
 }
 
-// Where the last kernel finds a token's results (kShared): the first range of
-// its row tile, how many ranges hold parts of it (1: the whole result), its
-// number in the tile, and whether it shares a prefix.
-__device__ __forceinline__ uint32_t place_of(int range, int parts, int tok, bool shares) {
-    static_assert(kMaxCtas <= 256 && kRows <= 128, "fields of a place");
-    return uint32_t(range) | uint32_t(parts) << 8 | uint32_t(tok) << 17 | uint32_t(shares) << 24;
-}
+static_assert(kMaxCtas <= kPlaceRanges && kRows <= kPlaceTokens, "fields of a place");
 
 // kShared counts the groups' prefixes as sequences of their own, before the
 // others: the rows of a prefix are those of all its sequences (they follow one
@@ -835,7 +830,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             held[0] = held[1];
             --behind;
         };
-        for (int i = 0; ok; ++i) {
+        // (kShared goes on without loads after a wait that gave up: the range's places
+        // must be this call's)
+        for (int i = 0; ok || F == kShared; ++i) {
             Part g{};
             int unit = 0;
             if (!cur.next<F>(p, blockIdx.x, g, unit)) g.nt = -1;
@@ -844,12 +841,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
 #pragma unroll 1
             while (ok && behind > 0 && (g.nt < 0 || held[0].part + kParts <= i)) load_held();
             if (ok && i >= kParts) ok = wait(part_empty(i % kParts), (i / kParts - 1) & 1);
-            if (!ok) break;
-            if (lane == 0) {
+            if (F != kShared && !ok) break;
+            if (ok && lane == 0) {
                 ring[i % kParts] = g;
                 mbar_arrive(part_full(i % kParts));
             }
-            if (g.nt > 0) {
+            if (ok && g.nt > 0) {
                 // Page ids of the part's boxes, 32 at a time, one per lane: two such
                 // batches at hand, so that each is loaded long before its use.
                 const int32_t *row = p.table + size_t(g.b) * p.width;
@@ -894,7 +891,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
             if (F == kShared && g.nt >= 0 && g.u == 0) {
                 // the tile's tokens are found from where it begins
                 const int first = unit - g.u, toks = g.rows / p.group, which = g.gap >= 0;
-                const int parts = split.owner(first + g.units - 1) - int(blockIdx.x) + 1;
+                const int parts = ok ? split.owner(first + g.units - 1) - int(blockIdx.x) + 1 : 0;
                 uint32_t *at = p.places + size_t(which) * p.n_tokens * p.kv_heads + g.kvh;
 #pragma unroll 1
                 for (int k = lane; k < toks; k += 32)
@@ -1560,10 +1557,12 @@ paged_attn_merge_kernel(const Args p) {
 #pragma unroll 1
     for (int kvh = blockIdx.y; kvh < p.kv_heads; kvh += gridDim.y) {
         const size_t at = size_t(t) * p.kv_heads + kvh;
-        const uint32_t own = p.places[tokens + at], pre = p.places[at];
+        const RowPlace own = read_place(p.places[tokens + at], kMaxCtas, p.slot_rows, p.group);
+        const RowPlace pre = read_place(p.places[at], kMaxCtas, p.slot_rows, p.group);
         __syncthreads();
         if (planned == 0 || covered == 0) return;            // a row of no sequence is left alone
-        const int n_own = own >> 8 & 0x1FF, n = n_own + ((own >> 24 & 1u) != 0u ? int(pre >> 8 & 0x1FF) : 0);
+        if (own.parts == 0 || (own.shares && pre.parts == 0)) continue;      // and one that was given up
+        const int n_own = own.parts, n = n_own + (own.shares ? pre.parts : 0);
 #pragma unroll 1
         for (int g = warp; g < p.group * kSlices; g += int(blockDim.x) / 32) {
             const int head = g / kSlices, col = g % kSlices * (32 * kCols) + lane * kCols;
@@ -1577,11 +1576,10 @@ paged_attn_merge_kernel(const Args p) {
             for (int i0 = 0; i0 < n; i0 += 32) {
                 const int i = i0 + lane;
                 const bool follows = i < n_own;
-                const uint32_t w = follows ? own : pre;
+                const RowPlace w = follows ? own : pre;
                 const int k = follows ? i : i - n_own;
                 size_t r = kept + (follows ? rows : 0) + row;
-                if ((w >> 8 & 0x1FF) != 1)
-                    r = size_t(2 * (int(w & 0xFF) + k) + (k == 0)) * p.slot_rows + (w >> 17 & 0x7F) * p.group + head;
+                if (w.parts != 1) r = part_slot(w.range, k) * p.slot_rows + w.tok * p.group + head;
                 float2 ml = make_float2(-INFINITY, 0.f);
                 if (i < n) ml = p.part_ml[r];
                 float v[kAhead][kCols];
