@@ -297,10 +297,11 @@ w4v_status w8_lmhead_argmax_noalloc(const uint16_t *X, const int8_t *W, const ui
  *     entropy[r]         = lse - sum_v p_v z_v, p_v = exp(z_v - lse);
  *     top_ids[r][j],     = the j-th largest logit's token and its log
  *     top_logprobs[r][j]   probability, of equal logits the lower token first.
- * Arithmetic is fp32.  Logits of -inf are tokens that cannot follow (p = 0); a
- * row of nothing else gives logprobs of -inf and an entropy of 0.  A row that
- * holds a NaN or +inf gives NaN for every token in [0, V) and for the entropy;
- * its top_ids count NaN as -inf, as the argmax does.
+ * Arithmetic is fp32, and the sums' error does not grow with V.  Logits of -inf
+ * are tokens that cannot follow (p = 0); a row of nothing else gives logprobs of
+ * -inf and an entropy of 0.  A row that holds a NaN or +inf gives NaN for every
+ * token in [0, V) and for the entropy; its top_ids count NaN as -inf, as the
+ * argmax does.
  *   logits        device, float rows of V logits (fp16 with W4V_LOGITS_FP16),
  *                 row_stride >= V elements apart; any address that is a
  *                 multiple of the element's size

@@ -33,8 +33,8 @@ def row(x, tokens, top, temperature=1.0):
 
 def bounds(x, temperature=1.0):
     """Forward error of a row's (log probability per unit of 1 + |z - z_max|, entropy) in fp32: a power is off by 2^-22
-    and 2^-22 of its exponent, a sum of up to 64 roundings in a chain by 2^-18 (each term less than that where
-    there are more, since they are summed thread by thread and then in pairs), the logarithm by 2^-22 of itself."""
+    and 2^-22 of its exponent, a sum by 64 roundings in a chain, 2^-18, whatever the row's length (longer sums
+    are made of such pieces, added up with what the additions round off), the logarithm by 2^-22 of itself."""
     x = np.asarray(x, np.float64)
     live = x[np.isfinite(x)]
     if not len(live) or np.isnan(x).any() or np.isposinf(x).any():

@@ -10,6 +10,10 @@
 // logit is more than a factor 2^kSlack above it, so nothing waits for a
 // maximum, and ln s stays so small that log probabilities near 0 keep their
 // digits.  The references meet at the end: t becomes w (t + (m - m') s).
+// Sums of 64 terms a thread are added up with what each addition rounds off
+// (Kahan), so that their error does not grow with V (equal terms, whose roundings
+// do not average out, were off by 7e-5 of s at 2^26 logits; for it 2048 rows of
+// 151,936 with five alternatives take 194 us against 191).
 //
 // A row is one CTA's, or with few rows cut over the CTAs of a cluster, joined
 // by the first of them through distributed shared memory: no workspace, no
@@ -30,9 +34,9 @@
 // row is gone through once more, a batch of every thread at a time.
 //
 // Measured (one GB300, device time; bound: the logits' bytes at 6.78 TB/s):
-//   1 row of 151,936                          4.7 us (0.1: latency); with 20 alternatives 9.2
-//   300 rows of 50,001 fp16, masked, 20       14.7 us (4.4: latency of a row's ends)
-//   2048 rows of 151,936, 5                   191 us (184: bytes, 6.5 TB/s); none 172, 20 197
+//   1 row of 151,936                          4.7 us (0.1: latency); with 20 alternatives 9.3
+//   300 rows of 50,001 fp16, masked, 20       15.3 us (4.4: latency of a row's ends)
+//   2048 rows of 151,936, 5                   194 us (184: bytes, 6.4 TB/s); none 172, 20 200
 // What bounds it: the bytes.  The powers, at 16 a clock and SM, take a third of
 // the time that 4-byte logits take from HBM.
 #include <climits>
@@ -106,6 +110,21 @@ __device__ __forceinline__ Sums join(const Sums &a, const Sums &b, float heat_lo
     return r;
 }
 
+// Long sums s and t, and what their last additions rounded off, which the next
+// ones make up for (Kahan): however many terms follow, they are off by little more
+// than their last bit.
+struct __align__(16) Long {
+    float s, s_rest, t, t_rest;
+    __device__ __forceinline__ void add(float ds, float dt) {
+        const float ys = __fadd_rn(ds, s_rest), yt = __fadd_rn(dt, t_rest);
+        const float next_s = __fadd_rn(s, ys), next_t = __fadd_rn(t, yt);
+        s_rest = __fsub_rn(ys, __fsub_rn(next_s, s));
+        t_rest = __fsub_rn(yt, __fsub_rn(next_t, t));
+        s = next_s;
+        t = next_t;
+    }
+};
+
 template <typename T>
 struct Vec;                                     // 16 bytes of logits
 template <>
@@ -142,9 +161,9 @@ struct Note {
     int first;                                  // see collect()
 };
 template <int kThreads>
-struct __align__(8) Shared {
+struct __align__(16) Shared {
     static constexpr int kLanes = kThreads / kGroups, kWarps = kThreads / 32;
-    static constexpr int kTies = kThreads;
+    static constexpr int kTies = kThreads < 256 ? kThreads : 256;
     // What a batch of every thread may add: all of 31 groups, what is equal to
     // the bound, what was there.
     static constexpr int kList = ((kMost - 1) * kLanes * kBatch + kTies + kMost + 127) / 128 * 128;
@@ -160,6 +179,7 @@ struct __align__(8) Shared {
     uint64_t best[kMost];                       // the CTA's largest, in order (0: none)
     uint64_t group_key[kGroups], bound_key;
     float group[2][kGroups], bound[2];          // by turns
+    Long sums[kThreads >= 512 ? kThreads : 1];  // see token_logprobs_kernel()
     Sums warp[kWarps], all;
     // Keys in the list, those equal to a bound, noted batches.  Counted up by
     // whoever adds one, cleared by thread 0; they are read only behind a barrier
@@ -364,11 +384,44 @@ token_logprobs_kernel(const Args p) {
     const int at_end = rank == 0 ? (tid < head ? tid : tail + tid - head < p.V ? tail + tid - head : -1) : -1;
 
     Sums mine{-INFINITY, 0.f, 0.f};
+    // s and t of this thread: of the last kFold rounds of loads, here, and of all before
+    constexpr int kFold = 8 * kRows / kLoads;    // (64 additions in a chain)
     float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
+    // (fp16 logits with alternatives, 512 threads: in shared memory, for in registers
+    // they spill where it counts, 300 masked rows 17.3 us against 14.5; elsewhere in
+    // registers, 400 rows of 151,936 55.4 against 56.3)
+    constexpr bool kFar = kTop && kThreads >= 512 && sizeof(T) == 2;
+    Long here;
+    Long &all = kFar ? sh.sums[kFar ? tid : 0] : here;
+    all = Long{0.f, 0.f, 0.f, 0.f};
+    auto fold = [&] {
+        Long x = all;
+        x.add(s.x + s.y, t.x + t.y);
+        all = x;
+        s = t = make_float2(0.f, 0.f);
+    };
+    // The thread's sums by a larger reference (none so far: they are 0, or NaN, which
+    // stays).  This rounds without making up for it: what was there shrinks to a
+    // quarter or less, so it happens few times to sums that still count.
+    auto raise = [&](float to) {
+        if (mine.m > -INFINITY) {
+            const Long x = all;
+            const float old_s = x.s + (s.x + s.y + x.s_rest), old_t = x.t + (t.x + t.y + x.t_rest);
+            const float d = mine.m - to, a = ex2(d * p.heat_log2);
+            all = Long{a * old_s, 0.f, a == 0.f ? 0.f : a * (old_t + d * old_s), 0.f};
+            s = t = make_float2(0.f, 0.f);
+        }
+        mine.m = to;
+    };
     float bound = -INFINITY, most = -INFINITY;
     bool again = false;                          // the row once more, every batch collected by all
     int listed = p.top;                          // keys in sh.list at the end (gone through again: each batch leaves top)
-    int renew = begin + 2 * kThreads * kLoads, turn = 1;     // where the next closer bound is taken
+    // Where the loop next stops for what is not done every round: folding the sums,
+    // and for CTAs of 128 threads a closer bound after 2, 4, 8, ... rounds.  (One
+    // comparison for both: a second one cost 3% of a round.)
+    constexpr int kRound = kThreads * kLoads;
+    constexpr bool kRenew = kTop && kThreads < 512;
+    int pause = begin + (kRenew ? 2 : kFold) * kRound, turn = 1;
     const float edge = at_end >= 0 ? Vec<T>::one(x0 + at_end) : -INFINITY;
     if (kTop) {
         if (tid == 0) sh.n = sh.n_notes = 0;
@@ -383,7 +436,7 @@ token_logprobs_kernel(const Args p) {
         };
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) w[i] = fetch(begin + i * kThreads + tid);
-        for (int v0 = begin; v0 == begin || v0 < end; v0 += kThreads * kLoads) {
+        for (int v0 = begin; v0 == begin || v0 < end; v0 += kRound) {
             const bool opening = kTop && !again && v0 == begin;
             if (opening) {
                 float x[W];
@@ -395,10 +448,14 @@ token_logprobs_kernel(const Args p) {
                 }
                 bound = bound_of_groups(sh, most, p.top, 0);
             }
-            if (kTop && kThreads < 512 && !again && v0 == renew) {
-                bound = bound_of_groups(sh, most, p.top, turn);
-                turn ^= 1;
-                renew += renew - begin;
+            if (v0 == pause) {                   // (never in the second pass: every one was met in the first)
+                fold();
+                const int rounds = (v0 - begin) / kRound;
+                pause += (kRenew ? min(rounds, kFold) : kFold) * kRound;
+                if (kRenew && (rounds & (rounds - 1)) == 0) {
+                    bound = bound_of_groups(sh, most, p.top, turn);
+                    turn ^= 1;
+                }
             }
 #pragma unroll
             for (int b = 0; b < kLoads; b += kRows) {
@@ -440,13 +497,7 @@ token_logprobs_kernel(const Args p) {
                         if (at < Sh::kNotes) sh.notes[at] = Note{top, first};
                     }
                 }
-                if (top > mine.m + p.slack || (mine.m == -INFINITY && top > -INFINITY)) {
-                    const float d = mine.m - top, a = mine.m == -INFINITY ? 1.f : ex2(d * p.heat_log2);
-                    if (mine.m > -INFINITY)
-                        t = a == 0.f ? make_float2(0.f, 0.f) : make_float2(a * (t.x + d * s.x), a * (t.y + d * s.y));
-                    s = make_float2(a * s.x, a * s.y);
-                    mine.m = top;
-                }
+                if (top > mine.m + p.slack || (mine.m == -INFINITY && top > -INFINITY)) raise(top);
                 const float ref = mine.m == -INFINITY ? 0.f : mine.m;
                 const float2 minus = make_float2(-ref, -ref), by = make_float2(p.heat_log2, p.heat_log2);
 #pragma unroll
@@ -494,19 +545,14 @@ token_logprobs_kernel(const Args p) {
     // last write, which no barrier has parted from this.
     if (kTop) best_of_list(sh, p.top, listed);
     if (at_end >= 0 && (edge > -INFINITY || edge != edge)) {
-        if (edge > mine.m) {
-            const float d = mine.m - edge, a = mine.m == -INFINITY ? 1.f : ex2(d * p.heat_log2);
-            if (mine.m > -INFINITY)
-                t = a == 0.f ? make_float2(0.f, 0.f) : make_float2(a * (t.x + d * s.x), a * (t.y + d * s.y));
-            s = make_float2(a * s.x, a * s.y);
-            mine.m = edge;
-        }
+        if (edge > mine.m) raise(edge);
         const float d = edge - (mine.m == -INFINITY ? 0.f : mine.m), e2 = ex2(d * p.heat_log2);
         s.x += e2;
         t.x += e2 * fmaxf(d, -3e38f);
     }
-    mine.s = s.x + s.y;
-    mine.t = t.x + t.y;
+    const Long last = all;
+    mine.s = last.s + (s.x + s.y + last.s_rest);
+    mine.t = last.t + (t.x + t.y + last.t_rest);
 
     // the warp's sums by its largest reference, the CTA's, then the cluster's
     {

@@ -176,6 +176,32 @@ def test_rows_anywhere(w4v_mod, gpu, half, off, pad):
     compare(x, t, 20, 1.0, got)
 
 
+@pytest.mark.parametrize("half,M,V,top", [(False, 4, 1 << 22, 0), (False, 4, 1 << 26, 0), (False, 4, 1 << 24, 3),
+                                          (True, 4, 1 << 26, 0), (True, 4, 1 << 26, 2), (False, 1300, 400_000, 0),
+                                          (True, 1300, 400_000, 0), (False, 1300, 800_000, 5)])
+def test_long_sums_of_equal_terms(w4v_mod, gpu, half, M, V, top):
+    """One value over and over beside a higher one: the terms are equal and no power of two, so that what the additions
+    round off adds up instead of averaging out.  The bound is that of any row (scores.bounds), the expectation a
+    period's."""
+    d = torch.tensor([-0.3, -1.7, -np.log(3.0), -2.9], device=gpu)
+    d = (d.half() if half else d).double()
+    low = d.cpu().numpy()[np.arange(M) % 4]
+    x = torch.zeros((M, V), device=gpu, dtype=torch.float16 if half else torch.float32)
+    for r in range(M):
+        x[r].view(-1, 4)[:, 1:] = float(low[r])
+    t = torch.tensor([[0, 1]], dtype=torch.int32, device=gpu).expand(M, 2).contiguous()
+    lp, h, _, _ = (y.cpu().numpy() for y in w4v_mod.token_logprobs(x, t, top=top))
+    for r in range(M):
+        period = np.array([0.0, low[r], low[r], low[r]])
+        per, eh = scores.bounds(period)
+        more = 2.0 ** -22 * np.log(V / 4)                  # the logarithm's own term in both bounds, of the whole row
+        lse = np.log(V / 4) + np.log(np.exp(period).sum())
+        p = np.exp(period - lse) * (V / 4)
+        assert abs(lp[r, 0] + lse) <= per + more
+        assert abs(lp[r, 1] - (low[r] - lse)) <= per + more + 2.0 ** -21 * abs(low[r])
+        assert abs(h[r] - (lse - (p * period).sum())) <= eh + more, (r, h[r], lse - (p * period).sum(), eh + more)
+
+
 def test_rows_past_32_bits(w4v_mod, gpu):
     """Rows 2^30 elements apart."""
     rng = np.random.default_rng(4)
