@@ -272,7 +272,8 @@ norm_rope_append_kernel(const Args p) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             if (i < pairs) put(x, g, w[n][x][1] * c, w[n][x][0] * s);
-            put(x, f, w[n][x][0] * c, -w[n][x][1] * s);
+            // (a single element's own is +0, as in the kernel below: -0 would give zeros another sign)
+            put(x, f, w[n][x][0] * c, i < pairs ? -w[n][x][1] * s : 0.f);
         }
     }
     long long slot = -1;                                         // head 0's elements of this token

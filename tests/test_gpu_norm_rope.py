@@ -236,6 +236,26 @@ def test_rows_do_not_depend_on_the_others(w4v_mod, gpu, D, rot, inter):
         assert torch.equal(got, whole[a:b]) and torch.equal(d["k"], kept)
 
 
+@pytest.mark.parametrize("D,rot,inter", [(128, 32, False), (64, 16, False), (256, 64, True), (64, 8, True), (128, 50, False),
+                                         (64, 22, True), (128, 0, False)])
+def test_zeros_keep_their_signs_in_every_call(w4v_mod, gpu, D, rot, inter):
+    """Bit for bit means zeros too: negative ones among the inputs, past the rotated part and in it."""
+    rng, w = np.random.default_rng([D, rot, 12]), w4v_mod
+    c = cache(rng, [4000], [4096], 1, 2, D, 64)
+    x = [np.where(rng.random(a.shape) < 0.3, np.float16(-0.0), np.where(rng.random(a.shape) < 0.2, np.float16(0.0), a))
+         for a in rows(rng, 4000, 6, 2, D)]
+    q, k, v = (to_dev(a, gpu) for a in x)
+    norm = w.HeadNorm(*(to_dev(g * np.where(rng.random(D) < 0.5, 1, -1).astype(np.float16), gpu) for g in weights(rng, D)))
+    d, rope = {a: to_dev(b, gpu) for a, b in c.items()}, w.Rope(rot, interleaved=inter)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=gpu)  # noqa: E731
+    bits = lambda a: a.view(torch.int16)  # noqa: E731
+    whole = w.norm_rope_append(q, k, v, d["k"], d["v"], d["table"], d["lengths"], d["offsets"], rope, norm)
+    kept = d["k"].clone()
+    for a, b in ((0, 2500), (17, 18), (1000, 1016), (3999, 4000)):
+        got = w.norm_rope_append(q[a:b], k[a:b], v[a:b], d["k"], d["v"], d["table"], i32(96 + b), i32(0, b - a), rope, norm)
+        assert torch.equal(bits(got), bits(whole[a:b])) and torch.equal(bits(d["k"]), bits(kept))
+
+
 def test_agrees_with_the_separate_steps(w4v_mod, gpu):
     """rope_append of heads normed beforehand: one more rounding to fp16, of the normed head."""
     rng, w = np.random.default_rng(10), w4v_mod
