@@ -204,7 +204,9 @@ norm_rope_append_kernel(const Args p) {
     const __half *qs = p.q + t * p.q_stride, *ks = p.k + t * p.k_stride, *vs = p.v + t * p.v_stride;
     const int e = 8 * (tid & (D / 8 - 1)), first = tid / (D / 8), step = kThreads / (D / 8);
     const int turned = p.q_heads + p.kv_heads, heads = turned + p.kv_heads;
-    // The lane that holds the partner piece (half layout), or this one.
+    // The lane that holds the partner piece (half layout), or this one.  (What is
+    // not rotated has itself for a partner in both layouts, by a factor of 0: an
+    // infinity then spoils no other element.)
     const int partner = kInter || e >= p.rot ? int(threadIdx.x & 31) : int(threadIdx.x & 31) + (e >= p.rot / 2 ? -p.rot / 16 : p.rot / 16);
     Piece a[kNormAhead];
     auto load = [&](int h0) {
@@ -313,7 +315,7 @@ norm_rope_append_kernel(const Args p) {
                         const float4 m = coef[h < p.q_heads ? 0 : 1][i][e / 8];
                         const uint32_t w = h2_as_u32(a[u].h[i]);
                         const float2 x = __half22float2(a[u].h[i]);
-                        const float2 y = kInter ? make_float2(x.y, x.x)
+                        const float2 y = kInter ? e < p.rot ? make_float2(x.y, x.x) : x
                                                 : __half22float2(u32_as_h2(__shfl_sync(0xFFFFFFFFu, w, partner)));
                         const float2 v = __ffma2_rn(y, make_float2(m.z, m.w), __fmul2_rn(x, make_float2(m.x, m.y)));
                         o.h[i] = __float22half2_rn(__fmul2_rn(v, make_float2(r, r)));
@@ -468,7 +470,7 @@ norm_rope_append_warp_kernel(const Args p) {
         Piece o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float2 y = make_float2(f[i].y, f[i].x);
+            float2 y = turn ? make_float2(f[i].y, f[i].x) : f[i];
             if (!kInter) y = __half22float2(u32_as_h2(__shfl_sync(0xFFFFFFFFu, h2_as_u32(x.h[i]), partner)));
             const float2 z = __ffma2_rn(y, other[i], __fmul2_rn(f[i], own[i]));
             o.h[i] = __float22half2_rn(__fmul2_rn(z, make_float2(r, r)));

@@ -118,6 +118,34 @@ def test_zeros_and_what_is_not_finite_stay_in_their_head(w4v_mod, gpu, rot, inte
     assert torch.equal(d["k"].nan_to_num(7.0), kept.nan_to_num(7.0))
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("rot", [64, 50, 0])
+@pytest.mark.parametrize("n", [3, 4000])
+def test_an_infinity_divides_the_rest_of_its_head(w4v_mod, gpu, n, rot, inter):
+    """x / sqrt(inf) is 0 for what is finite; the infinity itself, and what it is rotated with, becomes NaN."""
+    rng, w = np.random.default_rng([n, rot, inter]), w4v_mod
+    c = cache(rng, [n], [n + 3], 1, 2, 128, 64)
+    q, k, v = rows(rng, n, 3, 2, 128)
+    bad = {0: (100,), 1: (101,), 2: (66, 127)} if rot else {0: (0,), 1: (1,), 2: (66, 127)}
+    for h, at in bad.items():
+        for i in at:
+            q[:, h, i] = np.inf if i % 2 else -np.inf
+    k[:, 1, 111] = np.inf
+    d = {x: to_dev(a, gpu) for x, a in c.items()}
+    wq, wk = weights(rng, 128)
+    got = w.norm_rope_append(*(to_dev(x, gpu) for x in (q, k, v)), d["k"], d["v"], d["table"], d["lengths"], d["offsets"],
+                             w.Rope(rot, interleaved=inter), w.HeadNorm(to_dev(wq, gpu), to_dev(wk, gpu)))
+    for h, at in bad.items():
+        nan = torch.zeros(128, dtype=torch.bool, device=gpu)
+        nan[list(at)] = True
+        assert torch.equal(torch.isnan(got[:, h]), nan.expand(n, 128))
+        assert torch.all(got[:, h][:, ~nan] == 0)
+    page = d["k"][d["table"][0, 0].long(), 1, 3:10]               # the first new tokens' second key head
+    nan = torch.arange(128, device=gpu) == 111
+    for row in page[:min(n, 7)]:
+        assert torch.equal(torch.isnan(row), nan) and torch.all(row[~nan] == 0)
+
+
 def test_positions_and_scalings(w4v_mod, gpu):
     rng = np.random.default_rng(6)
     c = cache(rng, [6], [100], 1, 2, 128, 8)
