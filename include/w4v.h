@@ -301,7 +301,8 @@ w4v_status w8_lmhead_argmax_noalloc(const uint16_t *X, const int8_t *W, const ui
  * are tokens that cannot follow (p = 0); a row of nothing else gives logprobs of
  * -inf and an entropy of 0.  A row that holds a NaN or +inf gives NaN for every
  * token in [0, V) and for the entropy; its top_ids count NaN as -inf, as the
- * argmax does.
+ * argmax does.  Logits further apart than fp32's largest number count as
+ * infinitely far, whatever the temperature.
  *   logits        device, float rows of V logits (fp16 with W4V_LOGITS_FP16),
  *                 row_stride >= V elements apart; any address that is a
  *                 multiple of the element's size

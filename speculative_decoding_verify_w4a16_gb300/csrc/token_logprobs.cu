@@ -1,15 +1,17 @@
 // token_logprobs.cu -- log probabilities of given tokens, the rows' entropy
 // and their most likely tokens, from the lm_head's logits.
 //
-// With d_v = x_v - m, m a reference near a row's largest logit, and h = 1 /
-// temperature,
-//     s = sum_v e^(h d_v),  t = sum_v d_v e^(h d_v):
-//     log p_v = h d_v - ln s,   entropy = ln s - h t / s.
+// With y_v = (x_v - m) log2(e) / temperature, m a reference near a row's largest
+// logit,
+//     s = sum_v 2^y_v,  t = sum_v y_v 2^y_v:
+//     log p_v = (x_v - m) / temperature - ln s,   entropy = ln s - ln 2 t / s.
+// (t in the exponents' unit: in the logits' own, large ones overflow it.)
 // One pass: each logit is read once.  A thread has its own reference, the
 // largest of its first 16 logits, which it raises (s and t rescaled) when a
 // logit is more than a factor 2^kSlack above it, so nothing waits for a
 // maximum, and ln s stays so small that log probabilities near 0 keep their
-// digits.  The references meet at the end: t becomes w (t + (m - m') s).
+// digits.  The references meet at the end: t becomes w (t + y s), y the
+// exponent of w.
 // Sums of 64 terms a thread are added up with what each addition rounds off
 // (Kahan), so that their error does not grow with V (equal terms, whose roundings
 // do not average out, were off by 7e-5 of s at 2^26 logits; for it 2048 rows of
@@ -48,7 +50,7 @@ namespace w4v {
 namespace {
 
 constexpr int kBatch = 16;                      // logits of a thread that are looked at together
-constexpr float kSlack = 2.f;
+constexpr float kSlack = 2.f, kLn2 = 0.6931471805599453f;
 constexpr int kGroups = 64;
 constexpr int kMost = kLogprobsMaxTop;
 static_assert(kMost <= kGroups, "the bound is a group's largest");
@@ -99,11 +101,11 @@ __device__ __forceinline__ Sums join(const Sums &a, const Sums &b, float heat_lo
     const float m = fmaxf(a.m, b.m);
     Sums r{m, 0.f, 0.f};
     // Without a logit above -inf a side is s = t = 0, or NaN, which stays.  A
-    // weight of 0 leaves t's term out: the distance may be infinite.
+    // weight of 0 leaves t's term out: the exponent may be infinite.
     auto add = [&](const Sums &x) {
-        const float d = x.m - m, w = x.m == -INFINITY ? 1.f : ex2(d * heat_log2);
+        const float y = (x.m - m) * heat_log2, w = x.m == -INFINITY ? 1.f : ex2(y);
         r.s += w * x.s;
-        if (x.m > -INFINITY && w != 0.f) r.t += w * (x.t + d * x.s);
+        if (x.m > -INFINITY && w != 0.f) r.t += w * (x.t + y * x.s);
     };
     add(a);
     add(b);
@@ -407,8 +409,8 @@ token_logprobs_kernel(const Args p) {
         if (mine.m > -INFINITY) {
             const Long x = all;
             const float old_s = x.s + (s.x + s.y + x.s_rest), old_t = x.t + (t.x + t.y + x.t_rest);
-            const float d = mine.m - to, a = ex2(d * p.heat_log2);
-            all = Long{a * old_s, 0.f, a == 0.f ? 0.f : a * (old_t + d * old_s), 0.f};
+            const float y = (mine.m - to) * p.heat_log2, a = ex2(y);
+            all = Long{a * old_s, 0.f, a == 0.f ? 0.f : a * (old_t + y * old_s), 0.f};
             s = t = make_float2(0.f, 0.f);
         }
         mine.m = to;
@@ -502,14 +504,12 @@ token_logprobs_kernel(const Args p) {
                 const float2 minus = make_float2(-ref, -ref), by = make_float2(p.heat_log2, p.heat_log2);
 #pragma unroll
                 for (int k = 0; k < kBatch; k += 2) {
-                    float2 d = __fadd2_rn(make_float2(x[k], x[k + 1]), minus);
-                    float2 e = __fmul2_rn(d, by);
-                    e.x = ex2(e.x);
-                    e.y = ex2(e.y);
+                    float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[k], x[k + 1]), minus), by);
+                    const float2 e = make_float2(ex2(y.x), ex2(y.y));
                     s = __fadd2_rn(s, e);
-                    d.x = fmaxf(d.x, -3e38f);                    // 0 times -inf is 0 (a NaN is in s already)
-                    d.y = fmaxf(d.y, -3e38f);
-                    t = __ffma2_rn(e, d, t);
+                    y.x = fmaxf(y.x, -3e38f);                    // 0 times -inf is 0 (a NaN is in s already)
+                    y.y = fmaxf(y.y, -3e38f);
+                    t = __ffma2_rn(e, y, t);
                 }
                 refill();
             }
@@ -546,9 +546,9 @@ token_logprobs_kernel(const Args p) {
     if (kTop) best_of_list(sh, p.top, listed);
     if (at_end >= 0 && (edge > -INFINITY || edge != edge)) {
         if (edge > mine.m) raise(edge);
-        const float d = edge - (mine.m == -INFINITY ? 0.f : mine.m), e2 = ex2(d * p.heat_log2);
+        const float y = (edge - (mine.m == -INFINITY ? 0.f : mine.m)) * p.heat_log2, e2 = ex2(y);
         s.x += e2;
-        t.x += e2 * fmaxf(d, -3e38f);
+        t.x += e2 * fmaxf(y, -3e38f);
     }
     const Long last = all;
     mine.s = last.s + (s.x + s.y + last.s_rest);
@@ -588,7 +588,7 @@ token_logprobs_kernel(const Args p) {
         const float log_s = logf(a.s);
         // nothing above -inf: no token has a probability
         auto logprob = [&](float x) { return a.s == 0.f ? -INFINITY : p.heat * (x - a.m) - log_s; };
-        if (tid == 0 && p.entropy != nullptr) p.entropy[row] = a.s == 0.f ? 0.f : log_s - p.heat * a.t / a.s;
+        if (tid == 0 && p.entropy != nullptr) p.entropy[row] = a.s == 0.f ? 0.f : log_s - kLn2 * a.t / a.s;
         for (int i = tid; i < p.n; i += kThreads) {
             const int at = p.tokens[size_t(row) * p.n + i];
             p.logprobs[size_t(row) * p.n + i] = at >= 0 && at < p.V ? logprob(Vec<T>::one(x0 + at)) : -INFINITY;

@@ -163,6 +163,15 @@ def test_sizes(w4v_mod, gpu, size):
     check(w4v_mod, gpu, x, given(rng, 4, 6001, 3), top=9)
 
 
+@pytest.mark.parametrize("V", [500, 6001, 40_000])
+@pytest.mark.parametrize("size,temperature", [(1e30, 1e30), (1e37, 1e37), (3e37, 1e38), (1.0, 1e38), (1e-37, 1e-37)])
+def test_logits_and_temperatures_of_a_size(w4v_mod, gpu, V, size, temperature):
+    """Ordinary ratios of numbers at the ends of fp32: no sum is taken in the logits' own unit."""
+    rng = np.random.default_rng([V, 5])
+    x = np.clip(rng.standard_normal((3, V)) * size, -1.6e38, 1.6e38).astype(np.float32)
+    check(w4v_mod, gpu, x, given(rng, 3, V, 3), top=9, temperature=temperature)
+
+
 @pytest.mark.parametrize("half", [False, True])
 @pytest.mark.parametrize("off,pad", [(0, 1), (1, 0), (2, 3), (3, 2), (5, 7), (7, 8)])
 def test_rows_anywhere(w4v_mod, gpu, half, off, pad):
