@@ -601,6 +601,12 @@ w4v_status paged_attn_sinks(const w4v_kv_t *kv, const uint16_t *q, long long q_s
  * than prefix[g] tokens before its new ones; those attend over their own pages.
  * Sequences without new tokens may lie anywhere in a group.
  * A row that several sequences name gets no meaningful result.
+ * When to use it: where several sequences of a group bring few rows each (well
+ * under tok = 128 / (q_heads / kv_heads)) and the prefix is long.  On this GPU it
+ * is faster than paged_attn from about 16 one-token sequences over a prefix of
+ * 2000 tokens, 8 over 8000 or 4 over 32,000 on (64 over 32,000: seven times),
+ * slower by up to 5 us below, and slower by half for prompt chunks, whose rows
+ * fill tiles by themselves: those belong in paged_attn.
  * flags must be 0 (how a row's sum is cut depends on the batch).  Sizes as
  * paged_attn, 0 <= n_groups <= B (a group may be empty), and (2 (n_tokens / tok) + min(B,
  * n_tokens) + min(n_groups, n_tokens)) * kv_heads * (table_width * page / 128

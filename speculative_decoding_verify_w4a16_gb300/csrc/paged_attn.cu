@@ -37,7 +37,9 @@
 // a part leaves o, m and l in the workspace (at most two parts a CTA), and a
 // second kernel joins them, each boundary's CTAs a share of the tile's rows.
 // The lengths are on the device, so each CTA finds its own range by a scan
-// over the sequences.
+// over the sequences.  With batch invariance the unit is a fixed range of keys,
+// every one a part of its own: which keys meet in one running sum then depends
+// on the row alone.
 //
 // First tokens beside a window (kSinks): a row tile's key tiles are those of the
 // first tokens and those of the window, numbered without the gap between them;
@@ -51,9 +53,7 @@
 // once per sequence, and 128 rows are in use.  What follows the prefix is each
 // sequence's own.  Every part keeps its unnormalised output in 32 bits, and one
 // last kernel joins a row's parts of both kinds, told by a word per token and
-// key/value head where they are.  With batch invariance the unit is a fixed range of
-// keys, every one a part of its own: which keys meet in one running sum then
-// depends on the row alone.
+// key/value head where they are.
 //
 // A weight of 0 does not hide a value that is not finite (0 x inf is NaN),
 // and within a tile some rows see keys that others must not.  Where a tile
@@ -103,12 +103,17 @@
 // tensor pipe 61-71% active).
 // First tokens and shared prefixes (bounds as above):
 //   1 token over 20,000, window 1000, 4 first, 20 on 4 of 128        10.2 us (0.3: latency)
-//   24 x up to 21 over 12,000, window 2000, 300 first, 16 on 4 of 256 45.4 us (27.3: bytes)
+//   24 x up to 21 over 12,000, window 2000, 300 first, 16 on 4 of 256 45.6 us (27.3: bytes)
 //   8192 tokens, window 1024, 64 first, 20 heads of 128               111 us (45: products)
 //   8 x 1 token over 2000 shared and 100, 20 on 4 of 128             13.6 us (0.7: latency; apart 13.6)
 //   2 x 16 x up to 16 over 8200 shared and 700, 20 on 4 of 128       36.0 us (8.2: products; apart 59)
-//   64 x 1 over 32,781 shared and 900, 16 on 4 of 256                64.2 us (37.6: bytes; apart 784)
-// ("apart": kPlain, every sequence over all its pages.)  A window's row tiles are
+//   64 x 1 over 32,781 shared and 900, 16 on 4 of 256                63.7 us (37.6: bytes; apart 784)
+// ("apart": kPlain, every sequence over all its pages.  kShared gains where rows
+// of several sequences fill a row tile that each would have alone, over a prefix
+// long enough: 16 single tokens over 2000 14.4 us against 16.3, over 500 13.9
+// against 12.9; 64 over 32,000 42 against 307.  Rows that fill tiles by themselves
+// only pay for the results in 32 bits: 4 x 512 over 8000 193 against 132.)  With
+// batch invariance the first three take 13.2, 51.1 and 319 us.  A window's row tiles are
 // ten key tiles, and between two of them the product waits for O to be read and
 // stored (some 4000 cycles of 24,000; 106 us without the stores).  64 tokens are
 // two row tiles over the prefix: their 128 x 128 tiles of 256-wide heads run at

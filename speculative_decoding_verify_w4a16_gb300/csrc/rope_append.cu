@@ -26,7 +26,8 @@
 // brackets are worked out once per CTA and lie in shared memory by piece, and
 // r, the head's factor, multiplies last.  Measured (device time): 16 rows of 28 x
 // 128 2.9 us, 660 rows of 60 x 128 6.7 (bound 3.4: bytes), 8192 rows of 24 x 256
-// 38.1 (29.7; 5.3 TB/s).
+// 38.1 (29.7; 5.3 TB/s), interleaved 37.2; pair by pair (rot 50) 96, and 5.5 for
+// 16 rows of 28 x 128: 2-byte loads and stores.
 #include <algorithm>
 
 #include "runtime.h"
